@@ -18,9 +18,10 @@ from . import _build
 D, H, HI, DI, GROUP, BLOCK = 512, 16, 4, 128, 16, 8
 CODE_BYTES, SCALE_BYTES = 256, 32
 MAX_LAYERS = 16
+MAX_TREE, MAX_SEQS, MAX_MV_ROWS = 64, 8192, 32
 MODE_FULL, MODE_REINDEX, MODE_REUSE = 0, 1, 2
 OP_TOPK, OP_BLOCK_POOL, OP_SPARSE_ATTN, OP_GROUP_STEP, OP_INDEX_SELECT_PREFILL, OP_MERGE_PAIRS = 1, 2, 3, 4, 5, 6
-FLAG_APPEND_OOB, FLAG_INDEX_OOB, FLAG_TIMEOUT = 1, 2, 4
+FLAG_APPEND_OOB, FLAG_INDEX_OOB, FLAG_TIMEOUT, FLAG_PAGES_OUT = 1, 2, 4, 8
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_WORKSPACE, ERR_TOO_LARGE = 0, 1, 2, 3, 4, 5
 SWA_BF16, SWA_E4M3 = 0, 1
 
@@ -98,6 +99,13 @@ def lib():
             "csa2_merge_topk_pairs": [P, P, P, I32, I32, I32, P, P, P, SZ, P],
             "csa2_shard_indices": [P, I32, I32, I64, I64, P, P],
             "csa2_attn_merge_shards": [P, P, I32, I32, P, P, P],
+            "csa2_block_tables": [P, P, I32, I32, P, I32, P, I32, P, P, P, I32, P],
+            "csa2_context_slots": [P, P, P, I32, I32, P, I32, I32, P, I64, P, P],
+            "csa2_paged_append": [P, P, P, I64, P, P, P, I64, P],
+            "csa2_tree_attn": [P, I32, I32, P, P, P, P, I64, I32, P, P, I32, P, P, I32, F32, P, P, P],
+            "csa2_fp4_packed_bytes": [I64, I64],
+            "csa2_fp4_pack_weight": [P, P, I64, I64, P, P],
+            "csa2_fp4_matvec": [P, I32, P, I64, I64, P, P, I32, P],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -107,6 +115,7 @@ def lib():
         L.csa2_status_string.restype = ctypes.c_char_p
         L.csa2_group_desc_size.restype = SZ
         L.csa2_sparse_attn_static_scratch_bytes.restype = SZ
+        L.csa2_fp4_packed_bytes.restype = SZ
         if L.csa2_group_desc_size() != ctypes.sizeof(GroupDesc):
             raise RuntimeError("csa2_group_desc layout mismatch between binding and library")
         _lib = L
@@ -432,3 +441,155 @@ def csa2_attn_merge_shards(out_g, lse_g, out, lse=None, stream=None):
         _ptr(out_g, "out_g", _bf16_types(), G * rows * H * D), _ptr(lse_g, "lse_g", (torch.float32,), G * rows * H),
         G, rows, _ptr(out, "out", _bf16_types(), rows * H * D), _ptr(lse, "lse", (torch.float32,), rows * H),
         _stream(stream)))
+
+
+# ---------------------------------------------------------------------------------------------
+# drafted tokens over a paged cache, and 4-bit weights
+# ---------------------------------------------------------------------------------------------
+def _shape(t, name, shape):
+    """t has exactly `shape` (None entries are free); returns it as a tuple."""
+    if t is None:
+        return None
+    got = tuple(t.shape)
+    if len(got) != len(shape) or any(w is not None and g != w for g, w in zip(got, shape)):
+        raise ValueError(f"{name}: expected shape {tuple('?' if w is None else w for w in shape)}, got {got}")
+    return got
+
+
+def _one_device(*tensors):
+    """Every tensor lies on the current device, whose stream and kernels the call uses."""
+    torch = _torch()
+    cur = torch.cuda.current_device() if torch.cuda.is_available() else None
+    for t in tensors:
+        if t is not None and t.is_cuda and t.device.index != cur:
+            raise ValueError(f"expected tensors on the current device cuda:{cur}, got one on {t.device}")
+
+
+def csa2_block_tables(old_lens, new_lens, page_size, block_table, free_pages, pool_state, granted, *, slots=None,
+                      stream=None):
+    """Pages for the sequences that grow from old_lens to new_lens int32 [B], taken back from those that
+    shrink: block_table int32 [B, max_pages], free_pages int32 [free_cap], pool_state int32 [4] (the first
+    holds the number of free pages), granted int32 [B] the lengths in effect, slots int32 [B, n_new] the
+    slots of positions old_lens[b] + i (-1 from granted[b] on)."""
+    i32 = (_torch().int32,)
+    B, max_pages = _shape(block_table, "block_table", (None, None))
+    for t, name in ((old_lens, "old_lens"), (new_lens, "new_lens"), (granted, "granted")):
+        _shape(t, name, (B,))
+    _shape(free_pages, "free_pages", (None,))
+    _shape(pool_state, "pool_state", (4,))
+    n_new = _shape(slots, "slots", (B, None))[1] if slots is not None else 0
+    args = [_ptr(old_lens, "old_lens", i32), _ptr(new_lens, "new_lens", i32), B, int(page_size),
+            _ptr(block_table, "block_table", i32), max_pages, _ptr(free_pages, "free_pages", i32), free_pages.numel(),
+            _ptr(pool_state, "pool_state", i32), _ptr(granted, "granted", i32), _ptr(slots, "slots", i32), n_new]
+    _one_device(old_lens, new_lens, block_table, free_pages, pool_state, granted, slots)
+    _check("csa2_block_tables", lib().csa2_block_tables(*args, _stream(stream)))
+
+
+def csa2_context_slots(lens, slots, n_slots, *, block_table=None, page_size=0, parent=None, n_nodes=None, stream=None):
+    """slots int32 [B*N, ld]: per drafted node the slots of its sequence's lens[b] committed positions, then of
+    its ancestors and itself, then -1; n_slots int32 [B*N] their number.  parent int32 [B, N] (None: the
+    committed positions only); block_table int32 [B, max_pages] (None: positions instead of slots)."""
+    i32 = (_torch().int32,)
+    B, = _shape(lens, "lens", (None,))
+    rows, ld = _shape(slots, "slots", (None, None))
+    N = _shape(parent, "parent", (B, None))[1] if parent is not None else (rows // B if B else 0)
+    _shape(slots, "slots", (B * N, ld))
+    _shape(n_slots, "n_slots", (B * N,))
+    _shape(n_nodes, "n_nodes", (B,))
+    max_pages = _shape(block_table, "block_table", (B, None))[1] if block_table is not None else 0
+    args = [_ptr(lens, "lens", i32), _ptr(parent, "parent", i32), _ptr(n_nodes, "n_nodes", i32), B, N,
+            _ptr(block_table, "block_table", i32), max_pages, int(page_size), _ptr(slots, "slots", i32), ld,
+            _ptr(n_slots, "n_slots", i32)]
+    _one_device(lens, slots, n_slots, block_table, parent, n_nodes)
+    _check("csa2_context_slots", lib().csa2_context_slots(*args, _stream(stream)))
+
+
+def csa2_paged_append(slots, *, kv_new=None, codes=None, scales=None, ki_new=None, KI=None, stream=None):
+    """Row i of kv_new bf16 [n, 512] is quantised into row slots[i] of codes uint8 [n_slots, 256] and scales
+    uint8 [n_slots, 32], row i of ki_new bf16 [n, 128] copied to row slots[i] of KI bf16 [n_slots, 128];
+    negative slots are padding.  Either pair may be left out."""
+    torch = _torch()
+    n = slots.numel()
+    n_slots = codes.shape[0] if codes is not None else KI.shape[0] if KI is not None else 0
+    _shape(slots.reshape(-1) if slots.is_contiguous() else slots, "slots", (n,))
+    _shape(kv_new, "kv_new", (n, D))
+    _shape(ki_new, "ki_new", (n, DI))
+    _shape(codes, "codes", (n_slots, CODE_BYTES))
+    _shape(scales, "scales", (n_slots, SCALE_BYTES))
+    _shape(KI, "KI", (n_slots, DI))
+    u8 = (torch.uint8,)
+    args = [_ptr(kv_new, "kv_new", _bf16_types()), _ptr(ki_new, "ki_new", _bf16_types()),
+            _ptr(slots, "slots", (torch.int32,)), n, _ptr(codes, "codes", u8), _ptr(scales, "scales", u8),
+            _ptr(KI, "KI", _bf16_types()), n_slots]
+    _one_device(slots, kv_new, codes, scales, ki_new, KI)
+    _check("csa2_paged_append", lib().csa2_paged_append(*args, _stream(stream)))
+
+
+def csa2_tree_attn(q, parent, codes, scales, idx, out, *, n_nodes=None, n_valid=None, swa=None, win_len=None, W=0,
+                   softmax_scale=None, lse=None, stream=None):
+    """Attention of a tree of drafted tokens: q [B, N, 16, 512]; parent int32 [B, N]; codes / scales
+    [B, cap, *], or [cap, *] for one pool shared by all sequences; idx int32 [B*N, k] cache rows;
+    swa [B, W-1+N, 512] (the committed window, then the drafted rows); out as q, lse fp32 [B, N, 16]."""
+    torch = _torch()
+    i32, u8 = (torch.int32,), (torch.uint8,)
+    B, N = _shape(q, "q", (None, None, H, D))[:2]
+    _shape(parent, "parent", (B, N))
+    _shape(n_nodes, "n_nodes", (B,))
+    pool = codes.dim() == 2
+    cap = codes.shape[0 if pool else 1]
+    _shape(codes, "codes", (cap, CODE_BYTES) if pool else (B, cap, CODE_BYTES))
+    _shape(scales, "scales", (cap, SCALE_BYTES) if pool else (B, cap, SCALE_BYTES))
+    k = _shape(idx, "idx", (B * N, None))[1]
+    _shape(n_valid, "n_valid", (B * N,))
+    if swa is None:
+        W = 0
+    else:
+        _shape(swa, "swa", (B, W - 1 + N, D))
+    _shape(win_len, "win_len", (B,))
+    _shape(out, "out", (B, N, H, D))
+    _shape(lse, "lse", (B, N, H))
+    if softmax_scale is None:
+        softmax_scale = D ** -0.5
+    bf = _bf16_types()
+    args = [_ptr(q, "q", bf), B, N, _ptr(parent, "parent", i32), _ptr(n_nodes, "n_nodes", i32),
+            _ptr(codes, "codes", u8), _ptr(scales, "scales", u8), cap, int(pool), _ptr(idx, "idx", i32),
+            _ptr(n_valid, "n_valid", i32), k, _ptr(swa, "swa", bf), _ptr(win_len, "win_len", i32), int(W),
+            float(softmax_scale), _ptr(out, "out", bf), _ptr(lse, "lse", (torch.float32,))]
+    _one_device(q, parent, codes, scales, idx, out, n_nodes, n_valid, swa, win_len, lse)
+    _check("csa2_tree_attn", lib().csa2_tree_attn(*args, _stream(stream)))
+
+
+def fp4_weight_alloc(n_out, n_in, device="cuda"):
+    """An empty packed weight of n_out output rows and n_in input channels (a multiple of 16)."""
+    if n_in % GROUP:
+        raise ValueError(f"n_in: expected a multiple of {GROUP}, got {n_in}")
+    return _torch().empty(int(lib().csa2_fp4_packed_bytes(n_out, n_in)), dtype=_torch().uint8, device=device)
+
+
+def csa2_fp4_pack_weight(codes, scales, packed, stream=None):
+    """Lays codes uint8 [n_out, n_in/2] and scales uint8 [n_out, n_in/16] out for csa2_fp4_matvec."""
+    u8 = (_torch().uint8,)
+    n_out, half = _shape(codes, "codes", (None, None))
+    _shape(scales, "scales", (n_out, 2 * half // GROUP))
+    if (2 * half) % GROUP:
+        raise ValueError(f"codes: expected a multiple of {GROUP} input channels, got {2 * half}")
+    _shape(packed, "packed", (int(lib().csa2_fp4_packed_bytes(n_out, 2 * half)),))
+    args = [_ptr(codes, "codes", u8), _ptr(scales, "scales", u8), n_out, 2 * half, _ptr(packed, "packed", u8)]
+    _one_device(codes, scales, packed)
+    _check("csa2_fp4_pack_weight", lib().csa2_fp4_pack_weight(*args, _stream(stream)))
+
+
+def csa2_fp4_matvec(x, packed, y, *, row_scale=None, stream=None):
+    """y [m, n_out] (bf16 or fp32) = row_scale * (x bf16 [m, n_in] times the packed weight), m <= 32."""
+    torch = _torch()
+    m, n_in = _shape(x, "x", (None, None))
+    _, n_out = _shape(y, "y", (m, None))
+    if n_in % GROUP:
+        raise ValueError(f"x: expected a multiple of {GROUP} input channels, got {n_in}")
+    _shape(packed, "packed", (int(lib().csa2_fp4_packed_bytes(n_out, n_in)),))
+    _shape(row_scale, "row_scale", (n_out,))
+    args = [_ptr(x, "x", _bf16_types()), m, _ptr(packed, "packed", (torch.uint8,)), n_out, n_in,
+            _ptr(row_scale, "row_scale", (torch.float32,)), _ptr(y, "y", _bf16_types() + (torch.float32,)),
+            int(y.dtype == torch.float32)]
+    _one_device(x, packed, y, row_scale)
+    _check("csa2_fp4_matvec", lib().csa2_fp4_matvec(*args, _stream(stream)))

@@ -180,6 +180,39 @@ __global__ void __launch_bounds__(256) append_kernel(const uint16_t* __restrict_
   }
 }
 
+// The paged append: a warp per new row, lane g quantising channels 16g .. 16g+15 into the row's slot and
+// lanes 0..15 copying 16 bytes of its indexer key each.  Streaming, HBM-bound.
+__global__ void __launch_bounds__(256) paged_append_kernel(const uint16_t* __restrict__ kv_new,
+                                                           const uint16_t* __restrict__ ki_new,
+                                                           const int32_t* __restrict__ slots, int64_t n,
+                                                           uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
+                                                           uint16_t* __restrict__ KI, int64_t n_slots,
+                                                           unsigned int* flags) {
+  pdl_wait();
+  pdl_trigger();
+  const int64_t row = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+  const int g = threadIdx.x & 31;
+  if (row >= n) return;
+  const int64_t at = slots[row];
+  if (at < 0) return;  // padding
+  if (at >= n_slots) {
+    if (g == 0) atomicOr(flags, CSA2_FLAG_APPEND_OOB);
+    return;
+  }
+  uint4 key = make_uint4(0, 0, 0, 0);
+  if (ki_new && g < CSA2_DI / 8) key = ld_stream16(ki_new + row * CSA2_DI + g * 8);
+  if (kv_new) {
+    const uint16_t* src = kv_new + row * CSA2_D + g * CSA2_GROUP;
+    const uint4 v0 = ld_stream16(src), v1 = ld_stream16(src + 8);
+    const uint32_t wv[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+    uint32_t lo, hi, sb;
+    quantize_group(wv, lo, hi, sb);
+    *reinterpret_cast<uint2*>(codes + at * CSA2_CODE_BYTES + g * 8) = make_uint2(lo, hi);
+    scales[at * CSA2_SCALE_BYTES + g] = uint8_t(sb);
+  }
+  if (ki_new && g < CSA2_DI / 8) *reinterpret_cast<uint4*>(KI + at * CSA2_DI + g * 8) = key;
+}
+
 __global__ void __launch_bounds__(256) zero_kernel(uint4* __restrict__ p, int64_t n16) {
   pdl_wait();
   pdl_trigger();
@@ -422,6 +455,26 @@ extern "C" csa2_status csa2_block_keys_build(const uint16_t* KI, int B, int64_t 
   if (!KI || !lens || !block_keys || !al16(KI) || !al16(block_keys)) return CSA2_ERR_INVALID_ARG;
   return csa2::launch_block_keys(KI, B, cap, lens, block_keys, 0, 0,
                                  reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? CSA2_OK
+             : CSA2_ERR_CUDA;
+}
+
+extern "C" csa2_status csa2_paged_append(const uint16_t* kv_new, const uint16_t* ki_new, const int32_t* slots,
+                                         int64_t n, uint8_t* codes, uint8_t* scales, uint16_t* KI, int64_t n_slots,
+                                         csa2_stream_t stream) {
+  // one warp per row, eight rows a block
+  if (n < 0 || n > (int64_t(1) << 33) || n_slots < 0) return CSA2_ERR_INVALID_ARG;
+  const bool kv = kv_new || codes || scales, ki = ki_new || KI;
+  if (kv && (!kv_new || !codes || !scales)) return CSA2_ERR_INVALID_ARG;
+  if (ki && (!ki_new || !KI)) return CSA2_ERR_INVALID_ARG;
+  if (!al16(kv_new) || !al16(ki_new) || !al16(codes) || !al16(scales) || !al16(KI)) return CSA2_ERR_INVALID_ARG;
+  if (n == 0 || (!kv && !ki)) return CSA2_OK;
+  if (!slots || (reinterpret_cast<uintptr_t>(slots) & 3u)) return CSA2_ERR_INVALID_ARG;
+  unsigned int* flags = csa2::device_flags_ptr();
+  if (!flags) return CSA2_ERR_CUDA;
+  return csa2::launch_pdl(csa2::paged_append_kernel, dim3(csa2::grid_for(n * 32, 256)), dim3(256), 0,
+                          reinterpret_cast<cudaStream_t>(stream), kv_new, ki_new, slots, n, codes, scales, KI, n_slots,
+                          flags) == cudaSuccess
              ? CSA2_OK
              : CSA2_ERR_CUDA;
 }

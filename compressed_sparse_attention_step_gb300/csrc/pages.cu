@@ -1,0 +1,293 @@
+// Pages of a shared cache pool: block tables and slot maps built on the GPU from request lengths, and the
+// slot lists of what a drafted node may attend.  Integer work bound by launch latency for a decode step and
+// by the slots written for an admission or a long context.
+//
+// csa2_block_tables, one launch: sequence b asks for max(want - held, 0) pages and gives back
+// max(held - want, 0).  Both counts are summed over the sequences by every CTA for itself (two words per
+// sequence), after which the owner of the j-th page asked for, and the page it gets, follow from a search in
+// the sums: pages are handed out from the list's end and from those given back, never from what the same
+// launch writes (list entries at or past n_free, table entries of pages newly held).  So CTAs share
+// nothing but the count of free pages, which the last of them to finish updates.
+#include <algorithm>
+
+#include "common.cuh"
+
+namespace csa2 {
+namespace pages {
+
+constexpr int kThreads = 1024;
+
+__device__ __forceinline__ int pages_of(int len, int shift) {  // ceil(len / page), len up to 2^31 - 1
+  return (len >> shift) + ((len & ((1 << shift) - 1)) != 0);
+}
+// first b in [0, n) with incl[b] > v (incl ascending, incl[n - 1] > v)
+__device__ __forceinline__ int owner(const int* incl, int n, int v) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (incl[mid] > v) hi = mid;
+    else lo = mid + 1;
+  }
+  return lo;
+}
+__device__ __forceinline__ int slot_of(int page, int off, int shift) {  // -1: no such slot
+  return page >= 0 && page <= (0x7FFFFFFF >> shift) ? (page << shift) + off : -1;
+}
+
+__global__ void __launch_bounds__(kThreads) block_tables_kernel(
+    const int32_t* __restrict__ old_lens, const int32_t* __restrict__ new_lens, int B, int shift,
+    int32_t* block_table, int max_pages, int32_t* free_pages, int free_cap, int32_t* pool_state, int32_t* granted,
+    int32_t* __restrict__ slots, int n_new, unsigned int* flags) {
+  extern __shared__ int sums[];  // inclusive sums of the pages asked for, then of those given back
+  __shared__ uint32_t scan_tmp[32];
+  int* ask = sums;
+  int* back = sums + B;
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x;
+  const int64_t gtid = int64_t(blockIdx.x) * kThreads + tid, gthreads = int64_t(gridDim.x) * kThreads;
+  const int n_free = min(max(pool_state[0], 0), free_cap);
+  const int64_t room = int64_t(max_pages) << shift;
+  auto old_of = [&](int b) { return int(min(int64_t(max(old_lens[b], 0)), room)); };
+  auto new_of = [&](int b) { return max(new_lens[b], 0); };
+
+  uint32_t ask0 = 0, back0 = 0;
+  for (int c = 0; c < B; c += kThreads) {
+    const int b = c + tid;
+    uint32_t a = 0, r = 0;
+    if (b < B) {
+      const int held = pages_of(old_of(b), shift), want = pages_of(new_of(b), shift);
+      if (want > held && want <= max_pages) a = uint32_t(want - held);
+      if (want < held) r = uint32_t(held - want);
+    }
+    uint32_t ta, tr;
+    const uint32_t ea = block_exclusive_scan(a, scan_tmp, &ta), er = block_exclusive_scan(r, scan_tmp, &tr);
+    if (b < B) ask[b] = int(ask0 + ea + a), back[b] = int(back0 + er + r);
+    ask0 += ta, back0 += tr;
+  }
+  __syncthreads();
+  const int F = int(back0);
+  const int64_t budget = int64_t(n_free) + F;
+  // sequences ask in order, so the granted pages are a prefix of those asked for
+  int A = 0;
+  if (int64_t(ask0) <= budget) A = int(ask0);
+  else {
+    int lo = 0, hi = B - 1;  // first sequence whose sum passes the budget
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (int64_t(ask[mid]) > budget) hi = mid;
+      else lo = mid + 1;
+    }
+    A = lo > 0 ? ask[lo - 1] : 0;
+  }
+  auto given_back = [&](int f) {  // the f-th page given back
+    const int b = owner(back, B, f), first = b > 0 ? back[b - 1] : 0;
+    return block_table[int64_t(b) * max_pages + pages_of(new_of(b), shift) + (f - first)];
+  };
+  auto handed_out = [&](int j) { return j < F ? given_back(j) : free_pages[n_free - 1 - (j - F)]; };
+  auto is_granted = [&](int b) {
+    const int want = pages_of(new_of(b), shift), held = pages_of(old_of(b), shift);
+    return want <= held || (want <= max_pages && ask[b] <= A);
+  };
+
+  for (int64_t b = gtid; b < B; b += gthreads) {
+    const bool ok = is_granted(int(b));
+    granted[b] = ok ? new_of(int(b)) : old_of(int(b));
+    if (!ok) atomicOr(flags, CSA2_FLAG_PAGES_OUT);
+  }
+  for (int64_t j = gtid; j < A; j += gthreads) {
+    const int b = owner(ask, B, int(j)), first = b > 0 ? ask[b - 1] : 0;
+    block_table[int64_t(b) * max_pages + pages_of(old_of(b), shift) + (j - first)] = handed_out(int(j));
+  }
+  for (int64_t f = A + gtid; f < F; f += gthreads) {
+    const int64_t at = int64_t(n_free) + F - 1 - f;
+    if (at < free_cap) free_pages[at] = given_back(int(f));
+  }
+  const int64_t n_slots = int64_t(B) * n_new;
+  for (int64_t i = gtid; i < n_slots; i += gthreads) {
+    const int b = int(uint32_t(i) / uint32_t(n_new)), c = int(i) - b * n_new;
+    const int o = old_of(b);
+    int s = -1;
+    if (c < new_of(b) - o && is_granted(b)) {
+      const int pos = o + c, pg = pos >> shift, held = pages_of(o, shift);
+      const int page = pg < held ? block_table[int64_t(b) * max_pages + pg]
+                                 : handed_out((b > 0 ? ask[b - 1] : 0) + pg - held);
+      s = slot_of(page, pos & ((1 << shift) - 1), shift);
+      if (s < 0) atomicOr(flags, CSA2_FLAG_INDEX_OOB);
+    }
+    slots[i] = s;
+  }
+
+  // the last CTA to get here has seen every other read the old count
+  __syncthreads();
+  if (tid == 0) {
+    const unsigned int done = atomicAdd(reinterpret_cast<unsigned int*>(pool_state + 1), 1u);
+    if (done == gridDim.x - 1) {
+      pool_state[0] = int(min(budget - A, int64_t(free_cap)));
+      pool_state[1] = 0;
+    }
+  }
+}
+
+constexpr int kCtxThreads = 256;
+
+// A thread lists four columns for every node of its sequence: up to the committed length a column is the
+// same slot for all of them, so the block table is read once per page and thread.  kVec: rows are stored as
+// 16-byte pieces (ld a multiple of 4).
+template <bool kVec>
+__global__ void __launch_bounds__(kCtxThreads) context_slots_kernel(
+    const int32_t* __restrict__ lens, const int32_t* __restrict__ parent, const int32_t* __restrict__ n_nodes, int N,
+    const int32_t* __restrict__ block_table, int max_pages, int shift, int32_t* __restrict__ slots, int64_t ld,
+    int32_t* __restrict__ n_slots, unsigned int* flags) {
+  __shared__ unsigned long long anc[CSA2_MAX_TREE];
+  __shared__ int par[CSA2_MAX_TREE];
+  pdl_wait();
+  pdl_trigger();
+  const int b = blockIdx.y, tid = threadIdx.x;
+  const int len = max(lens[b], 0);
+  const int nn = n_nodes ? min(max(n_nodes[b], 0), N) : N;
+  if (parent && tid < N) par[tid] = parent[int64_t(b) * N + tid];
+  __syncthreads();
+  if (tid < N) {
+    unsigned long long m = 0;
+    bool bad = false;
+    if (parent && tid < nn)
+      for (int cur = tid; cur >= 0;) {
+        m |= 1ull << cur;
+        const int up = par[cur];
+        if (up < -1 || up >= cur) {
+          bad = true;
+          break;
+        }
+        cur = up;
+      }
+    anc[tid] = m;
+    if (blockIdx.x == 0) {
+      const int64_t n = tid < nn ? int64_t(len) + __popcll(m) : 0;
+      n_slots[int64_t(b) * N + tid] = int32_t(min(n, ld));
+      if (bad || n > ld) atomicOr(flags, CSA2_FLAG_INDEX_OOB);
+    }
+  }
+  __syncthreads();
+  const int32_t* table = block_table ? block_table + int64_t(b) * max_pages : nullptr;
+  auto slot = [&](int64_t pos) -> int {
+    if (!table) return pos <= 0x7FFFFFFF ? int(pos) : -1;
+    const int64_t pg = pos >> shift;
+    const int s = pg < max_pages ? slot_of(table[pg], int(pos & ((1 << shift) - 1)), shift) : -1;
+    if (s < 0) atomicOr(flags, CSA2_FLAG_INDEX_OOB);
+    return s;
+  };
+  const int64_t c0 = (int64_t(blockIdx.x) * kCtxThreads + tid) * 4;
+  if (c0 >= ld) return;
+  int common[4];
+  if (c0 + 3 < len && table) {  // four columns of one page
+    const int64_t pg = c0 >> shift;
+    const int s = pg < max_pages ? slot_of(table[pg], int(c0 & ((1 << shift) - 1)), shift) : -1;
+    if (s < 0 && nn > 0) atomicOr(flags, CSA2_FLAG_INDEX_OOB);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) common[i] = s < 0 ? -1 : s + i;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) common[i] = c0 + i < len && nn > 0 ? slot(c0 + i) : -1;
+  }
+  int32_t* dst = slots + int64_t(b) * N * ld + c0;
+  for (int r = 0; r < N; ++r, dst += ld) {
+    int v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = r < nn ? common[i] : -1;
+    if (c0 + 3 >= len && r < nn) {
+      unsigned long long m = anc[r];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t nth = c0 + i - len;  // the nth drafted row of the list
+        if (nth < 0 || nth >= __popcll(m)) continue;
+        unsigned long long w = m;
+        for (int64_t j = 0; j < nth; ++j) w &= w - 1;
+        v[i] = slot(int64_t(len) + __ffsll(static_cast<long long>(w)) - 1);
+      }
+    }
+    if (kVec) {
+      *reinterpret_cast<int4*>(dst) = make_int4(v[0], v[1], v[2], v[3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (c0 + i < ld) dst[i] = v[i];
+    }
+  }
+}
+
+inline int page_shift(int page_size) {  // -1: not a power of two in 16..1024
+  for (int s = 4; s <= 10; ++s)
+    if (page_size == 1 << s) return s;
+  return -1;
+}
+inline bool al(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + nb && y < x + na;
+}
+
+}  // namespace pages
+}  // namespace csa2
+
+extern "C" csa2_status csa2_block_tables(const int32_t* old_lens, const int32_t* new_lens, int B, int page_size,
+                                         int32_t* block_table, int max_pages, int32_t* free_pages, int free_cap,
+                                         int32_t* pool_state, int32_t* granted, int32_t* slots, int n_new,
+                                         csa2_stream_t stream) {
+  using namespace csa2;
+  using namespace csa2::pages;
+  const int shift = page_shift(page_size);
+  if (shift < 0 || B < 0 || B > CSA2_MAX_SEQS || max_pages < 1 || free_cap < 0 || n_new < 0 ||
+      int64_t(B) * max_pages > 0x7FFFFFFFll || int64_t(B) * n_new > 0x7FFFFFFFll ||
+      (int64_t(max_pages) << shift) > 0x7FFFFFFFll)
+    return CSA2_ERR_INVALID_ARG;
+  if (B == 0) return CSA2_OK;
+  if (!old_lens || !new_lens || !block_table || !free_pages || !pool_state || !granted || (n_new > 0 && !slots))
+    return CSA2_ERR_INVALID_ARG;
+  const void* all[] = {old_lens, new_lens, block_table, free_pages, pool_state, granted, slots};
+  for (const void* p : all)
+    if (!al(p, 4)) return CSA2_ERR_INVALID_ARG;
+  const struct { const void* p; size_t n; } in[] = {{old_lens, size_t(B) * 4}, {new_lens, size_t(B) * 4},
+      {block_table, size_t(B) * max_pages * 4}, {free_pages, size_t(free_cap) * 4}, {pool_state, 16}};
+  for (const auto& i : in)
+    if (overlap(granted, size_t(B) * 4, i.p, i.n) || overlap(slots, size_t(B) * n_new * 4, i.p, i.n))
+      return CSA2_ERR_INVALID_ARG;
+  if (overlap(granted, size_t(B) * 4, slots, size_t(B) * n_new * 4)) return CSA2_ERR_INVALID_ARG;
+  unsigned int* flags = device_flags_ptr();
+  const int sms = sm_count();
+  if (!flags || sms <= 0) return CSA2_ERR_CUDA;
+  // four items a thread; how many pages change hands is known on the device alone
+  const int64_t items = std::max(int64_t(B) * n_new, int64_t(B) * max_pages / 16);
+  const int grid = int(std::min<int64_t>(std::max<int64_t>(items / (4 * kThreads), 1), sms));
+  const size_t smem = size_t(B) * 8;
+  if (smem > 48 * 1024 && cudaFuncSetAttribute(block_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               int(smem)) != cudaSuccess)
+    return CSA2_ERR_CUDA;
+  return launch_pdl(block_tables_kernel, dim3(grid), dim3(kThreads), smem, reinterpret_cast<cudaStream_t>(stream),
+                    old_lens, new_lens, B, shift, block_table, max_pages, free_pages, free_cap, pool_state, granted,
+                    slots, n_new, flags) == cudaSuccess
+             ? CSA2_OK
+             : CSA2_ERR_CUDA;
+}
+
+extern "C" csa2_status csa2_context_slots(const int32_t* lens, const int32_t* parent, const int32_t* n_nodes, int B,
+                                          int N, const int32_t* block_table, int max_pages, int page_size,
+                                          int32_t* slots, int64_t ld, int32_t* n_slots, csa2_stream_t stream) {
+  using namespace csa2;
+  using namespace csa2::pages;
+  int shift = 4;
+  if (B < 0 || B > 65535 || N < 0 || N > CSA2_MAX_TREE || ld < 0 || ld > 0x7FFFFFFFll) return CSA2_ERR_INVALID_ARG;
+  if (block_table && (max_pages < 1 || (shift = page_shift(page_size)) < 0)) return CSA2_ERR_INVALID_ARG;
+  if (int64_t(B) * N == 0) return CSA2_OK;
+  if (!lens || !slots || !n_slots || !al(lens, 4) || !al(parent, 4) || !al(n_nodes, 4) || !al(block_table, 4) ||
+      !al(slots, 16) || !al(n_slots, 4))
+    return CSA2_ERR_INVALID_ARG;
+  unsigned int* flags = device_flags_ptr();
+  if (!flags) return CSA2_ERR_CUDA;
+  const unsigned gx = unsigned(std::max<int64_t>((ld + 4 * kCtxThreads - 1) / (4 * kCtxThreads), 1));
+  auto kern = ld % 4 == 0 ? context_slots_kernel<true> : context_slots_kernel<false>;
+  return launch_pdl(kern, dim3(gx, unsigned(B)), dim3(kCtxThreads), 0, reinterpret_cast<cudaStream_t>(stream), lens,
+                    parent, n_nodes, N, block_table, max_pages, shift, slots, ld, n_slots, flags) == cudaSuccess
+             ? CSA2_OK
+             : CSA2_ERR_CUDA;
+}

@@ -71,6 +71,9 @@ typedef enum {
 #define CSA2_MAX_ATTN_K 512 /* largest number of selected rows attended          */
 #define CSA2_MAX_W 128      /* largest sliding window                            */
 #define CSA2_MAX_LAYERS 16  /* layers per group descriptor                       */
+#define CSA2_MAX_TREE 64    /* drafted nodes per sequence                        */
+#define CSA2_MAX_SEQS 8192  /* sequences of one csa2_block_tables call           */
+#define CSA2_MAX_MV_ROWS 32 /* token rows of csa2_fp4_matvec                     */
 
 /* Layer modes (ai-maestro "Compressed Sparse Attention 2"). */
 #define CSA2_MODE_FULL 0
@@ -85,6 +88,7 @@ typedef enum {
 #define CSA2_FLAG_APPEND_OOB 1u /* an appended row fell outside [0, cap): row skipped   */
 #define CSA2_FLAG_INDEX_OOB 2u  /* a selected index was >= cap: row treated as empty    */
 #define CSA2_FLAG_TIMEOUT 4u    /* a kernel gave up waiting for its tensor-core work     */
+#define CSA2_FLAG_PAGES_OUT 8u  /* csa2_block_tables refused a sequence its pages        */
 
 /*
  * FP4 quantise-and-append.  "Main key-value cache quantises to E2M1 with one E4M3 scale per
@@ -394,6 +398,114 @@ csa2_status csa2_shard_indices(const int32_t* idx, int rows, int k, int64_t lo, 
  * row no shard attended gets out = 0, lse = -inf.  out_g and out 16-byte aligned. */
 csa2_status csa2_attn_merge_shards(const uint16_t* out_g, const float* lse_g, int G, int rows, uint16_t* out,
                                    float* lse, csa2_stream_t stream);
+
+/*
+ * Verifying drafted tokens over a paged cache.  The pages name the drafting (wpnews.pro "DeepSeek V4.1
+ * Flash Specs", "What other architectural components does it use?": DSpark drafts five tokens which the
+ * model verifies) and not how the cache serves it; this is the plainest exact form.  A pool of cache rows
+ * (codes, scales, KI) is cut into pages of page_size rows and shared by all sequences; position p of
+ * sequence b lives in slot block_table[b][p / page_size] * page_size + p % page_size.  A verify step:
+ *   csa2_block_tables    grants pages for the drafts and lists their slots;
+ *   csa2_paged_append    writes the drafts' FP4 rows and indexer keys into those slots;
+ *   csa2_context_slots   per drafted node: the slots it may select (the committed positions and its
+ *                        drafted ancestors), the `cand` of csa2_index_score and the `map` of csa2_topk,
+ *                        with the whole pool as one sequence (B = 1, Nq = rows);
+ *   csa2_tree_attn       every node's attention, with the pool as its cache;
+ *   csa2_block_tables    again, from the drafted to the accepted lengths: rejected pages go back.
+ */
+
+/*
+ * Block tables and slot maps from request lengths.  Sequence b grows or shrinks from old_lens[b] to
+ * new_lens[b] tokens and holds ceil(len / page_size) pages before and after.  Pages that shrinking
+ * sequences give back are on offer in the same call.  With F pages given back (numbered in sequence order,
+ * a sequence's own pages ascending) and n_free free ones, the j-th page asked for (numbered likewise) is
+ * the j-th given back while j < F, then free_pages[n_free - 1 - (j - F)]; what is left of the pages given
+ * back goes on top of the list, the first on the very top.  So a change followed by its undo restores the
+ * list and every table.  A sequence is granted its pages iff new_lens[b] fits max_pages pages and the pages
+ * asked for up to and including it are at most n_free + F; otherwise it keeps its old length and
+ * CSA2_FLAG_PAGES_OUT is set.
+ *   old_lens, new_lens int32 [B], B <= CSA2_MAX_SEQS (lengths below 0 count as 0, old lengths past the
+ *              table as the table's end);
+ *   block_table int32 [B][max_pages]: entries of new pages are written, all others are left as they are;
+ *   free_pages int32 [free_cap], pool_state int32 [4]: [0] the number of free pages, updated by the call;
+ *              [1] to [3] are the library's and zero between calls;
+ *   granted    int32 [B]: the length in effect after the call;
+ *   slots      int32 [B][n_new] or NULL: the slot of position old_lens[b] + i, -1 from granted[b] on.
+ * page_size is a power of two in 16..1024; B * max_pages and B * n_new are below 2^31.  granted and slots
+ * overlap no input.  Calls on one pool are ordered by the caller.
+ */
+csa2_status csa2_block_tables(const int32_t* old_lens, const int32_t* new_lens, int B, int page_size,
+                              int32_t* block_table, int max_pages, int32_t* free_pages, int free_cap,
+                              int32_t* pool_state, int32_t* granted, int32_t* slots, int n_new,
+                              csa2_stream_t stream);
+
+/*
+ * The slots of everything a drafted node may attend: row b*N + i of `slots` holds the slots of positions
+ * 0 .. lens[b]-1 of sequence b, then of lens[b] + j for the ancestors j of node i and i itself (node j of
+ * the draft lies at cache position lens[b] + j), and -1 behind them; n_slots[b*N + i] is their number.
+ *   lens    int32 [B]: committed positions;
+ *   parent  int32 [B][N] or NULL: parent[b][i] < i is node i's parent, -1 a child of the committed context;
+ *           NULL: no drafts, every row lists the committed positions only;
+ *   n_nodes int32 [B] or NULL (N): rows of nodes at or past it are all -1 with n_slots 0;
+ *   block_table int32 [B][max_pages] or NULL: NULL lists positions instead of slots;
+ *   slots   int32 [B*N][ld], n_slots int32 [B*N].  N <= CSA2_MAX_TREE.
+ * A slot past ld, a position past the table and a parent out of order (taken as -1) set
+ * CSA2_FLAG_INDEX_OOB; a position past the table is listed as -1.
+ * As `cand` of csa2_index_score over a pool (B = 1, cap = the pool's rows) the rows need not ascend,
+ * provided that q_pos lets every query see the whole pool (q_pos[r] >= ratio * cap - 1).
+ */
+csa2_status csa2_context_slots(const int32_t* lens, const int32_t* parent, const int32_t* n_nodes, int B, int N,
+                               const int32_t* block_table, int max_pages, int page_size, int32_t* slots, int64_t ld,
+                               int32_t* n_slots, csa2_stream_t stream);
+
+/*
+ * Paged append: row i of kv_new is quantised (as csa2_fp4_quantize_append) into cache row slots[i], and row
+ * i of ki_new copied into indexer-key row slots[i].  A negative slot is padding and skipped; a slot >= n_slots
+ * is skipped and sets CSA2_FLAG_APPEND_OOB.  Distinct rows need distinct slots.
+ *   kv_new bf16 [n][512] with codes uint8 [n_slots][256] and scales uint8 [n_slots][32], or all NULL;
+ *   ki_new bf16 [n][128] with KI bf16 [n_slots][128], or both NULL;  slots int32 [n].
+ */
+csa2_status csa2_paged_append(const uint16_t* kv_new, const uint16_t* ki_new, const int32_t* slots, int64_t n,
+                              uint8_t* codes, uint8_t* scales, uint16_t* KI, int64_t n_slots, csa2_stream_t stream);
+
+/*
+ * Attention of a tree of drafted tokens.  Node i of sequence b (depth d, 0 for a child of the committed
+ * context) attends its selected rows, the rows r >= d of the W - 1 committed window rows and the window rows
+ * of its ancestors of depth above d - W (itself included): the rows that the last of d + 1 tokens of a chain
+ * attends in csa2_sparse_attn_decode.  K = V = the row, softmax over the union.
+ *   q       bf16 [B][N][16][512], N <= CSA2_MAX_TREE;  parent, n_nodes as csa2_context_slots (parent required);
+ *           outputs of nodes at or past n_nodes[b] are left as they were.
+ *   codes   uint8, scales uint8: with shared_pool = 0 [B][cap][256] and [B][cap][32], with shared_pool = 1 one
+ *           pool [cap][256] and [cap][32] that every sequence's indices point into.
+ *   idx     int32 [B*N][k] cache rows (k <= 512), n_valid int32 [B*N] or NULL: entries < 0 or at or past
+ *           n_valid[r] are empty, entries >= cap are empty and set CSA2_FLAG_INDEX_OOB.
+ *   swa     bf16 [B][W-1+N][512]: W - 1 committed rows, oldest first, then the N drafted rows; or NULL with W = 0.
+ *   win_len int32 [B] or NULL (W - 1): the last win_len[b] committed rows hold tokens.
+ *   out     bf16 [B][N][16][512]; lse fp32 [B][N][16] (nullable), natural log; a node with no rows (W = 0 and
+ *           nothing selected) gets out = 0 and lse = -inf.
+ * No workspace.  The result does not depend on scheduling.
+ */
+csa2_status csa2_tree_attn(const uint16_t* q, int B, int N, const int32_t* parent, const int32_t* n_nodes,
+                           const uint8_t* codes, const uint8_t* scales, int64_t cap, int shared_pool,
+                           const int32_t* idx, const int32_t* n_valid, int k, const uint16_t* swa,
+                           const int32_t* win_len, int W, float softmax_scale, uint16_t* out, float* lse,
+                           csa2_stream_t stream);
+
+/*
+ * Products of a few token rows with a 4-bit weight in the cache's format: E2M1 codes, one E4M3 scale per 16
+ * input channels, and an fp32 scale per output row (NVFP4's global scale, per row):
+ *   y[m][n] = row_scale[n] * sum_k x[m][k] * E2M1(codes[n][k]) * E4M3(scales[n][k / 16]).
+ * csa2_fp4_pack_weight lays a row-major weight out once in the order the product reads it:
+ *   codes uint8 [n_out][n_in/2], scales uint8 [n_out][n_in/16] -> packed, csa2_fp4_packed_bytes(n_out, n_in)
+ *   bytes.  n_in a multiple of 16.
+ * csa2_fp4_matvec: x bf16 [m][n_in], m <= CSA2_MAX_MV_ROWS; row_scale fp32 [n_out] or NULL (1); y [m][n_out],
+ *   bf16 (y_fp32 = 0) or fp32 (y_fp32 = 1).  Accumulated in fp32, rounded once.  No workspace.
+ */
+size_t csa2_fp4_packed_bytes(int64_t n_out, int64_t n_in);
+csa2_status csa2_fp4_pack_weight(const uint8_t* codes, const uint8_t* scales, int64_t n_out, int64_t n_in,
+                                 uint8_t* packed, csa2_stream_t stream);
+csa2_status csa2_fp4_matvec(const uint16_t* x, int m, const uint8_t* packed, int64_t n_out, int64_t n_in,
+                            const float* row_scale, void* y, int y_fp32, csa2_stream_t stream);
 
 /* Workspace sizing. */
 #define CSA2_OP_TOPK 1

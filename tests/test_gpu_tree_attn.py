@@ -1,0 +1,224 @@
+"""Attention of a tree of drafted tokens against a plain 64-bit form, bound by bound."""
+import numpy as np
+import pytest
+
+from tests import _verify as V
+from tests._cases import bf16_dev, bf16_host, to_dev
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("no CUDA device", allow_module_level=True)
+import compressed_sparse_attention_step_gb300 as c  # noqa: E402
+
+SCALE = 512 ** -0.5
+
+
+class Case:
+    def __init__(self, seed, B, N, T, k, W, *, pool=True, shape="random", qscale=1.0, full=False):
+        g = self.g = np.random.default_rng(seed)
+        self.B, self.N, self.T, self.k, self.W, self.pool = B, N, T, k, W, pool
+        self.q = V.bf16(g, (B, N, 16, 512), qscale)
+        self.codes, self.scales = V.random_fp4(g, B * T, 512)
+        self.swa = V.bf16(g, (B, W - 1 + N, 512)) if W else None
+        self.parent = V.random_parents(g, B, N, shape)
+        self.n_nodes = np.array([N if full or b == 0 else g.integers(0, N + 1) for b in range(B)], np.int32)
+        self.win_len = np.array([max(W - 1, 0) if full or b == 0 else g.integers(0, max(W, 1)) for b in range(B)], np.int32)
+        self.idx = np.full((B * N, k), -1, np.int32)
+        self.n_valid = np.zeros(B * N, np.int32)
+        for r in range(B * N):
+            n = min(k, T)
+            rows = np.sort(g.choice(T, n, replace=False)) + (r // N * T if pool else 0)
+            if not full:
+                rows = np.where(g.random(n) < 0.05, -1, rows)          # empty entries anywhere
+            self.idx[r, :n] = rows
+            self.n_valid[r] = k if full or g.random() < 0.5 else g.integers(0, k + 1)
+
+    def dev(self):
+        B, T = self.B, self.T
+        codes, scales = to_dev(self.codes), to_dev(self.scales)
+        if not self.pool:
+            codes, scales = codes.view(B, T, 256), scales.view(B, T, 32)
+        return dict(q=bf16_dev(self.q), parent=to_dev(self.parent), codes=codes, scales=scales, idx=to_dev(self.idx),
+                    n_nodes=to_dev(self.n_nodes), n_valid=to_dev(self.n_valid),
+                    swa=bf16_dev(self.swa) if self.W else None, win_len=to_dev(self.win_len), W=self.W,
+                    out=torch.full((B, self.N, 16, 512), 9.0, dtype=torch.bfloat16, device="cuda"),
+                    lse=torch.full((B, self.N, 16), 9.0, dtype=torch.float32, device="cuda"))
+
+    def check(self, d, scale=SCALE):
+        out, lse = V.f64(bf16_host(d["out"])), d["lse"].cpu().numpy().astype(np.float64)
+        swa = V.f64(self.swa) if self.W else None
+        worst = 0.0
+        for b in range(self.B):
+            for i in range(self.N):
+                if i >= self.n_nodes[b]:                               # left as they were
+                    assert (out[b, i] == 9.0).all() and (lse[b, i] == 9.0).all()
+                    continue
+                r = b * self.N + i
+                at = self.idx[r, :self.n_valid[r]]
+                at = at[at >= 0]
+                base = 0 if self.pool else b * self.T
+                sel = V.dequant(self.codes[base + at], self.scales[base + at])
+                win = V.tree_rows(b, i, parent=self.parent, rows=None, swa=swa, W=self.W, win_len=self.win_len)
+                o, l, tol, tl = V.tree_node(V.f64(self.q[b, i]), sel, win, scale)
+                err = np.abs(out[b, i] - o)
+                assert (err <= tol).all(), f"b{b} node {i}: worst {np.max(err - tol):.3e} over the bound"
+                if sel.shape[0] + win.shape[0]:
+                    assert (np.abs(lse[b, i] - l) <= tl).all(), f"b{b} node {i}: lse off by {np.abs(lse[b, i] - l).max():.3e}"
+                    worst = max(worst, float((err / np.maximum(tol, 1e-30)).max()))
+                else:
+                    assert (lse[b, i] == -np.inf).all()
+        return worst
+
+
+@pytest.mark.parametrize("B,N,T,k,W,pool,shape", [
+    (1, 1, 1, 1, 1, True, "chain"), (1, 1, 40, 16, 0, True, "chain"), (1, 1, 40, 17, 0, False, "chain"),
+    (2, 5, 600, 512, 128, True, "random"), (3, 7, 333, 100, 128, False, "random"), (2, 13, 50, 33, 9, True, "random"),
+    (1, 64, 80, 31, 128, True, "chain"), (1, 64, 40, 15, 20, False, "chain"), (2, 20, 64, 48, 3, True, "star"),
+    (4, 3, 5, 512, 128, True, "random"), (3, 4, 30, 0, 40, True, "random"), (2, 3, 30, 0, 1, False, "chain"),
+    (40, 5, 100, 64, 30, True, "random"), (90, 4, 70, 40, 17, False, "random"),
+])
+def test_tree_attn(B, N, T, k, W, pool, shape):
+    cs = Case(B * 100 + N + W, B, N, T, k, W, pool=pool, shape=shape)
+    d = cs.dev()
+    c.csa2_device_flags()
+    c.csa2_tree_attn(**d)
+    assert c.csa2_device_flags() == 0
+    cs.check(d)
+    first = d["out"].clone(), d["lse"].clone()
+    c.csa2_tree_attn(**d)
+    assert torch.equal(first[0], d["out"]) and torch.equal(first[1], d["lse"])
+
+
+def test_no_rows_at_all():
+    """Nothing selected and no window: out 0, lse -inf, at both launch forms."""
+    for B in (1, 200):
+        cs = Case(3, B, 2, 8, 4, 0, full=True)
+        cs.n_valid[:] = 0
+        d = cs.dev()
+        c.csa2_tree_attn(**d)
+        assert (d["out"] == 0).all() and (d["lse"] == float("-inf")).all()
+
+
+@pytest.mark.parametrize("qscale", [2.0 ** -40, 2.0 ** -130, 2.0 ** 20, 1e3])
+def test_q_of_any_magnitude(qscale):
+    """Q is scaled to f16's range per head: tiny and huge queries, with the softmax scale making up for it."""
+    cs = Case(11, 2, 3, 90, 50, 12, qscale=qscale, full=True)
+    d = cs.dev()
+    scale = float(np.float32(min(SCALE / qscale, 1e38)))
+    c.csa2_tree_attn(**d, softmax_scale=scale)
+    cs.check(d, scale)
+
+
+def test_masked_rows_may_hold_anything():
+    """NaN and infinities in window rows that a node does not attend, in rows past the batch's nodes and in
+    unselected cache rows reach no output."""
+    cs = Case(21, 3, 6, 64, 20, 16, shape="star")
+    cs.n_nodes[:] = [6, 3, 1]
+    cs.win_len[:] = [15, 4, 0]
+    d = cs.dev()
+    swa = d["swa"]
+    for b in range(3):
+        swa[b, :15 - int(cs.win_len[b])] = float("nan")
+        swa[b, 15 + int(cs.n_nodes[b]):] = float("inf")
+    used = np.unique(cs.idx[cs.idx >= 0])
+    keep = np.zeros(cs.B * cs.T, bool)
+    keep[used] = True
+    d["scales"][to_dev(np.flatnonzero(~keep))] = 0x7F                  # E4M3 NaN
+    clean = {k: v for k, v in d.items()}
+    c.csa2_tree_attn(**clean)
+    cs.check(clean)
+    # a sibling's drafted row: node i of a star sees itself only
+    cs2 = Case(22, 1, 4, 16, 8, 4, shape="star", full=True)
+    d2 = cs2.dev()
+    c.csa2_tree_attn(**d2)
+    ref = d2["out"].clone()
+    d2["swa"][0, 3 + 2] = float("nan")
+    c.csa2_tree_attn(**d2)
+    assert torch.equal(ref[0, [0, 1, 3]], d2["out"][0, [0, 1, 3]]) and torch.isnan(d2["out"][0, 2].float()).all()
+
+
+def test_index_past_the_cache_is_empty_and_flagged():
+    cs = Case(31, 2, 3, 40, 20, 8, full=True)
+    d = cs.dev()
+    d["idx"][:, 3] = 2 * 40
+    d["idx"][:, 5] = 2 ** 31 - 1
+    cs.idx[:, 3] = cs.idx[:, 5] = -1
+    c.csa2_device_flags()
+    c.csa2_tree_attn(**d)
+    assert c.csa2_device_flags() == c.FLAG_INDEX_OOB
+    cs.check(d)
+
+
+def test_parents_out_of_order_are_roots_and_flagged():
+    cs = Case(32, 1, 5, 40, 20, 16, shape="chain", full=True)
+    d = cs.dev()
+    d["parent"].copy_(torch.tensor([[0, 4, 1, -9, 3]], dtype=torch.int32))
+    cs.parent[:] = [[-1, -1, 1, -1, 3]]
+    c.csa2_device_flags()
+    c.csa2_tree_attn(**d)
+    assert c.csa2_device_flags() == c.FLAG_INDEX_OOB
+    cs.check(d)
+
+
+def test_chain_equals_the_decode_entry_point():
+    """A chain is csa2_sparse_attn_decode with Nq queries: the same rows, within both kernels' bounds.  Rows
+    here reach 24 and outputs 16, where half a step of bf16 is 2^-8 of 16 = 0.06, so a fixed absolute bound
+    does not apply: each side is held to its own roundings (the decode kernels' P to bf16 at worst)."""
+    B, N, T, k, W = 3, 6, 700, 512, 128
+    cs = Case(41, B, N, T, k, W, pool=False, shape="chain", full=True)
+    d = cs.dev()
+    c.csa2_tree_attn(**d)
+    out, lse = torch.empty_like(d["out"]), torch.empty_like(d["lse"])
+    c.csa2_sparse_attn_decode(d["q"], d["codes"], d["scales"], d["idx"], out, n_valid=d["n_valid"], swa=d["swa"],
+                              swa_len=torch.full((B,), W - 1 + N, dtype=torch.int32, device="cuda"), W=W, lse=lse)
+    cs.check(d)
+    a, b = V.f64(bf16_host(d["out"])), V.f64(bf16_host(out))
+    for s in range(B):
+        for i in range(N):
+            at = s * T + cs.idx[s * N + i]
+            sel = V.dequant(cs.codes[at], cs.scales[at])
+            win = V.tree_rows(s, i, parent=cs.parent, rows=None, swa=V.f64(cs.swa), W=W, win_len=cs.win_len)
+            _, _, t1, _ = V.tree_node(V.f64(cs.q[s, i]), sel, win, SCALE)
+            _, _, t2, _ = V.tree_node(V.f64(cs.q[s, i]), sel, win, SCALE, sel_round=2.0 ** -8)
+            assert (np.abs(a[s, i] - b[s, i]) <= t1 + t2).all()
+    assert np.linalg.norm(a - b) <= 1e-2 * np.linalg.norm(b)
+    assert float((d["lse"] - lse).abs().max()) <= 1e-2
+
+
+def test_far_rows_of_a_long_pool():
+    """Rows whose byte offset passes 32 bits (16.8 million rows of 256 bytes)."""
+    cap, n = (1 << 24) + 4096, 64
+    codes = torch.zeros((cap, 256), dtype=torch.uint8, device="cuda")
+    scales = torch.zeros((cap, 32), dtype=torch.uint8, device="cuda")
+    cs = Case(51, 1, 2, n, n, 5, full=True)
+    at = torch.from_numpy(np.sort(np.random.default_rng(1).choice(4000, n, replace=False)) + (1 << 24)).cuda()
+    codes[at], scales[at] = to_dev(cs.codes), to_dev(cs.scales)
+    d = cs.dev()
+    d.update(codes=codes, scales=scales, idx=at[d["idx"].long()].to(torch.int32))
+    c.csa2_tree_attn(**d)
+    cs.check(d)
+
+
+def test_captured_and_on_another_stream():
+    cs = Case(61, 4, 6, 200, 100, 64)
+    d = cs.dev()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        c.csa2_tree_attn(**d)
+    s.synchronize()
+    cs.check(d)
+    ref = d["out"].clone()
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            c.csa2_tree_attn(**d)
+        graphs.append(g)
+    d["out"].fill_(9.0)
+    for g in graphs:
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(ref, d["out"])

@@ -1,0 +1,113 @@
+"""Refusals of the verify step's operators: answered from the arguments alone, nothing is launched."""
+import ctypes
+
+import pytest
+
+import compressed_sparse_attention_step_gb300 as csa2
+from compressed_sparse_attention_step_gb300 import _build
+
+FAKE, FAKE2, ODD, ODD4 = (ctypes.c_void_p(v) for v in (0x100000, 0x900000, 0x100001, 0x100004))
+
+
+@pytest.fixture(scope="module")
+def L():
+    _build.build()
+    return csa2.lib()
+
+
+def _p(i):  # distinct, aligned, never dereferenced on a rejected call
+    return ctypes.c_void_p(0x10000000 * (i + 1))
+
+
+def test_block_tables(L):
+    def call(old=_p(0), new=_p(1), B=4, page=64, table=_p(2), mp=8, free=_p(3), cap=16, state=_p(4), granted=_p(5),
+             slots=_p(6), n_new=8):
+        return L.csa2_block_tables(old, new, B, page, table, mp, free, cap, state, granted, slots, n_new, None)
+    for page in (0, -64, 8, 2048, 48):
+        assert call(page=page) == csa2.ERR_INVALID_ARG
+    assert call(B=-1) == 1 and call(B=csa2.MAX_SEQS + 1) == 1 and call(mp=0) == 1 and call(cap=-1) == 1
+    assert call(n_new=-1) == 1
+    assert call(B=8192, mp=1 << 18) == 1 and call(B=8192, n_new=1 << 18) == 1   # 2^31 entries
+    assert call(mp=1 << 25) == 1                                                # positions past 31 bits
+    for name in ("old", "new", "table", "free", "state", "granted", "slots"):
+        assert call(**{name: None}) == 1, name
+        assert call(**{name: ODD}) == 1, name
+    # granted and slots overlap no input, nor each other
+    assert call(granted=_p(0)) == 1 and call(granted=_p(1)) == 1 and call(granted=_p(4)) == 1
+    assert call(slots=_p(2)) == 1 and call(slots=_p(5)) == 1
+    assert call(granted=ctypes.c_void_p(_p(2).value + 4 * 8 * 4 - 4)) == 1
+    assert call(B=0) == csa2.OK
+
+
+def test_context_slots(L):
+    def call(lens=_p(0), parent=_p(1), nn=None, B=2, N=4, table=_p(2), mp=8, page=64, slots=_p(3), ld=64, ns=_p(4)):
+        return L.csa2_context_slots(lens, parent, nn, B, N, table, mp, page, slots, ld, ns, None)
+    assert call(N=csa2.MAX_TREE + 1) == 1 and call(N=-1) == 1 and call(B=-1) == 1 and call(B=65536) == 1
+    assert call(ld=-1) == 1 and call(ld=1 << 31) == 1 and call(mp=0) == 1 and call(page=24) == 1
+    assert call(lens=None) == 1 and call(slots=None) == 1 and call(ns=None) == 1
+    assert call(slots=ODD4) == 1 and call(lens=ODD) == 1 and call(parent=ODD) == 1
+    assert call(B=0) == 0 and call(N=0) == 0
+
+
+def test_paged_append(L):
+    def call(kv=_p(0), ki=_p(1), slots=_p(2), n=3, codes=_p(3), scales=_p(4), KI=_p(5), rows=64):
+        return L.csa2_paged_append(kv, ki, slots, n, codes, scales, KI, rows, None)
+    assert call(n=-1) == 1 and call(rows=-1) == 1 and call(slots=None) == 1 and call(slots=ODD) == 1
+    for name in ("kv", "ki", "codes", "scales", "KI"):
+        assert call(**{name: None}) == 1, name       # half a pair
+        assert call(**{name: ODD4}) == 1, name
+    assert call(n=0) == 0
+    assert call(kv=None, codes=None, scales=None, ki=None, KI=None) == 0   # nothing to write
+
+
+def test_tree_attn(L):
+    def call(q=_p(0), B=2, N=4, parent=_p(1), nn=None, codes=_p(2), scales=_p(3), cap=64, pool=1, idx=_p(4), nv=None,
+             k=8, swa=_p(5), wl=None, W=16, out=_p(6), lse=None):
+        return L.csa2_tree_attn(q, B, N, parent, nn, codes, scales, cap, pool, idx, nv, k, swa, wl, W, 0.1, out, lse, None)
+    assert call(N=csa2.MAX_TREE + 1) == 1 and call(k=513) == 1 and call(W=129) == 1 and call(cap=-1) == 1
+    assert call(B=-1) == 1 and call(N=-1) == 1 and call(k=-1) == 1 and call(W=-1) == 1
+    for name in ("q", "parent", "codes", "scales", "idx", "swa", "out"):
+        assert call(**{name: None}) == 1, name
+    for name in ("q", "codes", "scales", "swa", "out"):
+        assert call(**{name: ODD4}) == 1, name
+    assert call(B=0) == 0 and call(N=0) == 0
+
+
+def test_fp4_weight(L):
+    assert L.csa2_fp4_packed_bytes(16, 128) == 1152 and L.csa2_fp4_packed_bytes(17, 144) == 4 * 1152
+    assert L.csa2_fp4_packed_bytes(16, 100) == 0 and L.csa2_fp4_packed_bytes(-1, 128) == 0
+    assert L.csa2_fp4_pack_weight(_p(0), _p(1), 4, 24, _p(2), None) == 1
+    assert L.csa2_fp4_pack_weight(None, _p(1), 4, 32, _p(2), None) == 1
+    assert L.csa2_fp4_pack_weight(_p(0), _p(1), 4, 32, ODD4, None) == 1
+    assert L.csa2_fp4_pack_weight(_p(0), _p(1), 0, 32, _p(2), None) == 0
+
+    def call(x=_p(0), m=2, w=_p(1), n_out=8, n_in=32, rs=None, y=_p(2)):
+        return L.csa2_fp4_matvec(x, m, w, n_out, n_in, rs, y, 0, None)
+    assert call(m=csa2.MAX_MV_ROWS + 1) == 1 and call(m=-1) == 1 and call(n_in=40) == 1 and call(n_in=0) == 1
+    assert call(n_out=-1) == 1
+    assert call(x=None) == 1 and call(w=None) == 1 and call(y=None) == 1
+    assert call(x=ODD4) == 1 and call(w=ODD4) == 1 and call(y=ODD4) == 1 and call(rs=ODD) == 1
+    assert call(m=0) == 0 and call(n_out=0) == 0
+
+
+def test_binding_checks_shapes_and_types():
+    torch = pytest.importorskip("torch")
+    i32 = torch.int32
+    with pytest.raises(ValueError):   # not on a GPU
+        csa2.csa2_block_tables(torch.zeros(2, dtype=i32), torch.zeros(2, dtype=i32), 64, torch.zeros((2, 4), dtype=i32),
+                               torch.zeros(8, dtype=i32), torch.zeros(4, dtype=i32), torch.zeros(2, dtype=i32))
+    with pytest.raises(ValueError):   # granted of another batch
+        csa2.csa2_block_tables(torch.zeros(2, dtype=i32), torch.zeros(2, dtype=i32), 64, torch.zeros((2, 4), dtype=i32),
+                               torch.zeros(8, dtype=i32), torch.zeros(4, dtype=i32), torch.zeros(3, dtype=i32))
+    with pytest.raises(ValueError):
+        csa2.fp4_weight_alloc(16, 24, device="cpu")
+    with pytest.raises(ValueError):   # channels not a multiple of 16
+        csa2.csa2_fp4_matvec(torch.zeros((1, 24), dtype=torch.bfloat16), torch.zeros(1152, dtype=torch.uint8),
+                             torch.zeros((1, 16), dtype=torch.bfloat16))
+    with pytest.raises(ValueError):   # a weight of another size
+        csa2.csa2_fp4_matvec(torch.zeros((1, 32), dtype=torch.bfloat16), torch.zeros(1152, dtype=torch.uint8),
+                             torch.zeros((1, 17), dtype=torch.bfloat16))
+    with pytest.raises(ValueError):   # scales of another width
+        csa2.csa2_tree_attn(torch.zeros((1, 2, 16, 512), dtype=torch.bfloat16), torch.zeros((1, 2), dtype=i32),
+                            torch.zeros((8, 256), dtype=torch.uint8), torch.zeros((8, 16), dtype=torch.uint8),
+                            torch.zeros((2, 4), dtype=i32), torch.zeros((1, 2, 16, 512), dtype=torch.bfloat16))
