@@ -446,23 +446,71 @@ def csa2_attn_merge_shards(out_g, lse_g, out, lse=None, stream=None):
 # ---------------------------------------------------------------------------------------------
 # drafted tokens over a paged cache, and 4-bit weights
 # ---------------------------------------------------------------------------------------------
-def _shape(t, name, shape):
-    """t has exactly `shape` (None entries are free); returns it as a tuple."""
-    if t is None:
-        return None
-    got = tuple(t.shape)
-    if len(got) != len(shape) or any(w is not None and g != w for g, w in zip(got, shape)):
-        raise ValueError(f"{name}: expected shape {tuple('?' if w is None else w for w in shape)}, got {got}")
-    return got
-
-
-def _one_device(*tensors):
-    """Every tensor lies on the current device, whose stream and kernels the call uses."""
+# A verify step makes dozens of small calls, so the checks of these entry points are written to cost little:
+# one pass over a tensor's properties on the good path, and the reasons only where something is wrong.
+def _refuse(t, name, dtypes, shape, dev):
     torch = _torch()
-    cur = torch.cuda.current_device() if torch.cuda.is_available() else None
-    for t in tensors:
-        if t is not None and t.is_cuda and t.device.index != cur:
-            raise ValueError(f"expected tensors on the current device cuda:{cur}, got one on {t.device}")
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    raise ValueError(f"{name}: expected a tensor on the current device cuda:{dev}, got one on {t.device}")
+
+
+def _dims(t, name, n):
+    """The n dimensions of t."""
+    shape = getattr(t, "shape", None)
+    if shape is None:
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if len(shape) != n:
+        raise ValueError(f"{name}: expected {n} dimensions, got shape {tuple(shape)}")
+    return shape
+
+
+def _call_context():
+    """(check, current device, types): check(t, name, dtypes, shape) returns t's data pointer, or None for None,
+    where t is contiguous, of one of the types and that shape, and on the current device; types are the
+    accepted int32, uint8, fp32 and bf16 types."""
+    global _context
+    if _context is None:
+        torch = _torch()
+        types = ((torch.int32,), (torch.uint8,), (torch.float32,), _bf16_types())
+        get_device = getattr(torch._C, "_cuda_getDevice", None)
+        if get_device is None or not torch.cuda.is_available():
+            get_device = lambda: torch.cuda.current_device() if torch.cuda.is_available() else 0  # noqa: E731
+        raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw_stream is None:
+            raw_stream = lambda dev: torch.cuda.current_stream(dev).cuda_stream  # noqa: E731
+        else:
+            torch.cuda.init() if torch.cuda.is_available() else None
+        _context = (get_device, raw_stream, types)
+    get_device, raw_stream, types = _context
+    dev = get_device()
+
+    def check(t, name, dtypes, shape):
+        if t is None:
+            return None
+        try:
+            if t.dtype in dtypes and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+                return t.data_ptr()
+        except AttributeError:
+            pass
+        _refuse(t, name, dtypes, shape, dev)
+
+    return check, dev, types
+
+
+_context = None
+
+
+def _on(stream, dev):
+    return stream.cuda_stream if stream is not None else _context[1](dev)
 
 
 def csa2_block_tables(old_lens, new_lens, page_size, block_table, free_pages, pool_state, granted, *, slots=None,
@@ -471,125 +519,112 @@ def csa2_block_tables(old_lens, new_lens, page_size, block_table, free_pages, po
     shrink: block_table int32 [B, max_pages], free_pages int32 [free_cap], pool_state int32 [4] (the first
     holds the number of free pages), granted int32 [B] the lengths in effect, slots int32 [B, n_new] the
     slots of positions old_lens[b] + i (-1 from granted[b] on)."""
-    i32 = (_torch().int32,)
-    B, max_pages = _shape(block_table, "block_table", (None, None))
-    for t, name in ((old_lens, "old_lens"), (new_lens, "new_lens"), (granted, "granted")):
-        _shape(t, name, (B,))
-    _shape(free_pages, "free_pages", (None,))
-    _shape(pool_state, "pool_state", (4,))
-    n_new = _shape(slots, "slots", (B, None))[1] if slots is not None else 0
-    args = [_ptr(old_lens, "old_lens", i32), _ptr(new_lens, "new_lens", i32), B, int(page_size),
-            _ptr(block_table, "block_table", i32), max_pages, _ptr(free_pages, "free_pages", i32), free_pages.numel(),
-            _ptr(pool_state, "pool_state", i32), _ptr(granted, "granted", i32), _ptr(slots, "slots", i32), n_new]
-    _one_device(old_lens, new_lens, block_table, free_pages, pool_state, granted, slots)
-    _check("csa2_block_tables", lib().csa2_block_tables(*args, _stream(stream)))
+    check, dev, (i32, _, _, _) = _call_context()
+    B, max_pages = _dims(block_table, "block_table", 2)
+    free_cap, = _dims(free_pages, "free_pages", 1)
+    n_new = _dims(slots, "slots", 2)[1] if slots is not None else 0
+    st = lib().csa2_block_tables(
+        check(old_lens, "old_lens", i32, (B,)), check(new_lens, "new_lens", i32, (B,)), B, page_size,
+        check(block_table, "block_table", i32, (B, max_pages)), max_pages,
+        check(free_pages, "free_pages", i32, (free_cap,)), free_cap, check(pool_state, "pool_state", i32, (4,)),
+        check(granted, "granted", i32, (B,)), check(slots, "slots", i32, (B, n_new)), n_new, _on(stream, dev))
+    if st:
+        _check("csa2_block_tables", st)
 
 
 def csa2_context_slots(lens, slots, n_slots, *, block_table=None, page_size=0, parent=None, n_nodes=None, stream=None):
     """slots int32 [B*N, ld]: per drafted node the slots of its sequence's lens[b] committed positions, then of
     its ancestors and itself, then -1; n_slots int32 [B*N] their number.  parent int32 [B, N] (None: the
     committed positions only); block_table int32 [B, max_pages] (None: positions instead of slots)."""
-    i32 = (_torch().int32,)
-    B, = _shape(lens, "lens", (None,))
-    rows, ld = _shape(slots, "slots", (None, None))
-    N = _shape(parent, "parent", (B, None))[1] if parent is not None else (rows // B if B else 0)
-    _shape(slots, "slots", (B * N, ld))
-    _shape(n_slots, "n_slots", (B * N,))
-    _shape(n_nodes, "n_nodes", (B,))
-    max_pages = _shape(block_table, "block_table", (B, None))[1] if block_table is not None else 0
-    args = [_ptr(lens, "lens", i32), _ptr(parent, "parent", i32), _ptr(n_nodes, "n_nodes", i32), B, N,
-            _ptr(block_table, "block_table", i32), max_pages, int(page_size), _ptr(slots, "slots", i32), ld,
-            _ptr(n_slots, "n_slots", i32)]
-    _one_device(lens, slots, n_slots, block_table, parent, n_nodes)
-    _check("csa2_context_slots", lib().csa2_context_slots(*args, _stream(stream)))
+    check, dev, (i32, _, _, _) = _call_context()
+    B, = _dims(lens, "lens", 1)
+    rows, ld = _dims(slots, "slots", 2)
+    N = _dims(parent, "parent", 2)[1] if parent is not None else (rows // B if B else 0)
+    max_pages = _dims(block_table, "block_table", 2)[1] if block_table is not None else 0
+    st = lib().csa2_context_slots(
+        check(lens, "lens", i32, (B,)), check(parent, "parent", i32, (B, N)), check(n_nodes, "n_nodes", i32, (B,)), B, N,
+        check(block_table, "block_table", i32, (B, max_pages)), max_pages, page_size,
+        check(slots, "slots", i32, (B * N, ld)), ld, check(n_slots, "n_slots", i32, (B * N,)), _on(stream, dev))
+    if st:
+        _check("csa2_context_slots", st)
 
 
 def csa2_paged_append(slots, *, kv_new=None, codes=None, scales=None, ki_new=None, KI=None, stream=None):
     """Row i of kv_new bf16 [n, 512] is quantised into row slots[i] of codes uint8 [n_slots, 256] and scales
     uint8 [n_slots, 32], row i of ki_new bf16 [n, 128] copied to row slots[i] of KI bf16 [n_slots, 128];
-    negative slots are padding.  Either pair may be left out."""
-    torch = _torch()
-    n = slots.numel()
-    n_slots = codes.shape[0] if codes is not None else KI.shape[0] if KI is not None else 0
-    _shape(slots.reshape(-1) if slots.is_contiguous() else slots, "slots", (n,))
-    _shape(kv_new, "kv_new", (n, D))
-    _shape(ki_new, "ki_new", (n, DI))
-    _shape(codes, "codes", (n_slots, CODE_BYTES))
-    _shape(scales, "scales", (n_slots, SCALE_BYTES))
-    _shape(KI, "KI", (n_slots, DI))
-    u8 = (torch.uint8,)
-    args = [_ptr(kv_new, "kv_new", _bf16_types()), _ptr(ki_new, "ki_new", _bf16_types()),
-            _ptr(slots, "slots", (torch.int32,)), n, _ptr(codes, "codes", u8), _ptr(scales, "scales", u8),
-            _ptr(KI, "KI", _bf16_types()), n_slots]
-    _one_device(slots, kv_new, codes, scales, ki_new, KI)
-    _check("csa2_paged_append", lib().csa2_paged_append(*args, _stream(stream)))
+    slots int32 [n], negative ones are padding.  Either pair may be left out."""
+    check, dev, (i32, u8, _, bf) = _call_context()
+    n, = _dims(slots, "slots", 1)
+    pool, name = (codes, "codes") if codes is not None else (KI, "KI")
+    n_slots = _dims(pool, name, 2)[0] if pool is not None else 0
+    st = lib().csa2_paged_append(
+        check(kv_new, "kv_new", bf, (n, D)), check(ki_new, "ki_new", bf, (n, DI)), check(slots, "slots", i32, (n,)), n,
+        check(codes, "codes", u8, (n_slots, CODE_BYTES)), check(scales, "scales", u8, (n_slots, SCALE_BYTES)),
+        check(KI, "KI", bf, (n_slots, DI)), n_slots, _on(stream, dev))
+    if st:
+        _check("csa2_paged_append", st)
 
 
 def csa2_tree_attn(q, parent, codes, scales, idx, out, *, n_nodes=None, n_valid=None, swa=None, win_len=None, W=0,
                    softmax_scale=None, lse=None, stream=None):
     """Attention of a tree of drafted tokens: q [B, N, 16, 512]; parent int32 [B, N]; codes / scales
     [B, cap, *], or [cap, *] for one pool shared by all sequences; idx int32 [B*N, k] cache rows;
-    swa [B, W-1+N, 512] (the committed window, then the drafted rows); out as q, lse fp32 [B, N, 16]."""
-    torch = _torch()
-    i32, u8 = (torch.int32,), (torch.uint8,)
-    B, N = _shape(q, "q", (None, None, H, D))[:2]
-    _shape(parent, "parent", (B, N))
-    _shape(n_nodes, "n_nodes", (B,))
-    pool = codes.dim() == 2
-    cap = codes.shape[0 if pool else 1]
-    _shape(codes, "codes", (cap, CODE_BYTES) if pool else (B, cap, CODE_BYTES))
-    _shape(scales, "scales", (cap, SCALE_BYTES) if pool else (B, cap, SCALE_BYTES))
-    k = _shape(idx, "idx", (B * N, None))[1]
-    _shape(n_valid, "n_valid", (B * N,))
+    swa [B, W-1+N, 512] (the committed window, then the drafted rows; None: no window); out as q,
+    lse fp32 [B, N, 16]."""
+    check, dev, (i32, u8, f32, bf) = _call_context()
+    B, N = _dims(q, "q", 4)[:2]
+    lead = tuple(codes.shape[:-1])
+    pool = len(lead) == 1
+    if not pool and (len(lead) != 2 or lead[0] != B):
+        raise ValueError(f"codes: expected shape ({B}, cap, {CODE_BYTES}) or (cap, {CODE_BYTES}), got {tuple(codes.shape)}")
+    k = _dims(idx, "idx", 2)[1]
     if swa is None:
         W = 0
-    else:
-        _shape(swa, "swa", (B, W - 1 + N, D))
-    _shape(win_len, "win_len", (B,))
-    _shape(out, "out", (B, N, H, D))
-    _shape(lse, "lse", (B, N, H))
-    if softmax_scale is None:
-        softmax_scale = D ** -0.5
-    bf = _bf16_types()
-    args = [_ptr(q, "q", bf), B, N, _ptr(parent, "parent", i32), _ptr(n_nodes, "n_nodes", i32),
-            _ptr(codes, "codes", u8), _ptr(scales, "scales", u8), cap, int(pool), _ptr(idx, "idx", i32),
-            _ptr(n_valid, "n_valid", i32), k, _ptr(swa, "swa", bf), _ptr(win_len, "win_len", i32), int(W),
-            float(softmax_scale), _ptr(out, "out", bf), _ptr(lse, "lse", (torch.float32,))]
-    _one_device(q, parent, codes, scales, idx, out, n_nodes, n_valid, swa, win_len, lse)
-    _check("csa2_tree_attn", lib().csa2_tree_attn(*args, _stream(stream)))
+    rows = (B, N, H, D)
+    st = lib().csa2_tree_attn(
+        check(q, "q", bf, rows), B, N, check(parent, "parent", i32, (B, N)), check(n_nodes, "n_nodes", i32, (B,)),
+        check(codes, "codes", u8, lead + (CODE_BYTES,)), check(scales, "scales", u8, lead + (SCALE_BYTES,)), lead[-1], pool,
+        check(idx, "idx", i32, (B * N, k)), check(n_valid, "n_valid", i32, (B * N,)), k,
+        check(swa, "swa", bf, (B, W - 1 + N, D)), check(win_len, "win_len", i32, (B,)), W,
+        D ** -0.5 if softmax_scale is None else softmax_scale, check(out, "out", bf, rows),
+        check(lse, "lse", f32, (B, N, H)), _on(stream, dev))
+    if st:
+        _check("csa2_tree_attn", st)
+
+
+def _packed_bytes(n_out, n_in):
+    if n_in % GROUP:
+        raise ValueError(f"expected a multiple of {GROUP} input channels, got {n_in}")
+    return int(lib().csa2_fp4_packed_bytes(n_out, n_in))
 
 
 def fp4_weight_alloc(n_out, n_in, device="cuda"):
     """An empty packed weight of n_out output rows and n_in input channels (a multiple of 16)."""
-    if n_in % GROUP:
-        raise ValueError(f"n_in: expected a multiple of {GROUP}, got {n_in}")
-    return _torch().empty(int(lib().csa2_fp4_packed_bytes(n_out, n_in)), dtype=_torch().uint8, device=device)
+    return _torch().empty(_packed_bytes(n_out, n_in), dtype=_torch().uint8, device=device)
 
 
 def csa2_fp4_pack_weight(codes, scales, packed, stream=None):
     """Lays codes uint8 [n_out, n_in/2] and scales uint8 [n_out, n_in/16] out for csa2_fp4_matvec."""
-    u8 = (_torch().uint8,)
-    n_out, half = _shape(codes, "codes", (None, None))
-    _shape(scales, "scales", (n_out, 2 * half // GROUP))
-    if (2 * half) % GROUP:
-        raise ValueError(f"codes: expected a multiple of {GROUP} input channels, got {2 * half}")
-    _shape(packed, "packed", (int(lib().csa2_fp4_packed_bytes(n_out, 2 * half)),))
-    args = [_ptr(codes, "codes", u8), _ptr(scales, "scales", u8), n_out, 2 * half, _ptr(packed, "packed", u8)]
-    _one_device(codes, scales, packed)
-    _check("csa2_fp4_pack_weight", lib().csa2_fp4_pack_weight(*args, _stream(stream)))
+    check, dev, (_, u8, _, _) = _call_context()
+    n_out, half = _dims(codes, "codes", 2)
+    n_in = 2 * half
+    nbytes = _packed_bytes(n_out, n_in)
+    st = lib().csa2_fp4_pack_weight(
+        check(codes, "codes", u8, (n_out, half)), check(scales, "scales", u8, (n_out, n_in // GROUP)), n_out, n_in,
+        check(packed, "packed", u8, (nbytes,)), _on(stream, dev))
+    if st:
+        _check("csa2_fp4_pack_weight", st)
 
 
 def csa2_fp4_matvec(x, packed, y, *, row_scale=None, stream=None):
     """y [m, n_out] (bf16 or fp32) = row_scale * (x bf16 [m, n_in] times the packed weight), m <= 32."""
-    torch = _torch()
-    m, n_in = _shape(x, "x", (None, None))
-    _, n_out = _shape(y, "y", (m, None))
-    if n_in % GROUP:
-        raise ValueError(f"x: expected a multiple of {GROUP} input channels, got {n_in}")
-    _shape(packed, "packed", (int(lib().csa2_fp4_packed_bytes(n_out, n_in)),))
-    _shape(row_scale, "row_scale", (n_out,))
-    args = [_ptr(x, "x", _bf16_types()), m, _ptr(packed, "packed", (torch.uint8,)), n_out, n_in,
-            _ptr(row_scale, "row_scale", (torch.float32,)), _ptr(y, "y", _bf16_types() + (torch.float32,)),
-            int(y.dtype == torch.float32)]
-    _one_device(x, packed, y, row_scale)
-    _check("csa2_fp4_matvec", lib().csa2_fp4_matvec(*args, _stream(stream)))
+    check, dev, (_, u8, f32, bf) = _call_context()
+    m, n_in = _dims(x, "x", 2)
+    n_out = _dims(y, "y", 2)[1]
+    fp32 = y.dtype in f32
+    st = lib().csa2_fp4_matvec(
+        check(x, "x", bf, (m, n_in)), m, check(packed, "packed", u8, (_packed_bytes(n_out, n_in),)), n_out, n_in,
+        check(row_scale, "row_scale", f32, (n_out,)), check(y, "y", f32 if fp32 else bf, (m, n_out)), fp32,
+        _on(stream, dev))
+    if st:
+        _check("csa2_fp4_matvec", st)

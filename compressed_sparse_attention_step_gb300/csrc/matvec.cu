@@ -1,23 +1,24 @@
 // Products of a few token rows with a 4-bit weight: y[m][n] = row_scale[n] sum_k x[m][k] e2m1[n][k] e4m3[n][k/16].
 //
-// Bound: the weight's 0.5625 bytes per element from HBM (one pass; x and y are small beside it), and for more
-// than about 24 token rows the 1024 multiply-adds a cycle and SM of mma.m16n8k16.
+// Bound: the weight's 0.5625 bytes per element from HBM, in one pass; x and y are small beside it.
 //
-// Layout.  The weight is packed once into blocks of 16 output rows x 128 input channels, 1152 bytes each,
-// in the order in which a warp's lanes use them: lane (g, t) takes rows g and g + 8 and channels
-// 32t .. 32t+31 of the block, 16 bytes of codes a row (two coalesced 512-byte loads a warp), and the four
-// scale bytes of those (one 128-byte load).  The sum over a block's 128 channels may run in any order, so
-// the lane's j-th channel pair stands where the A fragment of m16n8k16 wants the lane's j-th pair, and x is
-// staged in the same order.  Rows and channels past the weight are zero codes.
+// Layout.  The weight is packed once into blocks of 32 output rows x 128 input channels, 2304 bytes each: four
+// pieces of 32 channels, 16 bytes of codes per row and piece, then eight scale bytes per row; row r of piece j lies
+// at place r ^ 2j, so that a warp's 16-byte reads fall into different banks of shared memory whether its lanes own a
+// row each or, as fragments of m16n8k16, eight rows and four pieces.  Blocks of the same rows follow each other
+// along the channels.  Rows and channels past the weight are zero codes.  A warp brings its blocks into shared
+// memory itself, by one bulk copy each, a few blocks ahead (plain loads into registers reached less than half of
+// the bandwidth, however many were in flight).
 //
-// Numbers.  A code times a scale is exact in f16 (6 significant bits, 2^-10 .. 2688).  x is bf16: each
-// (token, 128-channel block) is scaled by the power of two that brings its largest magnitude into [2^14, 2^15)
-// and is then exact in f16 down to 2^-28 of that magnitude, off by less than 2^-38 of it below; the block's
-// sum is scaled back in fp32.  All sums are fp32, in a fixed order.
+// Numbers.  A code times a scale is exact in f16 (6 significant bits, 2^-10 .. 2688).  x is bf16: it is scaled by
+// the power of two that brings the largest magnitude of a token's share of channels (a block's 128, or a CTA's)
+// into [2^14, 2^15), and is then exact in f16 down to 2^-28 of that magnitude, off by less than 2^-38 of it below;
+// the sums are scaled back in fp32.  All sums are fp32, in a fixed order, and are rounded once.
 //
-// Work.  A warp owns 32 output rows and every WK-th block of its CTA's share of the channels; a CTA holds
-// WR x WK = 8 warps, and a cluster of C CTAs splits the channels further.  Partial sums meet in shared memory
-// and over the cluster's distributed shared memory, in a fixed order: no atomics, no workspace.
+// Two kernels.  matvec_tc_kernel: the weight is the M = 128 operand of tcgen05.mma, dequantised into tensor
+// memory, so that a weight element costs one conversion and one multiplication and no pass through shared memory,
+// and the token rows (N = 16 or 32) cost the warps nothing.  matvec_kernel: mma.m16n8k16 from registers, with
+// less to set up.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -29,10 +30,13 @@ namespace mv {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kRows = 16, kChan = 128;     // block
-constexpr int kBlock = kRows * kChan / 2 + kRows * kChan / CSA2_GROUP;  // 1152 bytes
-constexpr int kStage = 64 * 1024;          // bytes of x staged at a time
+constexpr int kRows = 32, kChan = 128;     // block
+constexpr int kCodeBytes = kRows * kChan / 2;
+constexpr int kBlock = kCodeBytes + kRows * kChan / CSA2_GROUP;  // 2304 bytes
+constexpr int kStage = 48 * 1024;          // bytes of x staged at a time
+constexpr int kSlots = 3;                  // blocks a warp of matvec_kernel has under way
 constexpr int kMaxCluster = 8;
+constexpr size_t kMaxSmem = size_t(kWarps) * kSlots * kBlock + kWarps * 32 * (kChan * 2 + 4);  // of matvec_kernel
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -42,33 +46,42 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// One thread per 16 bytes of packed codes or 4 scale bytes: block (row tile, channel block), lane.
+// where piece j (32 channels) of row r lies in a block
+__device__ __forceinline__ int block_place(int r, int j) { return j * 512 + (r ^ (2 * j)) * 16; }
+
+// A block into shared memory; one thread.
+__device__ __forceinline__ void block_copy(void* dst, const uint8_t* src, uint64_t* bar) {
+  const uint32_t b = smem_u32(bar);
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(b), "r"(kBlock) : "memory");
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(kBlock), "r"(b)
+               : "memory");
+}
+
+// A warp per block, a lane per row.
 __global__ void __launch_bounds__(256) pack_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
                                                    int64_t n_out, int64_t n_in, int64_t n_kb, int64_t n_blocks,
                                                    uint8_t* __restrict__ packed) {
   pdl_wait();
   pdl_trigger();
-  const int64_t gid = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
-  const int64_t blk = gid >> 5;
+  const int64_t blk = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
   if (blk >= n_blocks) return;
-  const int lane = int(gid & 31), g = lane >> 2, t = lane & 3;
-  const int64_t tile = blk / n_kb, kb = blk - tile * n_kb;
-  const int64_t c0 = kb * kChan + 32 * t;  // this lane's 32 channels: two scale groups
+  const int lane = int(threadIdx.x & 31);
+  const int64_t rb = blk / n_kb, kb = blk - rb * n_kb, row = rb * kRows + lane;
   uint8_t* dst = packed + blk * kBlock;
-  uint32_t sb = 0;
+  uint32_t sb[2] = {0, 0};
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int64_t row = tile * kRows + 8 * h + g;
-    uint2 w[2] = {make_uint2(0, 0), make_uint2(0, 0)};
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-      if (row < n_out && c0 + 16 * j < n_in) {  // n_in is a multiple of 16: whole groups
-        w[j] = *reinterpret_cast<const uint2*>(codes + row * (n_in / 2) + (c0 + 16 * j) / 2);
-        sb |= uint32_t(scales[row * (n_in / CSA2_GROUP) + c0 / CSA2_GROUP + j]) << (16 * h + 8 * j);
-      }
-    *reinterpret_cast<uint4*>(dst + 512 * h + 16 * lane) = make_uint4(w[0].x, w[0].y, w[1].x, w[1].y);
+  for (int j = 0; j < 8; ++j) {  // groups of 16 channels; n_in is a multiple of 16
+    const int64_t c0 = kb * kChan + 16 * j;
+    uint2 w = make_uint2(0, 0);
+    if (row < n_out && c0 < n_in) {
+      w = *reinterpret_cast<const uint2*>(codes + row * (n_in / 2) + c0 / 2);
+      sb[j >> 2] |= uint32_t(scales[row * (n_in / CSA2_GROUP) + c0 / CSA2_GROUP]) << (8 * (j & 3));
+    }
+    *reinterpret_cast<uint2*>(dst + block_place(lane, j >> 1) + (j & 1) * 8) = w;
   }
-  *reinterpret_cast<uint32_t*>(dst + 1024 + 4 * lane) = sb;
+  *reinterpret_cast<uint2*>(dst + kCodeBytes + lane * 8) = make_uint2(sb[0], sb[1]);
 }
 
 __device__ __forceinline__ void cluster_arrive_wait() {
@@ -83,9 +96,9 @@ __device__ __forceinline__ float ld_cluster(uint32_t a, uint32_t rank) {
   return v;
 }
 
-struct Unit {  // 32 rows x 128 channels, as loaded
+struct Unit {  // a block as fragments: rows 16 r + 8 h + g, channels 32t .. 32t+31
   uint4 c[2][2];
-  uint32_t s[2];
+  uint32_t s[2][2];
 };
 
 struct Params {
@@ -94,9 +107,10 @@ struct Params {
   const float* row_scale;
   void* y;
   int64_t n_out, n_in;
-  int m, n_kb, n_tiles;  // token rows, channel blocks, 16-row tiles
+  int m, n_kb, n_rb;     // token rows, channel blocks, row blocks
   int stage_kb;          // channel blocks staged at a time (a multiple of 8)
   int y_fp32;
+  unsigned int* flags;
 };
 
 // TG: groups of 8 token rows; WR: warps along the output rows.
@@ -105,33 +119,36 @@ __global__ void __launch_bounds__(kThreads, TG <= 2 ? 2 : 1) matvec_kernel(const
   constexpr int WK = kWarps / WR;
   constexpr int kTok = TG * 8;
   constexpr int kCtaRows = WR * 32;
-  extern __shared__ __align__(16) unsigned char smem[];
-  uint4* xs = reinterpret_cast<uint4*>(smem);                                       // [kb][TG][4][32 lanes]
-  float* xf = reinterpret_cast<float*>(smem + size_t(p.stage_kb) * kTok * kChan * 2);  // [kb][kTok]
-  float* red = reinterpret_cast<float*>(smem);                                      // [WK][kTok][kCtaRows]
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ uint64_t full[kWarps][kSlots];
+  unsigned char* ring = smem + (threadIdx.x >> 5) * (kSlots * kBlock);                 // of this warp
+  unsigned char* stage = smem + kWarps * kSlots * kBlock;
+  uint4* xs = reinterpret_cast<uint4*>(stage);                                         // [kb][TG][4][32 lanes]
+  float* xf = reinterpret_cast<float*>(stage + size_t(p.stage_kb) * kTok * kChan * 2);  // [kb][kTok]
+  float* red = reinterpret_cast<float*>(stage);                                        // [WK][kTok][kCtaRows]
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, t = lane & 3, g = lane >> 2;
   const int wr = warp / WK, wk = warp % WK;
   const int rank = C > 1 ? int(blockIdx.x % unsigned(C)) : 0;
   const int64_t row0 = int64_t(blockIdx.x / unsigned(C)) * kCtaRows;
-  const int kb0 = int(int64_t(p.n_kb) * rank / C), kb1 = int(int64_t(p.n_kb) * (rank + 1) / C);
-  const int tile0 = int(row0 / kRows) + wr * 2;
-  const bool live0 = tile0 < p.n_tiles, live1 = tile0 + 1 < p.n_tiles;
+  const int kb0 = int(uint32_t(p.n_kb) * uint32_t(rank) / uint32_t(C)),
+            kb1 = int(uint32_t(p.n_kb) * uint32_t(rank + 1) / uint32_t(C));
+  const int rb = int(row0 / kRows) + wr;
 
-  auto load = [&](Unit& u, int kb) {
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const bool on = (r ? live1 : live0) && kb < kb1;
-      const uint8_t* src = p.packed + (int64_t(tile0 + r) * p.n_kb + kb) * kBlock;
-      u.c[r][0] = on ? ld_stream16(src + 16 * lane) : make_uint4(0, 0, 0, 0);
-      u.c[r][1] = on ? ld_stream16(src + 512 + 16 * lane) : make_uint4(0, 0, 0, 0);
-      u.s[r] = on ? __ldcs(reinterpret_cast<const uint32_t*>(src + 1024 + 4 * lane)) : 0u;
-    }
-  };
-  Unit u0, u1;
-  load(u0, kb0 + wk);
-  load(u1, kb0 + wk + WK);
+  // this warp's blocks: channel blocks kb0 + wk, + WK, ... of row block rb; none past the weight's rows
+  const int n_blk = rb < p.n_rb && kb1 - kb0 > wk ? (kb1 - kb0 - wk + WK - 1) / WK : 0;
+  const uint8_t* src = p.packed + (int64_t(rb) * p.n_kb + kb0 + wk) * kBlock;
+  if (lane == 0) {
+    for (int i = 0; i < kSlots; ++i)
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;\n" ::"r"(smem_u32(&full[warp][i])) : "memory");
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    for (int i = 0; i < min(n_blk, kSlots); ++i)
+      block_copy(ring + i * kBlock, src + int64_t(i) * WK * kBlock, &full[warp][i]);
+  }
+  __syncwarp();
+  int slot = 0, use = 0, done = 0;
+  bool late = false;  // a copy did not land within a second: flagged, and no more waiting
 
   float acc[2][TG][4];
 #pragma unroll
@@ -164,7 +181,27 @@ __global__ void __launch_bounds__(kThreads, TG <= 2 ? 2 : 1) matvec_kernel(const
       if (j == 0) xf[kb * kTok + tok] = __uint_as_float(uint32_t(127 - up) << 23);
     }
     __syncthreads();
-    for (int kb = wk; kb < nk; kb += WK) {
+    for (int kb = wk; kb < nk && done < n_blk; kb += WK, ++done) {
+      if (!late && !bar_wait(smem_u32(&full[warp][slot]), uint32_t(use) & 1u)) {
+        late = true;
+        atomicOr(p.flags, CSA2_FLAG_TIMEOUT);
+      }
+      Unit u0;
+      {
+        const unsigned char* blk = ring + slot * kBlock;
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int row = 16 * r + 8 * h + g;
+            u0.c[r][h] = *reinterpret_cast<const uint4*>(blk + block_place(row, t));
+            u0.s[r][h] = *reinterpret_cast<const uint16_t*>(blk + kCodeBytes + row * 8 + 2 * t);
+          }
+      }
+      __syncwarp();
+      if (lane == 0 && done + kSlots < n_blk)
+        block_copy(ring + slot * kBlock, src + int64_t(done + kSlots) * WK * kBlock, &full[warp][slot]);
+      if (++slot == kSlots) slot = 0, ++use;
       float d[2][TG][4];
 #pragma unroll
       for (int r = 0; r < 2; ++r)
@@ -175,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, TG <= 2 ? 2 : 1) matvec_kernel(const
       for (int r = 0; r < 2; ++r)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const __half2 s2 = attn::bits_h2(attn::e4m3x2_to_f16x2(uint16_t(u0.s[r] >> (16 * h))));
+          const __half2 s2 = attn::bits_h2(attn::e4m3x2_to_f16x2(uint16_t(u0.s[r][h])));
           sc[r][h][0] = __low2half2(s2), sc[r][h][1] = __high2half2(s2);
         }
 #pragma unroll
@@ -201,8 +238,6 @@ __global__ void __launch_bounds__(kThreads, TG <= 2 ? 2 : 1) matvec_kernel(const
           }
         }
       }
-      u0 = u1;
-      load(u1, c0 + kb + 2 * WK);
 #pragma unroll
       for (int j = 0; j < TG; ++j) {
         const float2 f = *reinterpret_cast<const float2*>(&xf[kb * kTok + 8 * j + 2 * t]);
@@ -251,13 +286,15 @@ template <int TG, int WR>
 cudaError_t launch(Params p, int C, cudaStream_t st) {
   constexpr int kTok = TG * 8, WK = kWarps / WR, kCtaRows = WR * 32;
   const int share = (p.n_kb + C - 1) / C;
-  p.stage_kb = std::min(kStage / (kTok * kChan * 2), (share + 7) / 8 * 8);
-  const size_t smem = std::max(size_t(p.stage_kb) * kTok * (kChan * 2 + 4), size_t(WK) * kTok * kCtaRows * 4);
+  p.stage_kb = std::min(std::max(kStage / (kTok * kChan * 2) / kWarps, 1) * kWarps, (share + kWarps - 1) / kWarps * kWarps);
+  const size_t smem = size_t(kWarps) * kSlots * kBlock +
+                      std::max(size_t(p.stage_kb) * kTok * (kChan * 2 + 4), size_t(WK) * kTok * kCtaRows * 4);
   auto kern = matvec_kernel<TG, WR>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), kMaxSmem, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned((p.n_tiles + 2 * WR - 1) / (2 * WR) * C));
+  cfg.gridDim = dim3(unsigned((p.n_rb + WR - 1) / WR * C));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -272,25 +309,442 @@ cudaError_t launch(Params p, int C, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, kern, p, C);
 }
 
+
+// ---- the tensor-memory form ----------------------------------------------------------------------------------
+// A cluster of C CTAs (one per SM) shares the channels of a contiguous range of row blocks, which it takes in
+// steps of four (128 rows).  Warps 4 .. 15, as three groups of four, take every third channel block: a lane reads its
+// row's 128 channels from its warp's ring of copied blocks, and dequantises them into 64 tensor-memory columns; warps 0 .. 3 issue
+// the eight MMAs of each channel block against the CTA's share of x, which was staged once in the
+// 128-byte-swizzled K-major layout; warps 16 .. 19 read the accumulators of a step and exchange the C partial sums
+// through distributed shared memory, while the next step is under way.
+namespace tc {
+
+constexpr int kGroups = 3;                        // dequantising groups of four warps
+constexpr int kSlots = 3;                         // blocks under way per dequantising warp
+constexpr int kIssuers = 4;                       // warps that issue MMAs: [half of a block][block parity]
+constexpr int kThreads = (4 + 4 * kGroups + 4) * 32;
+constexpr int kStep = 4;                          // row blocks per step: M = 128
+// Dequantised blocks in tensor memory, columns each.  A multiple of the groups and of 2: a buffer is filled by one
+// group and each of its halves used by one issuer only, so none waits for a phase of a barrier that lies two ahead.
+constexpr uint32_t kABufs = 6, kACols = kChan / 2;
+static_assert(kABufs % kGroups == 0 && kABufs % 2 == 0, "one filler and one user of each half per buffer");
+constexpr uint32_t kDCol = kABufs * kACols;       // accumulators of N columns, one per issuer
+constexpr int kXBytes = 128 * 1024;               // x staged by a CTA, at most
+constexpr int kCluster = 4;                       // CTAs that share the channels (2 and 8 measured slower)
+static_assert(kDCol + kIssuers * 32 <= 512, "tensor memory");
+
+struct Tail {
+  alignas(16) unsigned char ring[4 * kGroups][kSlots][kBlock];  // per dequantising warp
+  alignas(16) float red[32][128];                 // partial sums of a step: [token][row]
+  uint64_t full[4 * kGroups][kSlots];
+  float inv[32];                                  // per token: scale of its sums
+  uint64_t a_full[kABufs], a_empty[kABufs], d_full, d_empty, red_full, red_empty;
+  uint32_t tmem;
+};
+
+struct Params {
+  const uint16_t* x;
+  const uint8_t* packed;
+  const float* row_scale;
+  void* y;
+  int64_t n_out, n_in;
+  int m, n_kb, n_rb, y_fp32, x_bytes;
+  unsigned int* flags;
+};
+
+__device__ __forceinline__ void mbar_init(uint64_t* b, int n) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(smem_u32(b)), "r"(n) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t* b) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_u32(b)) : "memory");
+}
+// the barrier at the same place of CTA `rank` of the cluster; what this CTA wrote before is visible to its waiters
+__device__ __forceinline__ void mbar_arrive_cluster(uint64_t* b, uint32_t rank) {
+  asm volatile("{ .reg .u32 r; mapa.shared::cluster.u32 r, %0, %1;\n\t"
+               "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [r]; }\n" ::"r"(smem_u32(b)),
+               "r"(rank)
+               : "memory");
+}
+// D (+)= A B with A in tensor memory
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{ .reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};\n" ::"r"(a),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t a, uint32_t (&r)[16]) {  // valid after tcgen05.wait::ld
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(a)
+      : "memory");
+}
+// A loaded register used behind the wait (which the compiler does not tie to the load).
+__device__ __forceinline__ float tmem_value(uint32_t& r) {
+  asm volatile("" : "+r"(r));
+  return __uint_as_float(r);
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t a, uint32_t rank) {
+  float4 v;
+  asm volatile("{ .reg .u32 r; mapa.shared::cluster.u32 r, %4, %5; ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [r]; }\n"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(a), "r"(rank)
+               : "memory");
+  return v;
+}
+
+struct Row {  // a row's share of a block, as loaded
+  uint4 c[4];
+  uint2 s;
+};
+
+// kTok: token rows of the MMA (N), 16 or 32.
+template <int kTok>
+__global__ void __launch_bounds__(kThreads, 1) matvec_tc_kernel(const Params p, int C) {
+  extern __shared__ __align__(1024) unsigned char smem[];
+  Tail& sm = *reinterpret_cast<Tail*>(smem + p.x_bytes);
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = C > 1 ? int(blockIdx.x % unsigned(C)) : 0;
+  const int n_clusters = int(gridDim.x / unsigned(C)), cluster = int(blockIdx.x / unsigned(C));
+  // even shares (the products stay below 2^32: sizes_ok)
+  const int kb0 = int(uint32_t(p.n_kb) * uint32_t(rank) / uint32_t(C)),
+            nk = int(uint32_t(p.n_kb) * uint32_t(rank + 1) / uint32_t(C)) - kb0;
+  const int rb0 = int(uint32_t(p.n_rb) * uint32_t(cluster) / uint32_t(n_clusters)),
+            rb1 = int(uint32_t(p.n_rb) * uint32_t(cluster + 1) / uint32_t(n_clusters));
+  const int n_steps = (rb1 - rb0 + kStep - 1) / kStep;
+
+  bool late = false;  // a wait ran out: flagged, and no more waiting
+  auto wait = [&](uint64_t* b, uint32_t use) {  // the use-th completion of a barrier
+    if (!late && !bar_wait(smem_u32(b), use & 1u)) {
+      late = true;
+      atomicOr(p.flags, CSA2_FLAG_TIMEOUT);
+    }
+  };
+
+  if (tid == 0) {
+    for (uint32_t i = 0; i < kABufs; ++i) mbar_init(&sm.a_full[i], 4), mbar_init(&sm.a_empty[i], 2);
+    mbar_init(&sm.d_full, kIssuers), mbar_init(&sm.d_empty, 4);
+    mbar_init(&sm.red_full, C), mbar_init(&sm.red_empty, C);
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  }
+  if (warp == 3) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(smem_u32(&sm.tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
+  }
+  // A dequantising warp takes row block q of each step, of the channel blocks grp, grp + kGroups, ... of the steps
+  // one after the other; its first blocks are on their way while x is staged.
+  const int grp = (warp - 4) >> 2, q = warp & 3;
+  const int me = warp - 4;  // its ring
+  int l_k = grp, l_rb = rb0 + q;  // the next block to copy: of the share's channel blocks, and its row block
+  const uint8_t* l_src = p.packed + (int64_t(l_rb) * p.n_kb + kb0 + l_k) * kBlock;
+  auto copy = [&](int slot) {  // one thread; nothing where the step has no such row block
+    while (l_k >= nk && l_rb < rb1) l_k -= nk, l_rb += kStep, l_src += (int64_t(kStep) * p.n_kb - nk) * kBlock;
+    if (l_rb < rb1) block_copy(sm.ring[me][slot], l_src, &sm.full[me][slot]);
+    l_k += kGroups, l_src += kGroups * kBlock;
+  };
+  if (warp >= 4 && grp < kGroups) {
+    if (lane == 0) {
+      for (int i = 0; i < kSlots; ++i) mbar_init(&sm.full[me][i], 1);
+      asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+      for (int i = 0; i < kSlots; ++i) copy(i);
+    }
+    __syncwarp();
+  }
+  // x: a warp per token; groups of 64 channels, each [kTok rows][128 bytes], 16-byte pieces swizzled by the row.
+  // A lane keeps the first 2048 channels of the share between the two passes, and reads what lies behind again.
+  // Rows past the last token are left as they are: they reach their own columns of the sums alone.
+  for (int tok = (warp + kThreads / 32 - 4) % (kThreads / 32); tok < p.m; tok += kThreads / 32) {  // warp 3 comes last
+    const uint16_t* src = p.x + int64_t(tok) * p.n_in;
+    auto at = [&](int c) -> uint4 {  // channels c .. c+7 of the share
+      const int64_t ch = int64_t(kb0) * kChan + c;
+      return c < nk * kChan && ch < p.n_in ? __ldg(reinterpret_cast<const uint4*>(src + ch)) : make_uint4(0, 0, 0, 0);
+    };
+    auto mag = [](uint32_t am, const uint4& v) {
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) am = max(am, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
+      return am;
+    };
+    uint4 keep[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) keep[i] = at(lane * 8 + 256 * i);
+    uint32_t am = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) am = mag(am, keep[i]);
+    for (int c0 = 2048; c0 < nk * kChan; c0 += 2048) {
+      uint4 v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = at(c0 + lane * 8 + 256 * i);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) am = mag(am, v[i]);
+    }
+    am = __reduce_max_sync(0xffffffffu, am);
+    const int up = am ? min(max(141 - int(am >> 7), -126), 126) : 0;
+    const float f = __uint_as_float(uint32_t(127 + up) << 23);
+    auto put = [&](int c, const uint4& v) {
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      uint32_t o[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = attn::h2_bits(__floats2half2_rn(bf16lo(w[i]) * f, bf16hi(w[i]) * f));
+      if (c < nk * kChan)
+        *reinterpret_cast<uint4*>(smem + (c >> 6) * (kTok * 128) + tok * 128 + ((((c >> 3) & 7) ^ (tok & 7)) << 4)) =
+            make_uint4(o[0], o[1], o[2], o[3]);
+    };
+#pragma unroll
+    for (int i = 0; i < 8; ++i) put(lane * 8 + 256 * i, keep[i]);
+    for (int c0 = 2048; c0 < nk * kChan; c0 += 2048) {
+      uint4 v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = at(c0 + lane * 8 + 256 * i);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) put(c0 + lane * 8 + 256 * i, v[i]);
+    }
+    if (lane == 0) sm.inv[tok] = __uint_as_float(uint32_t(127 - up) << 23);
+  }
+  attn::fence_async_smem();
+  attn::tc_fence_before();
+  if (C > 1) cluster_arrive_wait();
+  else __syncthreads();
+  attn::tc_fence_after();
+  const uint32_t tmem = sm.tmem;
+
+  if (warp < kIssuers) {
+    // An issuer takes one half of every second channel block, into its own accumulator: one thread needs 54 cycles
+    // and more for an MMA and as much as several for a commit, the tensor core 16 for an MMA.
+    if (lane == 0) {
+      const uint32_t idesc = attn::instr_desc(128, false, false, kTok), d = tmem + kDCol + uint32_t(warp) * kTok;
+      const uint32_t half = uint32_t(warp) >> 1;
+      const uint64_t x0 = attn::smem_desc(smem_u32(smem) + half * (kTok * 128), 0, 1024);
+      uint32_t buf = uint32_t(warp) & 1u, use = 0;
+      int k = warp & 1;
+      for (int step = 0; step < n_steps; ++step, k -= nk) {
+        if (step > 0) wait(&sm.d_empty, uint32_t(step - 1));
+        for (bool first = true; k < nk; k += 2, first = false) {
+          wait(&sm.a_full[buf], use);
+          attn::tc_fence_after();
+          const uint32_t a = tmem + buf * kACols + half * (kACols / 2);
+          const uint64_t xk = x0 + uint64_t(uint32_t(2 * k) * (kTok * 128 / 16));
+#pragma unroll
+          for (uint32_t i = 0; i < kChan / 32; ++i) umma_ts(d, a + i * 8u, xk + uint64_t(i * 2u), idesc, !first || i > 0);
+          attn::umma_commit(smem_u32(&sm.a_empty[buf]));
+          buf += 2;
+          if (buf >= kABufs) buf -= kABufs, ++use;
+        }
+        attn::umma_commit(smem_u32(&sm.d_full));
+      }
+    }
+  } else if (warp >= 4 && grp < kGroups) {
+    const uint32_t lanes = uint32_t(32 * q) << 16, n_it = uint32_t(n_steps) * uint32_t(nk);
+    uint32_t buf = uint32_t(grp), use = 0;  // buffer, and how often it has been used
+    int k = grp, rb = rb0 + q;
+    int slot = 0, slot_use = 0;
+    for (uint32_t it = uint32_t(grp); it < n_it; it += kGroups) {
+      while (k >= nk) k -= nk, rb += kStep;
+      Row r;
+      if (rb < rb1) {
+        wait(&sm.full[me][slot], uint32_t(slot_use));
+        const unsigned char* blk = sm.ring[me][slot];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) r.c[j] = *reinterpret_cast<const uint4*>(blk + block_place(lane, j));
+        r.s = *reinterpret_cast<const uint2*>(blk + kCodeBytes + 8 * lane);
+        __syncwarp();
+        if (lane == 0) copy(slot);
+        if (++slot == kSlots) slot = 0, ++slot_use;
+      }
+      if (use > 0) wait(&sm.a_empty[buf], use - 1);
+      attn::tc_fence_after();
+      if (rb < rb1) {
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {  // 64 channels, 32 columns
+          const uint32_t sw = hf ? r.s.y : r.s.x;
+          const __half2 s01 = attn::bits_h2(attn::e4m3x2_to_f16x2(uint16_t(sw))),
+                        s23 = attn::bits_h2(attn::e4m3x2_to_f16x2(uint16_t(sw >> 16)));
+          uint32_t v[32];
+#pragma unroll
+          for (int w = 0; w < 8; ++w) {
+            const uint4 cw = r.c[2 * hf + (w >> 2)];
+            uint32_t* o = v + 4 * w;
+            attn::e2m1x8_to_f16x2x4((w & 3) == 0 ? cw.x : (w & 3) == 1 ? cw.y : (w & 3) == 2 ? cw.z : cw.w, o[0], o[1],
+                                    o[2], o[3]);
+            const __half2 sc = w < 2 ? __low2half2(s01) : w < 4 ? __high2half2(s01) : w < 6 ? __low2half2(s23)
+                                                                                          : __high2half2(s23);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[j] = attn::h2_bits(__hmul2(attn::bits_h2(o[j]), sc));
+          }
+          tmem_st32(tmem + lanes + buf * kACols + 32u * hf, v);
+        }
+        asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
+      }
+      attn::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.a_full[buf]);
+      k += kGroups, buf += kGroups;
+      if (buf >= kABufs) buf -= kABufs, ++use;
+    }
+  } else if (warp >= 4) {
+    const uint32_t lanes = uint32_t(32 * q) << 16;
+    for (int step = 0; step < n_steps; ++step) {
+      // the step's sums: this CTA's share of the channels, then the cluster's
+      const int rb = rb0 + step * kStep, nb = min(kStep, rb1 - rb);
+      wait(&sm.d_full, uint32_t(step));
+      attn::tc_fence_after();
+      if (step > 0 && C > 1 && !late && !bar_wait<true>(smem_u32(&sm.red_empty), uint32_t(step - 1) & 1u)) {
+        late = true;
+        atomicOr(p.flags, CSA2_FLAG_TIMEOUT);
+      }
+#pragma unroll
+      for (int j = 0; j < kTok; j += 16) {
+        uint32_t d[kIssuers][16];
+#pragma unroll
+        for (int c = 0; c < kIssuers; ++c) tmem_ld16(tmem + lanes + kDCol + uint32_t(c * kTok + j), d[c]);
+        asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          // (with one channel block in the share, a step has the issuers of one parity)
+          float v = 0.f;
+#pragma unroll
+          for (int c = 0; c < kIssuers; ++c) {
+            const float u = tmem_value(d[c][i]);
+            if (nk > 1 || (c & 1) == (step & 1)) v += u;
+          }
+          if (j + i < p.m) sm.red[j + i][32 * q + lane] = v * sm.inv[j + i];
+        }
+      }
+      attn::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.d_empty);
+      asm volatile("bar.sync 1, 128;\n" ::: "memory");  // warps 16 .. 19
+      const int t = tid & 127;
+      if (C > 1) {
+        if (t < C) mbar_arrive_cluster(&sm.red_full, uint32_t(t));
+        if (!late && !bar_wait<true>(smem_u32(&sm.red_full), uint32_t(step) & 1u)) {
+          late = true;
+          atomicOr(p.flags, CSA2_FLAG_TIMEOUT);
+        }
+      }
+      // this CTA finishes rows rank * 128 / C .. of the step, four rows of a token at a time
+      const int quads = 32 / C;
+      for (int e = t; e < quads * p.m; e += 128) {
+        const int tok = e / quads, r = (rank * quads + e - tok * quads) * 4;
+        if (r >= nb * kRows) continue;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        const uint32_t at = smem_u32(&sm.red[tok][r]);
+        for (int c = 0; c < C; ++c) {
+          const float4 u = C > 1 ? ld_cluster4(at, uint32_t(c)) : *reinterpret_cast<const float4*>(&sm.red[tok][r]);
+          v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+        }
+        const int64_t n = int64_t(rb) * kRows + r;
+        const float o[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (n + i >= p.n_out) break;
+          const float s = p.row_scale ? o[i] * __ldg(p.row_scale + n + i) : o[i];
+          if (p.y_fp32) static_cast<float*>(p.y)[int64_t(tok) * p.n_out + n + i] = s;
+          else static_cast<__nv_bfloat16*>(p.y)[int64_t(tok) * p.n_out + n + i] = __float2bfloat16_rn(s);
+        }
+      }
+      asm volatile("bar.sync 1, 128;\n" ::: "memory");
+      if (C > 1 && t < C) mbar_arrive_cluster(&sm.red_empty, uint32_t(t));
+    }
+  }
+  __syncwarp();
+  attn::tc_fence_before();
+  if (C > 1) cluster_arrive_wait();  // no CTA leaves while its sums are being read
+  else __syncthreads();
+  if (warp == 3) {
+    attn::tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(tmem) : "memory");
+  }
+}
+
+// Launches the tensor-memory form; cudaErrorNotSupported where a cluster's shared memory does not hold x.
+template <int kTok>
+cudaError_t launch_tc(const mv::Params& g, int sms, cudaStream_t st) {
+  constexpr int C = kCluster;
+  Params p = {};
+  p.x = g.x, p.packed = g.packed, p.row_scale = g.row_scale, p.y = g.y;
+  p.n_out = g.n_out, p.n_in = g.n_in, p.m = g.m, p.n_kb = g.n_kb, p.n_rb = g.n_rb, p.y_fp32 = g.y_fp32;
+  p.x_bytes = ((g.n_kb + C - 1) / C * kTok * kChan * 2 + 1023) / 1024 * 1024;
+  if (p.x_bytes > kXBytes || C > g.n_kb) return cudaErrorNotSupported;
+  p.flags = g.flags;
+  const size_t smem = size_t(p.x_bytes) + sizeof(Tail);
+  auto kern = matvec_tc_kernel<kTok>;
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), kXBytes + sizeof(Tail), done);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = unsigned(C);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  // clusters that run at once (one CTA per SM whatever the shared memory), looked up once per device
+  static std::atomic<int> room[64];
+  int dev = 0;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  int clusters = dev < 64 ? room[dev].load() : 0;
+  if (clusters <= 0) {
+    cfg.gridDim = dim3(unsigned(C));
+    cfg.dynamicSmemBytes = kXBytes + sizeof(Tail);
+    if (cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg) != cudaSuccess || clusters < 1) clusters = sms / C;
+    cfg.dynamicSmemBytes = smem;
+    if (dev < 64) room[dev] = clusters;
+  }
+  cfg.gridDim = dim3(unsigned(std::min(clusters, g.n_rb) * C));
+  return cudaLaunchKernelEx(&cfg, kern, p, C);
+}
+
+}  // namespace tc
+
 template <int TG>
 cudaError_t launch_wr(const Params& p, int sms, cudaStream_t st) {
-  // the widest CTA and the smallest cluster that still give two CTAs per SM, else the most CTAs there are
+  // The most CTAs that run at once and have a block for every warp, of these the widest (a CTA stages x for all its
+  // rows).  Measured, us at one row x 8200 x 4112: 264 CTAs of 8 row blocks 9.0, 258 of 2 10.9, twice as many of 4 13;
+  // at one row x 512 x 4096: 64 CTAs of 2 row blocks 4.4, 128 of 1 (half the warps without a block) 4.8.
+  int best_wr = 1, best_c = 1;
+  int64_t best = 0;
   for (int wr = 8; wr >= 1; wr /= 2)
-    for (int C = 1; C <= kMaxCluster; C *= 2) {
-      const int64_t ctas = int64_t((p.n_tiles + 2 * wr - 1) / (2 * wr)) * C;
-      const bool last = wr == 1 && C == kMaxCluster;
-      if (ctas < 2 * int64_t(sms) && !last) continue;
-      if (wr == 8) return launch<TG, 8>(p, C, st);
-      if (wr == 4) return launch<TG, 4>(p, C, st);
-      if (wr == 2) return launch<TG, 2>(p, C, st);
-      return launch<TG, 1>(p, C, st);
+    for (int c = 1; c <= kMaxCluster && c <= p.n_kb; c *= 2) {
+      const int64_t ctas = int64_t((p.n_rb + wr - 1) / wr) * c;
+      // three or four groups of tokens leave room for one CTA per SM, and for 15 clusters of 8
+      const int64_t room = TG <= 2 ? 2 * int64_t(sms) : c == 8 ? int64_t(sms) * 3 / 4 : int64_t(sms) * 15 / 16;
+      if (ctas > best && ctas <= room && ctas * kWarps <= std::max<int64_t>(int64_t(p.n_rb) * p.n_kb, kWarps))
+        best = ctas, best_wr = wr, best_c = c;
     }
-  return cudaErrorInvalidValue;
+  if (best == 0) best_wr = 8;  // more row blocks than run at once
+  switch (best_wr) {
+    case 8: return launch<TG, 8>(p, best_c, st);
+    case 4: return launch<TG, 4>(p, best_c, st);
+    case 2: return launch<TG, 2>(p, best_c, st);
+    default: return launch<TG, 1>(p, best_c, st);
+  }
 }
 
 inline bool al(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 inline bool sizes_ok(int64_t n_out, int64_t n_in) {
-  return n_out >= 0 && n_in >= 0 && n_in % CSA2_GROUP == 0 && n_out <= (int64_t(1) << 30) && n_in <= (int64_t(1) << 30);
+  return n_out >= 0 && n_in >= 0 && n_in % CSA2_GROUP == 0 && n_out <= (int64_t(1) << 28) && n_in <= (int64_t(1) << 28);
 }
 
 }  // namespace mv
@@ -309,7 +763,7 @@ extern "C" csa2_status csa2_fp4_pack_weight(const uint8_t* codes, const uint8_t*
   if (!sizes_ok(n_out, n_in)) return CSA2_ERR_INVALID_ARG;
   if (n_out * n_in == 0) return CSA2_OK;
   if (!codes || !scales || !packed || !al(codes, 16) || !al(scales, 16) || !al(packed, 16)) return CSA2_ERR_INVALID_ARG;
-  const int64_t n_kb = (n_in + kChan - 1) / kChan, n_blocks = (n_out + kRows - 1) / kRows * n_kb;
+  const int64_t n_kb = (n_in + kChan - 1) / kChan, n_blocks = (n_out + kRows - 1) / kRows * n_kb;  // a warp each
   if (n_blocks * 32 / 256 > 0x7FFFFFF0ll) return CSA2_ERR_INVALID_ARG;
   return launch_pdl(pack_kernel, dim3(unsigned((n_blocks * 32 + 255) / 256)), dim3(256), 0,
                     reinterpret_cast<cudaStream_t>(stream), codes, scales, n_out, n_in, n_kb, n_blocks,
@@ -331,9 +785,18 @@ extern "C" csa2_status csa2_fp4_matvec(const uint16_t* x, int m, const uint8_t* 
   Params p = {};
   p.x = x, p.packed = packed, p.row_scale = row_scale, p.y = y;
   p.n_out = n_out, p.n_in = n_in, p.m = m, p.y_fp32 = y_fp32;
-  p.n_kb = int((n_in + kChan - 1) / kChan), p.n_tiles = int((n_out + kRows - 1) / kRows);
+  p.flags = device_flags_ptr();
+  if (!p.flags) return CSA2_ERR_CUDA;
+  p.n_kb = int((n_in + kChan - 1) / kChan), p.n_rb = int((n_out + kRows - 1) / kRows);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e;
+  cudaError_t e = cudaErrorNotSupported;
+  // The tensor-memory form where there is enough weight to pay for its set-up.  Measured, us, this form against the
+  // other: 32 rows x 16384 x 8192 29 / 65, 24 x 4096 x 4096 10.7 / 12.6, 32 x 512 x 4096 9.5 / 9.3,
+  // 16 x 16384 x 8192 25.8 / 30, 16 x 8192 x 4096 11.8 / 12.0, 8 x 16384 x 8192 25.6 / 21.
+  const int64_t blocks = int64_t(p.n_rb) * p.n_kb;
+  if ((m > 16 && blocks >= 2048) || (m > 8 && blocks >= 16384))
+    e = m <= 16 ? tc::launch_tc<16>(p, sms, st) : tc::launch_tc<32>(p, sms, st);
+  if (e == cudaErrorNotSupported)
   switch ((m + 7) / 8) {
     case 1: e = launch_wr<1>(p, sms, st); break;
     case 2: e = launch_wr<2>(p, sms, st); break;

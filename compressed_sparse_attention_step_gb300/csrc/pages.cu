@@ -260,8 +260,8 @@ extern "C" csa2_status csa2_block_tables(const int32_t* old_lens, const int32_t*
   const int64_t items = std::max(int64_t(B) * n_new, int64_t(B) * max_pages / 16);
   const int grid = int(std::min<int64_t>(std::max<int64_t>(items / (4 * kThreads), 1), sms));
   const size_t smem = size_t(B) * 8;
-  if (smem > 48 * 1024 && cudaFuncSetAttribute(block_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               int(smem)) != cudaSuccess)
+  static std::atomic<uint64_t> done{0};
+  if (allow_smem(reinterpret_cast<const void*>(block_tables_kernel), size_t(CSA2_MAX_SEQS) * 8, done) != cudaSuccess)
     return CSA2_ERR_CUDA;
   return launch_pdl(block_tables_kernel, dim3(grid), dim3(kThreads), smem, reinterpret_cast<cudaStream_t>(stream),
                     old_lens, new_lens, B, shift, block_table, max_pages, free_pages, free_cap, pool_state, granted,

@@ -34,43 +34,43 @@ namespace tree {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = 4;
-constexpr int kTile = 16;                                          // rows per step
-constexpr int kMaxSel = CSA2_MAX_ATTN_K;                           // selected rows per node
-constexpr int kMaxWin = CSA2_MAX_W - 1 + CSA2_MAX_TREE;            // window rows and ancestors
-constexpr int kSelTiles = kMaxSel / kTile;
-constexpr int kWinTiles = (kMaxWin + kTile - 1) / kTile;
+constexpr int kMaxSel = CSA2_MAX_ATTN_K;                  // selected rows per node
+constexpr int kMaxWin = CSA2_MAX_W - 1 + CSA2_MAX_TREE;   // window rows and ancestors
+constexpr int kStep = 16, kSelRows = 32;                 // rows per step, selected rows per slot
+constexpr int kWinList = (kMaxWin + kStep - 1) / kStep * kStep;
 constexpr int kMaxCluster = 8;
 constexpr float kNegInf = -INFINITY;
 // The softmax reference m starts kHead below the largest score of a CTA's first step and moves only when a
 // score passes it by kHead + 8, so P lies below 2^15 and the largest is at least 2^kHead: in f16's range, whose
 // subnormal rounding (2^-25) is then 2^-32 of the largest P.
 constexpr float kHead = 7.0f;
+constexpr float kFloor = -1e30f;  // the reference before any score
 
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                               uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// 8 x 8 transpose of 16-bit elements held as matrix fragments (row lane / 4, columns 2 (lane % 4), + 1)
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(v));
+  return r;
 }
 template <bool kF16>
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
   if (kF16) mma_f16_16816(d, a0, a1, a2, a3, b0, b1);
   else mma_bf16(d, a0, a1, a2, a3, b0, b1);
-}
-// 8 x 8 transpose of 16-bit elements held as matrix fragments (row lane / 4, columns 2 (lane % 4), + 1)
-__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
-  uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(v));
-  return r;
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) { return attn::h2_bits(__floats2half2_rn(lo, hi)); }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -104,113 +104,124 @@ struct Params {
   unsigned int* flags;
 };
 
+// Staged rows.  The 16-byte pieces of a row are stored at their index XOR a function of the row, so that the
+// eight lanes of a 16-byte access phase (rows g and g + 1, four t) fall into different banks.
+constexpr int kSelSlots = 3, kWinSlots = 2;
+__device__ __forceinline__ int sel_swz(int r) { return (r & 1) << 2; }
+__device__ __forceinline__ int win_swz(int r) { return (r & 1) << 1; }
+
+struct alignas(128) SelSlot {
+  unsigned char codes[kSelRows][CSA2_CODE_BYTES];
+  unsigned char scales[kSelRows][CSA2_SCALE_BYTES];
+};
+struct alignas(128) WinSlot {
+  unsigned char rows[kStep][CSA2_D * 2];
+};
 struct Shared {
-  float4 part[2][kWarps][2][32];     // partial scores of a step: [buffer][warp][half][lane]
-  int32_t sel[kMaxSel];              // selected rows (-1: empty)
-  int32_t win[kWinTiles * kTile];    // window buffer rows (-1: empty)
-  uint32_t sel_mask[kSelTiles];      // valid rows of a step
+  WinSlot win_slot[kWinSlots];    // at the end: O of this CTA's part, for the merge
+  SelSlot sel_slot[kSelSlots];
+  float2 part[4][kWarps][32];     // partial scores of a step: [fragment register][warp][lane]
+  uint4 prob[32];                 // P fragment of a step, one register from each warp
+  uint64_t sel_full[kSelSlots], win_full[kWinSlots];  // mbarriers: a slot's copies have landed
+  int32_t sel[kMaxSel];           // this node's selected rows, without gaps; the last slot filled up
+  int32_t win[kWinList];          // its window buffer rows, likewise
+  int32_t n_sel, n_win;
   int32_t parent[CSA2_MAX_TREE];
   float qmax[kWarps][16];
-  float2 ml[16];                     // (reference maximum, sum) of this CTA's part, for the merge
+  float tops[kWarps][8];          // a step's largest scores per head, where the reference moves
+  float sums[kWarps][8];
+  float2 ml[16];                  // (reference, sum) of this CTA's part, for the merge
 };
-struct SharedMerge : Shared {
-  float o[16][CSA2_D];
-};
+static_assert(CSA2_H * CSA2_D * 4 <= sizeof(WinSlot) * kWinSlots, "a part's O fits the window slots");
+static_assert(3 * (sizeof(Shared) + 1024) <= 228 * 1024, "three CTAs per SM");
 
-// State of a lane: O of heads g and g + 8 over its 32 channels, and the softmax statistics of both.
+// State of a lane: O of heads g and g + 8 over its 32 channels, the references of both, and the sum of
+// the P values that this lane computes (warps 0 and 2: head g, warps 1 and 3: head g + 8).
 struct State {
   float o[16][4];
-  float m0, m1, l0, l1;
+  float m0, m1, l;
 };
 
-// One step of 16 rows held as fragments kf (rows g and g + 8; 16 channel pairs each).
-template <bool kF16>
-__device__ __forceinline__ void step(State& s, const uint32_t (&qf)[2][16], const uint32_t (&kf)[2][16], uint32_t vmask,
-                                     float sc0, float sc1, float4 (*part)[2][32], int warp, int lane) {
-  const int t = lane & 3;
-  float S0[4] = {0.f, 0.f, 0.f, 0.f}, S1[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    mma<kF16>(S0, qf[0][2 * i], qf[1][2 * i], qf[0][2 * i + 1], qf[1][2 * i + 1], kf[0][2 * i], kf[0][2 * i + 1]);
-    mma<kF16>(S1, qf[0][2 * i], qf[1][2 * i], qf[0][2 * i + 1], qf[1][2 * i + 1], kf[1][2 * i], kf[1][2 * i + 1]);
-  }
-  part[warp][0][lane] = make_float4(S0[0], S0[1], S0[2], S0[3]);
-  part[warp][1][lane] = make_float4(S1[0], S1[1], S1[2], S1[3]);
-  __syncthreads();
-  // every warp sums the four parts in the same order, so all of them take the same decisions below
-  float x[8];
+// One step of 16 rows held as fragments kf (rows g and g + 8; 16 channel pairs each), the first `left`
+// of them real.  Warp w sums the four warps' partial scores for register w of P's fragment, takes their
+// exponentials and hands the register to the others.  `loaded` runs when every warp holds its fragments.
+template <bool kF16, typename F>
+__device__ __forceinline__ void step(State& s, const uint32_t (&qf)[2][16], uint32_t (&kf)[2][16], int left, float scale,
+                                     Shared& sm, int warp, int lane, F loaded) {
+  const int t = lane & 3, g = lane >> 2;
   {
-    float4 a = part[0][0][lane], b = part[1][0][lane], c = part[2][0][lane], d = part[3][0][lane];
-    x[0] = (a.x + b.x) + (c.x + d.x), x[1] = (a.y + b.y) + (c.y + d.y);
-    x[2] = (a.z + b.z) + (c.z + d.z), x[3] = (a.w + b.w) + (c.w + d.w);
-    a = part[0][1][lane], b = part[1][1][lane], c = part[2][1][lane], d = part[3][1][lane];
-    x[4] = (a.x + b.x) + (c.x + d.x), x[5] = (a.y + b.y) + (c.y + d.y);
-    x[6] = (a.z + b.z) + (c.z + d.z), x[7] = (a.w + b.w) + (c.w + d.w);
-  }
-  // x[0..1]: head g, rows 2t, 2t+1; x[2..3]: head g+8; x[4..7]: the same of rows 8+2t, 9+2t
+    float S0[4] = {0.f, 0.f, 0.f, 0.f}, S1[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] *= (i & 2) ? sc1 : sc0;
-  if (vmask != 0xFFFFu) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (!((vmask >> (8 * (i >> 2) + 2 * t + (i & 1))) & 1u)) x[i] = kNegInf;
+    for (int i = 0; i < 8; ++i) {
+      mma<kF16>(S0, qf[0][2 * i], qf[1][2 * i], qf[0][2 * i + 1], qf[1][2 * i + 1], kf[0][2 * i], kf[0][2 * i + 1]);
+      mma<kF16>(S1, qf[0][2 * i], qf[1][2 * i], qf[0][2 * i + 1], qf[1][2 * i + 1], kf[1][2 * i], kf[1][2 * i + 1]);
+    }
+    sm.part[0][warp][lane] = make_float2(S0[0], S0[1]);  // head g, rows 2t, 2t + 1
+    sm.part[1][warp][lane] = make_float2(S0[2], S0[3]);  // head g + 8
+    sm.part[2][warp][lane] = make_float2(S1[0], S1[1]);  // rows 8 + 2t, 9 + 2t
+    sm.part[3][warp][lane] = make_float2(S1[2], S1[3]);
   }
-  const float t0 = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[4], x[5]));
-  const float t1 = fmaxf(fmaxf(x[2], x[3]), fmaxf(x[6], x[7]));
-  if (__any_sync(0xffffffffu, t0 > s.m0 + (kHead + 8.f) || t1 > s.m1 + (kHead + 8.f))) {
-    const float n0 = fmaxf(s.m0, quad_max(t0) - kHead), n1 = fmaxf(s.m1, quad_max(t1) - kHead);
-    const float c0 = s.m0 == kNegInf ? 0.f : attn::ex2(s.m0 - n0), c1 = s.m1 == kNegInf ? 0.f : attn::ex2(s.m1 - n1);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) kf[0][i] = transpose8(kf[0][i]), kf[1][i] = transpose8(kf[1][i]);
+  __syncthreads();
+  const float2 a = sm.part[warp][0][lane], b = sm.part[warp][1][lane], c = sm.part[warp][2][lane],
+               d = sm.part[warp][3][lane];
+  float x0 = ((a.x + b.x) + (c.x + d.x)) * scale, x1 = ((a.y + b.y) + (c.y + d.y)) * scale;
+  if (left < kStep) {
+    const int r = 8 * (warp >> 1) + 2 * t;
+    if (r >= left) x0 = kNegInf;
+    if (r + 1 >= left) x1 = kNegInf;
+  }
+  const float m = (warp & 1) ? s.m1 : s.m0;
+  float p0 = attn::ex2(x0 - m), p1 = attn::ex2(x1 - m);
+  uint32_t* prob = reinterpret_cast<uint32_t*>(&sm.prob[lane]) + warp;
+  *prob = kF16 ? pack_f16(p0, p1) : pack_bf16(p0, p1);
+  loaded();
+  if (__syncthreads_or(fmaxf(x0, x1) > m + (kHead + 8.f))) {
+    // the references move: to the largest scores of this step less kHead, where that is more
+    const float top = quad_max(fmaxf(x0, x1));
+    if (t == 0) sm.tops[warp][g] = top;
+    __syncthreads();
+    const float n0 = fmaxf(s.m0, fmaxf(sm.tops[0][g], sm.tops[2][g]) - kHead);
+    const float n1 = fmaxf(s.m1, fmaxf(sm.tops[1][g], sm.tops[3][g]) - kHead);
+    const float c0 = s.m0 == n0 ? 1.f : attn::ex2(s.m0 - n0), c1 = s.m1 == n1 ? 1.f : attn::ex2(s.m1 - n1);
     s.m0 = n0, s.m1 = n1;
-    s.l0 *= c0, s.l1 *= c1;
+    const float n = (warp & 1) ? n1 : n0;
+    s.l *= (warp & 1) ? c1 : c0;
 #pragma unroll
     for (int i = 0; i < 16; ++i) s.o[i][0] *= c0, s.o[i][1] *= c0, s.o[i][2] *= c1, s.o[i][3] *= c1;
+    p0 = attn::ex2(x0 - n), p1 = attn::ex2(x1 - n);
+    *prob = kF16 ? pack_f16(p0, p1) : pack_bf16(p0, p1);
+    __syncthreads();
   }
-  const float r0 = s.m0 == kNegInf ? 0.f : s.m0, r1 = s.m1 == kNegInf ? 0.f : s.m1;
+  s.l += p0 + p1;
+  const uint4 p = sm.prob[lane];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = attn::ex2(x[i] - ((i & 2) ? r1 : r0));
-  s.l0 += (x[0] + x[1]) + (x[4] + x[5]);
-  s.l1 += (x[2] + x[3]) + (x[6] + x[7]);
-  uint32_t p[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) p[i] = kF16 ? pack_f16(x[2 * i], x[2 * i + 1]) : pack_bf16(x[2 * i], x[2 * i + 1]);
-#pragma unroll
-  for (int i = 0; i < 16; ++i)
-    mma<kF16>(s.o[i], p[0], p[1], p[2], p[3], transpose8(kf[0][i]), transpose8(kf[1][i]));
+  for (int i = 0; i < 16; ++i) mma<kF16>(s.o[i], p.x, p.y, p.z, p.w, kf[0][i], kf[1][i]);
 }
 
-// The raw bytes of rows g and g + 8 of a step, as a lane loads them ahead.
-struct Raw {
-  uint4 c[2];
-  uint32_t s[2];
-};
-__device__ __forceinline__ void load_raw(Raw& r, const Params& p, const int32_t* sel, int64_t seq, int tile, int g,
-                                         int part) {
+// Rows g and g + 8 of a step of selected rows: f16 pairs of this lane's 32 channels.
+__device__ __forceinline__ void dequant(const unsigned char* codes, const unsigned char* scales, uint32_t (&kf)[2][16]) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const int32_t row = sel[tile * kTile + 8 * h + g];
-    r.c[h] = make_uint4(0, 0, 0, 0);
-    r.s[h] = 0;
-    if (row >= 0) {
-      const int64_t at = seq + row;
-      r.c[h] = __ldg(reinterpret_cast<const uint4*>(p.codes + at * CSA2_CODE_BYTES) + part);
-      r.s[h] = __ldg(reinterpret_cast<const uint16_t*>(p.scales + at * CSA2_SCALE_BYTES) + part);
+    const uint4 c = *reinterpret_cast<const uint4*>(codes + 8 * h * CSA2_CODE_BYTES);
+    const __half2 s2 =
+        attn::bits_h2(attn::e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(scales + 8 * h * CSA2_SCALE_BYTES)));
+    const __half2 lo = __low2half2(s2), hi = __high2half2(s2);
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      attn::e2m1x8_to_f16x2x4(w[i], kf[h][4 * i], kf[h][4 * i + 1], kf[h][4 * i + 2], kf[h][4 * i + 3]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        kf[h][4 * i + j] = attn::h2_bits(__hmul2(attn::bits_h2(kf[h][4 * i + j]), i < 2 ? lo : hi));
     }
   }
 }
-__device__ __forceinline__ void dequant(const Raw& r, uint32_t (&kf)[2][16]) {
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint32_t s2 = attn::e4m3x2_to_f16x2(uint16_t(r.s[h]));
-    const __half2 lo = __low2half2(attn::bits_h2(s2)), hi = __high2half2(attn::bits_h2(s2));
-    const uint32_t w[4] = {r.c[h].x, r.c[h].y, r.c[h].z, r.c[h].w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t f[4];
-      attn::e2m1x8_to_f16x2x4(w[i], f[0], f[1], f[2], f[3]);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) kf[h][4 * i + j] = attn::h2_bits(__hmul2(attn::bits_h2(f[j]), i < 2 ? lo : hi));
-    }
-  }
+
+// The calling thread's cp.async copies so far arrive at the mbarrier when they have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(bar) : "memory");
 }
 
 __device__ __forceinline__ void cluster_arrive_wait() {
@@ -239,7 +250,7 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t a) {
 // parts through distributed shared memory, in rank order.
 template <bool kMerge>
 __global__ void __launch_bounds__(kThreads, 3) tree_attn_kernel(const Params p, int C) {
-  extern __shared__ __align__(16) unsigned char smem_raw[];
+  extern __shared__ __align__(128) unsigned char smem_raw[];
   Shared& sm = *reinterpret_cast<Shared*>(smem_raw);
   pdl_wait();
   pdl_trigger();
@@ -253,95 +264,175 @@ __global__ void __launch_bounds__(kThreads, 3) tree_attn_kernel(const Params p, 
   // Q of heads g and g + 8, as bf16 pairs
   const uint16_t* qrow = p.q + row * (CSA2_H * CSA2_D) + chan;
   uint32_t qf[2][16];
-  auto load_q = [&]() {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+  for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(qrow + (g + 8 * h) * CSA2_D) + i);
-        qf[h][4 * i] = v.x, qf[h][4 * i + 1] = v.y, qf[h][4 * i + 2] = v.z, qf[h][4 * i + 3] = v.w;
-      }
-  };
-  load_q();
-
-  // the row lists
-  const int nv = p.n_valid ? min(max(p.n_valid[row], 0), p.k) : p.k;
-  const int nsel = (nv + kTile - 1) / kTile;
-  for (int i = tid; i < (nsel + 1) / 2 * 32; i += kThreads) {  // whole warps: two steps each
-    const int32_t r = i < nv ? p.idx[row * p.k + i] : -1;
-    const bool ok = r >= 0 && int64_t(r) < p.cap;
-    if (r >= 0 && !ok) atomicOr(p.flags, CSA2_FLAG_INDEX_OOB);
-    sm.sel[i] = ok ? r : -1;
-    const uint32_t bal = __ballot_sync(0xffffffffu, ok);
-    if ((i & 15) == 0) sm.sel_mask[i >> 4] = (bal >> (lane & 16)) & 0xFFFFu;
+    for (int i = 0; i < 4; ++i) {
+      // in the order of the window's pieces
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(qrow + (g + 8 * h) * CSA2_D) + (i ^ (t >> 1)));
+      qf[h][4 * i] = v.x, qf[h][4 * i + 1] = v.y, qf[h][4 * i + 2] = v.z, qf[h][4 * i + 3] = v.w;
+    }
+  if (tid == 0) {
+    for (int j = 0; j < kSelSlots; ++j)
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(smem_u32(&sm.sel_full[j])), "n"(kThreads) : "memory");
+    for (int j = 0; j < kWinSlots; ++j)
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(smem_u32(&sm.win_full[j])), "n"(kThreads) : "memory");
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
-  if (tid < p.N) sm.parent[tid] = p.parent[int64_t(b) * p.N + tid];
-  // per head: the largest magnitude of Q (as bf16 bits)
-  uint32_t am[2] = {0, 0};
+
+  // The row lists, without gaps: warp 0 the selected rows, warp 1 the window rows.  The entries that fill a
+  // list's last step repeat a row of the node's own; their P is zero.
+  if (warp == 0) {
+    const int nv = p.n_valid ? min(max(p.n_valid[row], 0), p.k) : p.k;
+    int n = 0;
+    for (int i0 = 0; i0 < nv; i0 += 128) {
+      int32_t r[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int i = i0 + 32 * j + lane;
+        r[j] = i < nv ? __ldg(p.idx + row * p.k + i) : -1;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bool ok = r[j] >= 0 && int64_t(r[j]) < p.cap;
+        if (r[j] >= 0 && !ok) atomicOr(p.flags, CSA2_FLAG_INDEX_OOB);
+        const uint32_t bal = __ballot_sync(0xffffffffu, ok);
+        if (ok) sm.sel[n + __popc(bal & ((1u << lane) - 1u))] = r[j];
+        n += __popc(bal);
+      }
+    }
+    __syncwarp();
+    if (n & (kSelRows - 1)) {
+      const int i = n + lane;
+      if (i < (n + kSelRows - 1) / kSelRows * kSelRows) sm.sel[i] = sm.sel[0];
+    }
+    if (lane == 0) sm.n_sel = n;
+  } else if (warp == 1) {
+    for (int i = lane; i < p.N; i += 32) sm.parent[i] = p.parent[int64_t(b) * p.N + i];
+    __syncwarp();
+    // ancestors of the node, itself included
+    uint64_t anc = 0;
+    int depth = -1;
+    for (int cur = node; cur >= 0;) {
+      anc |= 1ull << cur;
+      ++depth;
+      const int up = sm.parent[cur];
+      if (up < -1 || up >= cur) {  // not a tree in node order: taken as a root
+        if (lane == 0 && rank == 0) atomicOr(p.flags, CSA2_FLAG_INDEX_OOB);
+        break;
+      }
+      cur = up;
+    }
+    // the committed rows [first, W - 1), then the ancestors less than W tokens away
+    int nw = 0;
+    if (p.W > 0) {
+      const int wl = min(max(p.win_len ? p.win_len[b] : p.W - 1, 0), p.W - 1);
+      const int first = max(depth, p.W - 1 - wl), n_com = max(p.W - 1 - first, 0);
+      const int drop = max(depth + 1 - p.W, 0);  // the bits of anc ascend with the depth
+      for (int i = 0; i < drop; ++i) anc &= anc - 1;
+      nw = n_com + __popcll(anc);
+      for (int i = lane; i < (nw + kStep - 1) / kStep * kStep; i += 32) {
+        int32_t r = p.W - 1 + node;
+        if (i < n_com) r = first + i;
+        else if (i < nw) {
+          uint64_t m = anc;
+          for (int j = n_com; j < i; ++j) m &= m - 1;
+          r = p.W - 1 + (__ffsll(static_cast<long long>(m)) - 1);
+        }
+        sm.win[i] = r;
+      }
+    }
+    if (lane == 0) sm.n_win = nw;
+  }
+  // per head: the largest magnitude of Q
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
+    uint32_t am = 0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) am[h] = max(am[h], max(qf[h][i] & 0x7FFFu, (qf[h][i] >> 16) & 0x7FFFu));
-    am[h] = max(am[h], __shfl_xor_sync(0xffffffffu, am[h], 1));
-    am[h] = max(am[h], __shfl_xor_sync(0xffffffffu, am[h], 2));
-    if (t == 0) sm.qmax[warp][g + 8 * h] = __uint_as_float(am[h] << 16);
+    for (int i = 0; i < 16; ++i) am = max(am, max(qf[h][i] & 0x7FFFu, (qf[h][i] >> 16) & 0x7FFFu));
+    am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
+    am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
+    if (t == 0) sm.qmax[warp][g + 8 * h] = __uint_as_float(am << 16);
   }
   __syncthreads();
 
-  // ancestors of the node, itself included
-  uint64_t anc = 0;
-  int depth = -1;
-  for (int cur = node; cur >= 0;) {
-    anc |= 1ull << cur;
-    ++depth;
-    const int up = sm.parent[cur];
-    if (up < -1 || up >= cur) {  // not a tree in node order: taken as a root
-      if (tid == 0 && rank == 0) atomicOr(p.flags, CSA2_FLAG_INDEX_OOB);
-      break;
-    }
-    cur = up;
+  const int n_sel = sm.n_sel, n_win = sm.n_win;
+  const int win_steps = (n_win + kStep - 1) / kStep, sel_steps = (n_sel + kSelRows - 1) / kSelRows;
+  const bool any = win_steps + sel_steps > 0;
+  // this CTA's steps: of the list of window steps (weight 1) and selected steps (weight 2)
+  int w0 = 0, w1 = win_steps, s0 = 0, s1 = sel_steps;
+  if (kMerge) {
+    const int total = win_steps + 2 * sel_steps;
+    const int i0 = total * rank / C, i1 = total * (rank + 1) / C;
+    w0 = min(i0, win_steps), w1 = min(i1, win_steps);
+    s0 = (max(i0 - win_steps, 0) + 1) / 2, s1 = (max(i1 - win_steps, 0) + 1) / 2;
   }
-  // window rows: the committed rows [first, W - 1), then the ancestors less than W tokens away
-  int n_com = 0, nw = 0, first = 0;
-  if (p.W > 0) {
-    const int wl = min(max(p.win_len ? p.win_len[b] : p.W - 1, 0), p.W - 1);
-    first = max(depth, p.W - 1 - wl);
-    n_com = max(p.W - 1 - first, 0);
-    // the node's ancestors in order of depth: the bits of anc ascend with it
-    const int drop = max(depth + 1 - p.W, 0);
-    for (int i = 0; i < drop; ++i) anc &= anc - 1;
-    nw = n_com + __popcll(anc);
-    const int nwt = (nw + kTile - 1) / kTile * kTile;
-    for (int i = tid; i < nwt; i += kThreads) {
-      int32_t r = -1;
-      if (i < n_com) r = first + i;
-      else if (i < nw) {
-        uint64_t m = anc;
-        for (int j = n_com; j < i; ++j) m &= m - 1;
-        r = p.W - 1 + (__ffsll(static_cast<long long>(m)) - 1);
-      }
-      sm.win[i] = r;
+
+  // Copies of a step's rows, by all threads; every row of the lists is valid.
+  const int64_t win_base = int64_t(b) * (p.W - 1 + p.N), sel_base = int64_t(b) * p.seq_rows;
+  auto fill_win = [&](int i) {
+    if (i >= w1) return;
+    const int sl = (i - w0) % kWinSlots, r = tid >> 3, c = tid & 7;
+    const unsigned char* src = reinterpret_cast<const unsigned char*>(p.swa + (win_base + sm.win[i * kStep + r]) * CSA2_D);
+    const uint32_t dst = smem_u32(&sm.win_slot[sl].rows[r][(c ^ win_swz(r)) * 16]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) cp_async16(dst + 128 * j, src + 16 * c + 128 * j, 16);
+    cp_async_arrive(smem_u32(&sm.win_full[sl]));
+  };
+  auto fill_sel = [&](int i) {
+    if (i >= s1) return;
+    const int sl = (i - s0) % kSelSlots, r = tid >> 2, c = tid & 3;
+    const int64_t row = sel_base + sm.sel[i * kSelRows + r];
+    const uint8_t* src = p.codes + row * CSA2_CODE_BYTES + 16 * c;
+    const uint32_t dst = smem_u32(&sm.sel_slot[sl].codes[r][(c ^ sel_swz(r)) * 16]);  // piece c + 4j: XOR 4j
+#pragma unroll
+    for (int j = 0; j < 4; ++j) cp_async16((dst ^ (64 * (j & 1))) + 128 * (j >> 1), src + 64 * j, 16);
+    if (c < 2) cp_async16(smem_u32(&sm.sel_slot[sl].scales[r][16 * c]), p.scales + row * CSA2_SCALE_BYTES + 16 * c, 16);
+    cp_async_arrive(smem_u32(&sm.sel_full[sl]));
+  };
+  for (int j = 0; j < kWinSlots; ++j) fill_win(w0 + j);
+  for (int j = 0; j < kSelSlots; ++j) fill_sel(s0 + j);
+  bool late = false;  // copies did not land within a second: flagged, and no more waiting
+  auto wait_full = [&](uint64_t* bar, int use) {
+    if (!late && !bar_wait(smem_u32(bar), uint32_t(use) & 1u)) {
+      late = true;
+      atomicOr(p.flags, CSA2_FLAG_TIMEOUT);
     }
-  }
-  const int nwin = (nw + kTile - 1) / kTile;
-  const int steps = nsel + nwin;
-  const int i0 = kMerge ? steps * rank / C : 0, i1 = kMerge ? steps * (rank + 1) / C : steps;
-  const int s0 = i0, s1 = min(i1, nsel);                      // selected steps of this CTA
-  const int w0 = max(i0 - nsel, 0), w1 = max(i1 - nsel, 0);   // window steps
+  };
 
   State st;
-  st.m0 = st.m1 = kNegInf;
-  st.l0 = st.l1 = 0.f;
+  st.m0 = st.m1 = kFloor;
+  st.l = 0.f;
 #pragma unroll
   for (int i = 0; i < 16; ++i) st.o[i][0] = st.o[i][1] = st.o[i][2] = st.o[i][3] = 0.f;
-  int buf = 0;
 
+  for (int i = w0; i < w1; ++i) {
+    wait_full(&sm.win_full[(i - w0) % kWinSlots], (i - w0) / kWinSlots);
+    const unsigned char* src = &sm.win_slot[(i - w0) % kWinSlots].rows[g][0];
+    uint32_t kf[2][16];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        // lanes t >= 2 take their pieces in the order 1, 0, 3, 2 (as qf then holds Q's)
+        const int piece = (warp * 16 + t * 4 + (j ^ (t >> 1))) ^ win_swz(g);
+        const uint4 v = *reinterpret_cast<const uint4*>(src + 8 * h * CSA2_D * 2 + piece * 16);
+        kf[h][4 * j] = v.x, kf[h][4 * j + 1] = v.y, kf[h][4 * j + 2] = v.z, kf[h][4 * j + 3] = v.w;
+      }
+    step<false>(st, qf, kf, n_win - i * kStep, p.scale_log2, sm, warp, lane, [&]() { fill_win(i + kWinSlots); });
+  }
+  if (w0 < w1) {  // O in the order of the channels
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (!(i & 4)) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float a = st.o[i][e], c = st.o[i + 4][e];
+          st.o[i][e] = t < 2 ? a : c, st.o[i + 4][e] = t < 2 ? c : a;
+        }
+      }
+  }
   if (s0 < s1) {
-    const int64_t seq = int64_t(b) * p.seq_rows;
-    const int part = warp * 4 + t;
-    Raw ra, rb;
-    load_raw(ra, p, sm.sel, seq, s0, g, part);
-    if (s0 + 1 < s1) load_raw(rb, p, sm.sel, seq, s0 + 1, g, part);
     float sc[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -352,91 +443,89 @@ __global__ void __launch_bounds__(kThreads, 3) tree_attn_kernel(const Params p, 
       const float f = __uint_as_float(uint32_t(127 + up) << 23);
 #pragma unroll
       for (int i = 0; i < 16; ++i) qf[h][i] = pack_f16(bf16lo(qf[h][i]) * f, bf16hi(qf[h][i]) * f);
+#pragma unroll
+      for (int i = 0; i < 16; ++i)  // back to the order of the channels
+        if (!(i & 4)) {
+          const uint32_t a = qf[h][i], c = qf[h][i + 4];
+          qf[h][i] = t < 2 ? a : c, qf[h][i + 4] = t < 2 ? c : a;
+        }
       sc[h] = p.scale_log2 * __uint_as_float(uint32_t(127 - up) << 23);
     }
+    const float scale = (warp & 1) ? sc[1] : sc[0];
+    const int code_off = g * CSA2_CODE_BYTES + ((warp * 4 + t) ^ sel_swz(g)) * 16;
+    const int scale_off = g * CSA2_SCALE_BYTES + warp * 8 + t * 2;
     for (int i = s0; i < s1; ++i) {
-      uint32_t kf[2][16];
-      dequant(ra, kf);
-      ra = rb;
-      if (i + 2 < s1) load_raw(rb, p, sm.sel, seq, i + 2, g, part);
-      step<true>(st, qf, kf, sm.sel_mask[i], sc[0], sc[1], sm.part[buf], warp, lane);
-      buf ^= 1;
-    }
-  }
-  if (w0 < w1) {
-    if (s0 < s1) load_q();
-    else __syncthreads();  // the window list
-    const uint16_t* wrow = p.swa + int64_t(b) * (p.W - 1 + p.N) * CSA2_D + chan;
-    for (int i = w0; i < w1; ++i) {
-      uint32_t kf[2][16];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int32_t r = sm.win[i * kTile + 8 * h + g];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (r >= 0) v = __ldg(reinterpret_cast<const uint4*>(wrow + int64_t(r) * CSA2_D) + j);
-          kf[h][4 * j] = v.x, kf[h][4 * j + 1] = v.y, kf[h][4 * j + 2] = v.z, kf[h][4 * j + 3] = v.w;
-        }
+      const int k = i - s0;
+      wait_full(&sm.sel_full[k % kSelSlots], k / kSelSlots);
+      const unsigned char* codes = &sm.sel_slot[k % kSelSlots].codes[0][0] + code_off;
+      const unsigned char* scales = &sm.sel_slot[k % kSelSlots].scales[0][0] + scale_off;
+      int left = n_sel - i * kSelRows;
+      if (left > kStep) {
+        uint32_t kf[2][16];
+        dequant(codes, scales, kf);
+        step<true>(st, qf, kf, left, scale, sm, warp, lane, []() {});
+        codes += kStep * CSA2_CODE_BYTES, scales += kStep * CSA2_SCALE_BYTES, left -= kStep;
       }
-      const int left = nw - i * kTile;
-      step<false>(st, qf, kf, left >= kTile ? 0xFFFFu : (1u << left) - 1u, p.scale_log2, p.scale_log2, sm.part[buf], warp,
-                  lane);
-      buf ^= 1;
+      uint32_t kf[2][16];
+      dequant(codes, scales, kf);
+      step<true>(st, qf, kf, left, scale, sm, warp, lane, [&]() { fill_sel(i + kSelSlots); });
     }
   }
 
-  float l[2] = {quad_sum(st.l0), quad_sum(st.l1)};
-  float m[2] = {st.m0, st.m1};
+  {
+    const float l = quad_sum(st.l);
+    if (t == 0) sm.sums[warp][g] = l;
+  }
+  __syncthreads();
+  const float l[2] = {sm.sums[0][g] + sm.sums[2][g], sm.sums[1][g] + sm.sums[3][g]};
+  const float m[2] = {st.m0, st.m1};
   uint16_t* orow = p.out + row * (CSA2_H * CSA2_D);
   if (!kMerge) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const float inv = l[h] > 0.f ? __fdividef(1.0f, l[h]) : 0.f;
-      const float keep = inv;
+      const float inv = any ? __fdividef(1.0f, l[h]) : 0.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         uint32_t v[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          v[j] = pack_bf16(st.o[4 * i + j][2 * h] * keep, st.o[4 * i + j][2 * h + 1] * keep);
+        for (int j = 0; j < 4; ++j) v[j] = pack_bf16(st.o[4 * i + j][2 * h] * inv, st.o[4 * i + j][2 * h + 1] * inv);
         *(reinterpret_cast<uint4*>(orow + (g + 8 * h) * CSA2_D + chan) + i) = make_uint4(v[0], v[1], v[2], v[3]);
       }
       if (p.lse && warp == 0 && t == 0)
-        p.lse[row * CSA2_H + g + 8 * h] = l[h] > 0.f ? (m[h] + log2f(l[h])) * attn::kLn2 : kNegInf;
+        p.lse[row * CSA2_H + g + 8 * h] = any ? (m[h] + log2f(l[h])) * attn::kLn2 : kNegInf;
     }
     return;
   }
-  SharedMerge& mg = *reinterpret_cast<SharedMerge*>(smem_raw);
+  float(*mo)[CSA2_D] = reinterpret_cast<float(*)[CSA2_D]>(sm.win_slot);  // every copy into the slots has landed
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    if (warp == 0 && t == 0) mg.ml[g + 8 * h] = make_float2(m[h], l[h]);
+    if (warp == 0 && t == 0) sm.ml[g + 8 * h] = make_float2(m[h], l[h]);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      *reinterpret_cast<float4*>(&mg.o[g + 8 * h][chan + 4 * i]) =
+      *reinterpret_cast<float4*>(&mo[g + 8 * h][chan + 4 * i]) =
           make_float4(st.o[2 * i][2 * h], st.o[2 * i][2 * h + 1], st.o[2 * i + 1][2 * h], st.o[2 * i + 1][2 * h + 1]);
   }
   cluster_arrive_wait();
   // rank r finishes heads r * 16 / C ..
   const int heads = 16 / C;
-  const uint32_t ml_a = smem_u32(mg.ml), o_a = smem_u32(mg.o);
+  const uint32_t ml_a = smem_u32(sm.ml), o_a = smem_u32(mo);
   for (int e = tid; e < heads * (CSA2_D / 4); e += kThreads) {
     const int hd = rank * heads + e / (CSA2_D / 4), c4 = e % (CSA2_D / 4);
-    float mm = kNegInf;
+    float mm = kFloor;
     for (int r = 0; r < C; ++r) mm = fmaxf(mm, ld_cluster(cluster_addr(ml_a + uint32_t(hd) * 8u, r)));
     float sum = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int r = 0; r < C; ++r) {
       const float mr = ld_cluster(cluster_addr(ml_a + uint32_t(hd) * 8u, r));
-      const float w = mr == kNegInf ? 0.f : attn::ex2(mr - mm);
+      const float w = mr == mm ? 1.f : attn::ex2(mr - mm);
       sum += w * ld_cluster(cluster_addr(ml_a + uint32_t(hd) * 8u + 4u, r));
       const float4 v = ld_cluster4(cluster_addr(o_a + uint32_t(hd) * (CSA2_D * 4u) + uint32_t(c4) * 16u, r));
       acc.x += w * v.x, acc.y += w * v.y, acc.z += w * v.z, acc.w += w * v.w;
     }
-    const float inv = sum > 0.f ? __fdividef(1.0f, sum) : 0.f;
+    const float inv = any ? __fdividef(1.0f, sum) : 0.f;
     *reinterpret_cast<uint2*>(orow + hd * CSA2_D + 4 * c4) =
         make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-    if (p.lse && c4 == 0) p.lse[row * CSA2_H + hd] = sum > 0.f ? (mm + log2f(sum)) * attn::kLn2 : kNegInf;
+    if (p.lse && c4 == 0) p.lse[row * CSA2_H + hd] = any ? (mm + log2f(sum)) * attn::kLn2 : kNegInf;
   }
   cluster_arrive_wait();  // no CTA leaves while its part is being read
 }
@@ -454,15 +543,12 @@ cudaError_t launch(const Params& p, int64_t rows, int C, cudaStream_t st) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = C > 1 ? 2 : 1;
-  if (C == 1) {
-    cfg.dynamicSmemBytes = sizeof(Shared);
-    return cudaLaunchKernelEx(&cfg, tree_attn_kernel<false>, p, C);
-  }
-  cfg.dynamicSmemBytes = sizeof(SharedMerge);
-  const cudaError_t e = cudaFuncSetAttribute(tree_attn_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             int(sizeof(SharedMerge)));
+  auto kern = C == 1 ? tree_attn_kernel<false> : tree_attn_kernel<true>;
+  cfg.dynamicSmemBytes = sizeof(Shared);
+  static std::atomic<uint64_t> done[2];
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), sizeof(Shared), done[C > 1]);
   if (e != cudaSuccess) return e;
-  return cudaLaunchKernelEx(&cfg, tree_attn_kernel<true>, p, C);
+  return cudaLaunchKernelEx(&cfg, kern, p, C);
 }
 
 }  // namespace tree

@@ -42,6 +42,10 @@ def _check(y, x, w, rs, what=""):
     (1, 1, 16), (1, 4, 128), (2, 16, 128), (3, 17, 144), (8, 33, 112), (9, 100, 1040), (16, 64, 2048), (17, 40, 400),
     (24, 31, 272), (25, 512, 512), (32, 300, 640), (32, 5, 48), (1, 512, 4096), (5, 1000, 1056), (7, 5000, 256),
     (32, 5120, 384), (12, 20000, 48), (4, 16, 33008), (32, 16, 20000), (1, 40000, 32), (20, 9000, 160),
+    # the tensor-memory form: odd rows and channels, one and two channel blocks per CTA, shares of more than 2048
+    # channels, ten token rows; and an x that no cluster holds
+    (17, 2080, 4112), (24, 16500, 512), (20, 9001, 1024), (32, 1030, 8176), (18, 4100, 2320), (12, 8200, 8208),
+    (32, 1000, 33008),
 ])
 @pytest.mark.parametrize("fp32", [False, True])
 def test_matvec(M, N, K, fp32):

@@ -74,7 +74,7 @@ def test_tree_attn(L):
 
 
 def test_fp4_weight(L):
-    assert L.csa2_fp4_packed_bytes(16, 128) == 1152 and L.csa2_fp4_packed_bytes(17, 144) == 4 * 1152
+    assert L.csa2_fp4_packed_bytes(16, 128) == 2304 and L.csa2_fp4_packed_bytes(33, 144) == 4 * 2304
     assert L.csa2_fp4_packed_bytes(16, 100) == 0 and L.csa2_fp4_packed_bytes(-1, 128) == 0
     assert L.csa2_fp4_pack_weight(_p(0), _p(1), 4, 24, _p(2), None) == 1
     assert L.csa2_fp4_pack_weight(None, _p(1), 4, 32, _p(2), None) == 1
@@ -102,11 +102,11 @@ def test_binding_checks_shapes_and_types():
     with pytest.raises(ValueError):
         csa2.fp4_weight_alloc(16, 24, device="cpu")
     with pytest.raises(ValueError):   # channels not a multiple of 16
-        csa2.csa2_fp4_matvec(torch.zeros((1, 24), dtype=torch.bfloat16), torch.zeros(1152, dtype=torch.uint8),
+        csa2.csa2_fp4_matvec(torch.zeros((1, 24), dtype=torch.bfloat16), torch.zeros(2304, dtype=torch.uint8),
                              torch.zeros((1, 16), dtype=torch.bfloat16))
     with pytest.raises(ValueError):   # a weight of another size
-        csa2.csa2_fp4_matvec(torch.zeros((1, 32), dtype=torch.bfloat16), torch.zeros(1152, dtype=torch.uint8),
-                             torch.zeros((1, 17), dtype=torch.bfloat16))
+        csa2.csa2_fp4_matvec(torch.zeros((1, 32), dtype=torch.bfloat16), torch.zeros(2304, dtype=torch.uint8),
+                             torch.zeros((1, 33), dtype=torch.bfloat16))
     with pytest.raises(ValueError):   # scales of another width
         csa2.csa2_tree_attn(torch.zeros((1, 2, 16, 512), dtype=torch.bfloat16), torch.zeros((1, 2), dtype=i32),
                             torch.zeros((8, 256), dtype=torch.uint8), torch.zeros((8, 16), dtype=torch.uint8),
