@@ -150,16 +150,22 @@ __device__ __forceinline__ void step(State& s, const uint32_t (&qf)[2][16], uint
                                      Shared& sm, int warp, int lane, F loaded) {
   const int t = lane & 3, g = lane >> 2;
   {
-    float S0[4] = {0.f, 0.f, 0.f, 0.f}, S1[4] = {0.f, 0.f, 0.f, 0.f};
+    // two chains per accumulator: a dependent MMA waits 20 cycles
+    float S0[4] = {0.f, 0.f, 0.f, 0.f}, S1[4] = {0.f, 0.f, 0.f, 0.f}, T0[4] = {0.f, 0.f, 0.f, 0.f},
+          T1[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 8; i += 2) {
       mma<kF16>(S0, qf[0][2 * i], qf[1][2 * i], qf[0][2 * i + 1], qf[1][2 * i + 1], kf[0][2 * i], kf[0][2 * i + 1]);
       mma<kF16>(S1, qf[0][2 * i], qf[1][2 * i], qf[0][2 * i + 1], qf[1][2 * i + 1], kf[1][2 * i], kf[1][2 * i + 1]);
+      mma<kF16>(T0, qf[0][2 * i + 2], qf[1][2 * i + 2], qf[0][2 * i + 3], qf[1][2 * i + 3], kf[0][2 * i + 2],
+                kf[0][2 * i + 3]);
+      mma<kF16>(T1, qf[0][2 * i + 2], qf[1][2 * i + 2], qf[0][2 * i + 3], qf[1][2 * i + 3], kf[1][2 * i + 2],
+                kf[1][2 * i + 3]);
     }
-    sm.part[0][warp][lane] = make_float2(S0[0], S0[1]);  // head g, rows 2t, 2t + 1
-    sm.part[1][warp][lane] = make_float2(S0[2], S0[3]);  // head g + 8
-    sm.part[2][warp][lane] = make_float2(S1[0], S1[1]);  // rows 8 + 2t, 9 + 2t
-    sm.part[3][warp][lane] = make_float2(S1[2], S1[3]);
+    sm.part[0][warp][lane] = make_float2(S0[0] + T0[0], S0[1] + T0[1]);  // head g, rows 2t, 2t + 1
+    sm.part[1][warp][lane] = make_float2(S0[2] + T0[2], S0[3] + T0[3]);  // head g + 8
+    sm.part[2][warp][lane] = make_float2(S1[0] + T1[0], S1[1] + T1[1]);  // rows 8 + 2t, 9 + 2t
+    sm.part[3][warp][lane] = make_float2(S1[2] + T1[2], S1[3] + T1[3]);
   }
 #pragma unroll
   for (int i = 0; i < 16; ++i) kf[0][i] = transpose8(kf[0][i]), kf[1][i] = transpose8(kf[1][i]);
@@ -257,8 +263,17 @@ __global__ void __launch_bounds__(kThreads, 3) tree_attn_kernel(const Params p, 
   const int rank = kMerge ? int(blockIdx.x % unsigned(C)) : 0;
   const int64_t row = kMerge ? int64_t(blockIdx.x / unsigned(C)) : int64_t(blockIdx.x);
   const int b = int(row / p.N), node = int(row - int64_t(b) * p.N);
-  if (p.n_nodes && node >= p.n_nodes[b]) return;  // the whole cluster: its outputs stay as they were
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  // everything that the row lists need is asked for at once
+  const int nodes = p.n_nodes ? __ldg(p.n_nodes + b) : p.N;
+  int nv = p.k;
+  int32_t ids[kMaxSel / 32];
+  if (warp == 0) {
+    if (p.n_valid) nv = min(max(__ldg(p.n_valid + row), 0), p.k);
+#pragma unroll
+    for (int j = 0; j < kMaxSel / 32; ++j) ids[j] = 32 * j + lane < p.k ? __ldg(p.idx + row * p.k + 32 * j + lane) : -1;
+  }
+  if (node >= nodes) return;  // the whole cluster: its outputs stay as they were
   const int chan = warp * 128 + t * 32;  // this lane's 32 channels
 
   // Q of heads g and g + 8, as bf16 pairs
@@ -283,23 +298,14 @@ __global__ void __launch_bounds__(kThreads, 3) tree_attn_kernel(const Params p, 
   // The row lists, without gaps: warp 0 the selected rows, warp 1 the window rows.  The entries that fill a
   // list's last step repeat a row of the node's own; their P is zero.
   if (warp == 0) {
-    const int nv = p.n_valid ? min(max(p.n_valid[row], 0), p.k) : p.k;
     int n = 0;
-    for (int i0 = 0; i0 < nv; i0 += 128) {
-      int32_t r[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int i = i0 + 32 * j + lane;
-        r[j] = i < nv ? __ldg(p.idx + row * p.k + i) : -1;
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const bool ok = r[j] >= 0 && int64_t(r[j]) < p.cap;
-        if (r[j] >= 0 && !ok) atomicOr(p.flags, CSA2_FLAG_INDEX_OOB);
-        const uint32_t bal = __ballot_sync(0xffffffffu, ok);
-        if (ok) sm.sel[n + __popc(bal & ((1u << lane) - 1u))] = r[j];
-        n += __popc(bal);
-      }
+    for (int j = 0; j < kMaxSel / 32; ++j) {
+      const bool ok = 32 * j + lane < nv && ids[j] >= 0 && int64_t(ids[j]) < p.cap;
+      if (32 * j + lane < nv && int64_t(ids[j]) >= p.cap) atomicOr(p.flags, CSA2_FLAG_INDEX_OOB);
+      const uint32_t bal = __ballot_sync(0xffffffffu, ok);
+      if (ok) sm.sel[n + __popc(bal & ((1u << lane) - 1u))] = ids[j];
+      n += __popc(bal);
     }
     __syncwarp();
     if (n & (kSelRows - 1)) {
