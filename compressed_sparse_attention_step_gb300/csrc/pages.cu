@@ -37,9 +37,9 @@ __device__ __forceinline__ int slot_of(int page, int off, int shift) {  // -1: n
 __global__ void __launch_bounds__(kThreads) block_tables_kernel(
     const int32_t* __restrict__ old_lens, const int32_t* __restrict__ new_lens, int B, int shift,
     int32_t* block_table, int max_pages, int32_t* free_pages, int free_cap, int32_t* pool_state, int32_t* granted,
-    int32_t* __restrict__ slots, int n_new, unsigned int* flags) {
+    int32_t* __restrict__ slots, int n_new, bool vec, unsigned int* flags) {
   extern __shared__ int sums[];  // inclusive sums of the pages asked for, then of those given back
-  __shared__ uint32_t scan_tmp[32];
+  __shared__ unsigned long long warp_sum[2][kThreads / 32];
   int* ask = sums;
   int* back = sums + B;
   pdl_wait();
@@ -51,20 +51,37 @@ __global__ void __launch_bounds__(kThreads) block_tables_kernel(
   auto old_of = [&](int b) { return int(min(int64_t(max(old_lens[b], 0)), room)); };
   auto new_of = [&](int b) { return max(new_lens[b], 0); };
 
-  uint32_t ask0 = 0, back0 = 0;
-  for (int c = 0; c < B; c += kThreads) {
+  // both sums at once, in the halves of 64 bits (each stays below 2^31: B * max_pages does)
+  const int lane = tid & 31, warp = tid >> 5;
+  unsigned long long base = 0;
+  for (int c = 0, round = 0; c < B; c += kThreads, round ^= 1) {
     const int b = c + tid;
-    uint32_t a = 0, r = 0;
+    unsigned long long v = 0;
     if (b < B) {
       const int held = pages_of(old_of(b), shift), want = pages_of(new_of(b), shift);
-      if (want > held && want <= max_pages) a = uint32_t(want - held);
-      if (want < held) r = uint32_t(held - want);
+      if (want > held && want <= max_pages) v = uint32_t(want - held);
+      if (want < held) v = static_cast<unsigned long long>(held - want) << 32;
     }
-    uint32_t ta, tr;
-    const uint32_t ea = block_exclusive_scan(a, scan_tmp, &ta), er = block_exclusive_scan(r, scan_tmp, &tr);
-    if (b < B) ask[b] = int(ask0 + ea + a), back[b] = int(back0 + er + r);
-    ask0 += ta, back0 += tr;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += u;
+    }
+    if (lane == 31) warp_sum[round][warp] = v;
+    __syncthreads();
+    // every warp adds up the warps' sums for itself
+    unsigned long long w = warp_sum[round][lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long u = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) w += u;
+    }
+    const unsigned long long before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
+    v += base + (warp > 0 ? before : 0);
+    if (b < B) ask[b] = int(uint32_t(v)), back[b] = int(uint32_t(v >> 32));
+    base += __shfl_sync(0xffffffffu, w, 31);
   }
+  const uint32_t ask0 = uint32_t(base), back0 = uint32_t(base >> 32);
   __syncthreads();
   const int F = int(back0);
   const int64_t budget = int64_t(n_free) + F;
@@ -95,33 +112,68 @@ __global__ void __launch_bounds__(kThreads) block_tables_kernel(
     granted[b] = ok ? new_of(int(b)) : old_of(int(b));
     if (!ok) atomicOr(flags, CSA2_FLAG_PAGES_OUT);
   }
-  for (int64_t j = gtid; j < A; j += gthreads) {
-    const int b = owner(ask, B, int(j)), first = b > 0 ? ask[b - 1] : 0;
-    block_table[int64_t(b) * max_pages + pages_of(old_of(b), shift) + (j - first)] = handed_out(int(j));
-  }
-  for (int64_t f = A + gtid; f < F; f += gthreads) {
-    const int64_t at = int64_t(n_free) + F - 1 - f;
-    if (at < free_cap) free_pages[at] = given_back(int(f));
-  }
-  const int64_t n_slots = int64_t(B) * n_new;
-  for (int64_t i = gtid; i < n_slots; i += gthreads) {
-    const int b = int(uint32_t(i) / uint32_t(n_new)), c = int(i) - b * n_new;
-    const int o = old_of(b);
-    int s = -1;
-    if (c < new_of(b) - o && is_granted(b)) {
-      const int pos = o + c, pg = pos >> shift, held = pages_of(o, shift);
-      const int page = pg < held ? block_table[int64_t(b) * max_pages + pg]
-                                 : handed_out((b > 0 ? ask[b - 1] : 0) + pg - held);
-      s = slot_of(page, pos & ((1 << shift) - 1), shift);
-      if (s < 0) atomicOr(flags, CSA2_FLAG_INDEX_OOB);
+  // pages handed out, and pages put back: four at a time, so that their loads overlap
+  for (int64_t j0 = gtid; j0 < A; j0 += 4 * gthreads) {
+    int64_t to[4];
+    int32_t page[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t j = j0 + i * gthreads;
+      to[i] = -1;
+      if (j >= A) continue;
+      const int b = owner(ask, B, int(j)), first = b > 0 ? ask[b - 1] : 0;
+      to[i] = int64_t(b) * max_pages + pages_of(old_of(b), shift) + (j - first);
+      page[i] = handed_out(int(j));
     }
-    slots[i] = s;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (to[i] >= 0) block_table[to[i]] = page[i];
+  }
+  for (int64_t f0 = A + gtid; f0 < F; f0 += 4 * gthreads) {
+    int32_t page[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) page[i] = f0 + i * gthreads < F ? given_back(int(f0 + i * gthreads)) : 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t f = f0 + i * gthreads, at = int64_t(n_free) + F - 1 - f;
+      if (f >= F) continue;
+      if (at < free_cap) free_pages[at] = page[i];
+      else atomicOr(flags, CSA2_FLAG_INDEX_OOB);  // no room in the list: the page is lost
+    }
+  }
+  // four columns a thread: most of them lie in one page, whose number is looked up once
+  const int quads = (n_new + 3) / 4;
+  for (int64_t i = gtid; i < int64_t(B) * quads; i += gthreads) {
+    const int b = int(uint32_t(i) / uint32_t(quads)), c = (int(i) - b * quads) * 4;
+    const int o = old_of(b), end = is_granted(b) ? new_of(b) : o, held = pages_of(o, shift);
+    const int first = b > 0 ? ask[b - 1] : 0;
+    int s[4], pg = -1, page = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      s[j] = -1;
+      if (c + j >= end - o) continue;
+      const int pos = o + c + j;
+      if ((pos >> shift) != pg) {
+        pg = pos >> shift;
+        page = pg < held ? block_table[int64_t(b) * max_pages + pg] : handed_out(first + pg - held);
+      }
+      s[j] = slot_of(page, pos & ((1 << shift) - 1), shift);
+      if (s[j] < 0) atomicOr(flags, CSA2_FLAG_INDEX_OOB);
+    }
+    int32_t* dst = slots + int64_t(b) * n_new + c;
+    if (vec) {
+      *reinterpret_cast<int4*>(dst) = make_int4(s[0], s[1], s[2], s[3]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (c + j < n_new) dst[j] = s[j];
+    }
   }
 
   // the last CTA to get here has seen every other read the old count
   __syncthreads();
   if (tid == 0) {
-    const unsigned int done = atomicAdd(reinterpret_cast<unsigned int*>(pool_state + 1), 1u);
+    const unsigned int done = gridDim.x > 1 ? atomicAdd(reinterpret_cast<unsigned int*>(pool_state + 1), 1u) : 0u;
     if (done == gridDim.x - 1) {
       pool_state[0] = int(min(budget - A, int64_t(free_cap)));
       pool_state[1] = 0;
@@ -144,32 +196,40 @@ __global__ void __launch_bounds__(kCtxThreads) context_slots_kernel(
   pdl_wait();
   pdl_trigger();
   const int b = blockIdx.y, tid = threadIdx.x;
-  const int len = max(lens[b], 0);
-  const int nn = n_nodes ? min(max(n_nodes[b], 0), N) : N;
-  if (parent && tid < N) par[tid] = parent[int64_t(b) * N + tid];
-  __syncthreads();
-  if (tid < N) {
-    unsigned long long m = 0;
-    bool bad = false;
-    if (parent && tid < nn)
-      for (int cur = tid; cur >= 0;) {
-        m |= 1ull << cur;
-        const int up = par[cur];
-        if (up < -1 || up >= cur) {
-          bad = true;
-          break;
-        }
-        cur = up;
-      }
-    anc[tid] = m;
-    if (blockIdx.x == 0) {
-      const int64_t n = tid < nn ? int64_t(len) + __popcll(m) : 0;
-      n_slots[int64_t(b) * N + tid] = int32_t(min(n, ld));
-      if (bad || n > ld) atomicOr(flags, CSA2_FLAG_INDEX_OOB);
-    }
-  }
-  __syncthreads();
+  const int64_t c0 = (int64_t(blockIdx.x) * kCtxThreads + tid) * 4;
+  // everything that depends on the place alone is asked for at once
   const int32_t* table = block_table ? block_table + int64_t(b) * max_pages : nullptr;
+  const int page0 = table && (c0 >> shift) < max_pages ? table[c0 >> shift] : -1;
+  const int up0 = parent && tid < N ? parent[int64_t(b) * N + tid] : -1;
+  const int nn = n_nodes ? min(max(n_nodes[b], 0), N) : N;
+  const int len = max(lens[b], 0);
+  const int64_t cta0 = int64_t(blockIdx.x) * kCtxThreads * 4;
+  // the CTAs that hold drafted rows (and the first, which counts them) walk the tree
+  if (blockIdx.x == 0 || (cta0 + kCtxThreads * 4 > len && cta0 < int64_t(len) + CSA2_MAX_TREE)) {
+    if (tid < N) par[tid] = up0;
+    __syncthreads();
+    if (tid < N) {
+      unsigned long long m = 0;
+      bool bad = false;
+      if (parent && tid < nn)
+        for (int cur = tid; cur >= 0;) {
+          m |= 1ull << cur;
+          const int up = par[cur];
+          if (up < -1 || up >= cur) {
+            bad = true;
+            break;
+          }
+          cur = up;
+        }
+      anc[tid] = m;
+      if (blockIdx.x == 0) {
+        const int64_t n = tid < nn ? int64_t(len) + __popcll(m) : 0;
+        n_slots[int64_t(b) * N + tid] = int32_t(min(n, ld));
+        if (bad || n > ld) atomicOr(flags, CSA2_FLAG_INDEX_OOB);
+      }
+    }
+    __syncthreads();
+  }
   auto slot = [&](int64_t pos) -> int {
     if (!table) return pos <= 0x7FFFFFFF ? int(pos) : -1;
     const int64_t pg = pos >> shift;
@@ -177,25 +237,21 @@ __global__ void __launch_bounds__(kCtxThreads) context_slots_kernel(
     if (s < 0) atomicOr(flags, CSA2_FLAG_INDEX_OOB);
     return s;
   };
-  const int64_t c0 = (int64_t(blockIdx.x) * kCtxThreads + tid) * 4;
   if (c0 >= ld) return;
-  int common[4];
-  if (c0 + 3 < len && table) {  // four columns of one page
-    const int64_t pg = c0 >> shift;
-    const int s = pg < max_pages ? slot_of(table[pg], int(c0 & ((1 << shift) - 1)), shift) : -1;
-    if (s < 0 && nn > 0) atomicOr(flags, CSA2_FLAG_INDEX_OOB);
+  const bool tail = c0 + 3 >= len && c0 < int64_t(len) + CSA2_MAX_TREE;  // may hold drafted rows
+  int common[4];  // pages are multiples of four rows: the four columns lie in one
+  {
+    const int s = table ? slot_of(page0, int(c0 & ((1 << shift) - 1)), shift) : (c0 <= 0x7FFFFFFC ? int(c0) : -1);
+    if (s < 0 && c0 < len && nn > 0) atomicOr(flags, CSA2_FLAG_INDEX_OOB);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) common[i] = s < 0 ? -1 : s + i;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) common[i] = c0 + i < len && nn > 0 ? slot(c0 + i) : -1;
+    for (int i = 0; i < 4; ++i) common[i] = s >= 0 && c0 + i < len ? s + i : -1;
   }
   int32_t* dst = slots + int64_t(b) * N * ld + c0;
   for (int r = 0; r < N; ++r, dst += ld) {
     int v[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = r < nn ? common[i] : -1;
-    if (c0 + 3 >= len && r < nn) {
+    if (tail && r < nn) {
       unsigned long long m = anc[r];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -256,16 +312,17 @@ extern "C" csa2_status csa2_block_tables(const int32_t* old_lens, const int32_t*
   unsigned int* flags = device_flags_ptr();
   const int sms = sm_count();
   if (!flags || sms <= 0) return CSA2_ERR_CUDA;
-  // four items a thread; how many pages change hands is known on the device alone
-  const int64_t items = std::max(int64_t(B) * n_new, int64_t(B) * max_pages / 16);
-  const int grid = int(std::min<int64_t>(std::max<int64_t>(items / (4 * kThreads), 1), sms));
+  // a quad of slots or four pages a thread; how many pages change hands is known on the device alone (half of the
+  // table is taken for it)
+  const int64_t items = std::max(int64_t(B) * ((n_new + 3) / 4), int64_t(B) * max_pages / 8);
+  const int grid = int(std::min<int64_t>(std::max<int64_t>(items / kThreads, 1), sms));
   const size_t smem = size_t(B) * 8;
   static std::atomic<uint64_t> done{0};
   if (allow_smem(reinterpret_cast<const void*>(block_tables_kernel), size_t(CSA2_MAX_SEQS) * 8, done) != cudaSuccess)
     return CSA2_ERR_CUDA;
   return launch_pdl(block_tables_kernel, dim3(grid), dim3(kThreads), smem, reinterpret_cast<cudaStream_t>(stream),
                     old_lens, new_lens, B, shift, block_table, max_pages, free_pages, free_cap, pool_state, granted,
-                    slots, n_new, flags) == cudaSuccess
+                    slots, n_new, n_new % 4 == 0 && al(slots, 16), flags) == cudaSuccess
              ? CSA2_OK
              : CSA2_ERR_CUDA;
 }
