@@ -238,30 +238,29 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
-__device__ __forceinline__ float ld_cluster(uint32_t a) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];\n" : "=f"(v) : "r"(a) : "memory");
+// (not volatile: several may be under way; the cluster barriers around them order them)
+__device__ __forceinline__ float2 ld_cluster2(uint32_t a) {
+  float2 v;
+  asm("ld.shared::cluster.v2.f32 {%0,%1}, [%2];\n" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
   return v;
 }
 __device__ __forceinline__ float4 ld_cluster4(uint32_t a) {
   float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];\n"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(a)
-               : "memory");
+  asm("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];\n" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
   return v;
 }
 
 // One node per cluster of C CTAs (C = 1: per CTA), which share its steps of 16 rows and merge their
 // parts through distributed shared memory, in rank order.
-template <bool kMerge>
-__global__ void __launch_bounds__(kThreads, 3) tree_attn_kernel(const Params p, int C) {
+template <int C>
+__global__ void __launch_bounds__(kThreads, 3) tree_attn_kernel(const Params p) {
+  constexpr bool kMerge = C > 1;
   extern __shared__ __align__(128) unsigned char smem_raw[];
   Shared& sm = *reinterpret_cast<Shared*>(smem_raw);
   pdl_wait();
   pdl_trigger();
-  const int rank = kMerge ? int(blockIdx.x % unsigned(C)) : 0;
-  const int64_t row = kMerge ? int64_t(blockIdx.x / unsigned(C)) : int64_t(blockIdx.x);
+  const int rank = kMerge ? int(blockIdx.x % C) : 0;
+  const int64_t row = kMerge ? int64_t(blockIdx.x / C) : int64_t(blockIdx.x);
   const int b = int(row / p.N), node = int(row - int64_t(b) * p.N);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   // everything that the row lists need is asked for at once
@@ -502,59 +501,78 @@ __global__ void __launch_bounds__(kThreads, 3) tree_attn_kernel(const Params p, 
     }
     return;
   }
-  float(*mo)[CSA2_D] = reinterpret_cast<float(*)[CSA2_D]>(sm.win_slot);  // every copy into the slots has landed
+  if constexpr (kMerge) {
+    // O of this CTA's part into the window slots (every copy into them has landed), as 16-byte pieces placed at
+    // their index XOR a function of head and lane, so that eight lanes fall into different banks
+    float4(*mo)[CSA2_D / 4] = reinterpret_cast<float4(*)[CSA2_D / 4]>(sm.win_slot);
+    auto place = [](int head, int c4) { return c4 ^ (((c4 >> 3) & 3) | ((head & 1) << 2)); };
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    if (warp == 0 && t == 0) sm.ml[g + 8 * h] = make_float2(m[h], l[h]);
+    for (int h = 0; h < 2; ++h) {
+      if (warp == 0 && t == 0) sm.ml[g + 8 * h] = make_float2(m[h], l[h]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      *reinterpret_cast<float4*>(&mo[g + 8 * h][chan + 4 * i]) =
-          make_float4(st.o[2 * i][2 * h], st.o[2 * i][2 * h + 1], st.o[2 * i + 1][2 * h], st.o[2 * i + 1][2 * h + 1]);
-  }
-  cluster_arrive_wait();
-  // rank r finishes heads r * 16 / C ..
-  const int heads = 16 / C;
-  const uint32_t ml_a = smem_u32(sm.ml), o_a = smem_u32(mo);
-  for (int e = tid; e < heads * (CSA2_D / 4); e += kThreads) {
-    const int hd = rank * heads + e / (CSA2_D / 4), c4 = e % (CSA2_D / 4);
-    float mm = kFloor;
-    for (int r = 0; r < C; ++r) mm = fmaxf(mm, ld_cluster(cluster_addr(ml_a + uint32_t(hd) * 8u, r)));
-    float sum = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int r = 0; r < C; ++r) {
-      const float mr = ld_cluster(cluster_addr(ml_a + uint32_t(hd) * 8u, r));
-      const float w = mr == mm ? 1.f : attn::ex2(mr - mm);
-      sum += w * ld_cluster(cluster_addr(ml_a + uint32_t(hd) * 8u + 4u, r));
-      const float4 v = ld_cluster4(cluster_addr(o_a + uint32_t(hd) * (CSA2_D * 4u) + uint32_t(c4) * 16u, r));
-      acc.x += w * v.x, acc.y += w * v.y, acc.z += w * v.z, acc.w += w * v.w;
+      for (int i = 0; i < 8; ++i)
+        mo[g + 8 * h][place(g + 8 * h, chan / 4 + i)] = make_float4(st.o[2 * i][2 * h], st.o[2 * i][2 * h + 1],
+                                                                    st.o[2 * i + 1][2 * h], st.o[2 * i + 1][2 * h + 1]);
     }
-    const float inv = any ? __fdividef(1.0f, sum) : 0.f;
-    *reinterpret_cast<uint2*>(orow + hd * CSA2_D + 4 * c4) =
-        make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-    if (p.lse && c4 == 0) p.lse[row * CSA2_H + hd] = any ? (mm + log2f(sum)) * attn::kLn2 : kNegInf;
+    cluster_arrive_wait();
+    // rank r finishes heads r * 16 / C ..: the parts' weights first, then their sums, all loads of a thread at once
+    constexpr int kHeads = 16 / C;
+    float* weight = sm.qmax[0];  // [kHeads][C]
+    if (tid < kHeads) {
+      const int hd = rank * kHeads + tid;
+      float2 part[C];
+      float mm = kFloor, sum = 0.f;
+#pragma unroll
+      for (int r = 0; r < C; ++r) part[r] = ld_cluster2(cluster_addr(smem_u32(&sm.ml[hd]), r));
+#pragma unroll
+      for (int r = 0; r < C; ++r) mm = fmaxf(mm, part[r].x);
+#pragma unroll
+      for (int r = 0; r < C; ++r) {
+        part[r].x = part[r].x == mm ? 1.f : attn::ex2(part[r].x - mm);
+        sum += part[r].x * part[r].y;
+      }
+      const float inv = any ? __fdividef(1.0f, sum) : 0.f;
+#pragma unroll
+      for (int r = 0; r < C; ++r) weight[tid * C + r] = part[r].x * inv;
+      if (p.lse) p.lse[row * CSA2_H + hd] = any ? (mm + log2f(sum)) * attn::kLn2 : kNegInf;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i) {
+      const int hd = rank * kHeads + i;
+      const uint32_t at = smem_u32(&mo[hd][place(hd, tid)]);
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int r = 0; r < C; ++r) {
+        const float4 v = ld_cluster4(cluster_addr(at, r));
+        const float w = weight[i * C + r];
+        acc.x += w * v.x, acc.y += w * v.y, acc.z += w * v.z, acc.w += w * v.w;
+      }
+      *reinterpret_cast<uint2*>(orow + hd * CSA2_D + 4 * tid) = make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
+    }
+    cluster_arrive_wait();  // no CTA leaves while its part is being read
   }
-  cluster_arrive_wait();  // no CTA leaves while its part is being read
 }
 
-cudaError_t launch(const Params& p, int64_t rows, int C, cudaStream_t st) {
+template <int C>
+cudaError_t launch(const Params& p, int64_t rows, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(rows * C));
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = sizeof(Shared);
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = unsigned(C);
+  attr[1].val.clusterDim.x = C;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = C > 1 ? 2 : 1;
-  auto kern = C == 1 ? tree_attn_kernel<false> : tree_attn_kernel<true>;
-  cfg.dynamicSmemBytes = sizeof(Shared);
-  static std::atomic<uint64_t> done[2];
-  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), sizeof(Shared), done[C > 1]);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(tree_attn_kernel<C>), sizeof(Shared), done);
   if (e != cudaSuccess) return e;
-  return cudaLaunchKernelEx(&cfg, kern, p, C);
+  return cudaLaunchKernelEx(&cfg, tree_attn_kernel<C>, p);
 }
 
 }  // namespace tree
@@ -586,7 +604,17 @@ extern "C" csa2_status csa2_tree_attn(const uint16_t* q, int B, int N, const int
   p.idx = idx, p.n_valid = n_valid, p.swa = swa, p.win_len = win_len, p.out = out, p.lse = lse;
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
   p.N = N, p.k = k, p.W = W, p.flags = flags;
-  int C = 1;
-  while (C < tree::kMaxCluster && rows * C * 2 <= int64_t(sms) * 2) C *= 2;
-  return tree::launch(p, rows, C, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? CSA2_OK : CSA2_ERR_CUDA;
+  // Few nodes are shared by several CTAs each, which costs a merge.  Measured with 512 selected and 128 window
+  // rows, us for 1 / 2 / 4 / 8 CTAs a node: 5 nodes 24.2 / 17.9 / 11.8 / 9.7, 38 nodes 24.4 / 18.0 / 14.2 / 15.0,
+  // 91 nodes 24.6 / 21.8 / 18.1 / 28.4, 152 nodes 24.9 / 27.1 / 33.1 / 42.6; with 64 selected rows, 91 nodes
+  // 10.9 / 11.5 / 12.1 / 22.
+  const int C = rows * 8 <= sms ? 8 : rows * 4 <= sms || (rows * 8 <= 5 * int64_t(sms) && k >= 256) ? 4 : 1;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  switch (C) {
+    case 1: e = tree::launch<1>(p, rows, st); break;
+    case 4: e = tree::launch<4>(p, rows, st); break;
+    default: e = tree::launch<8>(p, rows, st); break;
+  }
+  return e == cudaSuccess ? CSA2_OK : CSA2_ERR_CUDA;
 }
