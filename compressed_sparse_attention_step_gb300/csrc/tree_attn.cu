@@ -3,21 +3,26 @@
 // included), o = sum_r softmax_r(q . row_r * scale) row_r with K = V = the (dequantised) row.
 //
 // A node has 16 heads and its own selected rows, so its two products are [16 x 512] x [512 x rows] and
-// [16 x rows] x [rows x 512]: the head count is exactly the M of mma.m16n8k16.  The tcgen05 forms feed
-// the gathered rows from shared memory as the M = 128 operand against N = 16 heads and are held to the
-// 1024 multiply-adds a cycle at which an SM reads that operand, after the dequantised rows have also been
-// written to shared memory once; m16n8k16 reaches the same 1024 (measured: 2.0 cycles an instruction
-// and SM) from registers, so here the rows never touch shared memory at all:
-//  - four warps split the 512 channels, lane (g, t) of a warp loads 16 bytes of codes of row g: 32
+// [16 x rows] x [rows x 512]: the head count is exactly the M of mma.m16n8k16, which multiplies from registers, so
+// that the dequantised rows never touch shared memory (the tcgen05 kernels of the chain's attention write them
+// there once and have them read twice; a chain of the same rows takes them 1.3 to 1.7 times as long):
+//  - four warps split the 512 channels, lane (g, t) of a warp reads 16 bytes of codes of row g: 32
 //    consecutive channels of its warp's 128.  Channels may be summed in any order, so the lane's j-th
 //    channel pair serves as the j-th pair of the B fragment of S = Q K^T as it is, with Q's fragment
 //    loaded in the same order;
 //  - the same registers, transposed 8 x 8 by movmatrix, are the B fragments of O = P V, and the
 //    accumulator of S has the layout of P's A fragment; a lane's 16 output pairs are again 32
 //    consecutive channels, stored as whole 16-byte pieces;
-//  - the only traffic through shared memory is the sum of the four warps' partial scores.
-// Bound: the tensor pipe (8192 cycles a node with 512 selected rows), then the transposes and the
-// conversions.
+//  - rows arrive by cp.async a few steps ahead; between the warps only partial scores and P pass.
+//
+// What bounds it.  A step of 16 rows needs 256 cycles of an SM's tensor pipe (2.0 an instruction), about 290 issue
+// slots of each scheduler and as many cycles of the shared-memory pipe (128 of them transposes), and takes a CTA
+// 1000 cycles from end to end alone.  Three CTAs an SM (their registers) give 560 cycles a step: no pipe is
+// full, the chain of a step is.  64 sequences x 32 nodes, 512 selected and 128 window rows: 166 us on the device,
+// 0.17 of the bf16 peak over the plain count of operations; 64 x 8 nodes 56 us.  Measured and not kept: rows
+// dequantised a second time for P V instead of transposed (181 us), Q in shared memory (205), steps of
+// 32 rows (179), a pipeline of three steps with two CTAs an SM (190), plain loads one step ahead (223), bulk
+// copies per row (307).
 //
 // FP4 rows are multiplied as f16: a code times a scale has at most 6 significant bits and lies between
 // 2^-10 and 2688, so the row is exact.  Q is scaled per head by a power of two that puts its largest
@@ -36,7 +41,7 @@ constexpr int kThreads = 128;
 constexpr int kWarps = 4;
 constexpr int kMaxSel = CSA2_MAX_ATTN_K;                  // selected rows per node
 constexpr int kMaxWin = CSA2_MAX_W - 1 + CSA2_MAX_TREE;   // window rows and ancestors
-constexpr int kStep = 16, kSelRows = 32;                 // rows per step, selected rows per slot
+constexpr int kStep = 16, kSelRows = 32;                  // rows per step, selected rows per slot
 constexpr int kWinList = (kMaxWin + kStep - 1) / kStep * kStep;
 constexpr int kMaxCluster = 8;
 constexpr float kNegInf = -INFINITY;
@@ -44,7 +49,7 @@ constexpr float kNegInf = -INFINITY;
 // score passes it by kHead + 8, so P lies below 2^15 and the largest is at least 2^kHead: in f16's range, whose
 // subnormal rounding (2^-25) is then 2^-32 of the largest P.
 constexpr float kHead = 7.0f;
-constexpr float kFloor = -1e30f;  // the reference before any score
+constexpr float kFloor = -3.402823466e38f;  // the reference before any score
 
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                               uint32_t b0, uint32_t b1) {
@@ -144,7 +149,8 @@ struct State {
 
 // One step of 16 rows held as fragments kf (rows g and g + 8; 16 channel pairs each), the first `left`
 // of them real.  Warp w sums the four warps' partial scores for register w of P's fragment, takes their
-// exponentials and hands the register to the others.  `loaded` runs when every warp holds its fragments.
+// exponentials and hands the register to the others.  `loaded` runs once every warp holds its fragments, behind
+// the second barrier, where its instructions pass beside the products (between the barriers they cost 2%).
 template <bool kF16, typename F>
 __device__ __forceinline__ void step(State& s, const uint32_t (&qf)[2][16], uint32_t (&kf)[2][16], int left, float scale,
                                      Shared& sm, int warp, int lane, F loaded) {
@@ -182,7 +188,6 @@ __device__ __forceinline__ void step(State& s, const uint32_t (&qf)[2][16], uint
   float p0 = attn::ex2(x0 - m), p1 = attn::ex2(x1 - m);
   uint32_t* prob = reinterpret_cast<uint32_t*>(&sm.prob[lane]) + warp;
   *prob = kF16 ? pack_f16(p0, p1) : pack_bf16(p0, p1);
-  loaded();
   if (__syncthreads_or(fmaxf(x0, x1) > m + (kHead + 8.f))) {
     // the references move: to the largest scores of this step less kHead, where that is more
     const float top = quad_max(fmaxf(x0, x1));
@@ -200,8 +205,9 @@ __device__ __forceinline__ void step(State& s, const uint32_t (&qf)[2][16], uint
     *prob = kF16 ? pack_f16(p0, p1) : pack_bf16(p0, p1);
     __syncthreads();
   }
-  s.l += p0 + p1;
   const uint4 p = sm.prob[lane];
+  s.l += p0 + p1;
+  loaded();
 #pragma unroll
   for (int i = 0; i < 16; ++i) mma<kF16>(s.o[i], p.x, p.y, p.z, p.w, kf[0][i], kf[1][i]);
 }

@@ -136,7 +136,8 @@ csa2_status csa2_fp4_dequantize(const uint8_t* codes, const uint8_t* scales, int
  *           iff ratio*j + ratio - 1 <= its position (causal mask over compressed entries).
  *   cand    NULL: row r of `scores` is [cap] and entry t holds the score of cache entry t.
  *           else int32 [B*Nq][n_cand] ascending cache positions (a pool) with cand_len[B*Nq]
- *           valid entries; entry i of the row holds the score of position cand[r][i].
+ *           valid entries; entry i of the row holds the score of position cand[r][i].  Any order
+ *           where q_pos lets the query see the whole cache (q_pos[r] >= ratio*cap - 1).
  *   scores  fp32 [B*Nq][cap or n_cand]: the visible entries form a prefix of length
  *           n_valid[r] (nullable output); the rest of the row is set to -inf.
  */
