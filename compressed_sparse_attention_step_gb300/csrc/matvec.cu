@@ -33,10 +33,11 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kRows = 32, kChan = 128;     // block
 constexpr int kCodeBytes = kRows * kChan / 2;
 constexpr int kBlock = kCodeBytes + kRows * kChan / CSA2_GROUP;  // 2304 bytes
-constexpr int kStage = 48 * 1024;          // bytes of x staged at a time
+constexpr int kStage = 36 * 1024;          // bytes of x staged at a time (two CTAs per SM with up to 16 tokens)
 constexpr int kSlots = 3;                  // blocks a warp of matvec_kernel has under way
 constexpr int kMaxCluster = 8;
-constexpr size_t kMaxSmem = size_t(kWarps) * kSlots * kBlock + kWarps * 32 * (kChan * 2 + 4);  // of matvec_kernel
+// of matvec_kernel: the rings, x of 8 blocks x 32 tokens (or kStage), the partial sums
+constexpr size_t kMaxSmem = size_t(kWarps) * kSlots * kBlock + 8 * 32 * (kChan * 2 + 4) + 8 * 32 * 32 * 4;
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -84,18 +85,20 @@ __global__ void __launch_bounds__(256) pack_kernel(const uint8_t* __restrict__ c
   *reinterpret_cast<uint2*>(dst + kCodeBytes + lane * 8) = make_uint2(sb[0], sb[1]);
 }
 
-__device__ __forceinline__ void cluster_arrive_wait() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");
 }
-__device__ __forceinline__ float ld_cluster(uint32_t a, uint32_t rank) {
-  float v;
-  asm volatile("{ .reg .u32 r; mapa.shared::cluster.u32 r, %1, %2; ld.shared::cluster.f32 %0, [r]; }\n"
-               : "=f"(v)
-               : "r"(a), "r"(rank)
-               : "memory");
-  return v;
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive_wait() { cluster_arrive(), cluster_wait(); }
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t a, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(rank));
+  return r;
 }
-
+// a shared-memory address of this CTA is one of the cluster's as well
+__device__ __forceinline__ void st_cluster(uint32_t a, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;\n" ::"r"(a), "f"(v) : "memory");
+}
 struct Unit {  // a block as fragments: rows 16 r + 8 h + g, channels 32t .. 32t+31
   uint4 c[2][2];
   uint32_t s[2][2];
@@ -125,11 +128,13 @@ __global__ void __launch_bounds__(kThreads, TG <= 2 ? 2 : 1) matvec_kernel(const
   unsigned char* stage = smem + kWarps * kSlots * kBlock;
   uint4* xs = reinterpret_cast<uint4*>(stage);                                         // [kb][TG][4][32 lanes]
   float* xf = reinterpret_cast<float*>(stage + size_t(p.stage_kb) * kTok * kChan * 2);  // [kb][kTok]
-  float* red = reinterpret_cast<float*>(stage);                                        // [WK][kTok][kCtaRows]
+  // partial sums of the rows that this CTA finishes: [rank][WK][kTok][kCtaRows / C]
+  float* red = reinterpret_cast<float*>(stage + size_t(p.stage_kb) * kTok * (kChan * 2 + 4));
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, t = lane & 3, g = lane >> 2;
   const int wr = warp / WK, wk = warp % WK;
+  if (C > 1) cluster_arrive();
   const int rank = C > 1 ? int(blockIdx.x % unsigned(C)) : 0;
   const int64_t row0 = int64_t(blockIdx.x / unsigned(C)) * kCtaRows;
   const int kb0 = int(uint32_t(p.n_kb) * uint32_t(rank) / uint32_t(C)),
@@ -251,35 +256,35 @@ __global__ void __launch_bounds__(kThreads, TG <= 2 ? 2 : 1) matvec_kernel(const
       }
     }
   }
-  __syncthreads();
-  // acc[r][j]: rows g (0, 1) and g + 8 (2, 3) of tile r, tokens 8j + 2t and + 1
+  // Each partial sum goes to the CTA of the cluster that finishes its row, rank row / (kCtaRows / C), which adds them
+  // up in order of rank and warp.  acc[r][j]: rows g (0, 1) and g + 8 (2, 3) of half r, tokens 8j + 2t and + 1.
+  const int rows = kCtaRows / C;
+  if (C > 1) cluster_wait();  // every CTA of the cluster has started
+  const uint32_t red_a = smem_u32(red) + 4u * uint32_t((rank * WK + wk) * kTok * rows);
 #pragma unroll
   for (int r = 0; r < 2; ++r)
 #pragma unroll
-    for (int j = 0; j < TG; ++j)
+    for (int h = 0; h < 2; ++h) {
+      const int row = wr * 32 + r * 16 + 8 * h + g, owner = row / rows;
+      const uint32_t at = C > 1 ? cluster_addr(red_a, uint32_t(owner)) : red_a;
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        red[(wk * kTok + 8 * j + 2 * t + (e & 1)) * kCtaRows + wr * 32 + r * 16 + g + 8 * (e >> 1)] = acc[r][j][e];
-  if (C > 1) cluster_arrive_wait();
+      for (int j = 0; j < TG; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          st_cluster(at + 4u * uint32_t((8 * j + 2 * t + e) * rows + row - owner * rows), acc[r][j][2 * h + e]);
+    }
+  if (C > 1) cluster_arrive(), cluster_wait();
   else __syncthreads();
-  const int rows = kCtaRows / C;
-  const uint32_t red_a = smem_u32(red);
   for (int e = tid; e < rows * p.m; e += kThreads) {
-    const int tok = e / rows, rr = rank * rows + e - tok * rows;
-    const int64_t n = row0 + rr;
+    const int tok = e / rows;
+    const int64_t n = row0 + rank * rows + e - tok * rows;
     if (n >= p.n_out) continue;
     float s = 0.f;
-    for (int q = 0; q < C; ++q)
-#pragma unroll
-      for (int w = 0; w < WK; ++w) {
-        const int at = (w * kTok + tok) * kCtaRows + rr;
-        s += C > 1 ? ld_cluster(red_a + 4u * uint32_t(at), uint32_t(q)) : red[at];
-      }
+    for (int w = 0; w < C * WK; ++w) s += red[w * kTok * rows + e];
     if (p.row_scale) s *= p.row_scale[n];
     if (p.y_fp32) static_cast<float*>(p.y)[int64_t(tok) * p.n_out + n] = s;
     else static_cast<__nv_bfloat16*>(p.y)[int64_t(tok) * p.n_out + n] = __float2bfloat16_rn(s);
   }
-  if (C > 1) cluster_arrive_wait();  // no CTA leaves while its sums are being read
 }
 
 template <int TG, int WR>
@@ -287,8 +292,8 @@ cudaError_t launch(Params p, int C, cudaStream_t st) {
   constexpr int kTok = TG * 8, WK = kWarps / WR, kCtaRows = WR * 32;
   const int share = (p.n_kb + C - 1) / C;
   p.stage_kb = std::min(std::max(kStage / (kTok * kChan * 2) / kWarps, 1) * kWarps, (share + kWarps - 1) / kWarps * kWarps);
-  const size_t smem = size_t(kWarps) * kSlots * kBlock +
-                      std::max(size_t(p.stage_kb) * kTok * (kChan * 2 + 4), size_t(WK) * kTok * kCtaRows * 4);
+  const size_t smem = size_t(kWarps) * kSlots * kBlock + size_t(p.stage_kb) * kTok * (kChan * 2 + 4) +
+                      size_t(WK) * kTok * kCtaRows * 4;
   auto kern = matvec_kernel<TG, WR>;
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), kMaxSmem, done);
