@@ -99,7 +99,7 @@ def tree_node(q, sel, win, scale, sel_round=2.0 ** -11):
         z = np.zeros((16, 512))
         return z, np.full(16, -np.inf), z, np.zeros(16)
     s = q @ rows.T * scale
-    es = 10 * 16 * 2.0 ** -22 / 16 * (np.abs(q) @ np.abs(rows).T) * scale + np.abs(s) * 2.0 ** -22 + 2.0 ** -20
+    es = 10 * 16 * 2.0 ** -22 / 16 * (np.abs(q) @ np.abs(rows).T) * abs(scale) + np.abs(s) * 2.0 ** -22 + 2.0 ** -20
     m = s.max(-1, keepdims=True)
     p = np.exp(s - m)
     lse = (m + np.log(p.sum(-1, keepdims=True)))[:, 0]

@@ -141,3 +141,22 @@ def test_captured_and_on_another_stream():
         gr.replay()
     torch.cuda.synchronize()
     assert torch.equal(ref, y)
+
+
+def test_two_calls_at_once():
+    """Two streams, both kernels, different inputs."""
+    g = np.random.default_rng(10)
+    jobs = []
+    for M, N, K in ((20, 2300, 4096), (3, 700, 640), (32, 4096, 2100 // 16 * 16)):
+        packed, w = _weight(g, N, K)
+        xb = V.bf16(g, (M, K))
+        jobs.append((bf16_dev(xb), packed, torch.empty((M, N), dtype=torch.float32, device="cuda"), xb, w,
+                     torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for x, packed, y, _, _, s in jobs:
+            c.csa2_fp4_matvec(x, packed, y, stream=s)
+    torch.cuda.synchronize()
+    for x, packed, y, xb, w, _ in jobs:
+        _check(y, V.f64(xb), w, np.ones(y.shape[1]))
+    assert c.csa2_device_flags() == 0

@@ -201,3 +201,64 @@ def test_paged_append(orc, n, S, what):
     assert np.array_equal(codes.cpu().numpy(), rc) and np.array_equal(scales.cpu().numpy(), rs)
     assert np.array_equal(bf16_host(KI), rk)
     assert c.csa2_device_flags() == (c.FLAG_APPEND_OOB if n > 1 else 0)
+
+
+def test_paged_append_every_value_scale_and_tie(orc):
+    """The paged append's codes are the oracle's for every finite bf16 value against 16 group maxima, every
+    positive maximum, and, under every scale, every midpoint of two codes with its neighbours."""
+    from tests.test_gpu_fp4 import _sweep_rows
+    rows = [_sweep_rows()]
+    ties = []
+    for sb in range(1, 0x7F):
+        s = V.e4m3(np.uint8(sb))
+        mids = syn.f32_to_bf16_bits((np.array([.25, .75, 1.25, 1.75, 2.5, 3.5, 5]) * s).astype(np.float32)).astype(np.int64)
+        top = int(syn.f32_to_bf16_bits(np.array([6 * s], np.float32))[0])      # makes the scale s, exactly
+        for sign in (0, 0x8000):
+            ties.append([top] + [(v | sign) for v in mids] + [(v - 1) | sign for v in mids] + [top | sign])
+            ties.append([top] + [(v + 1) | sign for v in mids] + [0, 0x8000] + [(v | (sign ^ 0x8000)) for v in mids[:6]])
+    ties = np.array(ties, np.int64).astype(np.uint16)
+    pad = np.zeros(((-len(ties)) % 32, 16), np.uint16)
+    rows.append(np.concatenate((ties, pad)).reshape(-1, 512))
+    x = np.concatenate(rows)
+    n = x.shape[0]
+    codes = torch.zeros((n, 256), dtype=torch.uint8, device="cuda")
+    scales = torch.zeros((n, 32), dtype=torch.uint8, device="cuda")
+    order = np.random.default_rng(8).permutation(n).astype(np.int32)
+    c.csa2_paged_append(to_dev(order), kv_new=bf16_dev(x), codes=codes, scales=scales)
+    ec, es = orc.fp4_quantize(x)
+    assert np.array_equal(scales.cpu().numpy()[order], es)
+    assert np.array_equal(codes.cpu().numpy()[order], ec)
+    ref_c, ref_s = torch.empty((1, n, 256), dtype=torch.uint8, device="cuda"), torch.empty((1, n, 32), dtype=torch.uint8, device="cuda")
+    c.csa2_fp4_quantize_append(bf16_dev(x)[None], ref_c, ref_s)
+    assert torch.equal(codes[to_dev(order).long()], ref_c[0]) and torch.equal(scales[to_dev(order).long()], ref_s[0])
+
+
+def test_block_tables_a_full_list_loses_pages_with_a_flag():
+    """More pages given back than the list holds: the first ones are kept, the rest flagged, none written past it."""
+    table = torch.arange(8, dtype=torch.int32, device="cuda").view(2, 4)
+    free = torch.full((6,), -1, dtype=torch.int32, device="cuda")
+    state = torch.zeros(4, dtype=torch.int32, device="cuda")
+    c.csa2_device_flags()
+    granted, _ = _run([64, 64], [0, 0], 16, table, free[:3], state, 0)
+    assert granted.tolist() == [0, 0] and state.tolist() == [3, 0, 0, 0]
+    assert free.tolist() == [7, 6, 5, -1, -1, -1]
+    assert c.csa2_device_flags() == c.FLAG_INDEX_OOB
+
+
+def test_binding_refuses_strides_types_and_places():
+    i32 = dict(dtype=torch.int32, device="cuda")
+    lens, slots, ns = torch.zeros(2, **i32), torch.zeros((2, 8), **i32), torch.zeros(2, **i32)
+    with pytest.raises(ValueError, match="contiguous"):
+        c.csa2_context_slots(lens, torch.zeros((8, 2), **i32).t(), ns)
+    with pytest.raises(TypeError, match="dtype"):
+        c.csa2_context_slots(lens.long(), slots, ns)
+    with pytest.raises(ValueError, match="CUDA"):
+        c.csa2_context_slots(lens.cpu(), slots, ns)
+    with pytest.raises(ValueError, match="shape"):
+        c.csa2_context_slots(lens, slots, ns[:1])
+    with pytest.raises(TypeError):
+        c.csa2_context_slots([0, 0], slots, ns)
+    with pytest.raises(c.Csa2Error):                      # rows of 16 bytes start at a multiple of 16
+        c.csa2_context_slots(lens, torch.zeros(17, **i32)[1:].view(2, 8), ns)
+    with pytest.raises(c.Csa2Error):
+        c.csa2_block_tables(lens, ns, 24, slots, torch.zeros(4, **i32), torch.zeros(4, **i32), torch.zeros(2, **i32))

@@ -222,3 +222,56 @@ def test_captured_and_on_another_stream():
         g.replay()
     torch.cuda.synchronize()
     assert torch.equal(ref, d["out"])
+
+
+def test_scores_far_below_zero():
+    """Scores of millions, of either sign: the softmax is that of their differences.  Heads whose largest score
+    leads by more than both scores' error bounds and 40 attend that row alone (e^-40 is below half of bf16's
+    and of fp32's last place), exactly, as an FP4 row is a bf16 row."""
+    led = 0
+    for sign in (-1.0, 1.0):
+        cs = Case(71, 2, 2, 40, 33, 0, full=True)
+        d = cs.dev()
+        scale = float(np.float32(sign * 1e5))
+        c.csa2_tree_attn(**d, softmax_scale=scale)
+        out = V.f64(bf16_host(d["out"]))
+        for r in range(4):
+            q, rows = V.f64(cs.q[r // 2, r % 2]), V.dequant(cs.codes[cs.idx[r]], cs.scales[cs.idx[r]])
+            sc = q @ rows.T * scale
+            es = 160 * 2.0 ** -22 / 16 * (np.abs(q) @ np.abs(rows).T) * abs(scale) + np.abs(sc) * 2.0 ** -22
+            top = np.argsort(sc, -1)[:, ::-1]
+            for h in range(16):
+                lead = sc[h, top[h, 0]] - sc[h, top[h, 1]]
+                if lead > 2 * es[h].max() + 40:
+                    led += 1
+                    assert np.array_equal(out[r // 2, r % 2, h], rows[top[h, 0]])
+    assert led > 100
+    # one cache row: P = 1 whatever the score
+    cs = Case(72, 1, 1, 1, 1, 0, full=True)
+    d = cs.dev()
+    for scale in (-1e35, 1e35, 0.0):
+        c.csa2_tree_attn(**d, softmax_scale=scale)
+        assert np.array_equal(V.f64(bf16_host(d["out"]))[0, 0], np.tile(V.dequant(cs.codes, cs.scales), (16, 1)))
+
+
+def test_more_nodes_than_run_at_once():
+    """Two waves and more of CTAs, a ragged batch."""
+    cs = Case(81, 70, 10, 48, 24, 9)
+    d = cs.dev()
+    c.csa2_tree_attn(**d)
+    cs.check(d)
+
+
+def test_two_calls_at_once():
+    """Two streams, different inputs."""
+    a, b = Case(91, 3, 9, 90, 70, 33), Case(92, 30, 6, 60, 40, 20, pool=False)
+    da, db = a.dev(), b.dev()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for s in (s1, s2):
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):
+        c.csa2_tree_attn(**da, stream=s1)
+        c.csa2_tree_attn(**db, stream=s2)
+    torch.cuda.synchronize()
+    a.check(da)
+    b.check(db)
