@@ -233,6 +233,41 @@ def test_paged_append_every_value_scale_and_tie(orc):
     assert torch.equal(codes[to_dev(order).long()], ref_c[0]) and torch.equal(scales[to_dev(order).long()], ref_s[0])
 
 
+@pytest.mark.parametrize("kv_off,ki_off", [(8, 0), (16, 8), (24, 8)])
+def test_paged_append_sources_at_any_16_bytes(kv_off, ki_off):
+    """Sources that start on 16 bytes and no more (a view into a larger buffer) append the same bytes."""
+    g = torch.Generator(device="cuda").manual_seed(kv_off)
+    n, n_slots = 37, 64
+    kv = torch.randn((n, 512), generator=g, device="cuda").bfloat16()
+    ki = torch.randn((n, 128), generator=g, device="cuda").bfloat16()
+    order = torch.randperm(n_slots, generator=g, device="cuda")[:n].int()
+    got = []
+    for a, b in ((0, 0), (kv_off, ki_off)):
+        src = torch.zeros(n * 512 + 32, dtype=torch.bfloat16, device="cuda")[a:a + n * 512].view(n, 512).copy_(kv)
+        key = torch.zeros(n * 128 + 32, dtype=torch.bfloat16, device="cuda")[b:b + n * 128].view(n, 128).copy_(ki)
+        codes, scales = (torch.zeros((n_slots, w), dtype=torch.uint8, device="cuda") for w in (256, 32))
+        KI = torch.zeros((n_slots, 128), dtype=torch.bfloat16, device="cuda")
+        c.csa2_paged_append(order, kv_new=src, codes=codes, scales=scales, ki_new=key, KI=KI)
+        got.append((codes, scales, KI))
+    assert all(torch.equal(x, y) for x, y in zip(*got))
+    assert torch.equal(got[0][2][order.long()], ki)
+
+
+def test_paged_append_of_infinities_and_nan():
+    """Infinities and NaN (any payload, any channel) are stored as csa2_fp4_quantize_append stores them."""
+    x = np.zeros((64, 512), np.uint16)
+    rng = np.random.default_rng(5)
+    x[:] = syn.f32_to_bf16_bits(rng.standard_normal(x.shape).astype(np.float32))
+    for i, v in enumerate([0x7F80, 0xFF80, 0x7FC0, 0xFFC0, 0x7F81, 0xFFFF, 0x7FFF, 0x7F7F]):
+        for j in range(16):
+            x[8 * i + j // 2, 16 * j + j::64] = v
+    codes, scales = (torch.zeros((64, w), dtype=torch.uint8, device="cuda") for w in (256, 32))
+    c.csa2_paged_append(torch.arange(64, dtype=torch.int32, device="cuda"), kv_new=bf16_dev(x), codes=codes, scales=scales)
+    ref_c, ref_s = (torch.zeros((1, 64, w), dtype=torch.uint8, device="cuda") for w in (256, 32))
+    c.csa2_fp4_quantize_append(bf16_dev(x)[None], ref_c, ref_s)
+    assert torch.equal(scales, ref_s[0]) and torch.equal(codes, ref_c[0])
+
+
 def test_block_tables_a_full_list_loses_pages_with_a_flag():
     """More pages given back than the list holds: the first ones are kept, the rest flagged, none written past it."""
     table = torch.arange(8, dtype=torch.int32, device="cuda").view(2, 4)
