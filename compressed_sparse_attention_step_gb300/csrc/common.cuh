@@ -202,6 +202,13 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
   }
 }
 
+// After a wait that gave up: waits once more, as long, for each slot's last phase, so that a CTA does not leave while
+// copies into it are under way.  bars: one per slot, n phases begun in turn (phase i on slot i % kSlots).
+template <int kSlots>
+__device__ __forceinline__ void bar_drain(uint64_t* bars, int n) {
+  for (int i = 0; i < min(n, kSlots); ++i) bar_wait(smem_u32(&bars[i]), uint32_t((n - i - 1) / kSlots) & 1u);
+}
+
 // Lets a kernel use `bytes` of dynamic shared memory on the current device; set once per device (`done`, one per
 // kernel, holds a bit for each device).
 inline cudaError_t allow_smem(const void* kern, size_t bytes, std::atomic<uint64_t>& done) {

@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, TG <= 2 ? 2 : 1) matvec_kernel(const
   }
   __syncwarp();
   int slot = 0, use = 0, done = 0;
-  bool late = false;  // a copy did not land within a second: flagged, and no more waiting
+  int late = 0;  // a copy did not land within a second: flagged, no more waiting or copying; the copies begun
 
   float acc[2][TG][4];
 #pragma unroll
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, TG <= 2 ? 2 : 1) matvec_kernel(const
     __syncthreads();
     for (int kb = wk; kb < nk && done < n_blk; kb += WK, ++done) {
       if (!late && !bar_wait(smem_u32(&full[warp][slot]), uint32_t(use) & 1u)) {
-        late = true;
+        late = min(n_blk, done + kSlots);
         atomicOr(p.flags, CSA2_FLAG_TIMEOUT);
       }
       Unit u0;
@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, TG <= 2 ? 2 : 1) matvec_kernel(const
           }
       }
       __syncwarp();
-      if (lane == 0 && done + kSlots < n_blk)
+      if (lane == 0 && !late && done + kSlots < n_blk)
         block_copy(ring + slot * kBlock, src + int64_t(done + kSlots) * WK * kBlock, &full[warp][slot]);
       if (++slot == kSlots) slot = 0, ++use;
       float d[2][TG][4];
@@ -256,6 +256,7 @@ __global__ void __launch_bounds__(kThreads, TG <= 2 ? 2 : 1) matvec_kernel(const
       }
     }
   }
+  if (lane == 0 && late) bar_drain<kSlots>(full[warp], late);
   // Each partial sum goes to the CTA of the cluster that finishes its row, rank row / (kCtaRows / C), which adds them
   // up in order of rank and warp.  acc[r][j]: rows g (0, 1) and g + 8 (2, 3) of half r, tokens 8j + 2t and + 1.
   const int rows = kCtaRows / C;
@@ -458,9 +459,10 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_tc_kernel(const Params p, 
   const int me = warp - 4;  // its ring
   int l_k = grp, l_rb = rb0 + q;  // the next block to copy: of the share's channel blocks, and its row block
   const uint8_t* l_src = p.packed + (int64_t(l_rb) * p.n_kb + kb0 + l_k) * kBlock;
+  int copied = 0;
   auto copy = [&](int slot) {  // one thread; nothing where the step has no such row block
     while (l_k >= nk && l_rb < rb1) l_k -= nk, l_rb += kStep, l_src += (int64_t(kStep) * p.n_kb - nk) * kBlock;
-    if (l_rb < rb1) block_copy(sm.ring[me][slot], l_src, &sm.full[me][slot]);
+    if (l_rb < rb1 && !late) block_copy(sm.ring[me][slot], l_src, &sm.full[me][slot]), ++copied;
     l_k += kGroups, l_src += kGroups * kBlock;
   };
   if (warp >= 4 && grp < kGroups) {
@@ -602,6 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_tc_kernel(const Params p, 
       k += kGroups, buf += kGroups;
       if (buf >= kABufs) buf -= kABufs, ++use;
     }
+    if (lane == 0 && late) bar_drain<kSlots>(sm.full[me], copied);
   } else if (warp >= 4) {
     const uint32_t lanes = uint32_t(32 * q) << 16;
     for (int step = 0; step < n_steps; ++step) {
@@ -673,6 +676,8 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_tc_kernel(const Params p, 
   if (C > 1) cluster_arrive_wait();  // no CTA leaves while its sums are being read
   else __syncthreads();
   if (warp == 3) {
+    if (lane == 0 && n_steps > 0) bar_wait(smem_u32(&sm.d_full), uint32_t(n_steps - 1) & 1u);  // (done, unless one is late)
+    __syncwarp();
     attn::tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(tmem) : "memory");
   }

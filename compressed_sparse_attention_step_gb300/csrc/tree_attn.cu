@@ -483,6 +483,7 @@ __global__ void __launch_bounds__(kThreads, 3) tree_attn_kernel(const Params p) 
     }
   }
 
+  if (late) bar_drain<kWinSlots>(sm.win_full, w1 - w0), bar_drain<kSelSlots>(sm.sel_full, s1 - s0);
   {
     const float l = quad_sum(st.l);
     if (t == 0) sm.sums[warp][g] = l;
