@@ -573,6 +573,8 @@ def csa2_tree_attn(q, parent, codes, scales, idx, out, *, n_nodes=None, n_valid=
     lse fp32 [B, N, 16]."""
     check, dev, (i32, u8, f32, bf) = _call_context()
     B, N = _dims(q, "q", 4)[:2]
+    if not hasattr(codes, "shape"):
+        raise TypeError("codes: expected a torch.Tensor")
     lead = tuple(codes.shape[:-1])
     pool = len(lead) == 1
     if not pool and (len(lead) != 2 or lead[0] != B):

@@ -298,7 +298,7 @@ extern "C" csa2_status csa2_block_tables(const int32_t* old_lens, const int32_t*
       (int64_t(max_pages) << shift) > 0x7FFFFFFFll)
     return CSA2_ERR_INVALID_ARG;
   if (B == 0) return CSA2_OK;
-  if (!old_lens || !new_lens || !block_table || !free_pages || !pool_state || !granted || (n_new > 0 && !slots))
+  if (!old_lens || !new_lens || !block_table || (free_cap > 0 && !free_pages) || !pool_state || !granted || (n_new > 0 && !slots))
     return CSA2_ERR_INVALID_ARG;
   const void* all[] = {old_lens, new_lens, block_table, free_pages, pool_state, granted, slots};
   for (const void* p : all)
@@ -336,7 +336,7 @@ extern "C" csa2_status csa2_context_slots(const int32_t* lens, const int32_t* pa
   if (B < 0 || B > 65535 || N < 0 || N > CSA2_MAX_TREE || ld < 0 || ld > 0x7FFFFFFFll) return CSA2_ERR_INVALID_ARG;
   if (block_table && (max_pages < 1 || (shift = page_shift(page_size)) < 0)) return CSA2_ERR_INVALID_ARG;
   if (int64_t(B) * N == 0) return CSA2_OK;
-  if (!lens || !slots || !n_slots || !al(lens, 4) || !al(parent, 4) || !al(n_nodes, 4) || !al(block_table, 4) ||
+  if (!lens || (ld > 0 && !slots) || !n_slots || !al(lens, 4) || !al(parent, 4) || !al(n_nodes, 4) || !al(block_table, 4) ||
       !al(slots, 16) || !al(n_slots, 4))
     return CSA2_ERR_INVALID_ARG;
   unsigned int* flags = device_flags_ptr();

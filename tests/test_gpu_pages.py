@@ -297,3 +297,20 @@ def test_binding_refuses_strides_types_and_places():
         c.csa2_context_slots(lens, torch.zeros(17, **i32)[1:].view(2, 8), ns)
     with pytest.raises(c.Csa2Error):
         c.csa2_block_tables(lens, ns, 24, slots, torch.zeros(4, **i32), torch.zeros(4, **i32), torch.zeros(2, **i32))
+
+
+def test_no_free_list_and_no_columns():
+    """A pool without a free list still moves pages between sequences; lists of no columns count nothing and say so."""
+    i32 = dict(dtype=torch.int32, device="cuda")
+    table = torch.tensor([[5, 3], [-1, -1]], **i32)
+    state, granted = torch.zeros(4, **i32), torch.zeros(2, **i32)
+    c.csa2_device_flags()
+    c.csa2_block_tables(torch.tensor([32, 0], **i32), torch.tensor([16, 16], **i32), 16, table, torch.empty(0, **i32), state,
+                        granted)
+    assert granted.tolist() == [16, 16] and table[1].tolist() == [3, -1] and state.tolist() == [0, 0, 0, 0]
+    assert c.csa2_device_flags() == 0
+    n = torch.full((2,), -5, **i32)
+    c.csa2_context_slots(torch.tensor([0, 0], **i32), torch.empty((2, 0), **i32), n)
+    assert n.tolist() == [0, 0] and c.csa2_device_flags() == 0
+    c.csa2_context_slots(torch.tensor([0, 3], **i32), torch.empty((2, 0), **i32), n)
+    assert n.tolist() == [0, 0] and c.csa2_device_flags() == c.FLAG_INDEX_OOB

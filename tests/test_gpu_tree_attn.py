@@ -275,3 +275,27 @@ def test_two_calls_at_once():
     torch.cuda.synchronize()
     a.check(da)
     b.check(db)
+
+
+def test_tree_attn_in_place_and_an_empty_pool():
+    """out may be q (at each number of CTAs a node); with a pool of no rows every entry is empty."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    for B, N, k in ((1, 5, 64), (7, 5, 64), (40, 8, 64)):
+        q = torch.randn((B, N, 16, 512), generator=g, device="cuda").bfloat16()
+        parent = torch.arange(-1, N - 1, device="cuda", dtype=torch.int32).repeat(B, 1)
+        codes = torch.randint(0, 256, (300, 256), generator=g, device="cuda", dtype=torch.uint8)
+        scales = torch.randint(40, 60, (300, 32), generator=g, device="cuda", dtype=torch.uint8)
+        idx = torch.randint(0, 300, (B * N, k), generator=g, device="cuda", dtype=torch.int32)
+        swa = torch.randn((B, 7 + N, 512), generator=g, device="cuda").bfloat16()
+        out = torch.empty_like(q)
+        c.csa2_tree_attn(q, parent, codes, scales, idx, out, swa=swa, W=8)
+        same = q.clone()
+        c.csa2_tree_attn(same, parent, codes, scales, idx, same, swa=swa, W=8)
+        assert torch.equal(out, same)
+        none, some = torch.empty_like(q), torch.empty_like(q)
+        c.csa2_device_flags()
+        c.csa2_tree_attn(q, parent, codes, scales, torch.full_like(idx, -1), some, swa=swa, W=8)
+        c.csa2_tree_attn(q, parent, codes[:0], scales[:0], torch.full_like(idx, -1), none, swa=swa, W=8)
+        assert c.csa2_device_flags() == 0 and torch.equal(none, some)
+        c.csa2_tree_attn(q, parent, codes[:0], scales[:0], idx, none, swa=swa, W=8)
+        assert c.csa2_device_flags() == c.FLAG_INDEX_OOB and torch.equal(none, some)

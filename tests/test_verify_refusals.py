@@ -88,6 +88,11 @@ def test_fp4_weight(L):
     assert call(x=None) == 1 and call(w=None) == 1 and call(y=None) == 1
     assert call(x=ODD4) == 1 and call(w=ODD4) == 1 and call(y=ODD4) == 1 and call(rs=ODD) == 1
     assert call(m=0) == 0 and call(n_out=0) == 0
+    # y over x's last bytes, packed over its sources
+    assert call(y=_p(0)) == 1 and call(y=ctypes.c_void_p(_p(0).value + 2 * 32 * 2 - 16)) == 1
+    assert call(x=ctypes.c_void_p(_p(2).value + 2 * 8 * 2 - 16)) == 1
+    assert L.csa2_fp4_pack_weight(_p(0), _p(1), 4, 32, _p(0), None) == 1
+    assert L.csa2_fp4_pack_weight(_p(0), ctypes.c_void_p(_p(2).value + 2304 - 16), 4, 32, _p(2), None) == 1
 
 
 def test_binding_checks_shapes_and_types():
