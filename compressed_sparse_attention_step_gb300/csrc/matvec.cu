@@ -336,7 +336,6 @@ constexpr uint32_t kABufs = 6, kACols = kChan / 2;
 static_assert(kABufs % kGroups == 0 && kABufs % 2 == 0, "one filler and one user of each half per buffer");
 constexpr uint32_t kDCol = kABufs * kACols;       // accumulators of N columns, one per issuer
 constexpr int kXBytes = 128 * 1024;               // x staged by a CTA, at most
-constexpr int kCluster = 4;                       // CTAs that share the channels (2 and 8 measured slower)
 static_assert(kDCol + kIssuers * 32 <= 512, "tensor memory");
 
 struct Tail {
@@ -418,15 +417,15 @@ struct Row {  // a row's share of a block, as loaded
   uint2 s;
 };
 
-// kTok: token rows of the MMA (N), 16 or 32.
-template <int kTok>
-__global__ void __launch_bounds__(kThreads, 1) matvec_tc_kernel(const Params p, int C) {
+// kTok: token rows of the MMA (N), 16 or 32.  C: CTAs of a cluster.
+template <int kTok, int C>
+__global__ void __launch_bounds__(kThreads, 1) matvec_tc_kernel(const Params p) {
   extern __shared__ __align__(1024) unsigned char smem[];
   Tail& sm = *reinterpret_cast<Tail*>(smem + p.x_bytes);
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int rank = C > 1 ? int(blockIdx.x % unsigned(C)) : 0;
+  const int rank = int(blockIdx.x % unsigned(C));
   const int n_clusters = int(gridDim.x / unsigned(C)), cluster = int(blockIdx.x / unsigned(C));
   // even shares (the products stay below 2^32: sizes_ok)
   const int kb0 = int(uint32_t(p.n_kb) * uint32_t(rank) / uint32_t(C)),
@@ -476,11 +475,15 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_tc_kernel(const Params p, 
   // x: a warp per token; groups of 64 channels, each [kTok rows][128 bytes], 16-byte pieces swizzled by the row.
   // A lane keeps the first 2048 channels of the share between the two passes, and reads what lies behind again.
   // Rows past the last token are left as they are: they reach their own columns of the sums alone.
-  for (int tok = (warp + kThreads / 32 - 4) % (kThreads / 32); tok < p.m; tok += kThreads / 32) {  // warp 3 comes last
-    const uint16_t* src = p.x + int64_t(tok) * p.n_in;
-    auto at = [&](int c) -> uint4 {  // channels c .. c+7 of the share
+  {
+    constexpr int W = kThreads / 32, U = (kTok + W - 1) / W;  // tokens of a warp, loaded together
+    const int tok0 = (warp + W - 4) % W;                      // warp 3 comes last
+    const uint16_t* src = p.x + int64_t(tok0) * p.n_in;
+    auto at = [&](int u, int c) -> uint4 {  // channels c .. c+7 of the share
       const int64_t ch = int64_t(kb0) * kChan + c;
-      return c < nk * kChan && ch < p.n_in ? __ldg(reinterpret_cast<const uint4*>(src + ch)) : make_uint4(0, 0, 0, 0);
+      return tok0 + u * W < p.m && c < nk * kChan && ch < p.n_in
+                 ? __ldg(reinterpret_cast<const uint4*>(src + u * W * p.n_in + ch))
+                 : make_uint4(0, 0, 0, 0);
     };
     auto mag = [](uint32_t am, const uint4& v) {
       const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -488,46 +491,52 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_tc_kernel(const Params p, 
       for (int i = 0; i < 4; ++i) am = max(am, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
       return am;
     };
-    uint4 keep[8];
+    uint4 keep[U][8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) keep[i] = at(lane * 8 + 256 * i);
-    uint32_t am = 0;
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) am = mag(am, keep[i]);
-    for (int c0 = 2048; c0 < nk * kChan; c0 += 2048) {
-      uint4 v[8];
+      for (int i = 0; i < 8; ++i) keep[u][i] = at(u, lane * 8 + 256 * i);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = at(c0 + lane * 8 + 256 * i);
+    for (int u = 0; u < U; ++u) {
+      const int tok = tok0 + u * W;
+      if (tok >= p.m) break;
+      uint32_t am = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) am = mag(am, v[i]);
+      for (int i = 0; i < 8; ++i) am = mag(am, keep[u][i]);
+      for (int c0 = 2048; c0 < nk * kChan; c0 += 1024) {
+        uint4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = at(u, c0 + lane * 8 + 256 * i);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) am = mag(am, v[i]);
+      }
+      am = __reduce_max_sync(0xffffffffu, am);
+      const int up = am ? min(max(141 - int(am >> 7), -126), 126) : 0;
+      const float f = __uint_as_float(uint32_t(127 + up) << 23);
+      auto put = [&](int c, const uint4& v) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = attn::h2_bits(__floats2half2_rn(bf16lo(w[i]) * f, bf16hi(w[i]) * f));
+        if (c < nk * kChan)
+          *reinterpret_cast<uint4*>(smem + (c >> 6) * (kTok * 128) + tok * 128 + ((((c >> 3) & 7) ^ (tok & 7)) << 4)) =
+              make_uint4(o[0], o[1], o[2], o[3]);
+      };
+#pragma unroll
+      for (int i = 0; i < 8; ++i) put(lane * 8 + 256 * i, keep[u][i]);
+      for (int c0 = 2048; c0 < nk * kChan; c0 += 1024) {
+        uint4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = at(u, c0 + lane * 8 + 256 * i);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) put(c0 + lane * 8 + 256 * i, v[i]);
+      }
+      if (lane == 0) sm.inv[tok] = __uint_as_float(uint32_t(127 - up) << 23);
     }
-    am = __reduce_max_sync(0xffffffffu, am);
-    const int up = am ? min(max(141 - int(am >> 7), -126), 126) : 0;
-    const float f = __uint_as_float(uint32_t(127 + up) << 23);
-    auto put = [&](int c, const uint4& v) {
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-      uint32_t o[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = attn::h2_bits(__floats2half2_rn(bf16lo(w[i]) * f, bf16hi(w[i]) * f));
-      if (c < nk * kChan)
-        *reinterpret_cast<uint4*>(smem + (c >> 6) * (kTok * 128) + tok * 128 + ((((c >> 3) & 7) ^ (tok & 7)) << 4)) =
-            make_uint4(o[0], o[1], o[2], o[3]);
-    };
-#pragma unroll
-    for (int i = 0; i < 8; ++i) put(lane * 8 + 256 * i, keep[i]);
-    for (int c0 = 2048; c0 < nk * kChan; c0 += 2048) {
-      uint4 v[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = at(c0 + lane * 8 + 256 * i);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) put(c0 + lane * 8 + 256 * i, v[i]);
-    }
-    if (lane == 0) sm.inv[tok] = __uint_as_float(uint32_t(127 - up) << 23);
   }
   attn::fence_async_smem();
   attn::tc_fence_before();
-  if (C > 1) cluster_arrive_wait();
-  else __syncthreads();
+  cluster_arrive_wait();
   attn::tc_fence_after();
   const uint32_t tmem = sm.tmem;
 
@@ -612,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_tc_kernel(const Params p, 
       const int rb = rb0 + step * kStep, nb = min(kStep, rb1 - rb);
       wait(&sm.d_full, uint32_t(step));
       attn::tc_fence_after();
-      if (step > 0 && C > 1 && !late && !bar_wait<true>(smem_u32(&sm.red_empty), uint32_t(step - 1) & 1u)) {
+      if (step > 0 && !late && !bar_wait<true>(smem_u32(&sm.red_empty), uint32_t(step - 1) & 1u)) {
         late = true;
         atomicOr(p.flags, CSA2_FLAG_TIMEOUT);
       }
@@ -639,24 +648,23 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_tc_kernel(const Params p, 
       if (lane == 0) mbar_arrive(&sm.d_empty);
       asm volatile("bar.sync 1, 128;\n" ::: "memory");  // warps 16 .. 19
       const int t = tid & 127;
-      if (C > 1) {
-        if (t < C) mbar_arrive_cluster(&sm.red_full, uint32_t(t));
-        if (!late && !bar_wait<true>(smem_u32(&sm.red_full), uint32_t(step) & 1u)) {
-          late = true;
-          atomicOr(p.flags, CSA2_FLAG_TIMEOUT);
-        }
+      if (t < C) mbar_arrive_cluster(&sm.red_full, uint32_t(t));
+      if (!late && !bar_wait<true>(smem_u32(&sm.red_full), uint32_t(step) & 1u)) {
+        late = true;
+        atomicOr(p.flags, CSA2_FLAG_TIMEOUT);
       }
       // this CTA finishes rows rank * 128 / C .. of the step, four rows of a token at a time
-      const int quads = 32 / C;
+      constexpr int quads = 32 / C;
       for (int e = t; e < quads * p.m; e += 128) {
         const int tok = e / quads, r = (rank * quads + e - tok * quads) * 4;
         if (r >= nb * kRows) continue;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        float4 part[C];  // (all loads before the first sum: one takes several hundred cycles)
         const uint32_t at = smem_u32(&sm.red[tok][r]);
-        for (int c = 0; c < C; ++c) {
-          const float4 u = C > 1 ? ld_cluster4(at, uint32_t(c)) : *reinterpret_cast<const float4*>(&sm.red[tok][r]);
-          v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
-        }
+#pragma unroll
+        for (int c = 0; c < C; ++c) part[c] = ld_cluster4(at, uint32_t(c));
+        float4 v = part[0];
+#pragma unroll
+        for (int c = 1; c < C; ++c) v.x += part[c].x, v.y += part[c].y, v.z += part[c].z, v.w += part[c].w;
         const int64_t n = int64_t(rb) * kRows + r;
         const float o[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -668,13 +676,12 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_tc_kernel(const Params p, 
         }
       }
       asm volatile("bar.sync 1, 128;\n" ::: "memory");
-      if (C > 1 && t < C) mbar_arrive_cluster(&sm.red_empty, uint32_t(t));
+      if (t < C) mbar_arrive_cluster(&sm.red_empty, uint32_t(t));
     }
   }
   __syncwarp();
   attn::tc_fence_before();
-  if (C > 1) cluster_arrive_wait();  // no CTA leaves while its sums are being read
-  else __syncthreads();
+  cluster_arrive_wait();  // no CTA leaves while its sums are being read
   if (warp == 3) {
     if (lane == 0 && n_steps > 0) bar_wait(smem_u32(&sm.d_full), uint32_t(n_steps - 1) & 1u);  // (done, unless one is late)
     __syncwarp();
@@ -684,9 +691,8 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_tc_kernel(const Params p, 
 }
 
 // Launches the tensor-memory form; cudaErrorNotSupported where a cluster's shared memory does not hold x.
-template <int kTok>
+template <int kTok, int C>
 cudaError_t launch_tc(const mv::Params& g, int sms, cudaStream_t st) {
-  constexpr int C = kCluster;
   Params p = {};
   p.x = g.x, p.packed = g.packed, p.row_scale = g.row_scale, p.y = g.y;
   p.n_out = g.n_out, p.n_in = g.n_in, p.m = g.m, p.n_kb = g.n_kb, p.n_rb = g.n_rb, p.y_fp32 = g.y_fp32;
@@ -694,7 +700,7 @@ cudaError_t launch_tc(const mv::Params& g, int sms, cudaStream_t st) {
   if (p.x_bytes > kXBytes || C > g.n_kb) return cudaErrorNotSupported;
   p.flags = g.flags;
   const size_t smem = size_t(p.x_bytes) + sizeof(Tail);
-  auto kern = matvec_tc_kernel<kTok>;
+  auto kern = matvec_tc_kernel<kTok, C>;
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), kXBytes + sizeof(Tail), done);
   if (e != cudaSuccess) return e;
@@ -723,7 +729,15 @@ cudaError_t launch_tc(const mv::Params& g, int sms, cudaStream_t st) {
     if (dev < 64) room[dev] = clusters;
   }
   cfg.gridDim = dim3(unsigned(std::min(clusters, g.n_rb) * C));
-  return cudaLaunchKernelEx(&cfg, kern, p, C);
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+// Four CTAs share the channels (two and eight measured slower), or eight, where four do not hold x: up to 32768
+// channels for 16 rows, 16384 for 32.
+template <int kTok>
+cudaError_t launch_tc(const mv::Params& g, int sms, cudaStream_t st) {
+  const cudaError_t e = launch_tc<kTok, 4>(g, sms, st);
+  return e == cudaErrorNotSupported ? launch_tc<kTok, 8>(g, sms, st) : e;
 }
 
 }  // namespace tc
