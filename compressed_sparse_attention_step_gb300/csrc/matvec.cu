@@ -621,10 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_tc_kernel(const Params p) 
       const int rb = rb0 + step * kStep, nb = min(kStep, rb1 - rb);
       wait(&sm.d_full, uint32_t(step));
       attn::tc_fence_after();
-      if (step > 0 && !late && !bar_wait<true>(smem_u32(&sm.red_empty), uint32_t(step - 1) & 1u)) {
-        late = true;
-        atomicOr(p.flags, CSA2_FLAG_TIMEOUT);
-      }
+      float sum[kTok];
 #pragma unroll
       for (int j = 0; j < kTok; j += 16) {
         uint32_t d[kIssuers][16];
@@ -640,12 +637,19 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_tc_kernel(const Params p) 
             const float u = tmem_value(d[c][i]);
             if (nk > 1 || (c & 1) == (step & 1)) v += u;
           }
-          if (j + i < p.m) sm.red[j + i][32 * q + lane] = v * sm.inv[j + i];
+          sum[j + i] = v;
         }
       }
       attn::tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.d_empty);
+      if (lane == 0) mbar_arrive(&sm.d_empty);  // the next step's products may begin
+      if (step > 0 && !late && !bar_wait<true>(smem_u32(&sm.red_empty), uint32_t(step - 1) & 1u)) {
+        late = true;
+        atomicOr(p.flags, CSA2_FLAG_TIMEOUT);
+      }
+#pragma unroll
+      for (int i = 0; i < kTok; ++i)
+        if (i < p.m) sm.red[i][32 * q + lane] = sum[i] * sm.inv[i];
       asm volatile("bar.sync 1, 128;\n" ::: "memory");  // warps 16 .. 19
       const int t = tid & 127;
       if (t < C) mbar_arrive_cluster(&sm.red_full, uint32_t(t));
@@ -824,17 +828,27 @@ extern "C" csa2_status csa2_fp4_matvec(const uint16_t* x, int m, const uint8_t* 
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = cudaErrorNotSupported;
   // The tensor-memory form where there is enough weight to pay for its set-up.  Measured, us, this form against the
-  // other: 32 rows x 16384 x 8192 29 / 65, 24 x 4096 x 4096 10.7 / 12.6, 32 x 512 x 4096 9.5 / 9.3,
-  // 16 x 16384 x 8192 25.8 / 30, 16 x 8192 x 4096 11.8 / 12.0, 8 x 16384 x 8192 25.6 / 21.
+  // other: 32 rows x 16384 x 8192 28.5 / 65, 24 x 4096 x 4096 10.4 / 12.6, 32 x 512 x 4096 9.5 / 9.3,
+  // 16 x 16384 x 8192 24.6 / 30, 16 x 8192 x 4096 11.8 / 12.0, 8 x 16384 x 8192 24.5 / 21.
   const int64_t blocks = int64_t(p.n_rb) * p.n_kb;
-  if ((m > 16 && blocks >= 2048) || (m > 8 && blocks >= 16384))
-    e = m <= 16 ? tc::launch_tc<16>(p, sms, st) : tc::launch_tc<32>(p, sms, st);
-  if (e == cudaErrorNotSupported)
-  switch ((m + 7) / 8) {
-    case 1: e = launch_wr<1>(p, sms, st); break;
-    case 2: e = launch_wr<2>(p, sms, st); break;
-    case 3: e = launch_wr<3>(p, sms, st); break;
-    default: e = launch_wr<4>(p, sms, st); break;
+  if ((m > 16 && blocks >= 2048) || (m > 8 && blocks >= 16384)) {
+    auto pass = [&](int r, int rows) {
+      Params q = p;
+      q.m = rows, q.x = x + int64_t(r) * n_in, q.y = static_cast<char*>(y) + int64_t(r) * n_out * (y_fp32 ? 4 : 2);
+      return tc::launch_tc<16>(q, sms, st);
+    };
+    if (m > 16) e = tc::launch_tc<32>(p, sms, st);
+    // more channels of 32 rows than a cluster holds: 16 rows at a time (4096 x 32768 68 us, the other form 100)
+    if (e == cudaErrorNotSupported) {
+      e = pass(0, std::min(m, 16));
+      if (e == cudaSuccess && m > 16) e = pass(16, m - 16);
+    }
   }
+  if (e == cudaErrorNotSupported) switch ((m + 7) / 8) {
+      case 1: e = launch_wr<1>(p, sms, st); break;
+      case 2: e = launch_wr<2>(p, sms, st); break;
+      case 3: e = launch_wr<3>(p, sms, st); break;
+      default: e = launch_wr<4>(p, sms, st); break;
+    }
   return e == cudaSuccess ? CSA2_OK : CSA2_ERR_CUDA;
 }

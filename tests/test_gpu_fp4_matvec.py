@@ -46,6 +46,8 @@ def _check(y, x, w, rs, what=""):
     # channels, ten token rows; and an x that no cluster holds
     (17, 2080, 4112), (24, 16500, 512), (20, 9001, 1024), (32, 1030, 8176), (18, 4100, 2320), (12, 8200, 8208),
     (32, 1000, 33008),
+    # clusters of eight, and two passes of 16 rows
+    (32, 1200, 12304), (16, 4200, 17008), (24, 1031, 16400), (17, 300, 32768),
 ])
 @pytest.mark.parametrize("fp32", [False, True])
 def test_matvec(M, N, K, fp32):
