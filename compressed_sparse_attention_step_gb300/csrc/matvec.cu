@@ -164,26 +164,38 @@ __global__ void __launch_bounds__(kThreads, TG <= 2 ? 2 : 1) matvec_kernel(const
   for (int c0 = kb0; c0 < kb1; c0 += p.stage_kb) {
     const int nk = min(p.stage_kb, kb1 - c0);
     if (c0 != kb0) __syncthreads();
-    // stage x: half a warp per (block, token), 8 channels a lane
-    for (int it = tid >> 4; it < nk * kTok; it += kThreads / 16) {
-      const int kb = it / kTok, tok = it - kb * kTok, j = lane & 15;
-      const int64_t ch = int64_t(c0 + kb) * kChan + 8 * j;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (tok < p.m && ch < p.n_in) v = __ldg(reinterpret_cast<const uint4*>(p.x + int64_t(tok) * p.n_in + ch));
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-      uint32_t am = 0;
+    // stage x: half a warp per (block, token), 8 channels a lane, four of them loaded together.  Rows past the last
+    // token are left as they are: they reach their own columns of the sums alone.
+    for (int it0 = tid >> 4; it0 < nk * p.m; it0 += 4 * (kThreads / 16)) {
+      const int j = tid & 15;
+      int kb[4], tok[4];
+      uint4 v[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) am = max(am, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
-      const unsigned half = 0xFFFFu << (lane & 16);
+      for (int e = 0; e < 4; ++e) {
+        const int it = it0 + e * (kThreads / 16);
+        kb[e] = it / p.m, tok[e] = it - kb[e] * p.m;
+        const int64_t ch = int64_t(c0 + kb[e]) * kChan + 8 * j;
+        v[e] = make_uint4(0, 0, 0, 0);
+        if (kb[e] < nk && ch < p.n_in) v[e] = __ldg(reinterpret_cast<const uint4*>(p.x + int64_t(tok[e]) * p.n_in + ch));
+      }
 #pragma unroll
-      for (int o = 8; o; o >>= 1) am = max(am, __shfl_xor_sync(half, am, o));
-      const int up = am ? min(max(141 - int(am >> 7), -126), 126) : 0;
-      const float f = __uint_as_float(uint32_t(127 + up) << 23);
-      uint32_t o[4];
+      for (int e = 0; e < 4; ++e) {
+        if (kb[e] >= nk) break;
+        const uint32_t w[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
+        uint32_t am = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = attn::h2_bits(__floats2half2_rn(bf16lo(w[i]) * f, bf16hi(w[i]) * f));
-      xs[((kb * TG + (tok >> 3)) * 4 + (j & 3)) * 32 + (tok & 7) * 4 + (j >> 2)] = make_uint4(o[0], o[1], o[2], o[3]);
-      if (j == 0) xf[kb * kTok + tok] = __uint_as_float(uint32_t(127 - up) << 23);
+        for (int i = 0; i < 4; ++i) am = max(am, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
+        const unsigned half = 0xFFFFu << (lane & 16);
+#pragma unroll
+        for (int o = 8; o; o >>= 1) am = max(am, __shfl_xor_sync(half, am, o));
+        const int up = am ? min(max(141 - int(am >> 7), -126), 126) : 0;
+        const float f = __uint_as_float(uint32_t(127 + up) << 23);
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = attn::h2_bits(__floats2half2_rn(bf16lo(w[i]) * f, bf16hi(w[i]) * f));
+        xs[((kb[e] * TG + (tok[e] >> 3)) * 4 + (j & 3)) * 32 + (tok[e] & 7) * 4 + (j >> 2)] = make_uint4(o[0], o[1], o[2], o[3]);
+        if (j == 0) xf[kb[e] * kTok + tok[e]] = __uint_as_float(uint32_t(127 - up) << 23);
+      }
     }
     __syncthreads();
     for (int kb = wk; kb < nk && done < n_blk; kb += WK, ++done) {
