@@ -180,17 +180,20 @@ __global__ void __launch_bounds__(256) append_kernel(const uint16_t* __restrict_
   }
 }
 
-// quantize_group in half as many instructions (the append below is bound by them), but for groups with a NaN: the
+// quantize_group in half as many instructions (the append below is bound by them; wv is overwritten): the
 // codes by the hardware conversion of x r, with r = fp32(1 / s).  x r is within 2^-23 of x / s, and x / s either is a
 // midpoint of two codes or differs from it by 2^-9 of its size (as above), so rounding x r to 13 significant bits
 // restores the midpoints, which have at most 3, and moves nothing across one.
-__device__ __forceinline__ void quantize_group_cvt(const uint32_t (&wv)[8], uint32_t& lo, uint32_t& hi, uint32_t& sb) {
+__device__ __forceinline__ void quantize_group_cvt(uint32_t (&wv)[8], uint32_t& lo, uint32_t& hi, uint32_t& sb) {
   auto bf2 = [](uint32_t u) { return *reinterpret_cast<const __nv_bfloat162*>(&u); };
   __nv_bfloat162 m2 = bf2(wv[0] & 0x7FFF7FFFu);
 #pragma unroll
   for (int i = 1; i < 8; ++i) m2 = __hmax2_nan(m2, bf2(wv[i] & 0x7FFF7FFFu));
   const uint32_t mm = *reinterpret_cast<const uint32_t*>(&m2), amax = max(mm & 0xFFFFu, mm >> 16);
-  if (amax > 0x7F80u) return quantize_group(wv, lo, hi, sb);
+  if (amax > 0x7F80u) {  // as there, a NaN is stored as a zero of its sign
+#pragma unroll
+    for (int i = 0; i < 8; ++i) wv[i] &= __heq2_mask(bf2(wv[i]), bf2(wv[i])) | 0x80008000u;
+  }
   sb = __nv_cvt_float_to_fp8(__fdiv_rn(__uint_as_float(amax << 16), 6.0f), __NV_SATFINITE, __NV_E4M3);
   const float s = e4m3_value(sb);
   lo = 0u;
@@ -219,11 +222,12 @@ __device__ __forceinline__ void quantize_group_cvt(const uint32_t (&wv)[8], uint
 // The paged append: a warp per new row, lane g quantising channels 16g .. 16g+15 into the row's slot and lanes
 // 0..15 copying 16 bytes of its indexer key.  HBM-bound: 65500 rows in 18.6 us, 17.1 us at the copy bandwidth (two
 // and four rows a warp 18.9 and 19.8).
+template <bool kWide>
 __global__ void __launch_bounds__(256) paged_append_kernel(const uint16_t* __restrict__ kv_new,
                                                            const uint16_t* __restrict__ ki_new,
                                                            const int32_t* __restrict__ slots, int64_t n,
                                                            uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
-                                                           uint16_t* __restrict__ KI, int64_t n_slots, bool wide,
+                                                           uint16_t* __restrict__ KI, int64_t n_slots,
                                                            unsigned int* flags) {
   pdl_wait();
   pdl_trigger();
@@ -235,7 +239,7 @@ __global__ void __launch_bounds__(256) paged_append_kernel(const uint16_t* __res
   uint4 key = make_uint4(0, 0, 0, 0);
   const int64_t at = __ldg(slots + row);
   const uint16_t* src = kv_new + row * CSA2_D + g * CSA2_GROUP;
-  if (kv_new && wide) {  // the rows start on 32 bytes
+  if (kWide && kv_new) {
     asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
                  : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
                  : "l"(src));
@@ -517,9 +521,10 @@ extern "C" csa2_status csa2_paged_append(const uint16_t* kv_new, const uint16_t*
   if (!slots || (reinterpret_cast<uintptr_t>(slots) & 3u)) return CSA2_ERR_INVALID_ARG;
   unsigned int* flags = csa2::device_flags_ptr();
   if (!flags) return CSA2_ERR_CUDA;
-  return csa2::launch_pdl(csa2::paged_append_kernel, dim3(csa2::grid_for(n * 32, 256)), dim3(256), 0,
+  auto kern = reinterpret_cast<uintptr_t>(kv_new) & 31u ? csa2::paged_append_kernel<false> : csa2::paged_append_kernel<true>;
+  return csa2::launch_pdl(kern, dim3(csa2::grid_for(n * 32, 256)), dim3(256), 0,
                           reinterpret_cast<cudaStream_t>(stream), kv_new, ki_new, slots, n, codes, scales, KI, n_slots,
-                          (reinterpret_cast<uintptr_t>(kv_new) & 31u) == 0, flags) == cudaSuccess
+                          flags) == cudaSuccess
              ? CSA2_OK
              : CSA2_ERR_CUDA;
 }
