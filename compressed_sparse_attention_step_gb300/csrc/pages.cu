@@ -312,9 +312,9 @@ extern "C" csa2_status csa2_block_tables(const int32_t* old_lens, const int32_t*
   unsigned int* flags = device_flags_ptr();
   const int sms = sm_count();
   if (!flags || sms <= 0) return CSA2_ERR_CUDA;
-  // a quad of slots or four pages a thread; how many pages change hands is known on the device alone (half of the
-  // table is taken for it)
-  const int64_t items = std::max(int64_t(B) * ((n_new + 3) / 4), int64_t(B) * max_pages / 8);
+  // a quad of slots or an entry of the tables a thread; how many pages change hands is known on the device alone.  64
+  // sequences x 512 pages, granted and given back: 13.6, 9.7, 7.7, 6.8 us with eight, four, two entries a thread and one
+  const int64_t items = std::max(int64_t(B) * ((n_new + 3) / 4), int64_t(B) * max_pages);
   const int grid = int(std::min<int64_t>(std::max<int64_t>(items / kThreads, 1), sms));
   const size_t smem = size_t(B) * 8;
   static std::atomic<uint64_t> done{0};
