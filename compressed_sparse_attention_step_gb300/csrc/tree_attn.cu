@@ -106,6 +106,7 @@ struct Params {
   float* lse;
   float scale_log2;  // softmax scale times log2 e
   int N, k, W;
+  int64_t row0;  // the launch's first node
   unsigned int* flags;
 };
 
@@ -263,10 +264,11 @@ __global__ void __launch_bounds__(kThreads, 3) tree_attn_kernel(const Params p) 
   constexpr bool kMerge = C > 1;
   extern __shared__ __align__(128) unsigned char smem_raw[];
   Shared& sm = *reinterpret_cast<Shared*>(smem_raw);
-  pdl_wait();
+  const bool tail = p.row0 != 0;  // a call's second launch: waits for the first at its end
+  if (!tail) pdl_wait();
   pdl_trigger();
   const int rank = kMerge ? int(blockIdx.x % C) : 0;
-  const int64_t row = kMerge ? int64_t(blockIdx.x / C) : int64_t(blockIdx.x);
+  const int64_t row = p.row0 + (kMerge ? int64_t(blockIdx.x / C) : int64_t(blockIdx.x));
   const int b = int(row / p.N), node = int(row - int64_t(b) * p.N);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   // everything that the row lists need is asked for at once
@@ -278,7 +280,10 @@ __global__ void __launch_bounds__(kThreads, 3) tree_attn_kernel(const Params p) 
 #pragma unroll
     for (int j = 0; j < kMaxSel / 32; ++j) ids[j] = 32 * j + lane < p.k ? __ldg(p.idx + row * p.k + 32 * j + lane) : -1;
   }
-  if (node >= nodes) return;  // the whole cluster: its outputs stay as they were
+  if (node >= nodes) {  // the whole cluster: its outputs stay as they were
+    if (tail) pdl_wait();
+    return;
+  }
   const int chan = warp * 128 + t * 32;  // this lane's 32 channels
 
   // Q of heads g and g + 8, as bf16 pairs
@@ -506,6 +511,7 @@ __global__ void __launch_bounds__(kThreads, 3) tree_attn_kernel(const Params p) 
       if (p.lse && warp == 0 && t == 0)
         p.lse[row * CSA2_H + g + 8 * h] = any ? (m[h] + log2f(l[h])) * attn::kLn2 : kNegInf;
     }
+    if (tail) pdl_wait();
     return;
   }
   if constexpr (kMerge) {
@@ -558,6 +564,7 @@ __global__ void __launch_bounds__(kThreads, 3) tree_attn_kernel(const Params p) 
       *reinterpret_cast<uint2*>(orow + hd * CSA2_D + 4 * tid) = make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
     }
     cluster_arrive_wait();  // no CTA leaves while its part is being read
+    if (tail) pdl_wait();
   }
 }
 
@@ -610,18 +617,33 @@ extern "C" csa2_status csa2_tree_attn(const uint16_t* q, int B, int N, const int
   p.cap = cap, p.seq_rows = shared_pool ? 0 : cap;
   p.idx = idx, p.n_valid = n_valid, p.swa = swa, p.win_len = win_len, p.out = out, p.lse = lse;
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
-  p.N = N, p.k = k, p.W = W, p.flags = flags;
+  p.N = N, p.k = k, p.W = W, p.row0 = 0, p.flags = flags;
   // Few nodes are shared by several CTAs each, which costs a merge.  Measured with 512 selected and 128 window
   // rows, us for 1 / 2 / 4 / 8 CTAs a node: 5 nodes 24.2 / 17.9 / 11.8 / 9.7, 38 nodes 24.4 / 18.0 / 14.2 / 15.0,
   // 91 nodes 24.6 / 21.8 / 18.1 / 28.4, 152 nodes 24.9 / 27.1 / 33.1 / 42.6; with 64 selected rows, 91 nodes
   // 10.9 / 11.5 / 12.1 / 22.
-  const int C = rows * 8 <= sms ? 8 : rows * 4 <= sms || (rows * 8 <= 5 * int64_t(sms) && k >= 256) ? 4 : 1;
+  auto ctas = [&](int64_t r) { return r * 8 <= sms ? 8 : r * 4 <= sms || (r * 8 <= 5 * int64_t(sms) && k >= 256) ? 4 : 1; };
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  auto launch = [&](int64_t row0, int64_t r) {
+    p.row0 = row0;
+    switch (ctas(r)) {
+      case 1: return tree::launch<1>(p, r, st);
+      case 4: return tree::launch<4>(p, r, st);
+      default: return tree::launch<8>(p, r, st);
+    }
+  };
+  // Three nodes an SM run at once.  A few nodes behind the last full wave would take as long as a whole one: they are
+  // shared by several CTAs each, in a second launch whose CTAs start as the first's leave.  It reads nothing that the
+  // first writes and starts behind all of the first's waits for what came before; it waits for the first at its end,
+  // so that whoever waits for it waits for both.  (58 x 8 nodes 57.8 -> 44.3 us, 64 x 8 58.4 -> 50.9, 68 x 8 58.6 ->
+  // 54.5, 120 x 8 95.0 -> 87.3.)
+  const int64_t wave = 3 * int64_t(sms), rest = rows % wave;
   cudaError_t e;
-  switch (C) {
-    case 1: e = tree::launch<1>(p, rows, st); break;
-    case 4: e = tree::launch<4>(p, rows, st); break;
-    default: e = tree::launch<8>(p, rows, st); break;
+  if (rows > wave && rest > 0 && ctas(rest) > 1) {
+    e = launch(0, rows - rest);
+    if (e == cudaSuccess) e = launch(rows - rest, rest);
+  } else {
+    e = launch(0, rows);
   }
   return e == cudaSuccess ? CSA2_OK : CSA2_ERR_CUDA;
 }

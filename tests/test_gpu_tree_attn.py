@@ -299,3 +299,49 @@ def test_tree_attn_in_place_and_an_empty_pool():
         assert c.csa2_device_flags() == 0 and torch.equal(none, some)
         c.csa2_tree_attn(q, parent, codes[:0], scales[:0], idx, none, swa=swa, W=8)
         assert c.csa2_device_flags() == c.FLAG_INDEX_OOB and torch.equal(none, some)
+
+
+SMS = torch.cuda.get_device_properties(0).multi_processor_count
+
+
+@pytest.mark.parametrize("rest,N,k", [(1, 1, 12), (19, 1, 20), (38, 2, 9), (40, 4, 260), (94, 2, 256), (100, 4, 30)])
+def test_a_few_nodes_behind_the_last_full_wave(rest, N, k):
+    """Just more nodes than run at once: the last ones go to a second launch."""
+    B = -(-(3 * SMS + rest) // N)
+    cs = Case(rest, B, N, k + 5, k, 7)
+    d = cs.dev()
+    c.csa2_tree_attn(**d)
+    cs.check(d)
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_two_launches_are_one_to_what_comes_next(captured):
+    """Each call's queries are the last call's outputs, with nothing between the calls, eager and captured: the
+    same bits as with a synchronisation after each."""
+    B, N = -(-(3 * SMS + 20) // 4), 4
+    cs = Case(21, B, N, 60, 48, 9, full=True)
+    d = cs.dev()
+    del d["out"]
+    a, b, keep = (torch.empty_like(d["q"]) for _ in range(3))
+    x = d.pop("q")
+
+    def chain(sync):
+        src = x
+        for i in range(6):
+            dst = (a, b)[i & 1]
+            c.csa2_tree_attn(q=src, out=dst, **d, softmax_scale=4.0)
+            if sync:
+                torch.cuda.synchronize()
+            src = dst
+        return src
+    keep.copy_(chain(True))
+    assert torch.isfinite(keep.float()).all() and not torch.equal(keep, x)
+    run = lambda: chain(False)  # noqa: E731
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run()
+        run = lambda: graph.replay() or b  # noqa: E731
+    for _ in range(20):
+        a.fill_(3.0), b.fill_(5.0)
+        assert torch.equal(run(), keep)
