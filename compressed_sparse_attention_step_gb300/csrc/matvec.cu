@@ -85,10 +85,16 @@ __global__ void __launch_bounds__(256) pack_kernel(const uint8_t* __restrict__ c
   *reinterpret_cast<uint2*>(dst + kCodeBytes + lane * 8) = make_uint2(sb[0], sb[1]);
 }
 
+// (A warp that comes to an aligned barrier in two parts is counted twice, and others pass before it has arrived: the
+// lanes are brought together first.)
 __device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");
 }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
 __device__ __forceinline__ void cluster_arrive_wait() { cluster_arrive(), cluster_wait(); }
 __device__ __forceinline__ uint32_t cluster_addr(uint32_t a, uint32_t rank) {
   uint32_t r;
@@ -197,6 +203,9 @@ __global__ void __launch_bounds__(kThreads, TG <= 2 ? 2 : 1) matvec_kernel(const
         if (j == 0) xf[kb[e] * kTok + tok[e]] = __uint_as_float(uint32_t(127 - up) << 23);
       }
     }
+    // Every CTA of the cluster has started.  All warps are past this wait before one comes to the next arrival: a warp
+    // that was still to wait would count as arrived there.
+    if (C > 1 && c0 == kb0) cluster_wait();
     __syncthreads();
     for (int kb = wk; kb < nk && done < n_blk; kb += WK, ++done) {
       if (!late && !bar_wait(smem_u32(&full[warp][slot]), uint32_t(use) & 1u)) {
@@ -272,7 +281,6 @@ __global__ void __launch_bounds__(kThreads, TG <= 2 ? 2 : 1) matvec_kernel(const
   // Each partial sum goes to the CTA of the cluster that finishes its row, rank row / (kCtaRows / C), which adds them
   // up in order of rank and warp.  acc[r][j]: rows g (0, 1) and g + 8 (2, 3) of half r, tokens 8j + 2t and + 1.
   const int rows = kCtaRows / C;
-  if (C > 1) cluster_wait();  // every CTA of the cluster has started
   const uint32_t red_a = smem_u32(red) + 4u * uint32_t((rank * WK + wk) * kTok * rows);
 #pragma unroll
   for (int r = 0; r < 2; ++r)
@@ -596,6 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_tc_kernel(const Params p) 
         if (++slot == kSlots) slot = 0, ++slot_use;
       }
       if (use > 0) wait(&sm.a_empty[buf], use - 1);
+      __syncwarp();
       attn::tc_fence_after();
       if (rb < rb1) {
 #pragma unroll
@@ -632,6 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_tc_kernel(const Params p) 
       // the step's sums: this CTA's share of the channels, then the cluster's
       const int rb = rb0 + step * kStep, nb = min(kStep, rb1 - rb);
       wait(&sm.d_full, uint32_t(step));
+      __syncwarp();
       attn::tc_fence_after();
       float sum[kTok];
 #pragma unroll
@@ -662,6 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_tc_kernel(const Params p) 
 #pragma unroll
       for (int i = 0; i < kTok; ++i)
         if (i < p.m) sm.red[i][32 * q + lane] = sum[i] * sm.inv[i];
+      __syncwarp();
       asm volatile("bar.sync 1, 128;\n" ::: "memory");  // warps 16 .. 19
       const int t = tid & 127;
       if (t < C) mbar_arrive_cluster(&sm.red_full, uint32_t(t));
@@ -691,6 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_tc_kernel(const Params p) 
           else static_cast<__nv_bfloat16*>(p.y)[int64_t(tok) * p.n_out + n + i] = __float2bfloat16_rn(s);
         }
       }
+      __syncwarp();
       asm volatile("bar.sync 1, 128;\n" ::: "memory");
       if (t < C) mbar_arrive_cluster(&sm.red_empty, uint32_t(t));
     }

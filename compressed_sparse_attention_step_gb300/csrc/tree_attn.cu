@@ -238,6 +238,7 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
 }
 
 __device__ __forceinline__ void cluster_arrive_wait() {
+  __syncwarp();  // an aligned barrier counts a warp that comes in two parts twice
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
 }
 __device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
@@ -414,6 +415,7 @@ __global__ void __launch_bounds__(kThreads, 3) tree_attn_kernel(const Params p) 
       late = true;
       atomicOr(p.flags, CSA2_FLAG_TIMEOUT);
     }
+    __syncwarp();  // (the lanes' waits end one by one)
   };
 
   State st;

@@ -162,3 +162,19 @@ def test_two_calls_at_once():
     for x, packed, y, xb, w, _ in jobs:
         _check(y, V.f64(xb), w, np.ones(y.shape[1]))
     assert c.csa2_device_flags() == 0
+
+
+@pytest.mark.parametrize("M,N,K", [(19, 28, 6240), (9, 35, 3568), (20, 9, 3792), (5, 64, 2048), (12, 100, 1040),
+                                   (32, 512, 4096), (16, 300, 8192), (24, 4100, 4112)])
+def test_calls_behind_one_another(M, N, K):
+    """Clusters that exchange partial sums, call upon call with nothing between: each gives the first one's bits."""
+    g = np.random.default_rng(M + N)
+    packed, w = _weight(g, N, K)
+    xb = V.bf16(g, (M, K))
+    x = bf16_dev(xb)
+    buf = torch.full((100, -(-M * N // 4) * 4), 7.0, dtype=torch.float32, device="cuda")      # each starts on 16 bytes
+    ys = [b[:M * N].view(M, N) for b in buf]
+    for y in ys:
+        c.csa2_fp4_matvec(x, packed, y)
+    _check(ys[0], V.f64(xb), w, np.ones(N))
+    assert torch.equal(buf, buf[:1].expand_as(buf))
