@@ -638,10 +638,11 @@ extern "C" csa2_status csa2_tree_attn(const uint16_t* q, int B, int N, const int
   // shared by several CTAs each, in a second launch whose CTAs start as the first's leave.  It reads nothing that the
   // first writes and starts behind all of the first's waits for what came before; it waits for the first at its end,
   // so that whoever waits for it waits for both.  (58 x 8 nodes 57.8 -> 44.3 us, 64 x 8 58.4 -> 50.9, 68 x 8 58.6 ->
-  // 54.5, 120 x 8 95.0 -> 87.3.)
+  // 54.5, 120 x 8 95.0 -> 87.3.)  Not with n_nodes: of 64 x 8 nodes, 437 to 496 real ones took 46.3 us in one launch on
+  // average and 48.0 in two.
   const int64_t wave = 3 * int64_t(sms), rest = rows % wave;
   cudaError_t e;
-  if (rows > wave && rest > 0 && ctas(rest) > 1) {
+  if (!n_nodes && rows > wave && rest > 0 && ctas(rest) > 1) {
     e = launch(0, rows - rest);
     if (e == cudaSuccess) e = launch(rows - rest, rest);
   } else {

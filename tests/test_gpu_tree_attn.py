@@ -309,7 +309,9 @@ def test_a_few_nodes_behind_the_last_full_wave(rest, N, k):
     """Just more nodes than run at once: the last ones go to a second launch."""
     B = -(-(3 * SMS + rest) // N)
     cs = Case(rest, B, N, k + 5, k, 7)
+    cs.n_nodes[:] = N
     d = cs.dev()
+    d["n_nodes"] = None
     c.csa2_tree_attn(**d)
     cs.check(d)
 
@@ -321,7 +323,7 @@ def test_two_launches_are_one_to_what_comes_next(captured):
     B, N = -(-(3 * SMS + 20) // 4), 4
     cs = Case(21, B, N, 60, 48, 9, full=True)
     d = cs.dev()
-    del d["out"]
+    del d["out"], d["n_nodes"]
     a, b, keep = (torch.empty_like(d["q"]) for _ in range(3))
     x = d.pop("q")
 
