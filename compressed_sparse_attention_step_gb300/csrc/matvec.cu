@@ -19,6 +19,16 @@
 // memory, so that a weight element costs one conversion and one multiplication and no pass through shared memory,
 // and the token rows (N = 16 or 32) cost the warps nothing.  matvec_kernel: mma.m16n8k16 from registers, with
 // less to set up.
+//
+// Measured (us, weights from HBM; in brackets at the copy bandwidth): one row x 512 x 4096 3.9 (0.17), 4096 x 4096
+// 6.2 (1.4), 16384 x 8192 17.1 (11.1), 32768 x 16384 54 (44.4); eight rows 4.2, 6.9, 19.6, 64; 32 rows x 16384 x 8192
+// 28 (26.7 with the weight partly in L2), 32768 x 16384 93.
+// What bounds matvec_kernel: 4 us of launch, staging and exchange, behind which the copies alone take as long as the
+// products alone (16384 x 8192, eight rows: 17.8 and 17.7 with those 4; more blocks under way, more CTAs or even shares
+// of the rows gain nothing).  matvec_tc_kernel: 6 us before the first product (x, 128 KB a CTA), then about 560 cycles
+// per 128 x 128 block, of which the copies need 390, a dequantising group 380 and the issuing threads 380, coupled by
+// the six tensor-memory buffers between them.  Copies of four blocks by warps of their own gained nothing (24.6 for 16
+// rows, 29.6 for 32, whose staging then spills).
 #include <cuda_bf16.h>
 
 #include <algorithm>

@@ -19,7 +19,7 @@
 // slots of each scheduler and as many cycles of the shared-memory pipe (128 of them transposes), and takes a CTA
 // 1000 cycles from end to end alone.  Three CTAs an SM (their registers) give 560 cycles a step: no pipe is
 // full, the chain of a step is.  64 sequences x 32 nodes, 512 selected and 128 window rows: 166 us on the device,
-// 0.17 of the bf16 peak over the plain count of operations; 64 x 8 nodes 56 us.  Measured and not kept: rows
+// 0.17 of the bf16 peak over the plain count of operations; 64 x 8 nodes 54 us.  Measured and not kept: rows
 // dequantised a second time for P V instead of transposed (181 us), Q in shared memory (205), steps of
 // 32 rows (179), a pipeline of three steps with two CTAs an SM (190), plain loads one step ahead (223), bulk
 // copies per row (307).
