@@ -234,6 +234,7 @@ __global__ void __launch_bounds__(kThreads, TG <= 2 ? 2 : 1) matvec_kernel(const
             u0.s[r][h] = *reinterpret_cast<const uint16_t*>(blk + kCodeBytes + row * 8 + 2 * t);
           }
       }
+      attn::fence_async_smem();  // what the lanes have read comes before what the copy writes
       __syncwarp();
       if (lane == 0 && !late && done + kSlots < n_blk)
         block_copy(ring + slot * kBlock, src + int64_t(done + kSlots) * WK * kBlock, &full[warp][slot]);
@@ -609,6 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_tc_kernel(const Params p) 
 #pragma unroll
         for (int j = 0; j < 4; ++j) r.c[j] = *reinterpret_cast<const uint4*>(blk + block_place(lane, j));
         r.s = *reinterpret_cast<const uint2*>(blk + kCodeBytes + 8 * lane);
+        attn::fence_async_smem();  // what the lanes have read comes before what the copy writes
         __syncwarp();
         if (lane == 0) copy(slot);
         if (++slot == kSlots) slot = 0, ++slot_use;

@@ -165,7 +165,9 @@ def test_two_calls_at_once():
 
 
 @pytest.mark.parametrize("M,N,K", [(19, 28, 6240), (9, 35, 3568), (20, 9, 3792), (5, 64, 2048), (12, 100, 1040),
-                                   (32, 512, 4096), (16, 300, 8192), (24, 4100, 4112)])
+                                   (32, 512, 4096), (16, 300, 8192), (24, 4100, 4112),
+                                   # many blocks a warp: slots of its ring are refilled behind their reads
+                                   (32, 1030, 8176), (32, 2048, 8192), (8, 1030, 16384), (2, 40, 32768)])
 def test_calls_behind_one_another(M, N, K):
     """Clusters that exchange partial sums, call upon call with nothing between: each gives the first one's bits."""
     g = np.random.default_rng(M + N)
