@@ -281,9 +281,11 @@ __global__ void __launch_bounds__(kThreads, 3) tree_attn_kernel(const Params p) 
 #pragma unroll
     for (int j = 0; j < kMaxSel / 32; ++j) ids[j] = 32 * j + lane < p.k ? __ldg(p.idx + row * p.k + 32 * j + lane) : -1;
   }
-  if (node >= nodes) {  // the whole cluster: its outputs stay as they were
-    if (tail) pdl_wait();
-    return;
+  int up0 = -1, up1 = -1, wl = p.W - 1;
+  if (warp == 1) {
+    if (lane < p.N) up0 = __ldg(p.parent + int64_t(b) * p.N + lane);
+    if (lane + 32 < p.N) up1 = __ldg(p.parent + int64_t(b) * p.N + lane + 32);
+    if (p.win_len) wl = __ldg(p.win_len + b);
   }
   const int chan = warp * 128 + t * 32;  // this lane's 32 channels
 
@@ -298,6 +300,10 @@ __global__ void __launch_bounds__(kThreads, 3) tree_attn_kernel(const Params p) 
       const uint4 v = __ldg(reinterpret_cast<const uint4*>(qrow + (g + 8 * h) * CSA2_D) + (i ^ (t >> 1)));
       qf[h][4 * i] = v.x, qf[h][4 * i + 1] = v.y, qf[h][4 * i + 2] = v.z, qf[h][4 * i + 3] = v.w;
     }
+  if (node >= nodes) {  // the whole cluster: its outputs stay as they were
+    if (tail) pdl_wait();
+    return;
+  }
   if (tid == 0) {
     for (int j = 0; j < kSelSlots; ++j)
       asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(smem_u32(&sm.sel_full[j])), "n"(kThreads) : "memory");
@@ -325,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 3) tree_attn_kernel(const Params p) 
     }
     if (lane == 0) sm.n_sel = n;
   } else if (warp == 1) {
-    for (int i = lane; i < p.N; i += 32) sm.parent[i] = p.parent[int64_t(b) * p.N + i];
+    sm.parent[lane] = up0, sm.parent[lane + 32] = up1;
     __syncwarp();
     // ancestors of the node, itself included
     uint64_t anc = 0;
@@ -343,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 3) tree_attn_kernel(const Params p) 
     // the committed rows [first, W - 1), then the ancestors less than W tokens away
     int nw = 0;
     if (p.W > 0) {
-      const int wl = min(max(p.win_len ? p.win_len[b] : p.W - 1, 0), p.W - 1);
+      wl = min(max(wl, 0), p.W - 1);
       const int first = max(depth, p.W - 1 - wl), n_com = max(p.W - 1 - first, 0);
       const int drop = max(depth + 1 - p.W, 0);  // the bits of anc ascend with the depth
       for (int i = 0; i < drop; ++i) anc &= anc - 1;
