@@ -18,11 +18,13 @@
 // What bounds it.  A step of 16 rows needs 256 cycles of an SM's tensor pipe (2.0 an instruction), about 290 issue
 // slots of each scheduler and as many cycles of the shared-memory pipe (128 of them transposes), and takes a CTA
 // 1000 cycles from end to end alone.  Three CTAs an SM (their registers) give 560 cycles a step: no pipe is
-// full, the chain of a step is.  64 sequences x 32 nodes, 512 selected and 128 window rows: 166 us on the device,
-// 0.17 of the bf16 peak over the plain count of operations; 64 x 8 nodes 54 us.  Measured and not kept: rows
+// full, the chain of a step is.  64 sequences x 32 nodes, 512 selected and 128 window rows: 162 us on the device,
+// 0.17 of the bf16 peak over the plain count of operations; 64 x 8 nodes 53 us.  Measured and not kept: rows
 // dequantised a second time for P V instead of transposed (181 us), Q in shared memory (205), steps of
 // 32 rows (179), a pipeline of three steps with two CTAs an SM (190), plain loads one step ahead (223), bulk
-// copies per row (307).
+// copies per row (307).  One sequence of five nodes, eight CTAs a node, 9.0 us: 4100 cycles until the lists stand, 1400
+// until the first rows do, 5000 for six steps, 5800 for the merge and its two barriers (parts pushed to the CTA that
+// finishes a head 10.2 us, 16 CTAs a node 8.9 and with nine nodes 10.5 instead of 9.3).
 //
 // FP4 rows are multiplied as f16: a code times a scale has at most 6 significant bits and lies between
 // 2^-10 and 2688, so the row is exact.  Q is scaled per head by a power of two that puts its largest
