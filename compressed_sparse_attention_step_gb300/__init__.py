@@ -11,6 +11,7 @@ bf16 tensors may be torch.bfloat16 or torch.int16/uint16 bit patterns.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 from . import _build
@@ -473,14 +474,16 @@ def _dims(t, name, n):
     return shape
 
 
-def _call_context():
-    """(check, current device, types): check(t, name, dtypes, shape) returns t's data pointer, or None for None,
-    where t is contiguous, of one of the types and that shape, and on the current device; types are the
-    accepted int32, uint8, fp32 and bf16 types."""
-    global _context
+_context = None  # (current device's number, current stream's handle on a device)
+_I32 = _U8 = _F32 = _BF16 = ()
+
+
+def _device():
+    """The current device's number."""
+    global _context, _I32, _U8, _F32, _BF16
     if _context is None:
         torch = _torch()
-        types = ((torch.int32,), (torch.uint8,), (torch.float32,), _bf16_types())
+        _I32, _U8, _F32, _BF16 = (torch.int32,), (torch.uint8,), (torch.float32,), _bf16_types()
         get_device = getattr(torch._C, "_cuda_getDevice", None)
         if get_device is None or not torch.cuda.is_available():
             get_device = lambda: torch.cuda.current_device() if torch.cuda.is_available() else 0  # noqa: E731
@@ -489,24 +492,21 @@ def _call_context():
             raw_stream = lambda dev: torch.cuda.current_stream(dev).cuda_stream  # noqa: E731
         else:
             torch.cuda.init() if torch.cuda.is_available() else None
-        _context = (get_device, raw_stream, types)
-    get_device, raw_stream, types = _context
-    dev = get_device()
-
-    def check(t, name, dtypes, shape):
-        if t is None:
-            return None
-        try:
-            if t.dtype in dtypes and t.shape == shape and t.get_device() == dev and t.is_contiguous():
-                return t.data_ptr()
-        except AttributeError:
-            pass
-        _refuse(t, name, dtypes, shape, dev)
-
-    return check, dev, types
+        _context = (get_device, raw_stream)
+    return _context[0]()
 
 
-_context = None
+def _arg(t, name, dtypes, shape, dev):
+    """t's data pointer, or None for None, where t is contiguous, of one of the types and that shape, and on the
+    current device dev."""
+    if t is None:
+        return None
+    try:
+        if t.dtype in dtypes and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, name, dtypes, shape, dev)
 
 
 def _on(stream, dev):
@@ -519,15 +519,15 @@ def csa2_block_tables(old_lens, new_lens, page_size, block_table, free_pages, po
     shrink: block_table int32 [B, max_pages], free_pages int32 [free_cap], pool_state int32 [4] (the first
     holds the number of free pages), granted int32 [B] the lengths in effect, slots int32 [B, n_new] the
     slots of positions old_lens[b] + i (-1 from granted[b] on)."""
-    check, dev, (i32, _, _, _) = _call_context()
+    dev = _device()
     B, max_pages = _dims(block_table, "block_table", 2)
     free_cap, = _dims(free_pages, "free_pages", 1)
     n_new = _dims(slots, "slots", 2)[1] if slots is not None else 0
     st = lib().csa2_block_tables(
-        check(old_lens, "old_lens", i32, (B,)), check(new_lens, "new_lens", i32, (B,)), B, page_size,
-        check(block_table, "block_table", i32, (B, max_pages)), max_pages,
-        check(free_pages, "free_pages", i32, (free_cap,)), free_cap, check(pool_state, "pool_state", i32, (4,)),
-        check(granted, "granted", i32, (B,)), check(slots, "slots", i32, (B, n_new)), n_new, _on(stream, dev))
+        _arg(old_lens, "old_lens", _I32, (B,), dev), _arg(new_lens, "new_lens", _I32, (B,), dev), B, page_size,
+        _arg(block_table, "block_table", _I32, (B, max_pages), dev), max_pages,
+        _arg(free_pages, "free_pages", _I32, (free_cap,), dev), free_cap, _arg(pool_state, "pool_state", _I32, (4,), dev),
+        _arg(granted, "granted", _I32, (B,), dev), _arg(slots, "slots", _I32, (B, n_new), dev), n_new, _on(stream, dev))
     if st:
         _check("csa2_block_tables", st)
 
@@ -536,15 +536,16 @@ def csa2_context_slots(lens, slots, n_slots, *, block_table=None, page_size=0, p
     """slots int32 [B*N, ld]: per drafted node the slots of its sequence's lens[b] committed positions, then of
     its ancestors and itself, then -1; n_slots int32 [B*N] their number.  parent int32 [B, N] (None: the
     committed positions only); block_table int32 [B, max_pages] (None: positions instead of slots)."""
-    check, dev, (i32, _, _, _) = _call_context()
+    dev = _device()
     B, = _dims(lens, "lens", 1)
     rows, ld = _dims(slots, "slots", 2)
     N = _dims(parent, "parent", 2)[1] if parent is not None else (rows // B if B else 0)
     max_pages = _dims(block_table, "block_table", 2)[1] if block_table is not None else 0
     st = lib().csa2_context_slots(
-        check(lens, "lens", i32, (B,)), check(parent, "parent", i32, (B, N)), check(n_nodes, "n_nodes", i32, (B,)), B, N,
-        check(block_table, "block_table", i32, (B, max_pages)), max_pages, page_size,
-        check(slots, "slots", i32, (B * N, ld)), ld, check(n_slots, "n_slots", i32, (B * N,)), _on(stream, dev))
+        _arg(lens, "lens", _I32, (B,), dev), _arg(parent, "parent", _I32, (B, N), dev),
+        _arg(n_nodes, "n_nodes", _I32, (B,), dev), B, N,
+        _arg(block_table, "block_table", _I32, (B, max_pages), dev), max_pages, page_size,
+        _arg(slots, "slots", _I32, (B * N, ld), dev), ld, _arg(n_slots, "n_slots", _I32, (B * N,), dev), _on(stream, dev))
     if st:
         _check("csa2_context_slots", st)
 
@@ -553,14 +554,15 @@ def csa2_paged_append(slots, *, kv_new=None, codes=None, scales=None, ki_new=Non
     """Row i of kv_new bf16 [n, 512] is quantised into row slots[i] of codes uint8 [n_slots, 256] and scales
     uint8 [n_slots, 32], row i of ki_new bf16 [n, 128] copied to row slots[i] of KI bf16 [n_slots, 128];
     slots int32 [n], negative ones are padding.  Either pair may be left out."""
-    check, dev, (i32, u8, _, bf) = _call_context()
+    dev = _device()
     n, = _dims(slots, "slots", 1)
     pool, name = (codes, "codes") if codes is not None else (KI, "KI")
     n_slots = _dims(pool, name, 2)[0] if pool is not None else 0
     st = lib().csa2_paged_append(
-        check(kv_new, "kv_new", bf, (n, D)), check(ki_new, "ki_new", bf, (n, DI)), check(slots, "slots", i32, (n,)), n,
-        check(codes, "codes", u8, (n_slots, CODE_BYTES)), check(scales, "scales", u8, (n_slots, SCALE_BYTES)),
-        check(KI, "KI", bf, (n_slots, DI)), n_slots, _on(stream, dev))
+        _arg(kv_new, "kv_new", _BF16, (n, D), dev), _arg(ki_new, "ki_new", _BF16, (n, DI), dev),
+        _arg(slots, "slots", _I32, (n,), dev), n,
+        _arg(codes, "codes", _U8, (n_slots, CODE_BYTES), dev), _arg(scales, "scales", _U8, (n_slots, SCALE_BYTES), dev),
+        _arg(KI, "KI", _BF16, (n_slots, DI), dev), n_slots, _on(stream, dev))
     if st:
         _check("csa2_paged_append", st)
 
@@ -571,7 +573,7 @@ def csa2_tree_attn(q, parent, codes, scales, idx, out, *, n_nodes=None, n_valid=
     [B, cap, *], or [cap, *] for one pool shared by all sequences; idx int32 [B*N, k] cache rows;
     swa [B, W-1+N, 512] (the committed window, then the drafted rows; None: no window); out as q,
     lse fp32 [B, N, 16]."""
-    check, dev, (i32, u8, f32, bf) = _call_context()
+    dev = _device()
     B, N = _dims(q, "q", 4)[:2]
     if not hasattr(codes, "shape"):
         raise TypeError("codes: expected a torch.Tensor")
@@ -584,16 +586,18 @@ def csa2_tree_attn(q, parent, codes, scales, idx, out, *, n_nodes=None, n_valid=
         W = 0
     rows = (B, N, H, D)
     st = lib().csa2_tree_attn(
-        check(q, "q", bf, rows), B, N, check(parent, "parent", i32, (B, N)), check(n_nodes, "n_nodes", i32, (B,)),
-        check(codes, "codes", u8, lead + (CODE_BYTES,)), check(scales, "scales", u8, lead + (SCALE_BYTES,)), lead[-1], pool,
-        check(idx, "idx", i32, (B * N, k)), check(n_valid, "n_valid", i32, (B * N,)), k,
-        check(swa, "swa", bf, (B, W - 1 + N, D)), check(win_len, "win_len", i32, (B,)), W,
-        D ** -0.5 if softmax_scale is None else softmax_scale, check(out, "out", bf, rows),
-        check(lse, "lse", f32, (B, N, H)), _on(stream, dev))
+        _arg(q, "q", _BF16, rows, dev), B, N, _arg(parent, "parent", _I32, (B, N), dev),
+        _arg(n_nodes, "n_nodes", _I32, (B,), dev), _arg(codes, "codes", _U8, lead + (CODE_BYTES,), dev),
+        _arg(scales, "scales", _U8, lead + (SCALE_BYTES,), dev), lead[-1], pool,
+        _arg(idx, "idx", _I32, (B * N, k), dev), _arg(n_valid, "n_valid", _I32, (B * N,), dev), k,
+        _arg(swa, "swa", _BF16, (B, W - 1 + N, D), dev), _arg(win_len, "win_len", _I32, (B,), dev), W,
+        D ** -0.5 if softmax_scale is None else softmax_scale, _arg(out, "out", _BF16, rows, dev),
+        _arg(lse, "lse", _F32, (B, N, H), dev), _on(stream, dev))
     if st:
         _check("csa2_tree_attn", st)
 
 
+@functools.lru_cache(maxsize=256)
 def _packed_bytes(n_out, n_in):
     if n_in % GROUP:
         raise ValueError(f"expected a multiple of {GROUP} input channels, got {n_in}")
@@ -607,26 +611,26 @@ def fp4_weight_alloc(n_out, n_in, device="cuda"):
 
 def csa2_fp4_pack_weight(codes, scales, packed, stream=None):
     """Lays codes uint8 [n_out, n_in/2] and scales uint8 [n_out, n_in/16] out for csa2_fp4_matvec."""
-    check, dev, (_, u8, _, _) = _call_context()
+    dev = _device()
     n_out, half = _dims(codes, "codes", 2)
     n_in = 2 * half
     nbytes = _packed_bytes(n_out, n_in)
     st = lib().csa2_fp4_pack_weight(
-        check(codes, "codes", u8, (n_out, half)), check(scales, "scales", u8, (n_out, n_in // GROUP)), n_out, n_in,
-        check(packed, "packed", u8, (nbytes,)), _on(stream, dev))
+        _arg(codes, "codes", _U8, (n_out, half), dev), _arg(scales, "scales", _U8, (n_out, n_in // GROUP), dev), n_out, n_in,
+        _arg(packed, "packed", _U8, (nbytes,), dev), _on(stream, dev))
     if st:
         _check("csa2_fp4_pack_weight", st)
 
 
 def csa2_fp4_matvec(x, packed, y, *, row_scale=None, stream=None):
     """y [m, n_out] (bf16 or fp32) = row_scale * (x bf16 [m, n_in] times the packed weight), m <= 32."""
-    check, dev, (_, u8, f32, bf) = _call_context()
+    dev = _device()
     m, n_in = _dims(x, "x", 2)
     n_out = _dims(y, "y", 2)[1]
-    fp32 = y.dtype in f32
+    fp32 = y.dtype in _F32
     st = lib().csa2_fp4_matvec(
-        check(x, "x", bf, (m, n_in)), m, check(packed, "packed", u8, (_packed_bytes(n_out, n_in),)), n_out, n_in,
-        check(row_scale, "row_scale", f32, (n_out,)), check(y, "y", f32 if fp32 else bf, (m, n_out)), fp32,
+        _arg(x, "x", _BF16, (m, n_in), dev), m, _arg(packed, "packed", _U8, (_packed_bytes(n_out, n_in),), dev), n_out, n_in,
+        _arg(row_scale, "row_scale", _F32, (n_out,), dev), _arg(y, "y", _F32 if fp32 else _BF16, (m, n_out), dev), fp32,
         _on(stream, dev))
     if st:
         _check("csa2_fp4_matvec", st)
