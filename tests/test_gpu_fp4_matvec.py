@@ -180,3 +180,21 @@ def test_calls_behind_one_another(M, N, K):
         c.csa2_fp4_matvec(x, packed, y)
     _check(ys[0], V.f64(xb), w, np.ones(N))
     assert torch.equal(buf, buf[:1].expand_as(buf))
+
+
+@pytest.mark.parametrize("M", [2, 32])
+def test_a_weight_of_more_than_4_gb(M):
+    """The last rows of a weight whose blocks lie past 32 bits; all others are zero."""
+    N, K, last = 1_000_100, 8192, 70
+    g = np.random.default_rng(M)
+    codes, scales = V.random_fp4(g, last, K)
+    dc, ds = torch.zeros((N, K // 2), dtype=torch.uint8, device="cuda"), torch.zeros((N, K // 16), dtype=torch.uint8, device="cuda")
+    dc[-last:], ds[-last:] = to_dev(codes), to_dev(scales)
+    packed = c.fp4_weight_alloc(N, K)
+    assert packed.numel() > 2 ** 32
+    c.csa2_fp4_pack_weight(dc, ds, packed)
+    xb = V.bf16(g, (M, K))
+    y = torch.full((M, N), 7.0, dtype=torch.float32, device="cuda")
+    c.csa2_fp4_matvec(bf16_dev(xb), packed, y)
+    _check(y[:, -last:], V.f64(xb), V.dequant(codes, scales), np.ones(last))
+    assert bool((y[:, :-last] == 0).all())

@@ -314,3 +314,35 @@ def test_no_free_list_and_no_columns():
     assert n.tolist() == [0, 0] and c.csa2_device_flags() == 0
     c.csa2_context_slots(torch.tensor([0, 3], **i32), torch.empty((2, 0), **i32), n)
     assert n.tolist() == [0, 0] and c.csa2_device_flags() == c.FLAG_INDEX_OOB
+
+
+def test_paged_append_into_far_rows():
+    """Rows whose byte offsets pass 32 bits hold what near rows hold."""
+    n, n_slots = 48, (1 << 24) + 64
+    g = torch.Generator(device="cuda").manual_seed(2)
+    kv = torch.randn((n, 512), generator=g, device="cuda").bfloat16()
+    ki = torch.randn((n, 128), generator=g, device="cuda").bfloat16()
+    codes, scales = (torch.empty((n_slots, w), dtype=torch.uint8, device="cuda") for w in (256, 32))
+    KI = torch.empty((n_slots, 128), dtype=torch.bfloat16, device="cuda")
+    for first in (0, (1 << 24) + 64 - n):
+        c.csa2_paged_append(torch.arange(first, first + n, dtype=torch.int32, device="cuda"), kv_new=kv, codes=codes,
+                            scales=scales, ki_new=ki, KI=KI)
+    assert torch.equal(codes[:n], codes[-n:]) and torch.equal(scales[:n], scales[-n:])
+    assert torch.equal(KI[-n:], ki) and torch.equal(KI[:n], ki)
+
+
+def test_context_slots_of_many_long_rows():
+    """Lists of more than 2^31 entries together."""
+    B, N, T = 33, 64, 1_050_000
+    lens = torch.full((B,), T, dtype=torch.int32, device="cuda")
+    parent = torch.arange(-1, N - 1, dtype=torch.int32, device="cuda").repeat(B, 1)
+    slots = torch.empty((B * N, T + N), dtype=torch.int32, device="cuda")
+    assert slots.numel() > 2 ** 31
+    n_slots = torch.empty(B * N, dtype=torch.int32, device="cuda")
+    c.csa2_device_flags()
+    c.csa2_context_slots(lens, slots, n_slots, parent=parent)
+    want = torch.arange(T + N, dtype=torch.int32, device="cuda")
+    for r in (0, N - 1, B * N - N, B * N - 2, B * N - 1):
+        k = T + r % N + 1
+        assert int(n_slots[r]) == k and torch.equal(slots[r, :k], want[:k]) and bool((slots[r, k:] == -1).all())
+    assert c.csa2_device_flags() == 0

@@ -347,3 +347,23 @@ def test_two_launches_are_one_to_what_comes_next(captured):
     for _ in range(20):
         a.fill_(3.0), b.fill_(5.0)
         assert torch.equal(run(), keep)
+
+
+def test_queries_and_caches_past_32_bits():
+    """The last nodes of a call whose queries, and whose caches of a sequence each, pass 4 GB together."""
+    B, N, cap, k = 4200, 64, 4096, 24
+    g = torch.Generator(device="cuda").manual_seed(4)
+    q = torch.zeros((B, N, 16, 512), dtype=torch.bfloat16, device="cuda")
+    codes = torch.zeros((B, cap, 256), dtype=torch.uint8, device="cuda")
+    scales = torch.zeros((B, cap, 32), dtype=torch.uint8, device="cuda")
+    q[-2:] = torch.randn((2, N, 16, 512), generator=g, device="cuda").bfloat16()
+    codes[-2:] = torch.randint(0, 256, (2, cap, 256), generator=g, device="cuda", dtype=torch.uint8)
+    scales[-2:] = torch.randint(0x28, 0x48, (2, cap, 32), generator=g, device="cuda", dtype=torch.uint8)
+    parent = torch.full((B, N), -1, dtype=torch.int32, device="cuda")
+    idx = torch.randint(0, cap, (B * N, k), generator=g, device="cuda", dtype=torch.int32)
+    out = torch.full_like(q, 9.0)
+    assert q.numel() * 2 > 2 ** 32 and codes.numel() > 2 ** 32
+    c.csa2_tree_attn(q, parent, codes, scales, idx, out)
+    near = torch.full_like(q[-2:], 9.0)
+    c.csa2_tree_attn(q[-2:].contiguous(), parent[-2:], codes[-2:], scales[-2:], idx[-2 * N:], near)
+    assert torch.equal(out[-2:], near) and bool((out[:-2] == 0).all())
