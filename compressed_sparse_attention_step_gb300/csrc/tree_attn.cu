@@ -269,6 +269,7 @@ __global__ void __launch_bounds__(kThreads, 3) tree_attn_kernel(const Params p) 
   Shared& sm = *reinterpret_cast<Shared*>(smem_raw);
   const bool tail = p.row0 != 0;  // a call's second launch: waits for the first at its end
   if (!tail) pdl_wait();
+  else __threadfence();  // (what came before the call has completed: read nothing older)
   pdl_trigger();
   const int rank = kMerge ? int(blockIdx.x % C) : 0;
   const int64_t row = p.row0 + (kMerge ? int64_t(blockIdx.x / C) : int64_t(blockIdx.x));
