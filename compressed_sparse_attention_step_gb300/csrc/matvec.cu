@@ -20,9 +20,9 @@
 // and the token rows (N = 16 or 32) cost the warps nothing.  matvec_kernel: mma.m16n8k16 from registers, with
 // less to set up.
 //
-// Measured (us, weights from HBM; in brackets at the copy bandwidth): one row x 512 x 4096 3.9 (0.17), 4096 x 4096
-// 6.2 (1.4), 16384 x 8192 17.1 (11.1), 32768 x 16384 54 (44.4); eight rows 4.2, 6.9, 19.6, 64; 32 rows x 16384 x 8192
-// 28 (26.7 with the weight partly in L2), 32768 x 16384 93.
+// Measured (us, weights from HBM; in brackets at the copy bandwidth): one row x 512 x 4096 4.0 (0.17), 4096 x 4096
+// 6.4 (1.4), 16384 x 8192 17.5 (11.1), 32768 x 16384 55 (44.4); eight rows 4.3, 6.9, 19.9, 66; 32 rows x 16384 x 8192
+// 29 (27.3 with the weight partly in L2), 32768 x 16384 96.
 // What bounds matvec_kernel: 4 us of launch, staging and exchange, behind which the copies alone take as long as the
 // products alone (16384 x 8192, eight rows: 17.8 and 17.7 with those 4; more blocks under way, more CTAs or even shares
 // of the rows gain nothing).  matvec_tc_kernel: 6 us before the first product (x, 128 KB a CTA), then about 560 cycles
@@ -864,8 +864,8 @@ extern "C" csa2_status csa2_fp4_matvec(const uint16_t* x, int m, const uint8_t* 
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = cudaErrorNotSupported;
   // The tensor-memory form where there is enough weight to pay for its set-up.  Measured, us, this form against the
-  // other: 32 rows x 16384 x 8192 28.5 / 65, 24 x 4096 x 4096 10.4 / 12.6, 32 x 512 x 4096 9.5 / 9.3,
-  // 16 x 16384 x 8192 24.6 / 30, 16 x 8192 x 4096 11.8 / 12.0, 8 x 16384 x 8192 24.5 / 21.
+  // other: 32 rows x 16384 x 8192 29 / 65, 24 x 4096 x 4096 10.6 / 12.6, 32 x 512 x 4096 9.5 / 9.3,
+  // 16 x 16384 x 8192 25 / 30, 16 x 8192 x 4096 11.8 / 12.0, 8 x 16384 x 8192 25 / 20.
   const int64_t blocks = int64_t(p.n_rb) * p.n_kb;
   if ((m > 16 && blocks >= 2048) || (m > 8 && blocks >= 16384)) {
     auto pass = [&](int r, int rows) {
