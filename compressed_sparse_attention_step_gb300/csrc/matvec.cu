@@ -568,6 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_tc_kernel(const Params p) 
   attn::fence_async_smem();
   attn::tc_fence_before();
   cluster_arrive_wait();
+  __syncthreads();  // all warps are past this wait before one comes to the last arrival (as in matvec_kernel)
   attn::tc_fence_after();
   const uint32_t tmem = sm.tmem;
 
