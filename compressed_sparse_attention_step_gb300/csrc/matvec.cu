@@ -34,6 +34,7 @@
 #include <algorithm>
 
 #include "attn_common.cuh"
+#include "matvec_plan.h"
 
 namespace csa2 {
 namespace mv {
@@ -366,7 +367,7 @@ constexpr int kStep = 4;                          // row blocks per step: M = 12
 constexpr uint32_t kABufs = 6, kACols = kChan / 2;
 static_assert(kABufs % kGroups == 0 && kABufs % 2 == 0, "one filler and one user of each half per buffer");
 constexpr uint32_t kDCol = kABufs * kACols;       // accumulators of N columns, one per issuer
-constexpr int kXBytes = 128 * 1024;               // x staged by a CTA, at most
+static_assert(kChan == kPlanChan, "the plan counts the blocks of this layout");
 static_assert(kDCol + kIssuers * 32 <= 512, "tensor memory");
 
 struct Tail {
@@ -731,14 +732,15 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_tc_kernel(const Params p) 
   }
 }
 
-// Launches the tensor-memory form; cudaErrorNotSupported where a cluster's shared memory does not hold x.
+// Launches the tensor-memory form, for sizes that plan() gives to it.
 template <int kTok, int C>
 cudaError_t launch_tc(const mv::Params& g, int sms, cudaStream_t st) {
   Params p = {};
   p.x = g.x, p.packed = g.packed, p.row_scale = g.row_scale, p.y = g.y;
   p.n_out = g.n_out, p.n_in = g.n_in, p.m = g.m, p.n_kb = g.n_kb, p.n_rb = g.n_rb, p.y_fp32 = g.y_fp32;
-  p.x_bytes = ((g.n_kb + C - 1) / C * kTok * kChan * 2 + 1023) / 1024 * 1024;
-  if (p.x_bytes > kXBytes || C > g.n_kb) return cudaErrorNotSupported;
+  const int64_t x = x_bytes(g.n_kb, C, kTok);
+  if (x > kXBytes || C > g.n_kb) return cudaErrorInvalidValue;
+  p.x_bytes = int(x);
   p.flags = g.flags;
   const size_t smem = size_t(p.x_bytes) + sizeof(Tail);
   auto kern = matvec_tc_kernel<kTok, C>;
@@ -773,12 +775,9 @@ cudaError_t launch_tc(const mv::Params& g, int sms, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-// Four CTAs share the channels (two and eight measured slower), or eight, where four do not hold x: up to 32768
-// channels for 16 rows, 16384 for 32.
 template <int kTok>
-cudaError_t launch_tc(const mv::Params& g, int sms, cudaStream_t st) {
-  const cudaError_t e = launch_tc<kTok, 4>(g, sms, st);
-  return e == cudaErrorNotSupported ? launch_tc<kTok, 8>(g, sms, st) : e;
+cudaError_t launch_tc(const mv::Params& g, int C, int sms, cudaStream_t st) {
+  return C == 4 ? launch_tc<kTok, 4>(g, sms, st) : launch_tc<kTok, 8>(g, sms, st);
 }
 
 }  // namespace tc
@@ -863,29 +862,24 @@ extern "C" csa2_status csa2_fp4_matvec(const uint16_t* x, int m, const uint8_t* 
   if (!p.flags) return CSA2_ERR_CUDA;
   p.n_kb = int((n_in + kChan - 1) / kChan), p.n_rb = int((n_out + kRows - 1) / kRows);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = cudaErrorNotSupported;
-  // The tensor-memory form where there is enough weight to pay for its set-up.  Measured, us, this form against the
-  // other: 32 rows x 16384 x 8192 29 / 65, 24 x 4096 x 4096 10.6 / 12.6, 32 x 512 x 4096 9.5 / 9.3,
-  // 16 x 16384 x 8192 25 / 30, 16 x 8192 x 4096 11.8 / 12.0, 8 x 16384 x 8192 25 / 20.
-  const int64_t blocks = int64_t(p.n_rb) * p.n_kb;
-  if ((m > 16 && blocks >= 2048) || (m > 8 && blocks >= 16384)) {
-    auto pass = [&](int r, int rows) {
+  cudaError_t e = cudaSuccess;
+  const tc::Plan plan = tc::plan(m, p.n_rb, p.n_kb);
+  if (plan.tok == 32) {
+    e = tc::launch_tc<32>(p, plan.C, sms, st);
+  } else if (plan.tok == 16) {
+    for (int r = 0; r < m && e == cudaSuccess; r += 16) {
       Params q = p;
-      q.m = rows, q.x = x + int64_t(r) * n_in, q.y = static_cast<char*>(y) + int64_t(r) * n_out * (y_fp32 ? 4 : 2);
-      return tc::launch_tc<16>(q, sms, st);
-    };
-    if (m > 16) e = tc::launch_tc<32>(p, sms, st);
-    // more channels of 32 rows than a cluster holds: 16 rows at a time (4096 x 32768 68 us, the other form 100)
-    if (e == cudaErrorNotSupported) {
-      e = pass(0, std::min(m, 16));
-      if (e == cudaSuccess && m > 16) e = pass(16, m - 16);
+      q.m = std::min(m - r, 16), q.x = x + int64_t(r) * n_in;
+      q.y = static_cast<char*>(y) + int64_t(r) * n_out * (y_fp32 ? 4 : 2);
+      e = tc::launch_tc<16>(q, plan.C, sms, st);
     }
-  }
-  if (e == cudaErrorNotSupported) switch ((m + 7) / 8) {
+  } else {
+    switch ((m + 7) / 8) {
       case 1: e = launch_wr<1>(p, sms, st); break;
       case 2: e = launch_wr<2>(p, sms, st); break;
       case 3: e = launch_wr<3>(p, sms, st); break;
       default: e = launch_wr<4>(p, sms, st); break;
     }
+  }
   return e == cudaSuccess ? CSA2_OK : CSA2_ERR_CUDA;
 }
