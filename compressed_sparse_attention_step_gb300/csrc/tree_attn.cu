@@ -267,9 +267,7 @@ __global__ void __launch_bounds__(kThreads, 3) tree_attn_kernel(const Params p) 
   constexpr bool kMerge = C > 1;
   extern __shared__ __align__(128) unsigned char smem_raw[];
   Shared& sm = *reinterpret_cast<Shared*>(smem_raw);
-  const bool tail = p.row0 != 0;  // a call's second launch: waits for the first at its end
-  if (!tail) pdl_wait();
-  else __threadfence();  // (what came before the call has completed: read nothing older)
+  pdl_wait();
   pdl_trigger();
   const int rank = kMerge ? int(blockIdx.x % C) : 0;
   const int64_t row = p.row0 + (kMerge ? int64_t(blockIdx.x / C) : int64_t(blockIdx.x));
@@ -303,10 +301,7 @@ __global__ void __launch_bounds__(kThreads, 3) tree_attn_kernel(const Params p) 
       const uint4 v = __ldg(reinterpret_cast<const uint4*>(qrow + (g + 8 * h) * CSA2_D) + (i ^ (t >> 1)));
       qf[h][4 * i] = v.x, qf[h][4 * i + 1] = v.y, qf[h][4 * i + 2] = v.z, qf[h][4 * i + 3] = v.w;
     }
-  if (node >= nodes) {  // the whole cluster: its outputs stay as they were
-    if (tail) pdl_wait();
-    return;
-  }
+  if (node >= nodes) return;  // the whole cluster: its outputs stay as they were
   if (tid == 0) {
     for (int j = 0; j < kSelSlots; ++j)
       asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(smem_u32(&sm.sel_full[j])), "n"(kThreads) : "memory");
@@ -522,7 +517,6 @@ __global__ void __launch_bounds__(kThreads, 3) tree_attn_kernel(const Params p) 
       if (p.lse && warp == 0 && t == 0)
         p.lse[row * CSA2_H + g + 8 * h] = any ? (m[h] + log2f(l[h])) * attn::kLn2 : kNegInf;
     }
-    if (tail) pdl_wait();
     return;
   }
   if constexpr (kMerge) {
@@ -575,7 +569,6 @@ __global__ void __launch_bounds__(kThreads, 3) tree_attn_kernel(const Params p) 
       *reinterpret_cast<uint2*>(orow + hd * CSA2_D + 4 * tid) = make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
     }
     cluster_arrive_wait();  // no CTA leaves while its part is being read
-    if (tail) pdl_wait();
   }
 }
 
@@ -629,10 +622,12 @@ extern "C" csa2_status csa2_tree_attn(const uint16_t* q, int B, int N, const int
   p.idx = idx, p.n_valid = n_valid, p.swa = swa, p.win_len = win_len, p.out = out, p.lse = lse;
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
   p.N = N, p.k = k, p.W = W, p.row0 = 0, p.flags = flags;
-  // Few nodes are shared by several CTAs each, which costs a merge.  Measured with 512 selected and 128 window
-  // rows, us for 1 / 2 / 4 / 8 CTAs a node: 5 nodes 24.2 / 17.9 / 11.8 / 9.7, 38 nodes 24.4 / 18.0 / 14.2 / 15.0,
-  // 91 nodes 24.6 / 21.8 / 18.1 / 28.4, 152 nodes 24.9 / 27.1 / 33.1 / 42.6; with 64 selected rows, 91 nodes
-  // 10.9 / 11.5 / 12.1 / 22.
+  // Few nodes are shared by several CTAs each, which costs a merge.  Measured, us for 1 / 2 / 4 / 8 CTAs a node, 512
+  // selected and 128 window rows: 5 nodes 23.5 / 16.6 / 11.3 / 9.3, 20 nodes 23.6 / 16.5 / 11.5 / 11.2, 38 nodes 23.9 /
+  // 16.8 / 13.4 / 14.6, 80 nodes 24.0 / 20.3 / 17.0 / 26.7, 95 nodes 24.0 / 20.6 / 17.3 / 27.7, 104 nodes 24.0 / 20.9 /
+  // 17.3 / 32.2, 112 nodes (whose clusters of four no longer run at once) 24.0 / 20.7 / 25.8 / 35.6.  Fewer rows at 95
+  // nodes, 1 / 4: 256 selected 12.5 / 11.9, 128 selected 8.4 / 10.0, 64 selected 6.6 / 9.9; at 38 nodes 64 selected
+  // rows 6.5 / 7.9, 128 of them 8.3 / 8.1.
   auto ctas = [&](int64_t r) { return r * 8 <= sms ? 8 : r * 4 <= sms || (r * 8 <= 5 * int64_t(sms) && k >= 256) ? 4 : 1; };
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   auto launch = [&](int64_t row0, int64_t r) {
@@ -644,14 +639,15 @@ extern "C" csa2_status csa2_tree_attn(const uint16_t* q, int B, int N, const int
     }
   };
   // Three nodes an SM run at once.  A few nodes behind the last full wave would take as long as a whole one: they are
-  // shared by several CTAs each, in a second launch whose CTAs start as the first's leave.  It reads nothing that the
-  // first writes and starts behind all of the first's waits for what came before; it waits for the first at its end,
-  // so that whoever waits for it waits for both.  (58 x 8 nodes 57.8 -> 44.3 us, 64 x 8 58.4 -> 50.9, 68 x 8 58.6 ->
-  // 54.5, 120 x 8 95.0 -> 87.3.)  Not with n_nodes: of 64 x 8 nodes, 437 to 496 real ones took 46.3 us in one launch on
-  // average and 48.0 in two.
+  // shared by several CTAs each, in a second launch.  Measured, us for two launches / one, 512 selected and 128 window
+  // rows: 58 x 8 nodes 49.8 / 59.1, 64 x 8 54.6 / 59.8, 247 x 2 57.2 / 62.1, 120 x 8 96.4 / 98.3; 256 and 128 rows: 58 x 8
+  // 35.5 / 39.1, 64 x 8 38.6 / 39.8; fewer rows than 320 gain nothing (256 and none 27.1 / 28.4, 29.6 / 29.2; 64 and 128
+  // 24.9 / 24.0; 64 and none 16.8 / 13.6), nor do more nodes than half the SMs (546 x 1, 90 behind the wave: 512 and
+  // none 51.2 / 50.6, 384 and none 41.6 / 40.4).  Not with n_nodes: nodes that are not real leave room in the last wave
+  // (of 64 x 8 nodes, 437 to 496 real ones took 46.3 us in one launch).
   const int64_t wave = 3 * int64_t(sms), rest = rows % wave;
   cudaError_t e;
-  if (!n_nodes && rows > wave && rest > 0 && ctas(rest) > 1) {
+  if (!n_nodes && rows > wave && rest > 0 && 2 * rest <= sms && k + W >= 320 && ctas(rest) > 1) {
     e = launch(0, rows - rest);
     if (e == cudaSuccess) e = launch(rows - rest, rest);
   } else {

@@ -367,3 +367,53 @@ def test_queries_and_caches_past_32_bits():
     near = torch.full_like(q[-2:], 9.0)
     c.csa2_tree_attn(q[-2:].contiguous(), parent[-2:], codes[-2:], scales[-2:], idx[-2 * N:], near)
     assert torch.equal(out[-2:], near) and bool((out[:-2] == 0).all())
+
+
+@pytest.mark.parametrize("rest,N,k,W", [(1, 1, 320, 0), (19, 1, 313, 7), (38, 2, 300, 20), (72, 4, 512, 3)])
+def test_many_rows_for_a_few_nodes_behind_the_last_full_wave(rest, N, k, W):
+    """As above with as many rows as make a second launch worth it."""
+    B = (3 * SMS + rest) // N
+    assert 2 * (B * N - 3 * SMS) <= SMS and k + W >= 320
+    cs = Case(rest, B, N, k + 5, k, W)
+    cs.n_nodes[:] = N
+    d = cs.dev()
+    d["n_nodes"] = None
+    c.csa2_device_flags()
+    c.csa2_tree_attn(**d)
+    assert c.csa2_device_flags() == 0
+    cs.check(d)
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_two_launches_of_many_rows_are_one_to_what_comes_next(captured):
+    """Each call's queries and lists are what the calls before it wrote, with nothing between them."""
+    B, N = (3 * SMS + 40) // 4, 4
+    cs = Case(23, B, N, 400, 330, 9, full=True)
+    d = cs.dev()
+    del d["out"], d["n_nodes"]
+    a, b, keep = (torch.empty_like(d["q"]) for _ in range(3))
+    x, idx = d.pop("q"), d.pop("idx")
+    lists = torch.full_like(idx, -1)
+
+    def chain(sync):
+        src = x
+        lists.fill_(-1)
+        for i in range(6):
+            lists[:, 50 * i:50 * i + 60].copy_(idx[:, 50 * i:50 * i + 60])      # the lists grow behind every call
+            dst = (a, b)[i & 1]
+            c.csa2_tree_attn(q=src, out=dst, idx=lists, **d, softmax_scale=4.0)
+            if sync:
+                torch.cuda.synchronize()
+            src = dst
+        return src
+    keep.copy_(chain(True))
+    assert torch.isfinite(keep.float()).all() and not torch.equal(keep, x)
+    run = lambda: chain(False)  # noqa: E731
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run()
+        run = lambda: graph.replay() or b  # noqa: E731
+    for _ in range(20):
+        a.fill_(3.0), b.fill_(5.0)
+        assert torch.equal(run(), keep)

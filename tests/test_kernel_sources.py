@@ -21,6 +21,7 @@ def kernels(name):
             if depth == 0:
                 break
         out.append((m.group(1), src[i:j + 1]))
+    assert len(out) == src.count("__global__")
     return out
 
 
@@ -40,3 +41,23 @@ def test_the_block_meets_between_cluster_barriers(source, n):
                 assert not waited, f"{name}: a cluster barrier behind another without __syncthreads between them"
             if t in ("cluster_wait", "cluster_arrive_wait"):
                 waited = True
+
+
+SOURCES = sorted(f for f in os.listdir(CSRC) if f.endswith(".cu"))
+
+
+@pytest.mark.parametrize("source", SOURCES)
+def test_every_kernel_waits_before_it_reads(source):
+    """A kernel that may start while the one before it in the stream still runs reads and writes global memory
+    behind griddepcontrol.wait alone: every kernel has one such wait, unconditional, before its first load, and lets
+    the next kernel start behind it."""
+    for name, body in kernels(source):
+        assert len(re.findall(r"\bpdl_wait\s*\(\s*\)", body)) == 1, f"{name}: one wait"
+        wait = re.search(r"[;{}]\s*pdl_wait\s*\(\s*\)\s*;", body)
+        assert wait, f"{name}: the wait is conditional"
+        head = body[1:wait.start() + 1]
+        assert not re.search(r"__ldg|\bld_|\basm\b|atomic|\bif\b|\bfor\b|\bwhile\b", head), f"{name}: work before the wait"
+        depth = head.count("{") - head.count("}")
+        assert depth == 0, f"{name}: the wait stands in a block of its own"
+        trigger = body.find("pdl_trigger")
+        assert trigger == -1 or trigger > wait.end() - 1, f"{name}: the next kernel may start before the wait"
