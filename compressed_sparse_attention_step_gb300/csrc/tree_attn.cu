@@ -607,11 +607,12 @@ extern "C" csa2_status csa2_tree_attn(const uint16_t* q, int B, int N, const int
   const int64_t rows = int64_t(B) * N;
   if (rows == 0) return CSA2_OK;
   auto al = [](const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; };
-  if (!q || !parent || !out || !al(q, 16) || !al(out, 16) || !al(parent, 4) || !al(n_nodes, 4) || !al(lse, 4))
+  if (!q || !parent || !out || !al(q, 16) || !al(out, 16) || !al(parent, 4) || !al(n_nodes, 4) ||
+      !al(n_valid, 4) || !al(win_len, 4) || !al(lse, 4))
     return CSA2_ERR_INVALID_ARG;
-  if (k > 0 && (!idx || (cap > 0 && (!codes || !scales)) || !al(codes, 16) || !al(scales, 16) || !al(idx, 4) || !al(n_valid, 4)))
+  if (k > 0 && (!idx || (cap > 0 && (!codes || !scales)) || !al(codes, 16) || !al(scales, 16) || !al(idx, 4)))
     return CSA2_ERR_INVALID_ARG;
-  if (W > 0 && (!swa || !al(swa, 16) || !al(win_len, 4))) return CSA2_ERR_INVALID_ARG;
+  if (W > 0 && (!swa || !al(swa, 16))) return CSA2_ERR_INVALID_ARG;
   if (rows * tree::kMaxCluster > 0x7FFFFFFFll) return CSA2_ERR_INVALID_ARG;
   unsigned int* flags = device_flags_ptr();
   const int sms = sm_count();

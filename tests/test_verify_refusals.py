@@ -116,3 +116,13 @@ def test_binding_checks_shapes_and_types():
         csa2.csa2_tree_attn(torch.zeros((1, 2, 16, 512), dtype=torch.bfloat16), torch.zeros((1, 2), dtype=i32),
                             torch.zeros((8, 256), dtype=torch.uint8), torch.zeros((8, 16), dtype=torch.uint8),
                             torch.zeros((2, 4), dtype=i32), torch.zeros((1, 2, 16, 512), dtype=torch.bfloat16))
+
+
+def test_tree_attn_alignment_of_lists_it_may_not_need(L):
+    """n_valid is read with k = 0 too, and win_len with W = 0: both on 4 bytes whatever the sizes."""
+    def call(nv, wl, k, W, N=4):
+        return L.csa2_tree_attn(_p(0), 2, N, _p(1), None, _p(2), _p(3), 64, 1, _p(4), nv, k, _p(5), wl, W, 0.1, _p(6),
+                                None, None)
+    assert call(ODD, None, 0, 16) == 1 and call(ODD, None, 8, 16) == 1
+    assert call(None, ODD, 8, 0) == 1 and call(None, ODD, 8, 16) == 1
+    assert call(ODD, ODD, 0, 0, N=0) == 0                # nothing to do: nothing is looked at
