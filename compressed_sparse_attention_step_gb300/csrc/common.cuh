@@ -209,6 +209,26 @@ __device__ __forceinline__ void bar_drain(uint64_t* bars, int n) {
   for (int i = 0; i < min(n, kSlots); ++i) bar_wait(smem_u32(&bars[i]), uint32_t((n - i - 1) / kSlots) & 1u);
 }
 
+// Checks of arguments: alignment (null passes), and whether two ranges share a byte.  `span`: rows of `per` bytes,
+// cut off far above any memory, so that no product or sum of a check wraps.
+inline bool al(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+struct Span {
+  uintptr_t at, end;
+};
+inline Span span(const void* p, int64_t rows, int64_t per) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(p);
+  const __int128 n = __int128(rows) * per, most = __int128(1) << 60;
+  return {x, x + (p ? uintptr_t(n < most ? n : most) : 0)};
+}
+inline bool overlap(const Span& a, const Span& b) { return a.at < b.end && b.at < a.end && a.at < a.end && b.at < b.end; }
+// Whether one of the first n_out spans, written, shares a byte with another span of the list.
+inline bool any_overlap(const Span* s, int n_out, int n) {
+  for (int i = 0; i < n_out; ++i)
+    for (int j = i + 1; j < n; ++j)
+      if (overlap(s[i], s[j])) return true;
+  return false;
+}
+
 // Lets a kernel use `bytes` of dynamic shared memory on the current device; set once per device (`done`, one per
 // kernel, holds a bit for each device).
 inline cudaError_t allow_smem(const void* kern, size_t bytes, std::atomic<uint64_t>& done) {

@@ -519,6 +519,11 @@ extern "C" csa2_status csa2_paged_append(const uint16_t* kv_new, const uint16_t*
   if (!al16(kv_new) || !al16(ki_new) || !al16(codes) || !al16(scales) || !al16(KI)) return CSA2_ERR_INVALID_ARG;
   if (n == 0 || (!kv && !ki)) return CSA2_OK;
   if (!slots || (reinterpret_cast<uintptr_t>(slots) & 3u)) return CSA2_ERR_INVALID_ARG;
+  using csa2::span;
+  const csa2::Span spans[] = {span(codes, n_slots, CSA2_CODE_BYTES), span(scales, n_slots, CSA2_SCALE_BYTES),
+                              span(KI, n_slots, CSA2_DI * 2),        span(kv_new, n, CSA2_D * 2),
+                              span(ki_new, n, CSA2_DI * 2),          span(slots, n, 4)};
+  if (csa2::any_overlap(spans, 3, 6)) return CSA2_ERR_INVALID_ARG;
   unsigned int* flags = csa2::device_flags_ptr();
   if (!flags) return CSA2_ERR_CUDA;
   auto kern = reinterpret_cast<uintptr_t>(kv_new) & 31u ? csa2::paged_append_kernel<false> : csa2::paged_append_kernel<true>;

@@ -806,11 +806,6 @@ cudaError_t launch_wr(const Params& p, int sms, cudaStream_t st) {
   }
 }
 
-inline bool al(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + nb && y < x + na;
-}
 inline bool sizes_ok(int64_t n_out, int64_t n_in) {
   return n_out >= 0 && n_in >= 0 && n_in % CSA2_GROUP == 0 && n_out <= (int64_t(1) << 28) && n_in <= (int64_t(1) << 28);
 }
@@ -831,10 +826,9 @@ extern "C" csa2_status csa2_fp4_pack_weight(const uint8_t* codes, const uint8_t*
   if (!sizes_ok(n_out, n_in)) return CSA2_ERR_INVALID_ARG;
   if (n_out * n_in == 0) return CSA2_OK;
   if (!codes || !scales || !packed || !al(codes, 16) || !al(scales, 16) || !al(packed, 16)) return CSA2_ERR_INVALID_ARG;
-  const size_t bytes = csa2_fp4_packed_bytes(n_out, n_in);
-  if (overlap(packed, bytes, codes, size_t(n_out * n_in / 2)) ||
-      overlap(packed, bytes, scales, size_t(n_out * n_in / CSA2_GROUP)))
-    return CSA2_ERR_INVALID_ARG;
+  const Span spans[] = {span(packed, int64_t(csa2_fp4_packed_bytes(n_out, n_in)), 1), span(codes, n_out, n_in / 2),
+                        span(scales, n_out, n_in / CSA2_GROUP)};
+  if (any_overlap(spans, 1, 3)) return CSA2_ERR_INVALID_ARG;
   const int64_t n_kb = (n_in + kChan - 1) / kChan, n_blocks = (n_out + kRows - 1) / kRows * n_kb;  // a warp each
   if (n_blocks * 32 / 256 > 0x7FFFFFF0ll) return CSA2_ERR_INVALID_ARG;
   return launch_pdl(pack_kernel, dim3(unsigned((n_blocks * 32 + 255) / 256)), dim3(256), 0,
@@ -852,7 +846,9 @@ extern "C" csa2_status csa2_fp4_matvec(const uint16_t* x, int m, const uint8_t* 
   if (m == 0 || n_out == 0) return CSA2_OK;
   if (!x || !packed || !y || !al(x, 16) || !al(packed, 16) || !al(y, 16) || !al(row_scale, 4))
     return CSA2_ERR_INVALID_ARG;
-  if (overlap(x, size_t(m) * n_in * 2, y, size_t(m) * n_out * (y_fp32 ? 4 : 2))) return CSA2_ERR_INVALID_ARG;
+  const Span spans[] = {span(y, m, n_out * (y_fp32 ? 4 : 2)), span(x, m, n_in * 2),
+                        span(packed, int64_t(csa2_fp4_packed_bytes(n_out, n_in)), 1), span(row_scale, n_out, 4)};
+  if (any_overlap(spans, 1, 4)) return CSA2_ERR_INVALID_ARG;
   const int sms = sm_count();
   if (sms <= 0) return CSA2_ERR_CUDA;
   Params p = {};

@@ -277,11 +277,6 @@ inline int page_shift(int page_size) {  // -1: not a power of two in 16..1024
     if (page_size == 1 << s) return s;
   return -1;
 }
-inline bool al(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return a && b && x < y + nb && y < x + na;
-}
 
 }  // namespace pages
 }  // namespace csa2
@@ -303,12 +298,10 @@ extern "C" csa2_status csa2_block_tables(const int32_t* old_lens, const int32_t*
   const void* all[] = {old_lens, new_lens, block_table, free_pages, pool_state, granted, slots};
   for (const void* p : all)
     if (!al(p, 4)) return CSA2_ERR_INVALID_ARG;
-  const struct { const void* p; size_t n; } in[] = {{old_lens, size_t(B) * 4}, {new_lens, size_t(B) * 4},
-      {block_table, size_t(B) * max_pages * 4}, {free_pages, size_t(free_cap) * 4}, {pool_state, 16}};
-  for (const auto& i : in)
-    if (overlap(granted, size_t(B) * 4, i.p, i.n) || overlap(slots, size_t(B) * n_new * 4, i.p, i.n))
-      return CSA2_ERR_INVALID_ARG;
-  if (overlap(granted, size_t(B) * 4, slots, size_t(B) * n_new * 4)) return CSA2_ERR_INVALID_ARG;
+  const Span all_spans[] = {span(granted, B, 4),   span(slots, int64_t(B) * n_new, 4), span(block_table, int64_t(B) * max_pages, 4),
+                            span(pool_state, 4, 4), span(free_pages, free_cap, 4),      span(old_lens, B, 4),
+                            span(new_lens, B, 4)};
+  if (any_overlap(all_spans, 5, 7)) return CSA2_ERR_INVALID_ARG;  // (the two lengths may be one array)
   unsigned int* flags = device_flags_ptr();
   const int sms = sm_count();
   if (!flags || sms <= 0) return CSA2_ERR_CUDA;
@@ -339,6 +332,10 @@ extern "C" csa2_status csa2_context_slots(const int32_t* lens, const int32_t* pa
   if (!lens || (ld > 0 && !slots) || !n_slots || !al(lens, 4) || !al(parent, 4) || !al(n_nodes, 4) || !al(block_table, 4) ||
       !al(slots, 16) || !al(n_slots, 4))
     return CSA2_ERR_INVALID_ARG;
+  const Span spans[] = {span(slots, int64_t(B) * N * ld, 4), span(n_slots, int64_t(B) * N, 4), span(lens, B, 4),
+                        span(parent, int64_t(B) * N, 4),     span(n_nodes, B, 4),
+                        span(block_table, int64_t(B) * max_pages, 4)};
+  if (any_overlap(spans, 2, 6)) return CSA2_ERR_INVALID_ARG;
   unsigned int* flags = device_flags_ptr();
   if (!flags) return CSA2_ERR_CUDA;
   const unsigned gx = unsigned(std::max<int64_t>((ld + 4 * kCtxThreads - 1) / (4 * kCtxThreads), 1));

@@ -34,6 +34,8 @@
 // are accumulated in fp32; the softmax sum takes P before its rounding.
 #include <cuda_bf16.h>
 
+#include <algorithm>
+
 #include "attn_common.cuh"
 
 namespace csa2 {
@@ -606,7 +608,6 @@ extern "C" csa2_status csa2_tree_attn(const uint16_t* q, int B, int N, const int
     return CSA2_ERR_INVALID_ARG;
   const int64_t rows = int64_t(B) * N;
   if (rows == 0) return CSA2_OK;
-  auto al = [](const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; };
   if (!q || !parent || !out || !al(q, 16) || !al(out, 16) || !al(parent, 4) || !al(n_nodes, 4) ||
       !al(n_valid, 4) || !al(win_len, 4) || !al(lse, 4))
     return CSA2_ERR_INVALID_ARG;
@@ -614,6 +615,19 @@ extern "C" csa2_status csa2_tree_attn(const uint16_t* q, int B, int N, const int
     return CSA2_ERR_INVALID_ARG;
   if (W > 0 && (!swa || !al(swa, 16))) return CSA2_ERR_INVALID_ARG;
   if (rows * tree::kMaxCluster > 0x7FFFFFFFll) return CSA2_ERR_INVALID_ARG;
+  const int64_t row_bytes = CSA2_H * CSA2_D * 2, pool = k == 0 ? 0 : shared_pool ? 1 : B;
+  const Span spans[] = {span(out, rows, row_bytes),
+                        span(lse, rows, CSA2_H * 4),
+                        span(parent, rows, 4),
+                        span(n_nodes, B, 4),
+                        span(codes, pool, std::min(cap, int64_t(1) << 48) * CSA2_CODE_BYTES),
+                        span(scales, pool, std::min(cap, int64_t(1) << 48) * CSA2_SCALE_BYTES),
+                        span(idx, rows, int64_t(k) * 4),
+                        span(n_valid, rows, 4),
+                        span(W > 0 ? swa : nullptr, B, (int64_t(W) - 1 + N) * CSA2_D * 2),
+                        span(win_len, B, 4),
+                        span(out == q ? nullptr : q, rows, row_bytes)};  // in place, but not moved by some rows
+  if (any_overlap(spans, 2, 11) || overlap(spans[1], span(q, rows, row_bytes))) return CSA2_ERR_INVALID_ARG;
   unsigned int* flags = device_flags_ptr();
   const int sms = sm_count();
   if (!flags || sms <= 0) return CSA2_ERR_CUDA;

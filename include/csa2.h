@@ -432,8 +432,8 @@ csa2_status csa2_attn_merge_shards(const uint16_t* out_g, const float* lse_g, in
  *              [1] to [3] are the library's and zero between calls;
  *   granted    int32 [B]: the length in effect after the call;
  *   slots      int32 [B][n_new] or NULL: the slot of position old_lens[b] + i, -1 from granted[b] on.
- * page_size is a power of two in 16..1024; B * max_pages and B * n_new are below 2^31.  granted and slots
- * overlap no input.  Calls on one pool are ordered by the caller.
+ * page_size is a power of two in 16..1024; B * max_pages and B * n_new are below 2^31.  No two arrays
+ * overlap, but old_lens and new_lens may be one.  Calls on one pool are ordered by the caller.
  */
 csa2_status csa2_block_tables(const int32_t* old_lens, const int32_t* new_lens, int B, int page_size,
                               int32_t* block_table, int max_pages, int32_t* free_pages, int free_cap,
@@ -449,7 +449,7 @@ csa2_status csa2_block_tables(const int32_t* old_lens, const int32_t* new_lens, 
  *           NULL: no drafts, every row lists the committed positions only;
  *   n_nodes int32 [B] or NULL (N): rows of nodes at or past it are all -1 with n_slots 0;
  *   block_table int32 [B][max_pages] or NULL: NULL lists positions instead of slots;
- *   slots   int32 [B*N][ld], n_slots int32 [B*N].  N <= CSA2_MAX_TREE, B <= 65535.
+ *   slots   int32 [B*N][ld], n_slots int32 [B*N], which overlap nothing.  N <= CSA2_MAX_TREE, B <= 65535.
  * A slot past ld, a position past the table and a parent out of order (taken as -1) set
  * CSA2_FLAG_INDEX_OOB; a position past the table is listed as -1.
  * As `cand` of csa2_index_score over a pool (B = 1, cap = the pool's rows) the rows need not ascend,
@@ -465,6 +465,7 @@ csa2_status csa2_context_slots(const int32_t* lens, const int32_t* parent, const
  * is skipped and sets CSA2_FLAG_APPEND_OOB.  Distinct rows need distinct slots.
  *   kv_new bf16 [n][512] with codes uint8 [n_slots][256] and scales uint8 [n_slots][32], or all NULL;
  *   ki_new bf16 [n][128] with KI bf16 [n_slots][128], or both NULL;  slots int32 [n].
+ * codes, scales and KI overlap nothing.
  */
 csa2_status csa2_paged_append(const uint16_t* kv_new, const uint16_t* ki_new, const int32_t* slots, int64_t n,
                               uint8_t* codes, uint8_t* scales, uint16_t* KI, int64_t n_slots, csa2_stream_t stream);
@@ -482,8 +483,8 @@ csa2_status csa2_paged_append(const uint16_t* kv_new, const uint16_t* ki_new, co
  *           n_valid[r] are empty, entries >= cap are empty and set CSA2_FLAG_INDEX_OOB.
  *   swa     bf16 [B][W-1+N][512]: W - 1 committed rows, oldest first, then the N drafted rows; or NULL with W = 0.
  *   win_len int32 [B] or NULL (W - 1): the last win_len[b] committed rows hold tokens.
- *   out     bf16 [B][N][16][512] (may be q); lse fp32 [B][N][16] (nullable), natural log; a node with no rows (W = 0 and
- *           nothing selected) gets out = 0 and lse = -inf.
+ *   out     bf16 [B][N][16][512] (may be q itself; out and lse overlap nothing else); lse fp32 [B][N][16]
+ *           (nullable), natural log; a node with no rows (W = 0 and nothing selected) gets out = 0 and lse = -inf.
  * No workspace.  The result does not depend on scheduling.
  */
 csa2_status csa2_tree_attn(const uint16_t* q, int B, int N, const int32_t* parent, const int32_t* n_nodes,
@@ -500,8 +501,8 @@ csa2_status csa2_tree_attn(const uint16_t* q, int B, int N, const int32_t* paren
  *   codes uint8 [n_out][n_in/2], scales uint8 [n_out][n_in/16] -> packed, csa2_fp4_packed_bytes(n_out, n_in)
  *   bytes.  n_in a multiple of 16.
  * csa2_fp4_matvec: x bf16 [m][n_in], m <= CSA2_MAX_MV_ROWS; row_scale fp32 [n_out] or NULL (1); y [m][n_out],
- *   bf16 (y_fp32 = 0) or fp32 (y_fp32 = 1).  Accumulated in fp32, rounded once.  No workspace.  y does not
- *   overlap x, nor packed its sources.
+ *   bf16 (y_fp32 = 0) or fp32 (y_fp32 = 1).  Accumulated in fp32, rounded once.  No workspace.  y overlaps
+ *   none of the inputs, packed none of its sources.
  */
 size_t csa2_fp4_packed_bytes(int64_t n_out, int64_t n_in);
 csa2_status csa2_fp4_pack_weight(const uint8_t* codes, const uint8_t* scales, int64_t n_out, int64_t n_in,

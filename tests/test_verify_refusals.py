@@ -126,3 +126,86 @@ def test_tree_attn_alignment_of_lists_it_may_not_need(L):
     assert call(ODD, None, 0, 16) == 1 and call(ODD, None, 8, 16) == 1
     assert call(None, ODD, 8, 0) == 1 and call(None, ODD, 8, 16) == 1
     assert call(ODD, ODD, 0, 0, N=0) == 0                # nothing to do: nothing is looked at
+
+
+def _over(i, nbytes):  # the last 4, 16 or fewer bytes of buffer i
+    return ctypes.c_void_p(_p(i).value + nbytes)
+
+
+def test_overlap_of_context_slots(L):
+    """What the call writes shares no byte with what it reads: n_slots may not be lens, though N = 1 gives both B
+    entries; the lists may not lie over a table, the parents or the counts."""
+    def call(lens=_p(0), parent=_p(1), nn=_p(5), B=2, N=4, table=_p(2), mp=8, slots=_p(3), ld=64, ns=_p(4)):
+        return L.csa2_context_slots(lens, parent, nn, B, N, table, mp, 64, slots, ld, ns, None)
+    assert call(ns=_p(0), N=1) == 1 and call(ns=_p(0), N=1, parent=None, nn=None, table=None) == 1
+    for i in (0, 1, 2, 3, 5):
+        assert call(ns=_p(i)) == 1, i
+    for i in (0, 1, 2, 5):
+        assert call(slots=_p(i)) == 1, i
+    assert call(ns=_over(3, 2 * 4 * 64 * 4 - 4)) == 1            # the lists' last entry
+    assert call(lens=_over(3, 2 * 4 * 64 * 4 - 4)) == 1 and call(table=_over(4, 2 * 4 * 4 - 4)) == 1
+
+
+def test_overlap_of_block_tables(L):
+    def call(old=_p(0), new=_p(1), table=_p(2), free=_p(3), state=_p(4), granted=_p(5), slots=_p(6)):
+        return L.csa2_block_tables(old, new, 4, 64, table, 8, free, 16, state, granted, slots, 8, None)
+    for name in ("table", "free", "state"):                      # changed in place
+        for i in range(7):
+            if _p(i).value != dict(table=_p(2), free=_p(3), state=_p(4))[name].value:
+                assert call(**{name: _p(i)}) == 1, (name, i)
+    assert call(free=_over(2, 4 * 8 * 4 - 4)) == 1 and call(state=_over(3, 16 * 4 - 4)) == 1
+
+
+def test_overlap_of_paged_append(L):
+    def call(kv=_p(0), ki=_p(1), slots=_p(2), codes=_p(3), scales=_p(4), KI=_p(5)):
+        return L.csa2_paged_append(kv, ki, slots, 3, codes, scales, KI, 64, None)
+    own = dict(codes=3, scales=4, KI=5)
+    for name, at in own.items():
+        for i in range(6):
+            if i != at:
+                assert call(**{name: _p(i)}) == 1, (name, i)
+    assert call(kv=_over(5, 64 * 256 - 16)) == 1 and call(slots=_over(3, 64 * 256 - 4)) == 1
+
+
+def test_overlap_of_tree_attn(L):
+    """out may be q itself, not q moved by some rows, and nothing else that the call reads or writes."""
+    row = 16 * 512 * 2
+
+    def call(q=_p(0), parent=_p(1), nn=_p(7), codes=_p(2), scales=_p(3), idx=_p(4), nv=_p(8), swa=_p(5), wl=_p(9), out=_p(6),
+             lse=_p(10), cap=64, pool=1, k=8, W=16):
+        return L.csa2_tree_attn(q, 2, 4, parent, nn, codes, scales, cap, pool, idx, nv, k, swa, wl, W, 0.1, out, lse, None)
+    for i in (1, 2, 3, 4, 5, 7, 8, 9, 10):
+        assert call(out=_p(i)) == 1, i
+    for i in (0, 1, 2, 3, 4, 5, 6, 7, 8, 9):
+        assert call(lse=_p(i)) == 1, i
+    assert call(out=_over(0, row)) == 1 and call(out=_over(0, 8 * row - 16)) == 1 and call(q=_over(6, row)) == 1
+    assert call(out=_p(0), lse=_over(0, row)) == 1
+    assert call(out=_over(2, 64 * 256 - 16)) == 1                                    # a pool's last row
+    assert call(out=_over(2, 2 * 64 * 256 - 16), pool=0) == 1                        # the last sequence's last row
+    assert call(out=_over(5, 2 * 19 * 1024 - 16)) == 1                               # the window's last row
+    assert call(out=_p(2), cap=(1 << 63) - 1, pool=0) == 1                           # sizes past 64 bits
+
+
+def test_overlap_of_fp4_matvec(L):
+    def call(x=_p(0), w=_p(1), rs=_p(3), y=_p(2), fp32=0):
+        return L.csa2_fp4_matvec(x, 2, w, 8, 32, rs, y, fp32, None)
+    assert call(y=_p(1)) == 1 and call(y=_over(1, 2304 - 16)) == 1 and call(y=_p(3)) == 1
+    assert call(w=_over(2, 16)) == 1 and call(rs=_over(2, 2 * 8 * 2 - 4)) == 1
+    assert call(rs=_over(2, 2 * 8 * 4 - 4), fp32=1) == 1
+
+
+def test_what_does_not_overlap_is_not_refused(L):
+    """Arrays that touch, an array given twice as an input, and arrays that the sizes leave without a byte pass the
+    checks (what comes behind them needs a GPU: not an invalid argument here, or done)."""
+    old = _p(0)
+    ok = (csa2.OK, csa2.ERR_CUDA)
+    if csa2._torch().cuda.is_available():
+        pytest.skip("the calls would run")
+    assert L.csa2_block_tables(old, old, 4, 64, _p(1), 8, _over(1, 4 * 8 * 4), 16, _p(2), _p(3), None, 0, None) in ok
+    assert L.csa2_context_slots(old, None, old, 2, 4, None, 0, 0, _p(1), 64, _over(1, 2 * 4 * 64 * 4), None) in ok
+    assert L.csa2_paged_append(None, _p(0), _p(1), 3, None, None, _over(0, 3 * 256), 64, None) in ok
+    assert L.csa2_tree_attn(_p(0), 2, 4, _p(1), None, _p(2), _p(2), 64, 1, _p(4), None, 8, None, None, 0, 0.1, _p(0),
+                            None, None) in ok
+    assert L.csa2_tree_attn(_p(0), 2, 4, _p(1), None, _p(6), _p(6), 64, 1, _p(6), None, 0, _p(6), None, 0, 0.1, _p(6),
+                            None, None) in ok                       # k = 0 and W = 0: neither cache nor window
+    assert L.csa2_fp4_matvec(_p(0), 2, _p(1), 8, 32, None, _over(1, 2304), 0, None) in ok
