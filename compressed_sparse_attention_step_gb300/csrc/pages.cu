@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kThreads) block_tables_kernel(
     }
   }
   // four columns a thread: most of them lie in one page, whose number is looked up once
-  const int quads = (n_new + 3) / 4;
+  const int quads = n_new / 4 + (n_new % 4 != 0);  // (n_new goes up to 2^31 - 1)
   for (int64_t i = gtid; i < int64_t(B) * quads; i += gthreads) {
     const int b = int(uint32_t(i) / uint32_t(quads)), c = (int(i) - b * quads) * 4;
     const int o = old_of(b), end = is_granted(b) ? new_of(b) : o, held = pages_of(o, shift);
@@ -307,7 +307,7 @@ extern "C" csa2_status csa2_block_tables(const int32_t* old_lens, const int32_t*
   if (!flags || sms <= 0) return CSA2_ERR_CUDA;
   // a quad of slots or an entry of the tables a thread; how many pages change hands is known on the device alone.  64
   // sequences x 512 pages, granted and given back: 13.6, 9.7, 7.7, 6.8 us with eight, four, two entries a thread and one
-  const int64_t items = std::max(int64_t(B) * ((n_new + 3) / 4), int64_t(B) * max_pages);
+  const int64_t items = std::max(int64_t(B) * ((int64_t(n_new) + 3) / 4), int64_t(B) * max_pages);
   const int grid = int(std::min<int64_t>(std::max<int64_t>(items / kThreads, 1), sms));
   const size_t smem = size_t(B) * 8;
   static std::atomic<uint64_t> done{0};

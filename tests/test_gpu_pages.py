@@ -346,3 +346,19 @@ def test_context_slots_of_many_long_rows():
         k = T + r % N + 1
         assert int(n_slots[r]) == k and torch.equal(slots[r, :k], want[:k]) and bool((slots[r, k:] == -1).all())
     assert c.csa2_device_flags() == 0
+
+
+def test_block_tables_of_the_widest_lists():
+    """Lists of 2^31 - 1 columns, the most that the call takes: every column is written, the last ones too."""
+    n_new = 2 ** 31 - 1
+    i32 = dict(dtype=torch.int32, device="cuda")
+    table, free = torch.full((1, 4), -1, **i32), torch.tensor([9, 5, 7], **i32)
+    state, granted = torch.tensor([3, 0, 0, 0], **i32), torch.zeros(1, **i32)
+    slots = torch.full((1, n_new), -5, **i32)
+    c.csa2_device_flags()
+    c.csa2_block_tables(torch.tensor([0], **i32), torch.tensor([40], **i32), 16, table, free, state, granted, slots=slots)
+    want = [p * 16 + i for p in (7, 5, 9) for i in range(16)][:40]
+    assert granted.tolist() == [40] and slots[0, :40].tolist() == want
+    for a in range(40, n_new, 1 << 28):
+        assert bool((slots[0, a:a + (1 << 28)] == -1).all())
+    assert state.tolist() == [0, 0, 0, 0] and c.csa2_device_flags() == 0
