@@ -137,7 +137,8 @@ csa2_status csa2_fp4_dequantize(const uint8_t* codes, const uint8_t* scales, int
  *   cand    NULL: row r of `scores` is [cap] and entry t holds the score of cache entry t.
  *           else int32 [B*Nq][n_cand] ascending cache positions (a pool) with cand_len[B*Nq]
  *           valid entries; entry i of the row holds the score of position cand[r][i].  Any order
- *           where q_pos lets the query see the whole cache (q_pos[r] >= ratio*cap - 1).
+ *           where the query sees the whole cache: lens[b] >= cap and q_pos[r] >= ratio*cap - 1
+ *           (elsewhere the visible entries are taken for a prefix of the list, as in an ascending one).
  *   scores  fp32 [B*Nq][cap or n_cand]: the visible entries form a prefix of length
  *           n_valid[r] (nullable output); the rest of the row is set to -inf.
  */
@@ -453,7 +454,8 @@ csa2_status csa2_block_tables(const int32_t* old_lens, const int32_t* new_lens, 
  * A slot past ld, a position past the table and a parent out of order (taken as -1) set
  * CSA2_FLAG_INDEX_OOB; a position past the table is listed as -1.
  * As `cand` of csa2_index_score over a pool (B = 1, cap = the pool's rows) the rows need not ascend,
- * provided that q_pos lets every query see the whole pool (q_pos[r] >= ratio * cap - 1).
+ * provided that every query sees the whole pool: lens[0] >= cap, whatever part of the pool is in use, and
+ * q_pos[r] >= ratio * cap - 1.
  */
 csa2_status csa2_context_slots(const int32_t* lens, const int32_t* parent, const int32_t* n_nodes, int B, int N,
                                const int32_t* block_table, int max_pages, int page_size, int32_t* slots, int64_t ld,

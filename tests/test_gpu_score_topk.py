@@ -272,3 +272,28 @@ def test_full_context_rows_of_decode_workload(orc):
         assert np.array_equal(sc[b].cpu().numpy(), exp)
         ei, _ = orc.topk(exp, 512)
         assert np.array_equal(idx[b].cpu().numpy(), ei)
+
+
+@pytest.mark.parametrize("ratio", [1, 2])
+def test_candidates_in_any_order_over_a_whole_cache(orc, ratio):
+    """Where a query sees the whole cache (lens at or past cap, q_pos at the last entry's last token) a candidate
+    list is scored whole in any order, its largest position first or last, with the bits of the oracle's scores."""
+    rows, cap, n = 5, 300, 257
+    qI, w, KI = _score_inputs(41, 1, rows, cap)
+    g = np.random.default_rng(6)
+    cand = np.stack([g.permutation(cap)[:n] for _ in range(rows)]).astype(np.int32)
+    cand[0, 0], cand[1, -1] = cap - 1, cap - 1
+    length = np.array([n, n, 1, 0, 100], np.int32)
+    for lens in (cap, cap + 7):
+        sc = torch.full((rows, n), 5.0, device="cuda")
+        nv = torch.full((rows,), -5, dtype=torch.int32, device="cuda")
+        c.csa2_device_flags()
+        c.csa2_index_score(bf16_dev(qI), to_dev(w), bf16_dev(KI), to_dev(np.array([lens], np.int32)), sc, cand=to_dev(cand),
+                           cand_len=to_dev(length), ratio=ratio, n_valid=nv,
+                           q_pos=torch.full((rows,), ratio * cap - 1, dtype=torch.int32, device="cuda"))
+        assert c.csa2_device_flags() == 0 and nv.tolist() == length.tolist()
+        sc = sc.cpu().numpy()
+        for r in range(rows):
+            exp = orc.index_score(qI[0, r], w[0, r], KI[0][cand[r, :length[r]].astype(np.int64)])
+            assert np.array_equal(sc[r, :length[r]].view(np.uint32), exp.view(np.uint32))
+            assert (sc[r, length[r]:] == -np.inf).all()
