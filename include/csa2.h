@@ -413,7 +413,13 @@ csa2_status csa2_attn_merge_shards(const uint16_t* out_g, const float* lse_g, in
  *                        drafted ancestors), the `cand` of csa2_index_score and the `map` of csa2_topk,
  *                        with the whole pool as one sequence (B = 1, Nq = rows);
  *   csa2_tree_attn       every node's attention, with the pool as its cache;
+ *   csa2_paged_append    again, where the accepted path is not the sequence's first nodes: the i-th node of
+ *                        the path goes into the slot of drafted position i, a node that is there already
+ *                        may be padding (-1).  Node j's row was written to position lens[b] + j, and the
+ *                        committed positions would otherwise hold rows of nodes that were rejected.  The
+ *                        same kv_new and ki_new rows, kept until then, give the same bytes;
  *   csa2_block_tables    again, from the drafted to the accepted lengths: rejected pages go back.
+ * The caller's window rows move likewise: swa's committed rows are those of the accepted path.
  */
 
 /*
