@@ -29,9 +29,12 @@
 // FP4 rows are multiplied as f16: a code times a scale has at most 6 significant bits and lies between
 // 2^-10 and 2688, so the row is exact.  Q is scaled per head by a power of two that puts its largest
 // magnitude into [2^14, 2^15), so its bf16 values are exact in f16 down to 2^-28 of that magnitude, and
-// below it they are off by less than 2^-38 of it.  P is rounded to f16 (2^-11 relative).  Window rows are
-// bf16 and are multiplied as bf16 with P rounded to bf16 (2^-8).  Scores, softmax statistics and outputs
-// are accumulated in fp32; the softmax sum takes P before its rounding.
+// below it they are off by less than 2^-38 of it.  P is rounded to f16 (2^-11 relative; held in two terms it
+// would cost 16%, 64 x 32 nodes 215 instead of 185 us, beside an output that is rounded to 2^-8).  Window rows are
+// bf16 and are multiplied as bf16, with P in two bf16 terms, the second for what the first left (2^-16): one term,
+// 2^-8, is as coarse as the output itself (of nodes with window rows alone a quarter of the outputs were not the
+// nearest bf16), and the second costs 2% (64 x 32 nodes 185 instead of 181 us).  Scores, softmax statistics and
+// outputs are accumulated in fp32; the softmax sum takes P before its rounding.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -86,6 +89,10 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
+// What rounding to a pair of bf16 leaves, rounded to bf16 itself.
+__device__ __forceinline__ uint32_t rest_bf16(float lo, float hi, uint32_t pair) {
+  return pack_bf16(lo - bf16lo(pair), hi - bf16hi(pair));
+}
 __device__ __forceinline__ float quad_max(float v) {
   v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
   return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
@@ -132,6 +139,7 @@ struct Shared {
   SelSlot sel_slot[kSelSlots];
   float2 part[4][kWarps][32];     // partial scores of a step: [fragment register][warp][lane]
   uint4 prob[32];                 // P fragment of a step, one register from each warp
+  uint4 rest[32];                 // what P's rounding to bf16 left, likewise (window rows)
   uint64_t sel_full[kSelSlots], win_full[kWinSlots];  // mbarriers: a slot's copies have landed
   int32_t sel[kMaxSel];           // this node's selected rows, without gaps; the last slot filled up
   int32_t win[kWinList];          // its window buffer rows, likewise
@@ -191,8 +199,12 @@ __device__ __forceinline__ void step(State& s, const uint32_t (&qf)[2][16], uint
   }
   const float m = (warp & 1) ? s.m1 : s.m0;
   float p0 = attn::ex2(x0 - m), p1 = attn::ex2(x1 - m);
-  uint32_t* prob = reinterpret_cast<uint32_t*>(&sm.prob[lane]) + warp;
-  *prob = kF16 ? pack_f16(p0, p1) : pack_bf16(p0, p1);
+  auto put = [&]() {
+    const uint32_t pair = kF16 ? pack_f16(p0, p1) : pack_bf16(p0, p1);
+    reinterpret_cast<uint32_t*>(&sm.prob[lane])[warp] = pair;
+    if (!kF16) reinterpret_cast<uint32_t*>(&sm.rest[lane])[warp] = rest_bf16(p0, p1, pair);
+  };
+  put();
   if (__syncthreads_or(fmaxf(x0, x1) > m + (kHead + 8.f))) {
     // the references move: to the largest scores of this step less kHead, where that is more
     const float top = quad_max(fmaxf(x0, x1));
@@ -207,7 +219,7 @@ __device__ __forceinline__ void step(State& s, const uint32_t (&qf)[2][16], uint
 #pragma unroll
     for (int i = 0; i < 16; ++i) s.o[i][0] *= c0, s.o[i][1] *= c0, s.o[i][2] *= c1, s.o[i][3] *= c1;
     p0 = attn::ex2(x0 - n), p1 = attn::ex2(x1 - n);
-    *prob = kF16 ? pack_f16(p0, p1) : pack_bf16(p0, p1);
+    put();
     __syncthreads();
   }
   const uint4 p = sm.prob[lane];
@@ -215,6 +227,11 @@ __device__ __forceinline__ void step(State& s, const uint32_t (&qf)[2][16], uint
   loaded();
 #pragma unroll
   for (int i = 0; i < 16; ++i) mma<kF16>(s.o[i], p.x, p.y, p.z, p.w, kf[0][i], kf[1][i]);
+  if (!kF16) {
+    const uint4 r = sm.rest[lane];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) mma<kF16>(s.o[i], r.x, r.y, r.z, r.w, kf[0][i], kf[1][i]);
+  }
 }
 
 // Rows g and g + 8 of a step of selected rows: f16 pairs of this lane's 32 channels.

@@ -417,3 +417,35 @@ def test_two_launches_of_many_rows_are_one_to_what_comes_next(captured):
     for _ in range(20):
         a.fill_(3.0), b.fill_(5.0)
         assert torch.equal(run(), keep)
+
+
+def _half_step(x):
+    """Half the spacing of bf16 at |x| (8 significant bits)."""
+    return 2.0 ** (np.floor(np.log2(np.maximum(np.abs(x), 2.0 ** -126))) - 8)
+
+
+@pytest.mark.parametrize("B,N,W,shape", [(2, 3, 128, "chain"), (3, 20, 128, "random"), (30, 4, 128, "random"),
+                                         (130, 4, 60, "star"), (1, 64, 128, "chain"), (2, 5, 1, "chain")])
+def test_window_rows_are_weighed_in_32_bits_but_for_the_output(B, N, W, shape):
+    """Window rows alone: the output is the exact value's own bf16 rounding but for P held in two bf16 terms (2^-16:
+    half a step of the first, 2^-8, times half a step of the second), the scores' and exponentials' errors (as in
+    V.tree_node, twice: numerator and sum) and 40 accumulations at 2^-22 (12 steps of two products, the merge of
+    eight parts, the division)."""
+    cs = Case(B + N + W, B, N, 4, 0, W, shape=shape)
+    d = cs.dev()
+    c.csa2_tree_attn(**d)
+    cs.check(d)
+    out, swa = V.f64(bf16_host(d["out"])), V.f64(cs.swa)
+    for b in range(B):
+        for i in range(int(cs.n_nodes[b])):
+            rows = V.tree_rows(b, i, parent=cs.parent, rows=None, swa=swa, W=W, win_len=cs.win_len)
+            q = V.f64(cs.q[b, i])
+            s = q @ rows.T * SCALE
+            es = (10 * 2.0 ** -22 * (np.abs(q) @ np.abs(rows).T) * SCALE + np.abs(s) * 2.0 ** -22 + 2.0 ** -20).max(-1)
+            p = np.exp(s - s.max(-1, keepdims=True))
+            p /= p.sum(-1, keepdims=True)
+            o = p @ rows
+            e = (p * (2.0 ** -16 + 2 * es[:, None] + 40 * 2.0 ** -22)) @ np.abs(rows)
+            err = np.abs(out[b, i] - o)
+            tol = e + _half_step(np.abs(o) + e)
+            assert (err <= tol).all(), f"b{b} node {i}: {(err > tol).sum()} of {err.size}, {np.max(err - tol):.3e} over"
