@@ -666,13 +666,9 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_tc_kernel(const Params p) 
         asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          // (with one channel block in the share, a step has the issuers of one parity)
           float v = 0.f;
 #pragma unroll
-          for (int c = 0; c < kIssuers; ++c) {
-            const float u = tmem_value(d[c][i]);
-            if (nk > 1 || (c & 1) == (step & 1)) v += u;
-          }
+          for (int c = 0; c < kIssuers; ++c) v += tmem_value(d[c][i]);
           sum[j + i] = v;
         }
       }
@@ -739,7 +735,7 @@ cudaError_t launch_tc(const mv::Params& g, int sms, cudaStream_t st) {
   p.x = g.x, p.packed = g.packed, p.row_scale = g.row_scale, p.y = g.y;
   p.n_out = g.n_out, p.n_in = g.n_in, p.m = g.m, p.n_kb = g.n_kb, p.n_rb = g.n_rb, p.y_fp32 = g.y_fp32;
   const int64_t x = x_bytes(g.n_kb, C, kTok);
-  if (x > kXBytes || C > g.n_kb) return cudaErrorInvalidValue;
+  if (x > kXBytes || g.n_kb < 2 * C) return cudaErrorInvalidValue;  // (every issuer has a block in every step)
   p.x_bytes = int(x);
   p.flags = g.flags;
   const size_t smem = size_t(p.x_bytes) + sizeof(Tail);

@@ -198,3 +198,20 @@ def test_a_weight_of_more_than_4_gb(M):
     c.csa2_fp4_matvec(bf16_dev(xb), packed, y)
     _check(y[:, -last:], V.f64(xb), V.dequant(codes, scales), np.ones(last))
     assert bool((y[:, :-last] == 0).all())
+
+
+@pytest.mark.parametrize("M,N,K", [
+    # on both sides of where the tensor-memory form begins: rows, channels and weight
+    (32, 4097, 2048), (25, 4100, 1920), (25, 5000, 2064), (24, 2080, 4096), (24, 4200, 3968), (17, 2016, 4096),
+    (16, 8200, 8192), (16, 16400, 8064), (9, 8170, 8192), (9, 10000, 8208), (8, 8200, 8192), (16, 33000, 4096),
+])
+def test_matvec_at_the_forms_borders(M, N, K):
+    g = np.random.default_rng(M + N + K)
+    packed, w = _weight(g, N, K)
+    xb = V.bf16(g, (M, K))
+    rs = (g.random(N) * 2 - 0.5).astype(np.float32)
+    y = torch.full((M, N), 7.0, dtype=torch.float32, device="cuda")
+    c.csa2_device_flags()
+    c.csa2_fp4_matvec(bf16_dev(xb), packed, y, row_scale=to_dev(rs))
+    assert c.csa2_device_flags() == 0
+    _check(y, V.f64(xb), w, rs.astype(np.float64))

@@ -45,15 +45,22 @@ def test_bytes_of_x(L):
 
 
 def test_no_plan_passes_what_a_cluster_holds(L):
+    taken = set()
     for n_kb in _kbs():
         for n_rb in (1, 2, 7, 64, 1000, 31250, 1 << 23):
-            for m in (1, 8, 9, 16, 17, 24, 32):
+            for m in range(1, 33):
                 v = L.plan_of(m, n_rb, n_kb)
                 tok, C = v // 16, v % 16
-                worth = (m > 16 and n_rb * n_kb >= 2048) or (m > 8 and n_rb * n_kb >= 16384)
+                blocks = n_rb * n_kb
+                worth = (m > 24 and blocks >= 2048 and n_kb >= 16) or (m > 16 and blocks >= 2048 and n_kb >= 32) \
+                    or (m > 8 and blocks >= 16384 and n_kb >= 64)
                 fits = [(t, c) for t in ((32, 16) if m > 16 else (16,)) for c in (4, 8)
-                        if c <= n_kb and -(-n_kb // c) * t * 256 <= X_BYTES]
+                        if -(-n_kb // c) * t * 256 <= X_BYTES]
                 assert (tok, C) == (fits[0] if worth and fits else (0, 0)), (m, n_rb, n_kb)
+                taken.add((tok, C))
+                if tok:                                       # each CTA of a cluster has two channel blocks and more
+                    assert n_kb >= 2 * C
+    assert taken == {(0, 0), (16, 4), (16, 8), (32, 4), (32, 8)}
 
 
 def test_the_largest_channels_go_to_the_form_without_clusters_of_x(L):
