@@ -657,10 +657,13 @@ extern "C" csa2_status csa2_tree_attn(const uint16_t* q, int B, int N, const int
   // Few nodes are shared by several CTAs each, which costs a merge.  Measured, us for 1 / 2 / 4 / 8 CTAs a node, 512
   // selected and 128 window rows: 5 nodes 23.5 / 16.6 / 11.3 / 9.3, 20 nodes 23.6 / 16.5 / 11.5 / 11.2, 38 nodes 23.9 /
   // 16.8 / 13.4 / 14.6, 80 nodes 24.0 / 20.3 / 17.0 / 26.7, 95 nodes 24.0 / 20.6 / 17.3 / 27.7, 104 nodes 24.0 / 20.9 /
-  // 17.3 / 32.2, 112 nodes (whose clusters of four no longer run at once) 24.0 / 20.7 / 25.8 / 35.6.  Fewer rows at 95
-  // nodes, 1 / 4: 256 selected 12.5 / 11.9, 128 selected 8.4 / 10.0, 64 selected 6.6 / 9.9; at 38 nodes 64 selected
-  // rows 6.5 / 7.9, 128 of them 8.3 / 8.1.
-  auto ctas = [&](int64_t r) { return r * 8 <= sms ? 8 : r * 4 <= sms || (r * 8 <= 5 * int64_t(sms) && k >= 256) ? 4 : 1; };
+  // 17.3 / 32.2, 112 nodes (whose clusters of four no longer run at once) 24.0 / 20.7 / 25.8 / 35.6.  Fewer rows, for
+  // 1 / 4: 95 nodes 256 rows 12.5 / 11.9, 192 of them 10.8 / 11.9, 128 of them 8.4 / 10.0; 38 nodes 128 rows 8.3 / 8.1,
+  // 64 of them 6.5 / 7.9; for 1 / 8: 5 nodes 128 rows 8.0 / 7.1, 64 of them 6.1 / 7.0.
+  auto ctas = [&](int64_t r) {
+    if (k + W < 128 || r * 8 > 5 * int64_t(sms) || (r * 4 > sms && k + W < 256)) return 1;
+    return r * 8 <= sms ? 8 : 4;
+  };
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   auto launch = [&](int64_t row0, int64_t r) {
     p.row0 = row0;

@@ -449,3 +449,63 @@ def test_window_rows_are_weighed_in_32_bits_but_for_the_output(B, N, W, shape):
             err = np.abs(out[b, i] - o)
             tol = e + _half_step(np.abs(o) + e)
             assert (err <= tol).all(), f"b{b} node {i}: {(err > tol).sum()} of {err.size}, {np.max(err - tol):.3e} over"
+
+
+# how many CTAs share a node goes by the nodes and by the rows that their lists may hold (k + W): at 128 and 256 rows,
+# at an eighth, a quarter and five eighths of the SMs, on both sides; fewer steps of 16 rows than CTAs among them
+@pytest.mark.parametrize("n", [SMS // 8, SMS // 8 + 1, SMS // 4, SMS // 4 + 1, 5 * SMS // 8, 5 * SMS // 8 + 1])
+@pytest.mark.parametrize("k,W", [(127, 0), (0, 127), (128, 0), (120, 8), (0, 128), (128, 127), (250, 6), (512, 0)])
+def test_a_node_shared_by_some_ctas(n, k, W):
+    cs = Case(n + k, n, 1, 600, k, W)
+    cs.n_nodes[:] = 1
+    cs.n_valid[n // 2:] = np.minimum(cs.n_valid[n // 2:], np.arange(n - n // 2) % 40)     # short lists, empty ones
+    d = cs.dev()
+    c.csa2_device_flags()
+    c.csa2_tree_attn(**d)
+    assert c.csa2_device_flags() == 0
+    cs.check(d)
+
+
+@pytest.mark.parametrize("B,N", [(1, 5), (7, 4), (19, 5)])
+def test_shared_nodes_without_rows_and_in_place(B, N):
+    """Eight and four CTAs a node: nothing selected gives out 0 and lse -inf; out may be q."""
+    assert B * N * 8 <= 5 * SMS
+    cs = Case(B, B, N, 700, 512, 0, full=True)
+    d = cs.dev()
+    d["n_valid"].zero_()
+    c.csa2_tree_attn(**d)
+    assert (d["out"] == 0).all() and (d["lse"] == float("-inf")).all()
+    cs = Case(B + 1, B, N, 700, 300, 40, full=True)
+    d = cs.dev()
+    c.csa2_tree_attn(**d)
+    cs.check(d)
+    same = d["q"].clone()
+    c.csa2_tree_attn(**{**d, "q": same, "out": same})
+    assert torch.equal(same, d["out"])
+    empty = {**d, "codes": d["codes"][:0], "scales": d["scales"][:0]}
+    some, none = torch.empty_like(same), torch.empty_like(same)
+    c.csa2_device_flags()
+    c.csa2_tree_attn(**{**d, "idx": torch.full_like(d["idx"], -1), "out": some})
+    assert c.csa2_device_flags() == 0
+    c.csa2_tree_attn(**{**empty, "out": none})
+    assert c.csa2_device_flags() == c.FLAG_INDEX_OOB and torch.equal(some, none)
+
+
+@pytest.mark.parametrize("scale", [-1e5, 1e5])
+def test_scores_far_from_zero_at_shared_nodes(scale):
+    """A row that leads by more than all errors and 40 is attended alone, whichever CTA of a node holds it."""
+    cs = Case(74, 2, 2, 200, 190, 0, full=True)
+    d = cs.dev()
+    s32 = float(np.float32(scale))
+    c.csa2_tree_attn(**d, softmax_scale=s32)
+    out, led = V.f64(bf16_host(d["out"])), 0
+    for r in range(4):
+        q, rows = V.f64(cs.q[r // 2, r % 2]), V.dequant(cs.codes[cs.idx[r]], cs.scales[cs.idx[r]])
+        sc = q @ rows.T * s32
+        es = 10 * 2.0 ** -22 * (np.abs(q) @ np.abs(rows).T) * abs(s32) + np.abs(sc) * 2.0 ** -22
+        top = np.argsort(sc, -1)[:, ::-1]
+        for h in range(16):
+            if sc[h, top[h, 0]] - sc[h, top[h, 1]] > 2 * es[h].max() + 40:
+                led += 1
+                assert np.array_equal(out[r // 2, r % 2, h], rows[top[h, 0]])
+    assert led > 20
