@@ -20,9 +20,10 @@
 // and the token rows (N = 16 or 32) cost the warps nothing.  matvec_kernel: mma.m16n8k16 from registers, with
 // less to set up.
 //
-// Measured (us, weights from HBM; in brackets at the copy bandwidth): one row x 512 x 4096 4.0 (0.17), 4096 x 4096
-// 6.4 (1.4), 16384 x 8192 17.5 (11.1), 32768 x 16384 55 (44.4); eight rows 4.3, 6.9, 19.9, 66; 32 rows x 16384 x 8192
-// 29 (27.3 with the weight partly in L2), 32768 x 16384 96.
+// Measured (us, weights from HBM; in brackets at the copy bandwidth): one row x 512 x 4096 3.8 (0.17), 4096 x 4096
+// 6.2 (1.4), 16384 x 8192 17.0 (11.1), 32768 x 16384 55 (44.4); eight rows 4.3, 6.8, 19.6, 65; five rows x 8200 x 4112
+// 9.4 (2.8; 8.2 with the weight in L2); 32 rows x 16384 x 8192 28.7 (26.9 with the weight partly in L2), 32768 x 16384
+// 92.  Packing 16384 x 8192: 65 us (22 at the copy bandwidth), once per weight: a lane reads eight bytes of its own row.
 // What bounds matvec_kernel: 4 us of launch, staging and exchange, behind which the copies alone take as long as the
 // products alone (16384 x 8192, eight rows: 17.8 and 17.7 with those 4; more blocks under way, more CTAs or even shares
 // of the rows gain nothing).  matvec_tc_kernel: 6 us before the first product (x, 128 KB a CTA), then about 560 cycles
@@ -781,8 +782,9 @@ cudaError_t launch_tc(const mv::Params& g, int C, int sms, cudaStream_t st) {
 template <int TG>
 cudaError_t launch_wr(const Params& p, int sms, cudaStream_t st) {
   // The most CTAs that run at once and have a block for every warp, of these the widest (a CTA stages x for all its
-  // rows).  Measured, us at one row x 8200 x 4112: 264 CTAs of 8 row blocks 9.0, 258 of 2 10.9, twice as many of 4 13;
-  // at one row x 512 x 4096: 64 CTAs of 2 row blocks 4.4, 128 of 1 (half the warps without a block) 4.8.
+  // rows).  Measured, us, weights from HBM, at five rows x 8200 x 4112: 264 CTAs of 8 row blocks 9.3, 260 of 4 9.1, 132
+  // of 8 9.0, 258 of 2 11.0, 520 of 4 13.1; at one row 8.7, 8.4, 8.2, 9.0, 12.1; at one row x 512 x 4096: 64 CTAs of 2
+  // row blocks 3.7, 128 of 1 (half the warps without a block) 3.8, 32 of 2 4.3.
   int best_wr = 1, best_c = 1;
   int64_t best = 0;
   for (int wr = 8; wr >= 1; wr /= 2)

@@ -5,7 +5,7 @@
 // A node has 16 heads and its own selected rows, so its two products are [16 x 512] x [512 x rows] and
 // [16 x rows] x [rows x 512]: the head count is exactly the M of mma.m16n8k16, which multiplies from registers, so
 // that the dequantised rows never touch shared memory (the tcgen05 kernels of the chain's attention write them
-// there once and have them read twice; a chain of the same rows takes them 1.3 to 1.7 times as long):
+// there once and have them read twice; a chain of the same rows takes them 1.5 to 1.8 times as long):
 //  - four warps split the 512 channels, lane (g, t) of a warp reads 16 bytes of codes of row g: 32
 //    consecutive channels of its warp's 128.  Channels may be summed in any order, so the lane's j-th
 //    channel pair serves as the j-th pair of the B fragment of S = Q K^T as it is, with Q's fragment
@@ -15,16 +15,17 @@
 //    consecutive channels, stored as whole 16-byte pieces;
 //  - rows arrive by cp.async a few steps ahead; between the warps only partial scores and P pass.
 //
-// What bounds it.  A step of 16 rows needs 256 cycles of an SM's tensor pipe (2.0 an instruction), about 290 issue
-// slots of each scheduler and as many cycles of the shared-memory pipe (128 of them transposes), and takes a CTA
-// 1000 cycles from end to end alone.  Three CTAs an SM (their registers) give 560 cycles a step: no pipe is
-// full, the chain of a step is.  64 sequences x 32 nodes, 512 selected and 128 window rows: 162 us on the device,
-// 0.17 of the bf16 peak over the plain count of operations; 64 x 8 nodes 53 us.  Measured and not kept: rows
-// dequantised a second time for P V instead of transposed (181 us), Q in shared memory (205), steps of
-// 32 rows (179), a pipeline of three steps with two CTAs an SM (190), plain loads one step ahead (223), bulk
-// copies per row (307).  One sequence of five nodes, eight CTAs a node, 9.0 us: 4100 cycles until the lists stand, 1400
-// until the first rows do, 5000 for six steps, 5800 for the merge and its two barriers (parts pushed to the CTA that
-// finishes a head 10.2 us, 16 CTAs a node 8.9 and with nine nodes 10.5 instead of 9.3).
+// What bounds it.  A step of 16 selected rows needs 256 cycles of an SM's tensor pipe (2.0 an instruction; a step of
+// window rows 384, for P's second term), about 290 issue slots of each scheduler and as many cycles of the
+// shared-memory pipe (128 of them transposes), and takes a CTA 960 cycles from end to end alone (1180).  Three CTAs an
+// SM (their registers) give 560 cycles a step (725): no pipe is full, the chain of a step is.  64 sequences x 32 nodes,
+// all real, 512 selected and 128 window rows: 185 us on the device (4.5 waves of 456 nodes), 0.12 of the bf16 peak over
+// the plain count of operations; 64 x 8 nodes 56 us.  Measured and not kept, for a ragged 64 x 32 batch that took 162
+// to 169 us in this form: rows dequantised a second time for P V instead of transposed (181 us), Q in shared memory
+// (205), steps of 32 rows (179), a pipeline of three steps with two CTAs an SM (190), plain loads one step ahead (223),
+// bulk copies per row (307).  One sequence of five nodes, eight CTAs a node, 9.1 us: 4100 cycles until the lists stand,
+// 1400 until the first rows do, 5000 for five or six steps, 5800 for the merge and its two barriers (parts pushed to the
+// CTA that finishes a head 10.2 us, 16 CTAs a node 8.9 and with nine nodes 10.5 instead of 9.3).
 //
 // FP4 rows are multiplied as f16: a code times a scale has at most 6 significant bits and lies between
 // 2^-10 and 2688, so the row is exact.  Q is scaled per head by a power of two that puts its largest

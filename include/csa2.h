@@ -490,6 +490,7 @@ csa2_status csa2_paged_append(const uint16_t* kv_new, const uint16_t* ki_new, co
  *   idx     int32 [B*N][k] cache rows (k <= 512), n_valid int32 [B*N] or NULL: entries < 0 or at or past
  *           n_valid[r] are empty, entries >= cap are empty and set CSA2_FLAG_INDEX_OOB.
  *   swa     bf16 [B][W-1+N][512]: W - 1 committed rows, oldest first, then the N drafted rows; or NULL with W = 0.
+ *           A window kept in 8 bits (CSA2_SWA_E4M3) is widened to bf16 first, which is exact.
  *   win_len int32 [B] or NULL (W - 1): the last win_len[b] committed rows hold tokens.
  *   out     bf16 [B][N][16][512] (may be q itself; out and lse overlap nothing else); lse fp32 [B][N][16]
  *           (nullable), natural log; a node with no rows (W = 0 and nothing selected) gets out = 0 and lse = -inf.
@@ -508,7 +509,7 @@ csa2_status csa2_tree_attn(const uint16_t* q, int B, int N, const int32_t* paren
  * csa2_fp4_pack_weight lays a row-major weight out once in the order the product reads it:
  *   codes uint8 [n_out][n_in/2], scales uint8 [n_out][n_in/16] -> packed, csa2_fp4_packed_bytes(n_out, n_in)
  *   bytes.  n_in a multiple of 16.
- * csa2_fp4_matvec: x bf16 [m][n_in], m <= CSA2_MAX_MV_ROWS; row_scale fp32 [n_out] or NULL (1); y [m][n_out],
+ * csa2_fp4_matvec: x bf16 [m][n_in], n_in > 0, m <= CSA2_MAX_MV_ROWS; row_scale fp32 [n_out] or NULL (1); y [m][n_out],
  *   bf16 (y_fp32 = 0) or fp32 (y_fp32 = 1).  Accumulated in fp32, rounded once.  No workspace.  y overlaps
  *   none of the inputs, packed none of its sources.
  */
