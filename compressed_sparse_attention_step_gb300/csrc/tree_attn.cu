@@ -656,11 +656,11 @@ extern "C" csa2_status csa2_tree_attn(const uint16_t* q, int B, int N, const int
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
   p.N = N, p.k = k, p.W = W, p.row0 = 0, p.flags = flags;
   // Few nodes are shared by several CTAs each, which costs a merge.  Measured, us for 1 / 2 / 4 / 8 CTAs a node, 512
-  // selected and 128 window rows: 5 nodes 23.5 / 16.6 / 11.3 / 9.3, 20 nodes 23.6 / 16.5 / 11.5 / 11.2, 38 nodes 23.9 /
-  // 16.8 / 13.4 / 14.6, 80 nodes 24.0 / 20.3 / 17.0 / 26.7, 95 nodes 24.0 / 20.6 / 17.3 / 27.7, 104 nodes 24.0 / 20.9 /
-  // 17.3 / 32.2, 112 nodes (whose clusters of four no longer run at once) 24.0 / 20.7 / 25.8 / 35.6.  Fewer rows, for
-  // 1 / 4: 95 nodes 256 rows 12.5 / 11.9, 192 of them 10.8 / 11.9, 128 of them 8.4 / 10.0; 38 nodes 128 rows 8.3 / 8.1,
-  // 64 of them 6.5 / 7.9; for 1 / 8: 5 nodes 128 rows 8.0 / 7.1, 64 of them 6.1 / 7.0.
+  // selected and 128 window rows: 5 nodes 24.0 / 16.6 / 11.6 / 9.3, 20 nodes 24.2 / 16.9 / 11.9 / 11.2, 38 nodes 24.4 /
+  // 17.1 / 14.0 / 14.7, 80 nodes 24.7 / 21.2 / 18.1 / 26.8, 95 nodes 24.6 / 21.8 / 18.2 / 27.9, 104 nodes 24.6 / 21.9 /
+  // 18.3 / 32.4, 112 nodes (whose clusters of four no longer run at once) 24.6 / 21.8 / 26.8 / 35.6.  Fewer rows, for
+  // 1 / 4: 95 nodes 256 rows 12.2 / 11.8, 192 of them 11.5 / 12.3, 128 of them 8.3 / 10.0; 38 nodes 128 rows 8.2 / 7.9,
+  // 64 of them 6.2 / 7.9; for 1 / 8: 5 nodes 128 rows 7.8 / 7.1, 64 of them 5.9 / 6.9.
   auto ctas = [&](int64_t r) {
     if (k + W < 128 || r * 8 > 5 * int64_t(sms) || (r * 4 > sms && k + W < 256)) return 1;
     return r * 8 <= sms ? 8 : 4;
@@ -675,15 +675,16 @@ extern "C" csa2_status csa2_tree_attn(const uint16_t* q, int B, int N, const int
     }
   };
   // Three nodes an SM run at once.  A few nodes behind the last full wave would take as long as a whole one: they are
-  // shared by several CTAs each, in a second launch.  Measured, us for two launches / one, 512 selected and 128 window
-  // rows: 58 x 8 nodes 49.8 / 59.1, 64 x 8 54.6 / 59.8, 247 x 2 57.2 / 62.1, 120 x 8 96.4 / 98.3; 256 and 128 rows: 58 x 8
-  // 35.5 / 39.1, 64 x 8 38.6 / 39.8; fewer rows than 320 gain nothing (256 and none 27.1 / 28.4, 29.6 / 29.2; 64 and 128
-  // 24.9 / 24.0; 64 and none 16.8 / 13.6), nor do more nodes than half the SMs (546 x 1, 90 behind the wave: 512 and
-  // none 51.2 / 50.6, 384 and none 41.6 / 40.4).  Not with n_nodes: nodes that are not real leave room in the last wave
-  // (of 64 x 8 nodes, 437 to 496 real ones took 46.3 us in one launch).
+  // shared by several CTAs each, in a second launch, where there are rows to pay for it.  Measured, us for two launches /
+  // one, selected + window rows: behind one wave, 58 x 8 nodes 512 + 128 50.8 / 60.6, 192 + 128 33.3 / 36.0, 256 + 0 27.0 /
+  // 28.2, 64 + 0 16.8 / 13.6; 64 x 8 nodes 56.2 / 61.3, 36.3 / 36.9, 29.5 / 28.9, 18.4 / 14.1; behind two, 120 x 8 nodes
+  // 512 + 128 98.1 / 99.9, 384 + 128 83.6 / 84.1, 256 + 128 68.4 / 67.8, 256 + 0 47.9 / 45.7; more nodes than half the SMs
+  // gain little or nothing (546 x 1, 90 behind the wave: 512 + 128 66.1 / 66.4, 512 + 0 50.9 / 50.0).  Not with n_nodes:
+  // nodes that are not real leave room in the last wave (of 64 x 8 nodes, 437 to 496 real ones took 46.3 us in one).
   const int64_t wave = 3 * int64_t(sms), rest = rows % wave;
   cudaError_t e;
-  if (!n_nodes && rows > wave && rest > 0 && 2 * rest <= sms && k + W >= 320 && ctas(rest) > 1) {
+  if (!n_nodes && rows > wave && rest > 0 && 2 * rest <= sms && k + W >= (rows < 2 * wave ? 320 : 512) &&
+      ctas(rest) > 1) {
     e = launch(0, rows - rest);
     if (e == cudaSuccess) e = launch(rows - rest, rest);
   } else {

@@ -509,3 +509,13 @@ def test_scores_far_from_zero_at_shared_nodes(scale):
                 led += 1
                 assert np.array_equal(out[r // 2, r % 2, h], rows[top[h, 0]])
     assert led > 20
+
+
+def test_a_few_nodes_behind_two_waves():
+    B, N, k, W = (6 * SMS + 30) // 6, 6, 500, 12
+    cs = Case(77, B, N, k + 3, k, W)
+    cs.n_nodes[:] = N
+    d = cs.dev()
+    d["n_nodes"] = None
+    c.csa2_tree_attn(**d)
+    cs.check(d)
