@@ -21,7 +21,10 @@ CODE_BYTES, SCALE_BYTES = 256, 32
 MAX_LAYERS = 16
 MAX_TREE, MAX_SEQS, MAX_MV_ROWS = 64, 8192, 32
 MODE_FULL, MODE_REINDEX, MODE_REUSE = 0, 1, 2
+MAX_EXPERTS, MAX_EXPERTS_PER_TOKEN, MAX_ROUTE_TOKENS, MAX_RANK, MAX_VOCAB, MAX_TOP = 1024, 16, 131072, 128, 1 << 20, 32
 OP_TOPK, OP_BLOCK_POOL, OP_SPARSE_ATTN, OP_GROUP_STEP, OP_INDEX_SELECT_PREFILL, OP_MERGE_PAIRS = 1, 2, 3, 4, 5, 6
+OP_EXPERT_ROUTE, OP_FP4_GROUPED = 7, 8
+ACT_NONE, ACT_SWIGLU = 0, 1
 FLAG_APPEND_OOB, FLAG_INDEX_OOB, FLAG_TIMEOUT, FLAG_PAGES_OUT = 1, 2, 4, 8
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_WORKSPACE, ERR_TOO_LARGE = 0, 1, 2, 3, 4, 5
 SWA_BF16, SWA_E4M3 = 0, 1
@@ -107,6 +110,11 @@ def lib():
             "csa2_fp4_packed_bytes": [I64, I64],
             "csa2_fp4_pack_weight": [P, P, I64, I64, P, P],
             "csa2_fp4_matvec": [P, I32, P, I64, I64, P, P, I32, P],
+            "csa2_expert_route": [P, I32, I32, I32, P, P, I32, F32, P, P, P, P, P, P, SZ, P],
+            "csa2_fp4_grouped": [P, I64, I64, P, I32, I64, P, P, P, I64, I32, P, I32, P, SZ, P],
+            "csa2_expert_combine": [P, I32, I64, P, P, I64, I32, I64, P, P, I32, P],
+            "csa2_lora_add": [P, I32, I32, P, P, I32, I32, I32, P, P, P, P, P, I32, P],
+            "csa2_token_logprobs": [P, I32, I32, I32, I64, P, I32, F32, P, P, P, I32, P, P, P],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -634,3 +642,149 @@ def csa2_fp4_matvec(x, packed, y, *, row_scale=None, stream=None):
         _on(stream, dev))
     if st:
         _check("csa2_fp4_matvec", st)
+
+
+# ---------------------------------------------------------------------------------------------
+# the experts of a layer, adapters of many requests, log probabilities
+# ---------------------------------------------------------------------------------------------
+@functools.lru_cache(maxsize=256)
+def route_workspace_size(m, E):
+    """Bytes of csa2_expert_route's workspace for m tokens and E experts."""
+    return workspace_size(OP_EXPERT_ROUTE, B=m, n=E)
+
+
+@functools.lru_cache(maxsize=256)
+def grouped_workspace_size(n_x, n_in):
+    """Bytes of csa2_fp4_grouped's workspace for n_x rows of x with n_in channels."""
+    return workspace_size(OP_FP4_GROUPED, B=n_x, cap=n_in)
+
+
+def _scratch(ws, need, device, dev, stream):
+    """(pointer, bytes, the tensor to keep) of a workspace: the caller's, or a new one where it gives none."""
+    if ws is None:
+        if not need:
+            return None, 0, None
+        ws = _torch().empty(need, dtype=_torch().uint8, device=device)
+        if stream is not None and ws.is_cuda:  # its memory is not handed on before that stream is done with it
+            ws.record_stream(stream)
+    return _arg(ws, "ws", _U8, (ws.numel(),) if hasattr(ws, "numel") else (), dev), _nbytes(ws), ws
+
+
+def csa2_expert_route(logits, experts, weights, offsets, src, pos, *, bias=None, active=None, renorm=True, scale=1.0,
+                      ws=None, stream=None):
+    """The k experts of each token by router logits fp32 [m, E] (+ bias fp32 [E]): experts int32 [m, k], weights fp32
+    [m, k] (softmax over the chosen, or over all with renorm=False), and the tokens in order of expert: offsets int32
+    [E + 1], src int32 [m * k] the tokens of each expert, pos int32 [m, k] the places of a token's entries in src.
+    active int32 [m]: tokens with 0 are padding."""
+    dev = _device()
+    m, E = _dims(logits, "logits", 2)
+    k = _dims(experts, "experts", 2)[1]
+    wp, wn, ws = _scratch(ws, route_workspace_size(m, E), logits.device, dev, stream)
+    st = lib().csa2_expert_route(
+        _arg(logits, "logits", _F32, (m, E), dev), m, E, k, _arg(bias, "bias", _F32, (E,), dev),
+        _arg(active, "active", _I32, (m,), dev), bool(renorm), scale, _arg(experts, "experts", _I32, (m, k), dev),
+        _arg(weights, "weights", _F32, (m, k), dev), _arg(offsets, "offsets", _I32, (E + 1,), dev),
+        _arg(src, "src", _I32, (m * k,), dev), _arg(pos, "pos", _I32, (m, k), dev), wp, wn, _on(stream, dev))
+    if st:
+        _check("csa2_expert_route", st)
+
+
+def fp4_pack_experts(codes, scales):
+    """The experts' weights, codes uint8 [E, n_out, n_in/2] and scales uint8 [E, n_out, n_in/16], packed for
+    csa2_fp4_grouped: uint8 [E, bytes]."""
+    E, n_out, half = _dims(codes, "codes", 3)
+    groups = _dims(scales, "scales", 3)[2]
+    packed = _torch().empty((E, _packed_bytes(n_out, 2 * half)), dtype=_torch().uint8, device=codes.device)
+    if n_out % 32 == 0 and E * n_out <= 1 << 28:  # whole row blocks: the experts follow one another
+        csa2_fp4_pack_weight(codes.reshape(-1, half), scales.reshape(-1, groups), packed.view(-1))
+        return packed
+    for e in range(E):
+        # (an expert's slice need not start on 16 bytes; a copy does)
+        c, s = (t[e] if t[e].data_ptr() % 16 == 0 else t[e].clone() for t in (codes, scales))
+        csa2_fp4_pack_weight(c, s, packed[e])
+    return packed
+
+
+def csa2_fp4_grouped(x, packed, offsets, y, *, src=None, row_scale=None, act=ACT_NONE, ws=None, stream=None):
+    """Products of ragged groups of rows with their experts' 4-bit weights: rows offsets[e] .. offsets[e+1] - 1 of
+    y [rows, n_out] (bf16 or fp32) are those of x bf16 [n_x, n_in] at src int32 [rows] (None: the same rows) times
+    packed[e] (fp4_pack_experts), times row_scale fp32 [E, n_out].  act=ACT_SWIGLU: y [rows, n_out / 2] from the even
+    (gate) and odd (up) rows of the weight.  ws: grouped_workspace_size(n_x, n_in) bytes, allocated where None."""
+    dev = _device()
+    n_x, n_in = _dims(x, "x", 2)
+    rows, width = _dims(y, "y", 2)
+    E = _dims(packed, "packed", 2)[0]
+    n_out = 2 * width if act == ACT_SWIGLU else width
+    if src is None and n_x < rows:
+        raise ValueError(f"x: expected at least {rows} rows, got {n_x}")
+    fp32 = y.dtype in _F32
+    wp, wn, ws = _scratch(ws, grouped_workspace_size(n_x, n_in), x.device, dev, stream)
+    st = lib().csa2_fp4_grouped(
+        _arg(x, "x", _BF16, (n_x, n_in), dev), n_x, n_in,
+        _arg(packed, "packed", _U8, (E, _packed_bytes(n_out, n_in)), dev), E, n_out,
+        _arg(row_scale, "row_scale", _F32, (E, n_out), dev), _arg(offsets, "offsets", _I32, (E + 1,), dev),
+        _arg(src, "src", _I32, (rows,), dev), rows, act, _arg(y, "y", _F32 if fp32 else _BF16, (rows, width), dev), fp32,
+        wp, wn, _on(stream, dev))
+    if st:
+        _check("csa2_fp4_grouped", st)
+
+
+def csa2_expert_combine(y, pos, weights, out, *, add=None, stream=None):
+    """out [m, n] (bf16 or fp32) = add bf16 [m, n] + sum over j of weights fp32 [m, k] times row pos int32 [m, k] of
+    y [rows, n] (bf16 or fp32); negative entries of pos are skipped."""
+    dev = _device()
+    rows, n = _dims(y, "y", 2)
+    m, k = _dims(pos, "pos", 2)
+    y32, out32 = getattr(y, "dtype", None) in _F32, getattr(out, "dtype", None) in _F32
+    st = lib().csa2_expert_combine(
+        _arg(y, "y", _F32 if y32 else _BF16, (rows, n), dev), y32, rows, _arg(pos, "pos", _I32, (m, k), dev),
+        _arg(weights, "weights", _F32, (m, k), dev), m, k, n, _arg(add, "add", _BF16, (m, n), dev),
+        _arg(out, "out", _F32 if out32 else _BF16, (m, n), dev), out32, _on(stream, dev))
+    if st:
+        _check("csa2_expert_combine", st)
+
+
+def csa2_lora_add(x, a, b, adapter, base, out, *, ranks=None, scale=None, stream=None):
+    """out [m, n_out] = base (both bf16 or both fp32; out may be base) + scale[l] * x A_l^T B_l^T for each row's adapter
+    l = adapter int32 [m] (negative: none): x bf16 [m, n_in], a bf16 [L, r, n_in], b bf16 [L, n_out, r], ranks int32 [L]
+    the ranks in use, scale fp32 [L]."""
+    dev = _device()
+    m, n_in = _dims(x, "x", 2)
+    L, r = _dims(a, "a", 3)[:2]
+    n_out = _dims(base, "base", 2)[1]
+    fp32 = base.dtype in _F32
+    kind = _F32 if fp32 else _BF16
+    st = lib().csa2_lora_add(
+        _arg(x, "x", _BF16, (m, n_in), dev), m, n_in, _arg(a, "a", _BF16, (L, r, n_in), dev),
+        _arg(b, "b", _BF16, (L, n_out, r), dev), L, r, n_out, _arg(adapter, "adapter", _I32, (m,), dev),
+        _arg(ranks, "ranks", _I32, (L,), dev), _arg(scale, "scale", _F32, (L,), dev), _arg(base, "base", kind, (m, n_out), dev),
+        _arg(out, "out", kind, (m, n_out), dev), fp32, _on(stream, dev))
+    if st:
+        _check("csa2_lora_add", st)
+
+
+def csa2_token_logprobs(logits, tokens=None, logprobs=None, *, lse=None, entropy=None, top_ids=None, top_logprobs=None,
+                        inv_temp=1.0, stream=None):
+    """Under softmax(inv_temp * logits [rows, V]) (bf16 or fp32; rows may be apart, as in a slice of a wider array):
+    logprobs fp32 [rows, n_tok] of tokens int32 [rows, n_tok] (negative: padding, 0), lse and entropy fp32 [rows], and
+    the likeliest tokens top_ids int32 [rows, n] with top_logprobs fp32 [rows, n]."""
+    dev = _device()
+    rows, V = _dims(logits, "logits", 2)
+    n_tok = _dims(tokens, "tokens", 2)[1] if tokens is not None else 0
+    top = top_ids if top_ids is not None else top_logprobs
+    n_top = _dims(top, "top_ids" if top_ids is not None else "top_logprobs", 2)[1] if top is not None else 0
+    fp32 = logits.dtype in _F32
+    if not fp32 and logits.dtype not in _BF16:
+        raise TypeError(f"logits: dtype {logits.dtype} not in {_F32 + _BF16}")
+    if logits.get_device() != dev:
+        raise ValueError(f"logits: expected a tensor on the current device cuda:{dev}, got one on {logits.device}")
+    ld = logits.stride(0) if rows > 1 else V
+    if (V > 1 and logits.stride(1) != 1) or ld < V:
+        raise ValueError(f"logits: expected rows of neighbouring elements that do not overlap, got strides {logits.stride()}")
+    st = lib().csa2_token_logprobs(
+        logits.data_ptr(), fp32, rows, V, ld, _arg(tokens, "tokens", _I32, (rows, n_tok), dev), n_tok, inv_temp,
+        _arg(logprobs, "logprobs", _F32, (rows, n_tok), dev), _arg(lse, "lse", _F32, (rows,), dev),
+        _arg(entropy, "entropy", _F32, (rows,), dev), n_top, _arg(top_ids, "top_ids", _I32, (rows, n_top), dev),
+        _arg(top_logprobs, "top_logprobs", _F32, (rows, n_top), dev), _on(stream, dev))
+    if st:
+        _check("csa2_token_logprobs", st)

@@ -17,7 +17,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIBDIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(LIBDIR, "libcsa2.so")
 SOURCES = ["fp4.cu", "index_score.cu", "topk.cu", "attn.cu", "attn_ws.cu", "attn_pair.cu", "attn_static.cu", "prefill.cu", "group.cu", "shard.cu",
-           "pages.cu", "tree_attn.cu", "matvec.cu"]
+           "pages.cu", "tree_attn.cu", "matvec.cu", "experts.cu", "grouped.cu", "adapters.cu", "logprobs.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include")]
 
@@ -31,7 +31,7 @@ def nvcc() -> str:
 
 def _deps():
     files = [os.path.join(CSRC, s) for s in SOURCES]
-    files += [os.path.join(CSRC, h) for h in ("common.cuh", "attn_common.cuh", "matvec_plan.h")]
+    files += [os.path.join(CSRC, h) for h in ("common.cuh", "attn_common.cuh", "cluster.cuh", "matvec_plan.h")]
     files += [os.path.join(ROOT, "include", "csa2.h")]
     return files
 

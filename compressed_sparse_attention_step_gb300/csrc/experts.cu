@@ -1,0 +1,376 @@
+// The experts of a layer around their products: each token's experts and weights from its router logits, the tokens
+// in order of expert, and the weighted sum of the experts' outputs.
+//
+// Order.  A token has an expert at most once, so a block of tokens is, for each expert, a bit mask over the block's
+// tokens: the number of bits is the block's share of the expert's list, the bits below a token's own are its place in
+// it.  Masks are set by atomic ORs, whose order changes nothing; the lists are in order of token whatever the schedule.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "cluster.cuh"
+
+namespace csa2 {
+namespace moe {
+
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kMaxE = CSA2_MAX_EXPERTS, kMaxK = CSA2_MAX_EXPERTS_PER_TOKEN;
+constexpr int kBlocks = 256;  // token blocks at most
+constexpr int kMaxM = CSA2_MAX_ROUTE_TOKENS;
+
+// Tokens of a block: 64, and twice that until there are few enough blocks for each to add up all their counts.
+inline int block_tokens(int64_t m) {
+  int t = 64;
+  while ((m + t - 1) / t > kBlocks) t *= 2;
+  return t;
+}
+
+struct Params {
+  const float *logits, *bias;
+  const int32_t* active;
+  int m, E, k, renorm, tokens;  // tokens: of a block
+  float scale;
+  int32_t *experts, *offsets, *src, *pos;
+  float* weights;
+  uint32_t* counts;  // [blocks][E]
+};
+
+// One warp: the k largest keys of a token, the lowest expert first among equals; lane j gets the j-th.
+template <int NE>
+__device__ __forceinline__ void choose(const Params& p, int t, int lane) {
+  const float* l = p.logits + int64_t(t) * p.E;
+  uint32_t key[NE];  // 0: none, or taken
+  float x[NE];
+#pragma unroll
+  for (int i = 0; i < NE; ++i) {
+    const int e = lane + 32 * i;
+    x[i] = e < p.E ? __ldg(l + e) : -INFINITY;
+  }
+#pragma unroll
+  for (int i = 0; i < NE; ++i) {
+    const int e = lane + 32 * i;
+    float v = p.bias && e < p.E ? __fadd_rn(x[i], __ldg(p.bias + e)) : x[i];
+    if (v != v) v = -INFINITY;
+    key[i] = e < p.E ? score_key(v) : 0u;
+  }
+  int mine = -1;
+  for (int j = 0; j < p.k; ++j) {
+    uint32_t best = 0;
+    int at = 0;
+#pragma unroll
+    for (int i = 0; i < NE; ++i)
+      if (key[i] > best) best = key[i], at = i;
+    const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+    const uint32_t e = __reduce_min_sync(0xffffffffu, best == top ? uint32_t(lane + 32 * at) : 0xFFFFFFFFu);
+    if (lane == j) mine = int(e);
+    if ((e & 31u) == uint32_t(lane)) {
+#pragma unroll
+      for (int i = 0; i < NE; ++i)
+        if (i == int(e >> 5)) key[i] = 0u;
+    }
+  }
+  float w = mine >= 0 ? __ldg(l + mine) : -INFINITY;
+  if (w != w) w = -INFINITY;
+  // softmax over the chosen, or over all
+  float m = w;
+  if (!p.renorm) {
+#pragma unroll
+    for (int i = 0; i < NE; ++i) m = fmaxf(m, x[i]);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  auto part = [&](float v) { return !(v > -INFINITY) ? 0.f : v == m ? 1.f : expf(v - m); };
+  w = part(w);
+  float s = w;
+  if (!p.renorm) {
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) s += part(x[i]);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (lane < p.k) {
+    const bool on = !p.active || p.active[t] != 0;
+    p.experts[int64_t(t) * p.k + lane] = on ? mine : -1;
+    p.weights[int64_t(t) * p.k + lane] = on && s > 0.f ? w / s * p.scale : 0.f;
+  }
+}
+
+// The block's masks from the experts chosen for its tokens.
+__device__ __forceinline__ void set_masks(const Params& p, uint32_t* mask, int t0, int t1, int words) {
+  for (int i = threadIdx.x; i < (t1 - t0) * p.k; i += kThreads) {
+    const int t = i / p.k, e = p.experts[int64_t(t0) * p.k + i];
+    if (e >= 0) atomicOr(&mask[e * words + (t >> 5)], 1u << (t & 31));
+  }
+}
+
+// Chooses for a block of tokens, and counts its share of each expert's list.
+template <int NE>
+__global__ void __launch_bounds__(kThreads) choose_kernel(const Params p) {
+  extern __shared__ uint32_t mask[];
+  pdl_wait();
+  pdl_trigger();
+  const int t0 = int(blockIdx.x) * p.tokens, t1 = min(p.m, t0 + p.tokens), words = p.tokens / 32;
+  for (int i = threadIdx.x; i < p.E * words; i += kThreads) mask[i] = 0u;
+  for (int t = t0 + int(threadIdx.x >> 5); t < t1; t += kWarps) choose<NE>(p, t, int(threadIdx.x & 31));
+  __syncthreads();
+  set_masks(p, mask, t0, t1, words);
+  __syncthreads();
+  for (int e = threadIdx.x; e < p.E; e += kThreads) {
+    uint32_t n = 0;
+    for (int w = 0; w < words; ++w) n += __popc(mask[e * words + w]);
+    p.counts[int64_t(blockIdx.x) * p.E + e] = n;
+  }
+}
+
+// Places of a block's tokens in the lists: the experts before, the blocks before, the block's tokens before.
+// kAlone: the only block, which chooses too.
+template <int NE, bool kAlone>
+__global__ void __launch_bounds__(kThreads) order_kernel(const Params p) {
+  extern __shared__ uint32_t mask[];
+  __shared__ uint32_t base[kMaxE], tmp[32];
+  pdl_wait();
+  pdl_trigger();
+  const int t0 = int(blockIdx.x) * p.tokens, t1 = min(p.m, t0 + p.tokens), words = p.tokens / 32;
+  for (int i = threadIdx.x; i < p.E * words; i += kThreads) mask[i] = 0u;
+  if (kAlone)
+    for (int t = t0 + int(threadIdx.x >> 5); t < t1; t += kWarps) choose<NE>(p, t, int(threadIdx.x & 31));
+  __syncthreads();
+  set_masks(p, mask, t0, t1, words);
+  __syncthreads();
+  uint32_t listed = 0;  // entries of the experts of this round's blocks before
+  for (int e0 = 0; e0 < p.E; e0 += kThreads) {
+    const int e = e0 + int(threadIdx.x);
+    uint32_t all = 0, before = 0;
+    if (e < p.E) {
+      if (kAlone) {
+        for (int w = 0; w < words; ++w) all += __popc(mask[e * words + w]);
+      } else {
+#pragma unroll 16
+        for (int b = 0; b < int(gridDim.x); ++b) {
+          const uint32_t c = p.counts[int64_t(b) * p.E + e];
+          all += c;
+          before += b < int(blockIdx.x) ? c : 0u;
+        }
+      }
+    }
+    uint32_t total;
+    const uint32_t at = listed + block_exclusive_scan(all, tmp, &total);
+    if (e < p.E) {
+      base[e] = at + before;
+      if (blockIdx.x == 0) p.offsets[e] = int(at);
+    }
+    listed += total;
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) p.offsets[p.E] = int(listed);
+  __syncthreads();
+  for (int i = threadIdx.x; i < (t1 - t0) * p.k; i += kThreads) {
+    const int t = i / p.k, e = p.experts[int64_t(t0) * p.k + i];
+    int at = -1;
+    if (e >= 0) {
+      uint32_t n = base[e];
+      for (int w = 0; w < (t >> 5); ++w) n += __popc(mask[e * words + w]);
+      n += __popc(mask[e * words + (t >> 5)] & ((1u << (t & 31)) - 1u));
+      at = int(n);
+      p.src[at] = t0 + t;
+    }
+    p.pos[int64_t(t0) * p.k + i] = at;
+  }
+  for (int64_t i = int64_t(listed) + int64_t(blockIdx.x) * kThreads + threadIdx.x; i < int64_t(p.m) * p.k;
+       i += int64_t(gridDim.x) * kThreads)
+    p.src[i] = -1;
+}
+
+template <int NE>
+cudaError_t route(const Params& p, cudaStream_t st) {
+  const int blocks = std::max((p.m + p.tokens - 1) / p.tokens, 1);  // (no tokens: the offsets are still written)
+  const size_t smem = size_t(p.E) * (p.tokens / 32) * 4;
+  static std::atomic<uint64_t> done[3];
+  const size_t most = size_t(NE) * 32 * (block_tokens(kMaxM) / 32) * 4;
+  cudaError_t e;
+  if (blocks == 1) return launch_pdl(order_kernel<NE, true>, dim3(1), dim3(kThreads), smem, st, p);
+  if ((e = allow_smem(reinterpret_cast<const void*>(choose_kernel<NE>), most, done[0])) != cudaSuccess) return e;
+  if ((e = allow_smem(reinterpret_cast<const void*>(order_kernel<NE, false>), most, done[1])) != cudaSuccess) return e;
+  if ((e = launch_pdl(choose_kernel<NE>, dim3(unsigned(blocks)), dim3(kThreads), smem, st, p)) != cudaSuccess) return e;
+  return launch_pdl(order_kernel<NE, false>, dim3(unsigned(blocks)), dim3(kThreads), smem, st, p);
+}
+
+struct Combine {
+  const void* y;
+  const int32_t* pos;
+  const float* weights;
+  const uint16_t* add;
+  void* out;
+  int64_t m, n, rows;
+  int k, chunks;  // chunks of a row
+  unsigned int* flags;
+};
+
+template <int V, bool kF32>
+__device__ __forceinline__ void load_row(const void* at, int64_t i, float (&v)[V]) {
+  if (kF32) {
+    const float* q = static_cast<const float*>(at) + i;
+    if (V == 8) {
+      const float4 a = __ldg(reinterpret_cast<const float4*>(q)), b = __ldg(reinterpret_cast<const float4*>(q) + 1);
+      const float w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int j = 0; j < V; ++j) v[j] = w[j];
+    } else if (V == 2) {
+      const float2 a = __ldg(reinterpret_cast<const float2*>(q));
+      v[0] = a.x, v[V - 1] = a.y;
+    } else {
+      v[0] = __ldg(q);
+    }
+  } else {
+    const uint16_t* q = static_cast<const uint16_t*>(at) + i;
+    if (V == 8) {
+      const uint4 a = __ldg(reinterpret_cast<const uint4*>(q));
+      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+      for (int j = 0; j < V / 2; ++j) v[2 * j] = bf16lo(w[j]), v[2 * j + 1] = bf16hi(w[j]);
+    } else if (V == 2) {
+      const uint32_t a = __ldg(reinterpret_cast<const uint32_t*>(q));
+      v[0] = bf16lo(a), v[V - 1] = bf16hi(a);
+    } else {
+      v[0] = bf16f(__ldg(q));
+    }
+  }
+}
+
+// A thread per V neighbouring channels of a token; products and sums in fp32, in the order of the token's experts.
+template <int V, bool kY32, bool kOut32>
+__global__ void __launch_bounds__(256) combine_kernel(const Combine p) {
+  pdl_wait();
+  pdl_trigger();
+  const int64_t it = int64_t(blockIdx.x) * 256 + threadIdx.x, t = it / p.chunks;
+  if (t >= p.m) return;
+  const int64_t c = (it - t * p.chunks) * V;
+  float s[V];
+  if (p.add) {
+    load_row<V, false>(p.add, t * p.n + c, s);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) s[i] = 0.f;
+  }
+  constexpr int kAhead = 4;  // experts whose rows are asked for together
+  for (int j0 = 0; j0 < p.k; j0 += kAhead) {
+    float v[kAhead][V], w[kAhead];
+    bool on[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      on[j] = false;
+      if (j0 + j < p.k) {
+        const int64_t r = __ldg(p.pos + t * p.k + j0 + j);
+        on[j] = r >= 0 && r < p.rows;
+        if (r >= p.rows && c == 0) atomicOr(p.flags, CSA2_FLAG_INDEX_OOB);
+        if (on[j]) w[j] = __ldg(p.weights + t * p.k + j0 + j), load_row<V, kY32>(p.y, r * p.n + c, v[j]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      if (on[j]) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) s[i] = fmaf(w[j], v[j][i], s[i]);
+      }
+  }
+  if (kOut32) {
+    float* o = static_cast<float*>(p.out) + t * p.n + c;
+    if (V == 8) {
+      reinterpret_cast<float4*>(o)[0] = make_float4(s[0], s[V > 1], s[V > 2 ? 2 : 0], s[V > 3 ? 3 : 0]);
+      reinterpret_cast<float4*>(o)[1] = make_float4(s[V > 4 ? 4 : 0], s[V > 5 ? 5 : 0], s[V > 6 ? 6 : 0], s[V > 7 ? 7 : 0]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) o[i] = s[i];
+    }
+  } else {
+    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + t * p.n + c;
+    uint32_t h[(V + 1) / 2];
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(s[2 * i], s[2 * i + 1]);
+      h[i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    if (V == 8) *reinterpret_cast<uint4*>(o) = make_uint4(h[0], h[V > 2], h[V > 4 ? 2 : 0], h[V > 6 ? 3 : 0]);
+    else if (V == 2) *reinterpret_cast<uint32_t*>(o) = h[0];
+    else o[0] = __float2bfloat16_rn(s[0]);
+  }
+}
+
+template <int V>
+cudaError_t combine(Combine p, bool y32, bool out32, cudaStream_t st) {
+  p.chunks = int(p.n / V);
+  const int64_t blocks = (p.m * p.chunks + 255) / 256;
+  if (blocks > 0x7FFFFFFFll) return cudaErrorInvalidValue;
+  const dim3 grid = dim3(unsigned(blocks)), block(256);
+  if (y32) return out32 ? launch_pdl(combine_kernel<V, true, true>, grid, block, 0, st, p)
+                        : launch_pdl(combine_kernel<V, true, false>, grid, block, 0, st, p);
+  return out32 ? launch_pdl(combine_kernel<V, false, true>, grid, block, 0, st, p)
+               : launch_pdl(combine_kernel<V, false, false>, grid, block, 0, st, p);
+}
+
+}  // namespace moe
+
+size_t expert_route_ws_bytes(int64_t m, int64_t E) {
+  if (m <= 0 || E <= 0 || m > moe::kMaxM || E > moe::kMaxE) return 0;
+  const int t = moe::block_tokens(m);
+  const int64_t blocks = (m + t - 1) / t;
+  return blocks > 1 ? size_t(blocks * E) * 4 : 0;
+}
+
+}  // namespace csa2
+
+extern "C" csa2_status csa2_expert_route(const float* logits, int m, int E, int k, const float* bias, const int32_t* active,
+                                         int renorm, float scale, int32_t* experts, float* weights, int32_t* offsets,
+                                         int32_t* src, int32_t* pos, void* ws, size_t ws_bytes, csa2_stream_t stream) {
+  using namespace csa2;
+  using namespace csa2::moe;
+  if (m < 0 || m > kMaxM || E < 1 || E > kMaxE || k < 1 || k > kMaxK || k > E) return CSA2_ERR_INVALID_ARG;
+  if (!offsets || !al(offsets, 4)) return CSA2_ERR_INVALID_ARG;
+  if (m > 0 && (!logits || !experts || !weights || !src || !pos)) return CSA2_ERR_INVALID_ARG;
+  if (!al(logits, 16) || !al(bias, 4) || !al(active, 4) || !al(experts, 4) || !al(weights, 4) || !al(src, 4) || !al(pos, 4) ||
+      !al(ws, 16))
+    return CSA2_ERR_INVALID_ARG;
+  const size_t need = expert_route_ws_bytes(m, E);
+  if (need && (!ws || ws_bytes < need)) return CSA2_ERR_WORKSPACE;
+  const Span spans[] = {span(experts, m, 4ll * k), span(weights, m, 4ll * k), span(offsets, E + 1, 4), span(src, m, 4ll * k),
+                        span(pos, m, 4ll * k), span(need ? ws : nullptr, int64_t(need), 1), span(logits, m, 4ll * E),
+                        span(bias, E, 4), span(active, m, 4)};
+  if (any_overlap(spans, 6, 9)) return CSA2_ERR_INVALID_ARG;
+  Params p = {};
+  p.logits = logits, p.bias = bias, p.active = active, p.m = m, p.E = E, p.k = k, p.renorm = renorm, p.scale = scale;
+  p.experts = experts, p.weights = weights, p.offsets = offsets, p.src = src, p.pos = pos;
+  p.counts = static_cast<uint32_t*>(ws);
+  p.tokens = block_tokens(m);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const int ne = (E + 31) / 32;
+  const cudaError_t e = ne <= 1 ? route<1>(p, st) : ne <= 2 ? route<2>(p, st) : ne <= 4 ? route<4>(p, st)
+                      : ne <= 8 ? route<8>(p, st) : ne <= 12 ? route<12>(p, st) : ne <= 16 ? route<16>(p, st)
+                                                                                         : route<32>(p, st);
+  return e == cudaSuccess ? CSA2_OK : CSA2_ERR_CUDA;
+}
+
+extern "C" csa2_status csa2_expert_combine(const void* y, int y_fp32, int64_t rows, const int32_t* pos, const float* weights,
+                                           int64_t m, int k, int64_t n, const uint16_t* add, void* out, int out_fp32,
+                                           csa2_stream_t stream) {
+  using namespace csa2;
+  using namespace csa2::moe;
+  if (rows < 0 || m < 0 || k < 0 || k > kMaxK || n < 0 || rows > (1ll << 31) || m > (1ll << 31) || n > (1ll << 28))
+    return CSA2_ERR_INVALID_ARG;
+  if (m == 0 || n == 0) return CSA2_OK;
+  if (!out || (k > 0 && (!pos || !weights)) || (k > 0 && rows > 0 && !y)) return CSA2_ERR_INVALID_ARG;
+  if (!al(y, 16) || !al(out, 16) || !al(add, 16) || !al(pos, 4) || !al(weights, 4)) return CSA2_ERR_INVALID_ARG;
+  const Span o = span(out, m, n * (out_fp32 ? 4 : 2)), a = span(add, m, n * 2);
+  // (add may be out itself: an element is read by the thread that writes it)
+  if (overlap(o, span(y, rows, n * (y_fp32 ? 4 : 2))) || overlap(o, span(pos, m, 4ll * k)) ||
+      overlap(o, span(weights, m, 4ll * k)) || (overlap(o, a) && (static_cast<const void*>(add) != out || out_fp32)))
+    return CSA2_ERR_INVALID_ARG;
+  Combine p = {};
+  p.y = y, p.pos = pos, p.weights = weights, p.add = add, p.out = out, p.m = m, p.n = n, p.rows = rows, p.k = k;
+  p.flags = device_flags_ptr();
+  if (!p.flags) return CSA2_ERR_CUDA;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (m * (n / (n % 8 == 0 ? 8 : n % 2 == 0 ? 2 : 1)) > 0x7FFFFFFFll * 256) return CSA2_ERR_INVALID_ARG;
+  const cudaError_t e = n % 8 == 0 ? combine<8>(p, y_fp32, out_fp32, st) : n % 2 == 0 ? combine<2>(p, y_fp32, out_fp32, st)
+                                                                                 : combine<1>(p, y_fp32, out_fp32, st);
+  return e == cudaSuccess ? CSA2_OK : CSA2_ERR_CUDA;
+}

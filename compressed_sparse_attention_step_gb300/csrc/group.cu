@@ -143,6 +143,10 @@ extern "C" size_t csa2_workspace_size(int op, const csa2_dims* d) {
       return (d->n >= 1 && d->n <= 64 && d->k >= 1 && d->k <= CSA2_MAX_K)
                  ? csa2::merge_pairs_ws_bytes(int(rows), int(d->n), d->k)
                  : 0;
+    case CSA2_OP_EXPERT_ROUTE:
+      return csa2::expert_route_ws_bytes(d->B, d->n);
+    case CSA2_OP_FP4_GROUPED:
+      return csa2::fp4_grouped_ws_bytes(d->B, d->cap);
     case CSA2_OP_GROUP_STEP:
       return csa2::group_ws_layout(d->B, d->Nq, d->cap, d->k, d->W, d->hierarchical, d->n_blocks_keep,
                                    d->n_split)

@@ -74,6 +74,12 @@ typedef enum {
 #define CSA2_MAX_TREE 64    /* drafted nodes per sequence                        */
 #define CSA2_MAX_SEQS 8192  /* sequences of one csa2_block_tables call           */
 #define CSA2_MAX_MV_ROWS 32 /* token rows of csa2_fp4_matvec                     */
+#define CSA2_MAX_EXPERTS 1024           /* experts of csa2_expert_route, csa2_fp4_grouped    */
+#define CSA2_MAX_EXPERTS_PER_TOKEN 16   /* experts of a token                                */
+#define CSA2_MAX_ROUTE_TOKENS 131072    /* tokens of one csa2_expert_route call              */
+#define CSA2_MAX_RANK 128               /* rank of csa2_lora_add's adapters                  */
+#define CSA2_MAX_VOCAB 1048576          /* tokens of a row of csa2_token_logprobs            */
+#define CSA2_MAX_TOP 32                 /* alternatives of csa2_token_logprobs               */
 
 /* Layer modes (ai-maestro "Compressed Sparse Attention 2"). */
 #define CSA2_MODE_FULL 0
@@ -83,6 +89,10 @@ typedef enum {
 /* Window row formats of csa2_group_desc.swa_format. */
 #define CSA2_SWA_BF16 0
 #define CSA2_SWA_E4M3 1
+
+/* Activations of csa2_fp4_grouped. */
+#define CSA2_ACT_NONE 0
+#define CSA2_ACT_SWIGLU 1
 
 /* Device flag bits (csa2_device_flags). */
 #define CSA2_FLAG_APPEND_OOB 1u /* an appended row fell outside [0, cap): row skipped   */
@@ -519,6 +529,97 @@ csa2_status csa2_fp4_pack_weight(const uint8_t* codes, const uint8_t* scales, in
 csa2_status csa2_fp4_matvec(const uint16_t* x, int m, const uint8_t* packed, int64_t n_out, int64_t n_in,
                             const float* row_scale, void* y, int y_fp32, csa2_stream_t stream);
 
+/*
+ * The experts of a layer (wpnews.pro "DeepSeek V4.1 Flash Specs": one shared and 384 routed experts, six of them
+ * active; the pages say no more, and this is the plain form), the adapters of many requests, and what a step answers
+ * with.  An expert layer is
+ *   csa2_expert_route    each token's experts and weights, and the tokens in order of expert;
+ *   csa2_fp4_grouped     the gate and up products and their activation, of every expert's own tokens;
+ *   csa2_fp4_grouped     the down products of those rows (src NULL);
+ *   csa2_expert_combine  the weighted sum of each token's rows, beside the shared expert's or the residual.
+ */
+
+/*
+ * Each token's k experts by logits[t][e] + bias[e] (one fp32 sum): the largest first, the lowest expert among equals,
+ * NaN as -inf.  Their weights are scale * softmax of the logits without the bias, over the chosen experts (renorm != 0)
+ * or over all of them (renorm = 0); an expert at -inf weighs 0.
+ *   logits  fp32 [m][E], m <= CSA2_MAX_ROUTE_TOKENS, E <= CSA2_MAX_EXPERTS, 1 <= k <= min(E, CSA2_MAX_EXPERTS_PER_TOKEN);
+ *   bias    fp32 [E] or NULL;  active int32 [m] or NULL: tokens with 0 are padding;
+ *   experts int32 [m][k], weights fp32 [m][k]: padding gets -1 and 0;
+ *   offsets int32 [E + 1], src int32 [m*k]: entries offsets[e] .. offsets[e+1] - 1 of src are the tokens of expert e,
+ *           ascending; the entries from offsets[E] on are -1;
+ *   pos     int32 [m][k]: where entry j of token t stands in src, -1 for padding.
+ *   ws      csa2_workspace_size(CSA2_OP_EXPERT_ROUTE, {B = m, n = E}) bytes; calls that may overlap need one each.
+ * logits is 16-byte aligned, the other arrays 4.  What the call writes overlaps nothing else.
+ */
+csa2_status csa2_expert_route(const float* logits, int m, int E, int k, const float* bias, const int32_t* active,
+                              int renorm, float scale, int32_t* experts, float* weights, int32_t* offsets, int32_t* src,
+                              int32_t* pos, void* ws, size_t ws_bytes, csa2_stream_t stream);
+
+/*
+ * Products of ragged groups of rows, each with its own 4-bit weight: for expert e and offsets[e] <= r < offsets[e+1]
+ *   h[n] = row_scale[e][n] * sum_c x[src[r]][c] * W_e[n][c],  W_e as in csa2_fp4_matvec, and
+ *   act = CSA2_ACT_NONE:    y[r][n] = h[n], n < n_out;
+ *   act = CSA2_ACT_SWIGLU:  y[r][n] = h[2n] / (1 + exp(-h[2n])) * h[2n+1], n < n_out / 2: the weight's even rows are the
+ *                           gate's, its odd ones the up product's.
+ *   x       bf16 [n_x][n_in], n_in a positive multiple of 16;  src int32 [rows], or NULL (row r of x; n_x >= rows then).
+ *           A row with src outside [0, n_x) counts as zeros; at or past n_x it sets CSA2_FLAG_INDEX_OOB;
+ *   packed  [E][csa2_fp4_packed_bytes(n_out, n_in)], each expert's weight by csa2_fp4_pack_weight.  With n_out a
+ *           multiple of 32 that is the packing of the E * n_out rows at once;
+ *   row_scale fp32 [E][n_out] or NULL (1);
+ *   offsets int32 [E + 1], not descending, within [0, rows] (values outside are cut off there); rows of y before
+ *           offsets[0] and from offsets[E] on are left as they were;
+ *   y       bf16 (y_fp32 = 0) or fp32 (1) [rows][n_out, or half of it].
+ *   ws      csa2_workspace_size(CSA2_OP_FP4_GROUPED, {B = n_x, cap = n_in}) bytes; calls that may overlap need one each.
+ * Accumulated in fp32, rounded once.  y and ws overlap nothing else.  E = 1 is a product of any number of rows with one
+ * weight.
+ */
+csa2_status csa2_fp4_grouped(const uint16_t* x, int64_t n_x, int64_t n_in, const uint8_t* packed, int E, int64_t n_out,
+                             const float* row_scale, const int32_t* offsets, const int32_t* src, int64_t rows, int act,
+                             void* y, int y_fp32, void* ws, size_t ws_bytes, csa2_stream_t stream);
+
+/*
+ * out[t] = add[t] + sum_j weights[t][j] * y[pos[t][j]], summed in fp32 in the order of j and rounded once.
+ *   y bf16 or fp32 [rows][n], pos int32 [m][k] (negative entries are skipped; entries >= rows too, and set
+ *   CSA2_FLAG_INDEX_OOB), weights fp32 [m][k], add bf16 [m][n] or NULL, out bf16 or fp32 [m][n] (a bf16 out may be add
+ *   itself; it overlaps nothing else).  0 <= k <= CSA2_MAX_EXPERTS_PER_TOKEN.
+ */
+csa2_status csa2_expert_combine(const void* y, int y_fp32, int64_t rows, const int32_t* pos, const float* weights,
+                                int64_t m, int k, int64_t n, const uint16_t* add, void* out, int out_fp32,
+                                csa2_stream_t stream);
+
+/*
+ * Low-rank adapters of many requests beside a shared projection:
+ *   out[i] = base[i] + scale[l] * B_l (A_l x[i]),  l = adapter[i];  out[i] = base[i] where adapter[i] < 0.
+ *   x       bf16 [m][n_in], n_in a multiple of 8;  a bf16 [L][r][n_in], b bf16 [L][n_out][r], r a multiple of 8 up to
+ *           CSA2_MAX_RANK;
+ *   adapter int32 [m], in any order (rows at or past L count as having none and set CSA2_FLAG_INDEX_OOB);
+ *   ranks   int32 [L] or NULL (r): adapter l uses its first ranks[l] ranks, the others are not used, whatever they hold;
+ *   scale   fp32 [L] or NULL (1);
+ *   base, out bf16 (out_fp32 = 0) or fp32 (1) [m][n_out]; out may be base itself and overlaps nothing else.
+ * No workspace.  Accumulated in fp32, rounded once.
+ */
+csa2_status csa2_lora_add(const uint16_t* x, int m, int n_in, const uint16_t* a, const uint16_t* b, int L, int r, int n_out,
+                          const int32_t* adapter, const int32_t* ranks, const float* scale, const void* base, void* out,
+                          int out_fp32, csa2_stream_t stream);
+
+/*
+ * Log probabilities under softmax(inv_temp * logits[r]) of each row: of given tokens (a drafted node's children, the
+ * next token of a prompt), the log-sum-exp, the entropy in nats, and the n_top likeliest tokens.
+ *   logits  bf16 (logits_fp32 = 0) or fp32 (1), row r at logits + r * ld, V <= ld of them; aligned to an element.
+ *           -inf rules a token out.  Neither NaN nor +inf.  inv_temp > 0;
+ *   tokens  int32 [rows][n_tok], n_tok <= CSA2_MAX_TREE: logprobs fp32 [rows][n_tok]; a token below 0 is padding and
+ *           gets 0, one at or past V gets -inf and sets CSA2_FLAG_INDEX_OOB;
+ *   lse, entropy fp32 [rows] (nullable): a row whose tokens are all ruled out has lse = -inf, log probabilities -inf and
+ *           entropy 0;
+ *   top_ids int32 [rows][n_top], top_logprobs fp32 [rows][n_top] (either may be NULL), n_top <= CSA2_MAX_TOP: the
+ *           largest logits first, the lowest token among equals; behind all V tokens -1 and -inf.
+ * No workspace.  What the call writes overlaps nothing else.
+ */
+csa2_status csa2_token_logprobs(const void* logits, int logits_fp32, int rows, int V, int64_t ld, const int32_t* tokens,
+                                int n_tok, float inv_temp, float* logprobs, float* lse, float* entropy, int n_top,
+                                int32_t* top_ids, float* top_logprobs, csa2_stream_t stream);
+
 /* Workspace sizing. */
 #define CSA2_OP_TOPK 1
 #define CSA2_OP_BLOCK_POOL 2
@@ -526,11 +627,14 @@ csa2_status csa2_fp4_matvec(const uint16_t* x, int m, const uint8_t* packed, int
 #define CSA2_OP_GROUP_STEP 4
 #define CSA2_OP_INDEX_SELECT_PREFILL 5
 #define CSA2_OP_MERGE_PAIRS 6
+#define CSA2_OP_EXPERT_ROUTE 7
+#define CSA2_OP_FP4_GROUPED 8
 
 typedef struct csa2_dims {
-  int B, Nq;
-  int64_t cap;          /* cache capacity per sequence                        */
-  int64_t n;            /* CSA2_OP_TOPK: columns per row; CSA2_OP_MERGE_PAIRS: shards */
+  int B, Nq;            /* CSA2_OP_EXPERT_ROUTE: tokens; CSA2_OP_FP4_GROUPED: rows of x, both in B */
+  int64_t cap;          /* cache capacity per sequence; CSA2_OP_FP4_GROUPED: n_in */
+  int64_t n;            /* CSA2_OP_TOPK: columns per row; CSA2_OP_MERGE_PAIRS: shards;
+                           CSA2_OP_EXPERT_ROUTE: experts */
   int k;                /* Top-K / selected rows                              */
   int W;                /* window                                             */
   int n_split;          /* CSA2_OP_SPARSE_ATTN / GROUP_STEP: 0 = automatic    */

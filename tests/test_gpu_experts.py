@@ -1,0 +1,240 @@
+"""The router, the grouped 4-bit products and the weighted sum of an expert layer against plain 64-bit forms."""
+import numpy as np
+import pytest
+
+from tests import _layer as P
+from tests import _verify as V
+from tests._cases import bf16_dev, to_dev
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("no CUDA device", allow_module_level=True)
+import compressed_sparse_attention_step_gb300 as c  # noqa: E402
+
+
+def host(t):
+    return t.float().cpu().numpy().astype(np.float64) if t.is_floating_point() else t.cpu().numpy()
+
+
+def routed(logits, k, bias=None, active=None, **kw):
+    m, E = logits.shape
+    o = dict(experts=torch.full((m, k), 99, dtype=torch.int32, device="cuda"),
+             weights=torch.full((m, k), 99.0, device="cuda"), offsets=torch.full((E + 1,), 99, dtype=torch.int32, device="cuda"),
+             src=torch.full((m * k,), 99, dtype=torch.int32, device="cuda"),
+             pos=torch.full((m, k), 99, dtype=torch.int32, device="cuda"))
+    c.csa2_expert_route(to_dev(logits), *o.values(), bias=None if bias is None else to_dev(bias),
+                        active=None if active is None else to_dev(np.asarray(active, np.int32)), **kw)
+    return {n: host(t) for n, t in o.items()}
+
+
+def check_route(got, logits, k, bias=None, active=None, **kw):
+    want = dict(zip(("experts", "weights", "offsets", "src", "pos"), P.route(logits, k, bias, active, **kw)))
+    for n in ("experts", "offsets", "src", "pos"):
+        assert np.array_equal(got[n], want[n]), n
+    assert (np.abs(got["weights"] - want["weights"]) <= P.route_tol(logits, want["weights"])).all()
+
+
+@pytest.mark.parametrize("m,E,k", [
+    (0, 5, 2), (1, 1, 1), (1, 384, 6), (2, 33, 16), (63, 32, 8), (64, 384, 6), (65, 31, 3), (200, 8, 2), (300, 512, 4),
+    (513, 100, 7), (1000, 1024, 16), (2049, 64, 1), (17000, 16, 2), (40000, 3, 3),
+])
+def test_route(m, E, k):
+    g = np.random.default_rng(m * 31 + E + k)
+    logits = g.standard_normal((m, E)).astype(np.float32)
+    bias = g.standard_normal(E).astype(np.float32) if m % 2 else None
+    active = (g.random(m) < 0.8).astype(np.int32) if m % 3 else None
+    check_route(routed(logits, k, bias, active, renorm=bool(m % 2), scale=2.5), logits, k, bias, active, renorm=bool(m % 2),
+                scale=2.5)
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+def test_route_ties_infinities_and_nan(renorm):
+    g = np.random.default_rng(5)
+    logits = g.integers(-1, 2, (130, 70)).astype(np.float32) * np.float32(0.0)   # both zeros
+    logits[::2] = g.integers(-2, 3, (65, 70))
+    logits[4] = -np.inf                       # every expert ruled out
+    logits[5, 3:] = -np.inf                   # fewer than k left
+    logits[6, ::3] = np.nan
+    logits[8, 7] = 1e30
+    logits[9] = np.finfo(np.float32).min
+    logits[10] = -1e30
+    logits[10, 60] = -2e30
+    active = np.ones(130, np.int32)
+    active[[0, 20, 129]] = 0
+    check_route(routed(logits, 5, None, active, renorm=renorm), logits, 5, None, active, renorm=renorm)
+    none = np.zeros(130, np.int32)            # a batch that is all padding
+    check_route(routed(logits, 5, None, none, renorm=renorm), logits, 5, None, none, renorm=renorm)
+
+
+def weights(g, E, n_out, n_in, lo=0x20, hi=0x50):
+    codes, scales = V.random_fp4(g, E * n_out, n_in, lo, hi)
+    w = V.dequant(codes, scales).reshape(E, n_out, n_in)
+    return c.fp4_pack_experts(to_dev(codes).view(E, n_out, -1), to_dev(scales).view(E, n_out, -1)), w
+
+
+def check_grouped(y, x, w, rs, offsets, src, act, before):
+    """x float64 [n_x, n_in]; before: what y held.  Rows outside of the lists are as they were, bit for bit."""
+    rows = y.shape[0]
+    got, covered = host(y), np.zeros(rows, bool)
+    for e in range(w.shape[0]):
+        a, b = (int(min(max(v, 0), rows)) for v in offsets[e:e + 2])
+        if b <= a:
+            continue
+        covered[a:b] = True
+        at = np.arange(a, b) if src is None else src[a:b]
+        ok = (at >= 0) & (at < x.shape[0])
+        xe = np.where(ok[:, None], x[np.where(ok, at, 0)], 0.0)
+        exact, tol = P.product(xe, w[e], np.ones(w.shape[1]) if rs is None else rs[e])
+        if act:
+            exact, tol = P.swiglu(exact, tol)
+        tol = P.rounded(exact, tol, y.dtype == torch.bfloat16)
+        err = np.abs(got[a:b] - exact)
+        assert (err <= tol).all(), f"expert {e}: {np.max(err - tol):.3e} over the bound"
+    assert np.array_equal(got[~covered], host(before)[~covered])
+
+
+def run_grouped(seed, counts, n_in, n_out, act=False, fp32=False, n_x=None, idle=0, lead=0, with_rs=True, xscale=1.0):
+    g = np.random.default_rng(seed)
+    E = len(counts)
+    offsets = (lead + np.concatenate(([0], np.cumsum(counts)))).astype(np.int32)
+    rows = int(offsets[-1]) + idle
+    n_x = rows if n_x is None else n_x
+    packed, w = weights(g, E, n_out, n_in)
+    xb = V.bf16(g, (n_x, n_in), xscale)
+    src = g.integers(0, max(n_x, 1), rows).astype(np.int32) if n_x else np.full(rows, -1, np.int32)
+    rs = (g.random((E, n_out)) * 2 - 0.5).astype(np.float32) if with_rs else None
+    y = torch.full((rows, n_out // 2 if act else n_out), 7.0, dtype=torch.float32 if fp32 else torch.bfloat16, device="cuda")
+    before = y.clone()
+    c.csa2_fp4_grouped(bf16_dev(xb), packed, to_dev(offsets), y, src=to_dev(src), row_scale=None if rs is None else to_dev(rs),
+                       act=c.ACT_SWIGLU if act else c.ACT_NONE)
+    check_grouped(y, V.f64(xb), w, None if rs is None else rs.astype(np.float64), offsets, src, act, before)
+
+
+@pytest.mark.parametrize("counts,n_in,n_out", [
+    ([1], 16, 2), ([0, 0, 3], 128, 32), ([5, 0, 1, 17], 144, 34), ([16, 15, 33], 272, 130), ([2] * 40, 512, 64),
+    ([0] * 30 + [129] + [0] * 9 + [1], 400, 258), ([64, 65, 63, 1, 0, 127, 128], 1040, 96), ([300, 7], 4112, 200),
+    ([1], 8208, 4100), ([31, 32], 48, 1030), ([257], 256, 514), ([3, 250, 20, 0, 90], 640, 384), ([1] * 200, 96, 18),
+    ([40, 0, 513], 2064, 62),
+])
+@pytest.mark.parametrize("act,fp32", [(False, False), (True, False), (False, True), (True, True)])
+def test_grouped(counts, n_in, n_out, act, fp32):
+    run_grouped(sum(counts) + n_in, counts, n_in, n_out, act, fp32, n_x=sum(counts) // 2 + 3, idle=4, lead=sum(counts) % 3,
+                with_rs=n_in != 512)
+
+
+def test_grouped_scales_of_x():
+    """Rows whose magnitudes are far apart, one of zeros, and the type's ends (f16 holds none of them as they are)."""
+    g = np.random.default_rng(3)
+    packed, w = weights(g, 2, 96, 384)
+    xb = V.bf16(g, (40, 384))
+    x = V.f64(xb) * 2.0 ** np.linspace(-100, 100, 40)[:, None].round()
+    x[7] = 0
+    x[9, 1:] *= 2.0 ** -30
+    xt = torch.from_numpy(x).to(torch.bfloat16).cuda()
+    x = host(xt)
+    off = np.array([0, 13, 40], np.int32)
+    y = torch.full((40, 96), 7.0, device="cuda")
+    before = y.clone()
+    c.csa2_fp4_grouped(xt, packed, to_dev(off), y)
+    check_grouped(y, x, w, None, off, None, False, before)
+
+
+def test_grouped_offsets_and_rows_out_of_range():
+    """Offsets past the rows are cut off, src past x counts as zeros and is flagged, no rows of x at all."""
+    c.csa2_device_flags()
+    g = np.random.default_rng(4)
+    packed, w = weights(g, 4, 66, 160)
+    xb = V.bf16(g, (9, 160))
+    src = g.integers(0, 9, 50).astype(np.int32)
+    src[[3, 30]] = -1, 9
+    off = np.array([-5, 4, 4, 47, 90], np.int32)
+    y = torch.full((50, 66), 7.0, dtype=torch.bfloat16, device="cuda")
+    before = y.clone()
+    c.csa2_fp4_grouped(bf16_dev(xb), packed, to_dev(off), y, src=to_dev(src))
+    check_grouped(y, V.f64(xb), w, None, off, src, False, before)
+    assert c.csa2_device_flags() == c.FLAG_INDEX_OOB
+    y.fill_(7.0)
+    c.csa2_fp4_grouped(torch.empty((0, 160), dtype=torch.bfloat16, device="cuda"), packed, to_dev(off), y,
+                       src=to_dev(np.full(50, -1, np.int32)))
+    assert (y[:50] == 0).all() and c.csa2_device_flags() == 0
+
+
+def test_grouped_is_the_same_whatever_else_is_in_the_call():
+    """An expert's rows do not change with the rows and experts beside them, nor from call to call."""
+    g = np.random.default_rng(6)
+    packed, _ = weights(g, 3, 256, 512)
+    x = bf16_dev(V.bf16(g, (300, 512)))
+    off = to_dev(np.array([0, 100, 260, 300], np.int32))
+    out = [torch.zeros((300, 256), dtype=torch.bfloat16, device="cuda") for _ in range(3)]
+    for y in out[:2]:
+        c.csa2_fp4_grouped(x, packed, off, y)
+    c.csa2_fp4_grouped(x, packed, to_dev(np.array([0, 100, 100, 100], np.int32)), out[2])
+    assert torch.equal(out[0], out[1]) and torch.equal(out[0][:100], out[2][:100])
+
+
+@pytest.mark.parametrize("m,k,n", [(1, 1, 1), (5, 3, 7), (64, 6, 4096), (33, 5, 130), (700, 16, 8), (3, 2, 1001), (9, 0, 16)])
+@pytest.mark.parametrize("y32,out32,add", [(False, False, True), (False, True, False), (True, False, False), (True, True, True)])
+def test_combine(m, k, n, y32, out32, add):
+    g = np.random.default_rng(m + k * 3 + n)
+    rows = m * k + 2
+    c.csa2_device_flags()
+    y = torch.from_numpy(g.standard_normal((rows, n))).to(torch.float32 if y32 else torch.bfloat16).cuda()
+    pos = g.permutation(rows)[:m * k].reshape(m, k).astype(np.int32)
+    if k:
+        pos[m // 2, :] = -1
+        pos[0, k - 1] = rows
+    w = g.standard_normal((m, k)).astype(np.float32)
+    a = torch.from_numpy(g.standard_normal((m, n))).to(torch.bfloat16).cuda() if add else None
+    out = torch.full((m, n), 9.0, dtype=torch.float32 if out32 else torch.bfloat16, device="cuda")
+    c.csa2_expert_combine(y, to_dev(pos), to_dev(w), out, add=a)
+    ok = (pos >= 0) & (pos < rows)
+    terms = np.where(ok[..., None], w[..., None].astype(np.float64) * host(y)[np.where(ok, pos, 0)], 0)
+    base = host(a) if add else np.zeros((m, n))
+    exact, mag = base + terms.sum(1), np.abs(base) + np.abs(terms).sum(1)
+    tol = P.rounded(exact, mag * (k + 1) * P.H32 * 2, not out32)
+    assert (np.abs(host(out) - exact) <= tol).all()
+    assert c.csa2_device_flags() == (c.FLAG_INDEX_OOB if k else 0)
+    if add and not out32:   # in place
+        c.csa2_expert_combine(y, to_dev(pos), to_dev(w), a, add=a)
+        assert torch.equal(a, out)
+
+
+def test_captured_and_on_another_stream():
+    """Route and products captured into a graph on a stream of their own, replayed on new logits and rows."""
+    g = np.random.default_rng(12)
+    m, E, k, n_in, n_out = 96, 12, 3, 256, 192
+    packed, w = weights(g, E, n_out, n_in)
+    x = bf16_dev(V.bf16(g, (m, n_in)))
+    logits = torch.zeros((m, E), device="cuda")
+    o = [torch.zeros(s, dtype=d, device="cuda") for s, d in (((m, k), torch.int32), ((m, k), torch.float32), ((E + 1,), torch.int32),
+                                                              ((m * k,), torch.int32), ((m, k), torch.int32))]
+    y = torch.zeros((m * k, n_out // 2), dtype=torch.bfloat16, device="cuda")
+    out = torch.zeros((m, n_out // 2), device="cuda")
+    ws = torch.empty(c.grouped_workspace_size(m, n_in), dtype=torch.uint8, device="cuda")
+    rws = torch.empty(max(1, c.route_workspace_size(m, E)), dtype=torch.uint8, device="cuda")
+
+    def step():
+        c.csa2_expert_route(logits, *o, ws=rws)
+        c.csa2_fp4_grouped(x, packed, o[2], y, src=o[3], act=c.ACT_SWIGLU, ws=ws)
+        c.csa2_expert_combine(y, o[4], o[1], out)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for seed in (1, 2):
+        h = np.random.default_rng(seed)
+        l = h.standard_normal((m, E)).astype(np.float32)
+        logits.copy_(to_dev(l))
+        x.copy_(bf16_dev(V.bf16(h, (m, n_in))))
+        y.fill_(7.0)
+        before = y.clone()
+        graph.replay()
+        torch.cuda.synchronize()
+        check_route(dict(zip(("experts", "weights", "offsets", "src", "pos"), map(host, o))), l, k)
+        check_grouped(y, host(x), w, None, host(o[2]), host(o[3]), True, before)

@@ -1,0 +1,138 @@
+"""Refusals of the expert layer, the adapters and the log probabilities: answered from the arguments alone, nothing is
+launched."""
+import ctypes
+
+import pytest
+
+import compressed_sparse_attention_step_gb300 as csa2
+from compressed_sparse_attention_step_gb300 import _build
+
+
+@pytest.fixture(scope="module")
+def L():
+    _build.build()
+    return csa2.lib()
+
+
+def _p(i, off=0):  # distinct, aligned, never dereferenced on a rejected call
+    return ctypes.c_void_p(0x10000000 * (i + 1) + off)
+
+
+def test_expert_route(L):
+    def call(logits=_p(0), m=4, E=8, k=2, bias=None, active=None, experts=_p(1), weights=_p(2), offsets=_p(3), src=_p(4),
+             pos=_p(5), ws=None, n=0):
+        return L.csa2_expert_route(logits, m, E, k, bias, active, 1, 1.0, experts, weights, offsets, src, pos, ws, n, None)
+    assert call(m=-1) == 1 and call(m=csa2.MAX_ROUTE_TOKENS + 1) == 1 and call(E=0) == 1 and call(E=csa2.MAX_EXPERTS + 1) == 1
+    assert call(k=0) == 1 and call(k=9) == 1 and call(E=64, k=csa2.MAX_EXPERTS_PER_TOKEN + 1) == 1
+    for name in ("logits", "experts", "weights", "offsets", "src", "pos"):
+        assert call(**{name: None}) == 1, name
+        assert call(**{name: _p(9, 2)}) == 1, name
+    assert call(logits=_p(0, 4)) == 1 and call(bias=_p(9, 1)) == 1 and call(active=_p(9, 1)) == 1
+    need = csa2.route_workspace_size(1000, 8)
+    assert need > 0 and csa2.route_workspace_size(64, 8) == 0
+    assert call(m=1000) == 4 and call(m=1000, ws=_p(8), n=need - 1) == 4 and call(m=1000, ws=_p(8, 4), n=need) == 1
+    assert call(m=1000, ws=_p(0), n=need) == 1                      # over the logits
+    assert call(experts=_p(0)) == 1 and call(weights=_p(1)) == 1 and call(pos=_p(4)) == 1
+    assert call(src=_p(0, 4 * 8 * 4 - 4)) == 1 and call(offsets=_p(2, 4 * 2 * 4 - 4)) == 1
+    assert call(active=_p(5)) == 1 and call(bias=_p(3, 8 * 4)) == 1
+
+
+def test_fp4_grouped(L):
+    def call(x=_p(0), n_x=4, n_in=32, w=_p(1), E=2, n_out=8, rs=None, off=_p(2), src=None, rows=4, act=0, y=_p(3), ws=_p(4),
+             n=1 << 20):
+        return L.csa2_fp4_grouped(x, n_x, n_in, w, E, n_out, rs, off, src, rows, act, y, 0, ws, n, None)
+    for bad in (dict(n_x=-1), dict(n_in=24), dict(n_in=0), dict(n_in=-16), dict(E=-1), dict(E=csa2.MAX_EXPERTS + 1), dict(n_out=-1),
+                dict(rows=-1), dict(act=2), dict(act=1, n_out=7), dict(n_x=1 << 31), dict(rows=1 << 31), dict(n_in=1 << 25)):
+        assert call(**bad) == 1, bad
+    for name in ("x", "w", "off", "y"):
+        assert call(**{name: None}) == 1, name
+    for name in ("x", "w", "y", "ws"):
+        assert call(**{name: _p(9, 4)}) == 1, name
+    assert call(rs=_p(9, 1)) == 1 and call(off=_p(9, 1)) == 1 and call(src=_p(9, 1)) == 1
+    need = csa2.grouped_workspace_size(4, 32)
+    assert call(ws=None) == 4 and call(n=need - 1) == 4
+    assert call(y=_p(0)) == 1 and call(ws=_p(1)) == 1 and call(ws=_p(3)) == 1 and call(y=_p(1, 2 * 2304 - 16)) == 1
+    assert call(x=_p(3, 4 * 8 * 2 - 16)) == 1
+    assert call(rows=3, src=None, n_x=2) == 1                       # rows of x that are not there
+    assert call(rows=0) == 0 and call(n_out=0) == 0 and call(E=0) == 0
+
+
+def test_expert_combine(L):
+    def call(y=_p(0), rows=8, pos=_p(1), w=_p(2), m=4, k=2, n=16, add=None, out=_p(3), out32=0):
+        return L.csa2_expert_combine(y, 0, rows, pos, w, m, k, n, add, out, out32, None)
+    assert call(m=-1) == 1 and call(k=-1) == 1 and call(k=csa2.MAX_EXPERTS_PER_TOKEN + 1) == 1 and call(n=-1) == 1 and call(rows=-1) == 1
+    for name in ("y", "pos", "w", "out"):
+        assert call(**{name: None}) == 1, name
+    for name in ("y", "add", "out"):
+        assert call(**{name: _p(9, 4)}) == 1, name
+    assert call(out=_p(0)) == 1 and call(out=_p(1)) == 1 and call(out=_p(2)) == 1 and call(out=_p(0, 8 * 16 * 2 - 16)) == 1
+    assert call(add=_p(3), out32=1) == 1 and call(add=_p(3, 16)) == 1   # not the same elements
+    assert call(m=0) == 0 and call(n=0) == 0
+
+
+def test_lora_add(L):
+    def call(x=_p(0), m=4, n_in=16, a=_p(1), b=_p(2), n_l=3, r=8, n_out=16, which=_p(3), ranks=None, scale=None, base=_p(4), out=_p(5),
+             f32=0):
+        return L.csa2_lora_add(x, m, n_in, a, b, n_l, r, n_out, which, ranks, scale, base, out, f32, None)
+    assert call(m=-1) == 1 and call(n_in=12) == 1 and call(n_in=-8) == 1 and call(r=0) == 1 and call(r=12) == 1
+    assert call(r=csa2.MAX_RANK + 8) == 1 and call(n_out=-1) == 1 and call(n_l=-1) == 1
+    for name in ("x", "a", "b", "which", "base", "out"):
+        assert call(**{name: None}) == 1, name
+    for name in ("x", "a", "b", "base", "out"):
+        assert call(**{name: _p(9, 4)}) == 1, name
+    assert call(which=_p(9, 1)) == 1 and call(ranks=_p(9, 1)) == 1 and call(scale=_p(9, 1)) == 1
+    for i in range(4):
+        assert call(out=_p(i)) == 1, i
+    assert call(out=_p(4, 16)) == 1                                  # base moved by a few elements
+    assert call(m=0) == 0 and call(n_out=0) == 0
+
+
+def test_token_logprobs(L):
+    def call(x=_p(0), f32=0, rows=3, V=100, ld=100, tok=_p(1), n_tok=1, t=1.0, lp=_p(2), lse=None, ent=None, n_top=0, ids=None,
+             top=None):
+        return L.csa2_token_logprobs(x, f32, rows, V, ld, tok, n_tok, t, lp, lse, ent, n_top, ids, top, None)
+    for bad in (dict(rows=-1), dict(V=0), dict(V=csa2.MAX_VOCAB + 1, ld=1 << 30), dict(ld=99), dict(n_tok=-1), dict(n_tok=65), dict(t=0.0),
+                dict(t=-1.0), dict(t=float("nan")), dict(t=float("inf")), dict(n_top=-1), dict(n_top=csa2.MAX_TOP + 1, ids=_p(3)),
+                dict(n_top=2)):
+        assert call(**bad) == 1, bad
+    for name in ("x", "tok", "lp"):
+        assert call(**{name: None}) == 1, name
+        assert call(**{name: _p(9, 1)}) == 1, name
+    assert call(f32=1, x=_p(0, 2)) == 1 and call(lse=_p(9, 2)) == 1 and call(ent=_p(9, 2)) == 1
+    assert call(lp=_p(0, 400)) == 1 and call(lse=_p(2)) == 1 and call(lse=_p(3), ent=_p(3, 4)) == 1
+    assert call(n_top=2, ids=_p(1)) == 1 and call(n_top=2, ids=_p(3), top=_p(3)) == 1
+    assert call(rows=0) == 0
+
+
+def test_binding_checks_shapes_and_types():
+    torch = pytest.importorskip("torch")
+    i32, bf, f32, u8 = torch.int32, torch.bfloat16, torch.float32, torch.uint8
+    z = torch.zeros
+    route = lambda **k: csa2.csa2_expert_route(**{**dict(  # noqa: E731
+        logits=z((4, 8)), experts=z((4, 2), dtype=i32), weights=z((4, 2)), offsets=z(9, dtype=i32), src=z(8, dtype=i32),
+        pos=z((4, 2), dtype=i32)), **k})
+    for bad in (dict(), dict(logits=z((4, 8, 1))), dict(offsets=z(8, dtype=i32)), dict(src=z(7, dtype=i32)), dict(bias=z(7))):
+        with pytest.raises(ValueError):   # the first: not on a GPU
+            route(**bad)
+    with pytest.raises(TypeError):
+        route(logits=z((4, 8), dtype=bf))
+    lora = lambda **k: csa2.csa2_lora_add(**{**dict(  # noqa: E731
+        x=z((4, 16), dtype=bf), a=z((3, 8, 16), dtype=bf), b=z((3, 24, 8), dtype=bf), adapter=z(4, dtype=i32),
+        base=z((4, 24), dtype=bf), out=z((4, 24), dtype=bf)), **k})
+    for bad in (dict(), dict(b=z((3, 8, 24), dtype=bf)), dict(adapter=z(5, dtype=i32)), dict(out=z((4, 25), dtype=bf))):
+        with pytest.raises(ValueError):
+            lora(**bad)
+    with pytest.raises(TypeError):
+        lora(x=z((4, 16)))
+    grouped = lambda **k: csa2.csa2_fp4_grouped(**{**dict(  # noqa: E731
+        x=z((4, 32), dtype=bf), packed=z((2, 2304), dtype=u8), offsets=z(3, dtype=i32), y=z((4, 8), dtype=bf)), **k})
+    for bad in (dict(), dict(x=z((3, 32), dtype=bf)), dict(x=z((4, 24), dtype=bf)), dict(offsets=z(2, dtype=i32)),
+                dict(y=z((4, 33), dtype=bf)), dict(src=z(3, dtype=i32)), dict(row_scale=z((2, 9)))):
+        with pytest.raises(ValueError):
+            grouped(**bad)
+    with pytest.raises(ValueError):
+        csa2.csa2_expert_combine(z((8, 16)), z((4, 2), dtype=i32), z((4, 3)), z((4, 16)))
+    with pytest.raises(ValueError):
+        csa2.csa2_token_logprobs(z((4, 100)), lse=z(4))
+    with pytest.raises(TypeError):
+        csa2.csa2_token_logprobs(z((4, 100), dtype=torch.float64), lse=z(4))
