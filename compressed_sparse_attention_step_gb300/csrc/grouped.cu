@@ -1,5 +1,14 @@
 // Products of the token rows of each expert with its 4-bit weight (E2M1 codes, one E4M3 scale per 16 channels):
 // y[r] = act(row_scale[e] * W_e x[src[r]]) for the rows offsets[e] <= r < offsets[e + 1] of expert e.
+//
+// The weight is the M = 128 operand of tcgen05.mma, dequantised into tensor memory, the token rows are the other one
+// (N = 16 .. 128, by the rows that a tile has): a weight element costs one conversion and one multiplication whatever
+// the number of rows, and a tile with few rows little tensor time.  The packed weight's layout and numbers are those
+// of matvec.cu: a code times a scale is exact in f16, and so is x scaled by the power of two that brings a row's
+// largest magnitude into [2^14, 2^15), down to 2^-28 of it (off by less than 2^-38 of it below).
+//
+// Two launches: scale_kernel writes the rows of x as f16 and each row's factor into the workspace; grouped_kernel, one
+// persistent CTA per SM, takes units of an expert, up to 128 of its rows, and 128 or 256 outputs.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -9,151 +18,465 @@
 namespace csa2 {
 namespace grp {
 
-constexpr int kWarps = 8, kThreads = kWarps * 32;
-constexpr int kRows = 32, kChan = 128;  // of a block of the packed weight (matvec.cu has its layout)
+constexpr int kRows = 32, kChan = 128;  // of a block of the packed weight (matvec.cu)
 constexpr int kCodeBytes = kRows * kChan / 2;
-constexpr int kBlock = kCodeBytes + kRows * kChan / CSA2_GROUP;
-constexpr int kTok = 16;
+constexpr int kBlock = kCodeBytes + kRows * kChan / CSA2_GROUP;  // 2304 bytes
+
+constexpr int kTile = 128;       // token rows of a unit, at most
+constexpr int kStages = 4;       // channel blocks of x under way
+constexpr int kStage = kTile * kChan * 2;
+constexpr int kBehind = 2;       // channel blocks that a producer has asked for and not yet handed on
+constexpr int kSlots = 4;        // weight blocks under way per dequantising warp
+constexpr int kABufs = 2;        // dequantised blocks per pipeline
+// Two pipelines (s = 0, 1), each of an issuing thread, four dequantising warps, kABufs blocks in tensor memory and one
+// accumulator.  With two row tiles (MT = 2) each has its own 128 outputs; with one they share its channel blocks, even
+// and odd, and the accumulators are added.
+constexpr int kProducers = 4, kDequant = 8, kEpilogue = 4;
+constexpr int kWarpProd = 2, kWarpDeq = kWarpProd + kProducers, kWarpEpi = kWarpDeq + kDequant;
+constexpr int kThreads = (kWarpEpi + kEpilogue) * 32;
+constexpr uint32_t kACols = kChan / 2, kDCols = kTile;
+constexpr uint32_t kACol = 2 * kDCols;
+static_assert(kACol + 2 * kABufs * kACols <= 512, "tensor memory");
+static_assert(kWarpDeq % 4 == 2 && kWarpEpi % 4 == 2, "four neighbouring warps reach all lanes");
+
+struct Tail {
+  alignas(16) unsigned char ring[kDequant][kSlots][kBlock];
+  float inv[kTile];
+  int idx[2][kTile];
+  int off[CSA2_MAX_EXPERTS + 1];    // the experts' first rows, within [0, rows]
+  int start[CSA2_MAX_EXPERTS + 1];  // their first token tiles
+  uint32_t tmp[32];
+  uint64_t full[kDequant][kSlots];
+  uint64_t x_full[kStages], x_empty[kStages];
+  uint64_t a_full[2][kABufs], a_empty[2][kABufs], d_full, d_empty[2];
+  uint32_t tmem;
+};
+constexpr size_t kSmem = size_t(kStages) * kStage + sizeof(Tail);
+static_assert(kSmem <= 227 * 1024, "shared memory");
 
 struct Params {
   const uint16_t* x;
+  uint16_t* xs;   // f16 rows of x
+  float* inv;     // a row's factor
   const uint8_t* packed;
   const float* row_scale;
   const int32_t *offsets, *src;
   void* y;
-  int64_t n_out, n_in, w_bytes;
-  int64_t rows, n_x;
-  int E, n_kb, n_rb, y_fp32, act;
+  int64_t n_out, n_in, w_bytes, rows, n_x;
+  int E, n_kb, n_rb, n_mt, y_fp32, act;
   unsigned int* flags;
 };
 
 __device__ __forceinline__ int block_place(int r, int j) { return j * 512 + (r ^ (2 * j)) * 16; }
 
-__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                        uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+__device__ __forceinline__ void block_copy(void* dst, const uint8_t* src, uint64_t* bar) {
+  const uint32_t b = smem_u32(bar);
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(b), "r"(kBlock) : "memory");
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(kBlock), "r"(b)
+               : "memory");
 }
-
+__device__ __forceinline__ void mbar_init(uint64_t* b, int n) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(smem_u32(b)), "r"(n) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t* b) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_u32(b)) : "memory");
+}
+// D (+)= A B with A in tensor memory
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{ .reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};\n" ::"r"(a),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t a, uint32_t (&r)[16]) {  // valid after tcgen05.wait::ld
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(a)
+      : "memory");
+}
+// A loaded register used behind the wait (which the compiler does not tie to the load).
+__device__ __forceinline__ float tmem_value(uint32_t& r) {
+  asm volatile("" : "+r"(r));
+  return __uint_as_float(r);
+}
 __device__ __forceinline__ float silu(float v) { return v / (1.f + expf(-v)); }
 
-// A CTA: eight row blocks of an expert, one a warp, and its rows 16 at a time.
-__global__ void __launch_bounds__(kThreads) grouped_kernel(const Params p) {
-  __shared__ uint4 xs[2][4][32];
-  __shared__ float xf[kTok];
+// A warp per row of x.  The first 2048 channels are kept between the two passes, those behind are read again.
+__global__ void __launch_bounds__(128) scale_kernel(const Params p) {
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, t = lane & 3, g = lane >> 2;
-  const int e = blockIdx.y;
-  const int64_t lo = min(max(int64_t(p.offsets[e]), int64_t(0)), p.rows), hi = min(max(int64_t(p.offsets[e + 1]), lo), p.rows);
-  const int rb = int(blockIdx.x) * kWarps + warp;
-  const uint8_t* w = p.packed + int64_t(e) * p.w_bytes + int64_t(min(rb, p.n_rb - 1)) * p.n_kb * kBlock;
-  for (int64_t r0 = lo; r0 < hi; r0 += kTok) {
-    float acc[2][2][4] = {};
-    for (int kb = 0; kb < p.n_kb; ++kb) {
-      __syncthreads();
-      {  // half a warp per token, 8 channels a lane
-        const int tok = tid >> 4, j = tid & 15;
-        const int64_t ch = int64_t(kb) * kChan + 8 * j;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (r0 + tok < hi && ch < p.n_in) {
-          const int64_t s = p.src ? p.src[r0 + tok] : r0 + tok;
-          if (s >= 0 && s < p.n_x) v = __ldg(reinterpret_cast<const uint4*>(p.x + s * p.n_in + ch));
-          else if (s >= p.n_x && kb == 0 && j == 0 && blockIdx.x == 0) atomicOr(p.flags, CSA2_FLAG_INDEX_OOB);
+  const int64_t row = (int64_t(blockIdx.x) * 128 + threadIdx.x) >> 5;
+  if (row >= p.n_x) return;
+  const int lane = int(threadIdx.x & 31);
+  const uint16_t* src = p.x + row * p.n_in;
+  uint16_t* dst = p.xs + row * p.n_in;
+  const int n_in = int(p.n_in);
+  auto at = [&](int c) { return c < n_in ? __ldg(reinterpret_cast<const uint4*>(src + c)) : make_uint4(0, 0, 0, 0); };
+  auto mag = [](uint32_t am, const uint4& v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) am = max(am, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
+    return am;
+  };
+  uint4 keep[8];
+  uint32_t am = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) keep[i] = at(lane * 8 + 256 * i);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) am = mag(am, keep[i]);
+  for (int c0 = 2048; c0 < n_in; c0 += 1024) {
+    uint4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = at(c0 + lane * 8 + 256 * i);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) am = mag(am, v[i]);
+  }
+  am = __reduce_max_sync(0xffffffffu, am);
+  const int up = am ? min(max(141 - int(am >> 7), -126), 126) : 0;
+  const float f = __uint_as_float(uint32_t(127 + up) << 23);
+  auto put = [&](int c, const uint4& v) {
+    if (c >= n_in) return;
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = attn::h2_bits(__floats2half2_rn(bf16lo(w[i]) * f, bf16hi(w[i]) * f));
+    *reinterpret_cast<uint4*>(dst + c) = make_uint4(o[0], o[1], o[2], o[3]);
+  };
+#pragma unroll
+  for (int i = 0; i < 8; ++i) put(lane * 8 + 256 * i, keep[i]);
+  for (int c0 = 2048; c0 < n_in; c0 += 1024) {
+    uint4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = at(c0 + lane * 8 + 256 * i);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) put(c0 + lane * 8 + 256 * i, v[i]);
+  }
+  if (lane == 0) p.inv[row] = __uint_as_float(uint32_t(127 - up) << 23);
+}
+
+struct Unit {
+  int e, r0, n, mt;  // expert, first row, rows, row tile of the weight
+};
+
+template <int MT>
+__global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const Params p) {
+  extern __shared__ __align__(1024) unsigned char smem[];
+  Tail& sm = *reinterpret_cast<Tail*>(smem + kStages * kStage);
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, q = warp & 3;
+
+  bool late = false;  // a wait ran out: flagged, and no more waiting
+  auto wait = [&](uint64_t* b, uint32_t use) {  // the use-th completion of a barrier
+    if (!late && !bar_wait(smem_u32(b), use & 1u)) {
+      late = true;
+      atomicOr(p.flags, CSA2_FLAG_TIMEOUT);
+    }
+  };
+
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) mbar_init(&sm.x_full[i], kProducers), mbar_init(&sm.x_empty[i], MT);
+    for (int s = 0; s < 2; ++s) {
+      for (int i = 0; i < kABufs; ++i) mbar_init(&sm.a_full[s][i], 4), mbar_init(&sm.a_empty[s][i], 1);
+      mbar_init(&sm.d_empty[s], kEpilogue);
+    }
+    mbar_init(&sm.d_full, 2);
+    for (int w = 0; w < kDequant; ++w)
+      for (int i = 0; i < kSlots; ++i) mbar_init(&sm.full[w][i], 1);
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  }
+  if (warp == kWarpProd) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(smem_u32(&sm.tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
+  }
+  // the experts' rows and token tiles
+  for (int e = tid; e <= p.E; e += kThreads) sm.off[e] = int(min(max(int64_t(p.offsets[e]), int64_t(0)), p.rows));
+  __syncthreads();
+  uint32_t tiles = 0;
+  for (int e0 = 0; e0 < p.E; e0 += kThreads) {
+    const int e = e0 + tid;
+    const uint32_t n = e < p.E ? uint32_t(max(sm.off[e + 1] - sm.off[e], 0)) : 0u;
+    uint32_t total;
+    const uint32_t at = block_exclusive_scan((n + kTile - 1) / kTile, sm.tmp, &total);
+    if (e < p.E) sm.start[e] = int(tiles + at);
+    tiles += total;
+  }
+  if (tid == 0) sm.start[p.E] = int(tiles);
+  attn::tc_fence_before();
+  __syncthreads();
+  attn::tc_fence_after();
+  const uint32_t tmem = sm.tmem;
+  const int64_t n_units = int64_t(tiles) * p.n_mt;
+
+  // Unit u: neighbouring units share their rows of x.  An expert's tiles have nearly the same number of rows.
+  auto unit = [&](int64_t u) {
+    const int tile = int(u / p.n_mt);
+    int lo = 0, hi = p.E;  // start[lo] <= tile < start[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (sm.start[mid] <= tile) lo = mid;
+      else hi = mid;
+    }
+    const int first = sm.off[lo], n = sm.off[lo + 1] - first, n_tiles = sm.start[lo + 1] - sm.start[lo];
+    const int per = ((n + n_tiles - 1) / n_tiles + 15) / 16 * 16, at = (tile - sm.start[lo]) * per;
+    return Unit{lo, first + at, min(per, n - at), int(u - int64_t(tile) * p.n_mt)};
+  };
+
+  if (warp < 2) {
+    if (lane == 0) {
+      const int s = warp;
+      const uint32_t d = tmem + uint32_t(s) * kDCols, a0 = tmem + kACol + uint32_t(s) * (kABufs * kACols);
+      const uint64_t x0 = attn::smem_desc(smem_u32(smem), 0, 1024);
+      uint32_t a_use = 0, x_use = 0, i = 0;
+      for (int64_t u = blockIdx.x; u < n_units; u += gridDim.x, ++i, x_use += uint32_t(p.n_kb)) {
+        const Unit un = unit(u);
+        const uint32_t idesc = attn::instr_desc(128, false, false, (un.n + 15) / 16 * 16);
+        if (i > 0) wait(&sm.d_empty[s], i - 1);
+        attn::tc_fence_after();
+        bool first = true;
+        for (int k = MT == 2 ? 0 : s; k < p.n_kb; k += MT == 2 ? 1 : 2, first = false, ++a_use) {
+          const uint32_t xu = x_use + uint32_t(k), stage = xu % kStages, buf = a_use % kABufs;
+          wait(&sm.x_full[stage], xu / kStages);
+          wait(&sm.a_full[s][buf], a_use / kABufs);
+          attn::tc_fence_after();
+          const uint64_t xk = x0 + uint64_t(stage * (kStage / 16));
+#pragma unroll
+          for (uint32_t j = 0; j < kChan / 16; ++j)
+            umma_ts(d, a0 + buf * kACols + j * 8u, xk + uint64_t((j >> 2) * (kTile * 128 / 16) + (j & 3u) * 2u), idesc, !first || j > 0);
+          attn::umma_commit(smem_u32(&sm.a_empty[s][buf]));
+          attn::umma_commit(smem_u32(&sm.x_empty[stage]));
         }
-        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-        uint32_t am = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) am = max(am, max(u[i] & 0x7FFFu, (u[i] >> 16) & 0x7FFFu));
-#pragma unroll
-        for (int o = 8; o; o >>= 1) am = max(am, __shfl_xor_sync(0xffffffffu, am, o));
-        const int up = am ? min(max(141 - int(am >> 7), -126), 126) : 0;
-        const float f = __uint_as_float(uint32_t(127 + up) << 23);
-        uint32_t o[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = attn::h2_bits(__floats2half2_rn(bf16lo(u[i]) * f, bf16hi(u[i]) * f));
-        xs[tok >> 3][j & 3][(tok & 7) * 4 + (j >> 2)] = make_uint4(o[0], o[1], o[2], o[3]);
-        if (j == 0) xf[tok] = __uint_as_float(uint32_t(127 - up) << 23);
+        attn::umma_commit(smem_u32(&sm.d_full));
       }
-      __syncthreads();
-      const uint8_t* blk = w + int64_t(kb) * kBlock;
-      float d[2][2][4] = {};
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        uint4 c[2];
-        __half2 sc[2][2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int row = 16 * r + 8 * h + g;
-          c[h] = __ldg(reinterpret_cast<const uint4*>(blk + block_place(row, t)));
-          const __half2 s2 = attn::bits_h2(attn::e4m3x2_to_f16x2(__ldg(reinterpret_cast<const uint16_t*>(blk + kCodeBytes + row * 8 + 2 * t))));
-          sc[h][0] = __low2half2(s2), sc[h][1] = __high2half2(s2);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t a[2][4];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            attn::e2m1x8_to_f16x2x4(i == 0 ? c[h].x : i == 1 ? c[h].y : i == 2 ? c[h].z : c[h].w, a[h][0], a[h][1], a[h][2], a[h][3]);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) a[h][q] = attn::h2_bits(__hmul2(attn::bits_h2(a[h][q]), sc[h][i >> 1]));
-          }
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const uint4 xb = xs[j][i][lane];
-            mma_f16(d[r][j], a[0][0], a[1][0], a[0][1], a[1][1], xb.x, xb.y);
-            mma_f16(d[r][j], a[0][2], a[1][2], a[0][3], a[1][3], xb.z, xb.w);
-          }
-        }
+    }
+  } else if (warp < kWarpDeq) {
+    // x: 16 threads per row of a channel block, in groups of 64 channels, each [kTile rows][128 bytes], 16-byte pieces
+    // swizzled by the row.  Rows past the unit's last are left as they are: they reach their own columns alone.
+    const int t = tid - kWarpProd * 32, j = t & 15, rr = t >> 4;
+    uint32_t xu = 0, i = 0;
+    auto hand_on = [&](uint32_t use) {
+      attn::fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.x_full[use % kStages]);
+    };
+    for (int64_t u = blockIdx.x; u < n_units; u += gridDim.x, ++i) {
+      const Unit un = unit(u);
+      int from = -1;
+      if (t < un.n) {
+        const int64_t s = p.src ? int64_t(p.src[un.r0 + t]) : int64_t(un.r0 + t);
+        if (s >= 0 && s < p.n_x) from = int(s);
+        else if (s >= p.n_x) atomicOr(p.flags, CSA2_FLAG_INDEX_OOB);
       }
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float f0 = xf[8 * j + 2 * t], f1 = xf[8 * j + 2 * t + 1];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          acc[r][j][0] = fmaf(d[r][j][0], f0, acc[r][j][0]);
-          acc[r][j][1] = fmaf(d[r][j][1], f1, acc[r][j][1]);
-          acc[r][j][2] = fmaf(d[r][j][2], f0, acc[r][j][2]);
-          acc[r][j][3] = fmaf(d[r][j][3], f1, acc[r][j][3]);
+      sm.idx[i & 1][t] = from;
+      asm volatile("bar.sync 2, 128;\n" ::: "memory");
+      const int* idx = sm.idx[i & 1];
+      for (int k = 0; k < p.n_kb; ++k, ++xu) {
+        const uint32_t stage = xu % kStages;
+        if (xu >= kStages) wait(&sm.x_empty[stage], xu / kStages - 1);
+        const int64_t ch = int64_t(k) * kChan + 8 * j;
+        const uint32_t dst = smem_u32(smem) + stage * kStage + uint32_t(j >> 3) * (kTile * 128);
+        const uint16_t* src = p.xs + ch;
+#pragma unroll 4
+        for (int r = rr; r < un.n; r += 8) {
+          const int f = idx[r];
+          const bool on = f >= 0 && ch < p.n_in;
+          cp_async16(dst + uint32_t(r) * 128u + uint32_t(((j & 7) ^ (r & 7)) << 4), on ? static_cast<const void*>(src + int64_t(f) * p.n_in) : p.packed, on ? 16 : 0);
+        }
+        cp_async_commit();
+        if (xu >= kBehind) {
+          cp_async_wait<kBehind>();
+          hand_on(xu - kBehind);
         }
       }
     }
-    const int64_t width = p.act ? p.n_out / 2 : p.n_out;
-#pragma unroll
-    for (int r = 0; r < 2; ++r)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int64_t n = int64_t(rb) * kRows + 16 * r + 8 * h + g;
-        const float rs = n < p.n_out && p.row_scale ? p.row_scale[int64_t(e) * p.n_out + n] : 1.f;
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const int64_t row = r0 + 8 * j + 2 * t + q;
-            float v = acc[r][j][2 * h + q] * rs;
-            int64_t at = n;
-            bool mine = n < p.n_out && row < hi;
-            if (p.act) {
-              const float up = __shfl_xor_sync(0xffffffffu, v, 4);  // output n + 1
-              v = silu(v) * up;
-              mine = mine && !(g & 1);
-              at = n / 2;
-            }
-            if (!mine) continue;
-            if (p.y_fp32) static_cast<float*>(p.y)[row * width + at] = v;
-            else static_cast<__nv_bfloat16*>(p.y)[row * width + at] = __float2bfloat16_rn(v);
-          }
+    cp_async_wait<0>();
+    for (uint32_t b = min(uint32_t(kBehind), xu); b > 0; --b) hand_on(xu - b);
+  } else if (warp < kWarpEpi) {
+    const int me = warp - kWarpDeq, s = me >> 2;
+    const uint32_t lanes = uint32_t(32 * q) << 16, a0 = tmem + kACol + uint32_t(s) * (kABufs * kACols);
+    constexpr int kStep = MT == 2 ? 1 : 2;
+    const int k_first = MT == 2 ? 0 : s;
+    auto row_block = [&](const Unit& un) { return un.mt * (4 * MT) + (MT == 2 ? 4 * s : 0) + q; };
+    // the next block to copy
+    int64_t lu = int64_t(blockIdx.x) - gridDim.x;
+    int lk = p.n_kb;
+    const uint8_t* l_src = nullptr;
+    int copied = 0;
+    auto copy = [&](int slot) {  // one thread
+      while (lk >= p.n_kb) {
+        lu += gridDim.x;
+        if (lu >= n_units) return;
+        const Unit un = unit(lu);
+        const int rb = row_block(un);
+        if (rb >= p.n_rb) continue;
+        lk = k_first;
+        l_src = p.packed + int64_t(un.e) * p.w_bytes + (int64_t(rb) * p.n_kb + lk) * kBlock;
       }
+      if (!late) block_copy(sm.ring[me][slot], l_src, &sm.full[me][slot]), ++copied;
+      lk += kStep, l_src += kStep * kBlock;
+    };
+    if (lane == 0)
+      for (int i = 0; i < kSlots; ++i) copy(i);
+    __syncwarp();
+    uint32_t a_use = 0, w_use = 0;
+    for (int64_t u = blockIdx.x; u < n_units; u += gridDim.x) {
+      const bool on = row_block(unit(u)) < p.n_rb;
+      for (int k = k_first; k < p.n_kb; k += kStep, ++a_use) {
+        const uint32_t buf = a_use % kABufs, slot = w_use % kSlots;
+        uint4 c[4];
+        uint2 sc;
+        if (on) {
+          wait(&sm.full[me][slot], w_use / kSlots);
+          const unsigned char* blk = sm.ring[me][slot];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) c[j] = *reinterpret_cast<const uint4*>(blk + block_place(lane, j));
+          sc = *reinterpret_cast<const uint2*>(blk + kCodeBytes + 8 * lane);
+          attn::fence_async_smem();  // what the lanes have read comes before what the copy writes
+          __syncwarp();
+          if (lane == 0) copy(int(slot));
+          ++w_use;
+        }
+        if (a_use >= kABufs) wait(&sm.a_empty[s][buf], a_use / kABufs - 1);
+        __syncwarp();
+        attn::tc_fence_after();
+        if (on) {
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {  // 64 channels, 32 columns
+            const uint32_t sw = hf ? sc.y : sc.x;
+            const __half2 s01 = attn::bits_h2(attn::e4m3x2_to_f16x2(uint16_t(sw))),
+                          s23 = attn::bits_h2(attn::e4m3x2_to_f16x2(uint16_t(sw >> 16)));
+            uint32_t v[32];
+#pragma unroll
+            for (int w = 0; w < 8; ++w) {
+              const uint4 cw = c[2 * hf + (w >> 2)];
+              uint32_t* o = v + 4 * w;
+              attn::e2m1x8_to_f16x2x4((w & 3) == 0 ? cw.x : (w & 3) == 1 ? cw.y : (w & 3) == 2 ? cw.z : cw.w, o[0], o[1], o[2],
+                                      o[3]);
+              const __half2 f = w < 2 ? __low2half2(s01) : w < 4 ? __high2half2(s01) : w < 6 ? __low2half2(s23) : __high2half2(s23);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) o[j] = attn::h2_bits(__hmul2(attn::bits_h2(o[j]), f));
+            }
+            tmem_st32(a0 + lanes + buf * kACols + 32u * hf, v);
+          }
+          asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
+        }
+        attn::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.a_full[s][buf]);
+      }
+    }
+    if (lane == 0 && late) bar_drain<kSlots>(sm.full[me], copied);
+  } else {
+    const uint32_t lanes = uint32_t(32 * q) << 16;
+    const int t = tid - kWarpEpi * 32;
+    const int64_t width = p.act ? p.n_out / 2 : p.n_out;
+    uint32_t i = 0;
+    for (int64_t u = blockIdx.x; u < n_units; u += gridDim.x, ++i) {
+      const Unit un = unit(u);
+      float inv = 0.f;
+      if (t < un.n) {
+        const int64_t s = p.src ? int64_t(p.src[un.r0 + t]) : int64_t(un.r0 + t);
+        if (s >= 0 && s < p.n_x) inv = p.inv[s];
+      }
+      asm volatile("bar.sync 1, 128;\n" ::: "memory");  // the last unit's are done with
+      sm.inv[t] = inv;
+      asm volatile("bar.sync 1, 128;\n" ::: "memory");
+      wait(&sm.d_full, i);
+      __syncwarp();
+      attn::tc_fence_after();
+#pragma unroll 1
+      for (int s = 0; s < MT; ++s) {
+        const int64_t n = int64_t(un.mt) * (128 * MT) + 128 * s + 32 * q + lane;
+        const float rs = p.row_scale && n < p.n_out ? __ldg(p.row_scale + int64_t(un.e) * p.n_out + n) : 1.f;
+#pragma unroll 1
+        for (int c = 0; c < un.n; c += 16) {
+          uint32_t d[2][16];
+          tmem_ld16(tmem + lanes + uint32_t(s) * kDCols + uint32_t(c), d[0]);
+          if (MT == 1) tmem_ld16(tmem + lanes + kDCols + uint32_t(c), d[1]);
+          asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
+          float v[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            v[j] = tmem_value(d[0][j]);
+            if (MT == 1 && p.n_kb > 1) v[j] += tmem_value(d[1][j]);
+            v[j] = v[j] * sm.inv[c + j] * rs;
+          }
+          if (p.act) {
+            // outputs 2i and 2i + 1 are neighbouring lanes': the even one finishes every other row, the odd one the others
+            const bool odd = lane & 1;
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {
+              const float got = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
+              const float o = odd ? silu(got) * v[j + 1] : silu(v[j]) * got;
+              const int r = c + j + (odd ? 1 : 0);
+              if (n >= p.n_out || r >= un.n) continue;
+              const int64_t at = int64_t(un.r0 + r) * width + (n >> 1);
+              if (p.y_fp32) static_cast<float*>(p.y)[at] = o;
+              else static_cast<__nv_bfloat16*>(p.y)[at] = __float2bfloat16_rn(o);
+            }
+          } else if (n < p.n_out) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              if (c + j >= un.n) break;
+              const int64_t at = int64_t(un.r0 + c + j) * width + n;
+              if (p.y_fp32) static_cast<float*>(p.y)[at] = v[j];
+              else static_cast<__nv_bfloat16*>(p.y)[at] = __float2bfloat16_rn(v[j]);
+            }
+          }
+          __syncwarp();
+        }
+        attn::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&sm.d_empty[s]);
+          if (MT == 1) mbar_arrive(&sm.d_empty[1]);
+        }
+      }
+    }
   }
+  __syncwarp();
+  attn::tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpProd) {
+    attn::tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(tmem) : "memory");
+  }
+}
+
+inline size_t xs_bytes(int64_t n_x, int64_t n_in) { return size_t(n_x * n_in * 2 + 255) / 256 * 256; }
+
+template <int MT>
+cudaError_t launch(Params p, int64_t tiles, int sms, cudaStream_t st) {
+  p.n_mt = (p.n_rb + 4 * MT - 1) / (4 * MT);
+  static std::atomic<uint64_t> done{0};
+  auto kern = grouped_kernel<MT>;
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), kSmem, done);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3(unsigned(std::min<int64_t>(tiles * p.n_mt, sms))), dim3(kThreads), kSmem, st, p);
 }
 
 }  // namespace grp
 
 size_t fp4_grouped_ws_bytes(int64_t n_x, int64_t n_in) {
   if (n_x <= 0 || n_in <= 0 || n_in % CSA2_GROUP || n_x > (int64_t(1) << 31) || n_in > (1 << 28)) return 0;
-  return size_t((n_x * (n_in * 2 + 4) + 255) / 256 * 256 + 1024);
+  return grp::xs_bytes(n_x, n_in) + size_t(n_x) * 4;
 }
 
 }  // namespace csa2
@@ -182,11 +505,20 @@ extern "C" csa2_status csa2_fp4_grouped(const uint16_t* x, int64_t n_x, int64_t 
   if (any_overlap(spans, 2, 7)) return CSA2_ERR_INVALID_ARG;
   Params p = {};
   p.x = x, p.packed = packed, p.row_scale = row_scale, p.offsets = offsets, p.src = src, p.y = y;
+  p.xs = static_cast<uint16_t*>(ws);
+  p.inv = reinterpret_cast<float*>(static_cast<char*>(ws) + xs_bytes(n_x, n_in));
   p.n_out = n_out, p.n_in = n_in, p.w_bytes = w_bytes, p.rows = rows, p.n_x = n_x, p.E = E, p.y_fp32 = y_fp32, p.act = act;
   p.n_kb = int((n_in + kChan - 1) / kChan), p.n_rb = int((n_out + kRows - 1) / kRows);
   p.flags = device_flags_ptr();
-  if (!p.flags) return CSA2_ERR_CUDA;
-  const cudaError_t e = launch_pdl(grouped_kernel, dim3(unsigned((p.n_rb + kWarps - 1) / kWarps), unsigned(E)), dim3(kThreads), 0,
-                                   reinterpret_cast<cudaStream_t>(stream), p);
+  const int sms = sm_count();
+  if (!p.flags || sms <= 0) return CSA2_ERR_CUDA;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+  if (n_x > 0) e = launch_pdl(scale_kernel, dim3(unsigned((n_x + 3) / 4)), dim3(128), 0, st, p);
+  if (e != cudaSuccess) return CSA2_ERR_CUDA;
+  // token tiles, at most and about
+  const int64_t most = std::min<int64_t>(rows, E) + rows / kTile, about = std::max<int64_t>(std::min<int64_t>(rows, E), rows / kTile);
+  if (about * ((p.n_rb + 7) / 8) >= 2 * sms) e = launch<2>(p, most, sms, st);
+  else e = launch<1>(p, most, sms, st);
   return e == cudaSuccess ? CSA2_OK : CSA2_ERR_CUDA;
 }
