@@ -191,7 +191,7 @@ def prepare(case, seed):
         if own:
             c = _csa2()
             st["packed"] = c.fp4_pack_experts(st["codes"], st["scales"])
-            st["ws"] = torch.empty((c.grouped_workspace_size(m, n_in),), dtype=torch.uint8, device=DEV)
+            st["ws"] = torch.empty((c.grouped_workspace_size(m * k, n_in),), dtype=torch.uint8, device=DEV)
     elif kind == "combine":
         m, k, n = case["m"], case["k"], case["n"]
         pos = torch.randperm(m * k, generator=g, device=DEV).view(m, k).to(torch.int32)
