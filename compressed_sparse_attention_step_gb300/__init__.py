@@ -654,9 +654,9 @@ def route_workspace_size(m, E):
 
 
 @functools.lru_cache(maxsize=256)
-def grouped_workspace_size(n_x, n_in):
-    """Bytes of csa2_fp4_grouped's workspace for n_x rows of x with n_in channels."""
-    return workspace_size(OP_FP4_GROUPED, B=n_x, cap=n_in)
+def grouped_workspace_size(rows, n_in):
+    """Bytes of csa2_fp4_grouped's workspace for `rows` rows of y and n_in channels of x."""
+    return workspace_size(OP_FP4_GROUPED, B=rows, cap=n_in)
 
 
 def _scratch(ws, need, device, dev, stream):
@@ -709,7 +709,7 @@ def csa2_fp4_grouped(x, packed, offsets, y, *, src=None, row_scale=None, act=ACT
     """Products of ragged groups of rows with their experts' 4-bit weights: rows offsets[e] .. offsets[e+1] - 1 of
     y [rows, n_out] (bf16 or fp32) are those of x bf16 [n_x, n_in] at src int32 [rows] (None: the same rows) times
     packed[e] (fp4_pack_experts), times row_scale fp32 [E, n_out].  act=ACT_SWIGLU: y [rows, n_out / 2] from the even
-    (gate) and odd (up) rows of the weight.  ws: grouped_workspace_size(n_x, n_in) bytes, allocated where None."""
+    (gate) and odd (up) rows of the weight.  ws: grouped_workspace_size(rows, n_in) bytes, allocated where None."""
     dev = _device()
     n_x, n_in = _dims(x, "x", 2)
     rows, width = _dims(y, "y", 2)
@@ -718,7 +718,7 @@ def csa2_fp4_grouped(x, packed, offsets, y, *, src=None, row_scale=None, act=ACT
     if src is None and n_x < rows:
         raise ValueError(f"x: expected at least {rows} rows, got {n_x}")
     fp32 = y.dtype in _F32
-    wp, wn, ws = _scratch(ws, grouped_workspace_size(n_x, n_in), x.device, dev, stream)
+    wp, wn, ws = _scratch(ws, grouped_workspace_size(rows, n_in), x.device, dev, stream)
     st = lib().csa2_fp4_grouped(
         _arg(x, "x", _BF16, (n_x, n_in), dev), n_x, n_in,
         _arg(packed, "packed", _U8, (E, _packed_bytes(n_out, n_in)), dev), E, n_out,

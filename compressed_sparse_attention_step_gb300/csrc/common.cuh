@@ -365,9 +365,9 @@ cudaError_t launch_bitmap_select(const uint16_t* qI, const float* w, int B, int 
 int bitmap_list_cap();  // marked keys that one list round of the selection rescores
 // Context split: workspace of csa2_merge_topk_pairs for G shards' k pairs per row (shard.cu).
 size_t merge_pairs_ws_bytes(int rows, int G, int k);
-// The experts' operators: csa2_expert_route's counts (experts.cu), csa2_fp4_grouped's rows of x (grouped.cu).
+// The experts' operators: csa2_expert_route's counts (experts.cu), csa2_fp4_grouped's rows (grouped.cu).
 size_t expert_route_ws_bytes(int64_t m, int64_t E);
-size_t fp4_grouped_ws_bytes(int64_t n_x, int64_t n_in);
+size_t fp4_grouped_ws_bytes(int64_t rows, int64_t n_in);
 int attn_auto_split(int64_t instances, int k, int W);
 
 // Library-owned side stream (highest priority) and events of the current device, created on first

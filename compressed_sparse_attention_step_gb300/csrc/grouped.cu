@@ -7,8 +7,9 @@
 // of matvec.cu: a code times a scale is exact in f16, and so is x scaled by the power of two that brings a row's
 // largest magnitude into [2^14, 2^15), down to 2^-28 of it (off by less than 2^-38 of it below).
 //
-// Two launches: scale_kernel writes the rows of x as f16 and each row's factor into the workspace; grouped_kernel, one
-// persistent CTA per SM, takes units of an expert, up to 128 of its rows, and 128 or 256 outputs.
+// Two launches: scale_kernel writes the rows as f16 into the workspace, each unit's in the order in which the products
+// read them, and each row's factor; grouped_kernel, one persistent CTA per SM, takes units of an expert, up to 128 of
+// its rows, and 128 or 256 outputs.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -25,28 +26,27 @@ constexpr int kBlock = kCodeBytes + kRows * kChan / CSA2_GROUP;  // 2304 bytes
 constexpr int kTile = 128;       // token rows of a unit, at most
 constexpr int kStages = 4;       // channel blocks of x under way
 constexpr int kStage = kTile * kChan * 2;
-constexpr int kBehind = 2;       // channel blocks that a producer has asked for and not yet handed on
-constexpr int kSlots = 4;        // weight blocks under way per dequantising warp
+constexpr int kSlots = 4;        // steps of four weight blocks (128 outputs) under way per pipeline
 constexpr int kABufs = 2;        // dequantised blocks per pipeline
-// Two pipelines (s = 0, 1), each of an issuing thread, four dequantising warps, kABufs blocks in tensor memory and one
-// accumulator.  With two row tiles (MT = 2) each has its own 128 outputs; with one they share its channel blocks, even
-// and odd, and the accumulators are added.
-constexpr int kProducers = 4, kDequant = 8, kEpilogue = 4;
-constexpr int kWarpProd = 2, kWarpDeq = kWarpProd + kProducers, kWarpEpi = kWarpDeq + kDequant;
+// Two pipelines (s = 0, 1), each of a copying warp, two groups of four dequantising warps, a block in tensor memory for
+// each group, an issuing warp and one accumulator.  With two row tiles (MT = 2) each pipeline has its own 128 outputs; with one they
+// share its channel blocks, even and odd, and the accumulators are added.  The groups of a pipeline take its blocks in
+// turn.  (A buffer has one filler and one user: none waits for a phase of a barrier that lies two ahead.)
+constexpr int kDequant = 8 * kABufs, kEpilogue = 4;
+constexpr int kWarpX = 2, kWarpCopy = 3, kWarpDeq = 5, kWarpEpi = kWarpDeq + kDequant;
 constexpr int kThreads = (kWarpEpi + kEpilogue) * 32;
 constexpr uint32_t kACols = kChan / 2, kDCols = kTile;
 constexpr uint32_t kACol = 2 * kDCols;
 static_assert(kACol + 2 * kABufs * kACols <= 512, "tensor memory");
-static_assert(kWarpDeq % 4 == 2 && kWarpEpi % 4 == 2, "four neighbouring warps reach all lanes");
+static_assert(kThreads <= 1024, "warps");
 
 struct Tail {
-  alignas(16) unsigned char ring[kDequant][kSlots][kBlock];
+  alignas(16) unsigned char ring[2][kSlots][4][kBlock];
   float inv[kTile];
-  int idx[2][kTile];
   int off[CSA2_MAX_EXPERTS + 1];    // the experts' first rows, within [0, rows]
   int start[CSA2_MAX_EXPERTS + 1];  // their first token tiles
   uint32_t tmp[32];
-  uint64_t full[kDequant][kSlots];
+  uint64_t w_full[2][kSlots], w_empty[2][kSlots];
   uint64_t x_full[kStages], x_empty[kStages];
   uint64_t a_full[2][kABufs], a_empty[2][kABufs], d_full, d_empty[2];
   uint32_t tmem;
@@ -54,10 +54,24 @@ struct Tail {
 constexpr size_t kSmem = size_t(kStages) * kStage + sizeof(Tail);
 static_assert(kSmem <= 227 * 1024, "shared memory");
 
+// Row r of expert rows [first, first + n): the first row and the rows of its tile.  The tiles of an expert are as few as
+// can be, of nearly the same height, multiples of 16 but the last.
+struct Span16 {
+  int r0, n;
+};
+__device__ __forceinline__ Span16 tile_of(int first, int n, int tile) {
+  const int tiles = (n + kTile - 1) / kTile, per = ((n + tiles - 1) / tiles + 15) / 16 * 16, at = tile * per;
+  return Span16{first + at, min(per, n - at)};
+}
+__device__ __forceinline__ int tile_at(int n, int r) {  // the tile of the r-th row of n
+  const int tiles = (n + kTile - 1) / kTile;
+  return r / (((n + tiles - 1) / tiles + 15) / 16 * 16);
+}
+
 struct Params {
   const uint16_t* x;
-  uint16_t* xs;   // f16 rows of x
-  float* inv;     // a row's factor
+  unsigned char* xs;  // the units' rows as f16: [channel block][64 channels][row][128 bytes, pieces swizzled by the row]
+  float* inv;         // a row's factor
   const uint8_t* packed;
   const float* row_scale;
   const int32_t *offsets, *src;
@@ -69,13 +83,13 @@ struct Params {
 
 __device__ __forceinline__ int block_place(int r, int j) { return j * 512 + (r ^ (2 * j)) * 16; }
 
-__device__ __forceinline__ void block_copy(void* dst, const uint8_t* src, uint64_t* bar) {
-  const uint32_t b = smem_u32(bar);
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(b), "r"(kBlock) : "memory");
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
-                   smem_u32(dst)),
-               "l"(src), "r"(kBlock), "r"(b)
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
                : "memory");
+}
+__device__ __forceinline__ void mbar_expect(uint64_t* bar, uint32_t bytes) {  // an arrival, and bytes still to come
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void mbar_init(uint64_t* b, int n) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(smem_u32(b)), "r"(n) : "memory");
@@ -83,13 +97,21 @@ __device__ __forceinline__ void mbar_init(uint64_t* b, int n) {
 __device__ __forceinline__ void mbar_arrive(uint64_t* b) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_u32(b)) : "memory");
 }
-// D (+)= A B with A in tensor memory
+// D (+)= A B with A in tensor memory; called by a whole warp, issued by one lane (the same each time)
 __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{ .reg .pred p;\n\t"
+      "{ .reg .pred p, one;\n\t"
+      "elect.sync _|one, 0xffffffff;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }\n" ::"r"(d),
+      "@one tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }\n" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void commit_one(uint64_t* bar) {
+  asm volatile(
+      "{ .reg .pred one;\n\t"
+      "elect.sync _|one, 0xffffffff;\n\t"
+      "@one tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }\n" ::"r"(smem_u32(bar))
       : "memory");
 }
 __device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t (&r)[32]) {
@@ -116,59 +138,77 @@ __device__ __forceinline__ float tmem_value(uint32_t& r) {
   asm volatile("" : "+r"(r));
   return __uint_as_float(r);
 }
-__device__ __forceinline__ float silu(float v) { return v / (1.f + expf(-v)); }
+// off by a few 2^-22 of it: the exponent's rounding, the hardware's exponential, sum and quotient
+__device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.f + attn::ex2(v * -1.4426950408889634f)); }
 
-// A warp per row of x.  The first 2048 channels are kept between the two passes, those behind are read again.
+// A warp per row r of the lists.  The first 2048 channels are kept between the two passes, those behind are read again.
 __global__ void __launch_bounds__(128) scale_kernel(const Params p) {
+  __shared__ int off[CSA2_MAX_EXPERTS + 1];
   pdl_wait();
   pdl_trigger();
+  for (int e = threadIdx.x; e <= p.E; e += 128) off[e] = int(min(max(int64_t(p.offsets[e]), int64_t(0)), p.rows));
+  __syncthreads();
   const int64_t row = (int64_t(blockIdx.x) * 128 + threadIdx.x) >> 5;
-  if (row >= p.n_x) return;
-  const int lane = int(threadIdx.x & 31);
-  const uint16_t* src = p.x + row * p.n_in;
-  uint16_t* dst = p.xs + row * p.n_in;
-  const int n_in = int(p.n_in);
+  if (row >= p.rows) return;
+  const int lane = int(threadIdx.x & 31), r = int(row);
+  int lo = 0, hi = p.E;  // the last expert that begins at or before the row
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (off[mid] <= r) lo = mid;
+    else hi = mid;
+  }
+  if (r < off[lo] || r >= off[lo + 1]) return;
+  const int n_e = off[lo + 1] - off[lo];
+  const Span16 tile = tile_of(off[lo], n_e, tile_at(n_e, r - off[lo]));
+  const int i = r - tile.r0;
+  const int64_t from = p.src ? int64_t(p.src[r]) : row;
+  const bool on = from >= 0 && from < p.n_x;
+  if (from >= p.n_x && lane == 0) atomicOr(p.flags, CSA2_FLAG_INDEX_OOB);
+  const uint16_t* src = p.x + (on ? from : 0) * p.n_in;
+  unsigned char* dst = p.xs + (int64_t(tile.r0) * p.n_kb) * (kChan * 2) + i * 128;
+  const int n_in = on ? int(p.n_in) : 0, n_all = p.n_kb * kChan;
   auto at = [&](int c) { return c < n_in ? __ldg(reinterpret_cast<const uint4*>(src + c)) : make_uint4(0, 0, 0, 0); };
   auto mag = [](uint32_t am, const uint4& v) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) am = max(am, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
+    for (int j = 0; j < 4; ++j) am = max(am, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
     return am;
   };
   uint4 keep[8];
   uint32_t am = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) keep[i] = at(lane * 8 + 256 * i);
+  for (int j = 0; j < 8; ++j) keep[j] = at(lane * 8 + 256 * j);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) am = mag(am, keep[i]);
+  for (int j = 0; j < 8; ++j) am = mag(am, keep[j]);
   for (int c0 = 2048; c0 < n_in; c0 += 1024) {
     uint4 v[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = at(c0 + lane * 8 + 256 * i);
+    for (int j = 0; j < 4; ++j) v[j] = at(c0 + lane * 8 + 256 * j);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) am = mag(am, v[i]);
+    for (int j = 0; j < 4; ++j) am = mag(am, v[j]);
   }
   am = __reduce_max_sync(0xffffffffu, am);
   const int up = am ? min(max(141 - int(am >> 7), -126), 126) : 0;
   const float f = __uint_as_float(uint32_t(127 + up) << 23);
-  auto put = [&](int c, const uint4& v) {
-    if (c >= n_in) return;
+  auto put = [&](int c, const uint4& v) {  // channels c .. c + 7; zeros behind the last
+    if (c >= n_all) return;
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     uint32_t o[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = attn::h2_bits(__floats2half2_rn(bf16lo(w[i]) * f, bf16hi(w[i]) * f));
-    *reinterpret_cast<uint4*>(dst + c) = make_uint4(o[0], o[1], o[2], o[3]);
+    for (int j = 0; j < 4; ++j) o[j] = attn::h2_bits(__floats2half2_rn(bf16lo(w[j]) * f, bf16hi(w[j]) * f));
+    *reinterpret_cast<uint4*>(dst + int64_t(c >> 6) * (tile.n * 128) + ((((c >> 3) & 7) ^ (i & 7)) << 4)) =
+        make_uint4(o[0], o[1], o[2], o[3]);
   };
 #pragma unroll
-  for (int i = 0; i < 8; ++i) put(lane * 8 + 256 * i, keep[i]);
-  for (int c0 = 2048; c0 < n_in; c0 += 1024) {
+  for (int j = 0; j < 8; ++j) put(lane * 8 + 256 * j, keep[j]);
+  for (int c0 = 2048; c0 < n_all; c0 += 1024) {
     uint4 v[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = at(c0 + lane * 8 + 256 * i);
+    for (int j = 0; j < 4; ++j) v[j] = at(c0 + lane * 8 + 256 * j);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) put(c0 + lane * 8 + 256 * i, v[i]);
+    for (int j = 0; j < 4; ++j) put(c0 + lane * 8 + 256 * j, v[j]);
   }
-  if (lane == 0) p.inv[row] = __uint_as_float(uint32_t(127 - up) << 23);
+  if (lane == 0) p.inv[r] = __uint_as_float(uint32_t(127 - up) << 23);
 }
 
 struct Unit {
@@ -192,17 +232,17 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const Params p) {
   };
 
   if (tid == 0) {
-    for (int i = 0; i < kStages; ++i) mbar_init(&sm.x_full[i], kProducers), mbar_init(&sm.x_empty[i], MT);
+    for (int i = 0; i < kStages; ++i) mbar_init(&sm.x_full[i], 1), mbar_init(&sm.x_empty[i], MT);
     for (int s = 0; s < 2; ++s) {
       for (int i = 0; i < kABufs; ++i) mbar_init(&sm.a_full[s][i], 4), mbar_init(&sm.a_empty[s][i], 1);
       mbar_init(&sm.d_empty[s], kEpilogue);
     }
     mbar_init(&sm.d_full, 2);
-    for (int w = 0; w < kDequant; ++w)
-      for (int i = 0; i < kSlots; ++i) mbar_init(&sm.full[w][i], 1);
+    for (int s = 0; s < 2; ++s)
+      for (int i = 0; i < kSlots; ++i) mbar_init(&sm.w_full[s][i], 1), mbar_init(&sm.w_empty[s][i], 4);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
-  if (warp == kWarpProd) {
+  if (warp == kWarpX) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(smem_u32(&sm.tmem)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
   }
@@ -225,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const Params p) {
   const uint32_t tmem = sm.tmem;
   const int64_t n_units = int64_t(tiles) * p.n_mt;
 
-  // Unit u: neighbouring units share their rows of x.  An expert's tiles have nearly the same number of rows.
+  // Unit u: neighbouring units share their rows of x.
   auto unit = [&](int64_t u) {
     const int tile = int(u / p.n_mt);
     int lo = 0, hi = p.E;  // start[lo] <= tile < start[hi]
@@ -234,126 +274,105 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const Params p) {
       if (sm.start[mid] <= tile) lo = mid;
       else hi = mid;
     }
-    const int first = sm.off[lo], n = sm.off[lo + 1] - first, n_tiles = sm.start[lo + 1] - sm.start[lo];
-    const int per = ((n + n_tiles - 1) / n_tiles + 15) / 16 * 16, at = (tile - sm.start[lo]) * per;
-    return Unit{lo, first + at, min(per, n - at), int(u - int64_t(tile) * p.n_mt)};
+    const Span16 rows = tile_of(sm.off[lo], sm.off[lo + 1] - sm.off[lo], tile - sm.start[lo]);
+    return Unit{lo, rows.r0, rows.n, int(u - int64_t(tile) * p.n_mt)};
   };
 
   if (warp < 2) {
-    if (lane == 0) {
-      const int s = warp;
-      const uint32_t d = tmem + uint32_t(s) * kDCols, a0 = tmem + kACol + uint32_t(s) * (kABufs * kACols);
-      const uint64_t x0 = attn::smem_desc(smem_u32(smem), 0, 1024);
-      uint32_t a_use = 0, x_use = 0, i = 0;
-      for (int64_t u = blockIdx.x; u < n_units; u += gridDim.x, ++i, x_use += uint32_t(p.n_kb)) {
-        const Unit un = unit(u);
-        const uint32_t idesc = attn::instr_desc(128, false, false, (un.n + 15) / 16 * 16);
-        if (i > 0) wait(&sm.d_empty[s], i - 1);
-        attn::tc_fence_after();
-        bool first = true;
-        for (int k = MT == 2 ? 0 : s; k < p.n_kb; k += MT == 2 ? 1 : 2, first = false, ++a_use) {
-          const uint32_t xu = x_use + uint32_t(k), stage = xu % kStages, buf = a_use % kABufs;
-          wait(&sm.x_full[stage], xu / kStages);
-          wait(&sm.a_full[s][buf], a_use / kABufs);
-          attn::tc_fence_after();
-          const uint64_t xk = x0 + uint64_t(stage * (kStage / 16));
-#pragma unroll
-          for (uint32_t j = 0; j < kChan / 16; ++j)
-            umma_ts(d, a0 + buf * kACols + j * 8u, xk + uint64_t((j >> 2) * (kTile * 128 / 16) + (j & 3u) * 2u), idesc, !first || j > 0);
-          attn::umma_commit(smem_u32(&sm.a_empty[s][buf]));
-          attn::umma_commit(smem_u32(&sm.x_empty[stage]));
-        }
-        attn::umma_commit(smem_u32(&sm.d_full));
-      }
-    }
-  } else if (warp < kWarpDeq) {
-    // x: 16 threads per row of a channel block, in groups of 64 channels, each [kTile rows][128 bytes], 16-byte pieces
-    // swizzled by the row.  Rows past the unit's last are left as they are: they reach their own columns alone.
-    const int t = tid - kWarpProd * 32, j = t & 15, rr = t >> 4;
-    uint32_t xu = 0, i = 0;
-    auto hand_on = [&](uint32_t use) {
-      attn::fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.x_full[use % kStages]);
-    };
-    for (int64_t u = blockIdx.x; u < n_units; u += gridDim.x, ++i) {
+    // The whole warp runs the loop, so that the operands of the MMAs are the same in all lanes; one lane issues them.
+    const int s = warp;
+    const uint32_t d = tmem + uint32_t(s) * kDCols, a0 = tmem + kACol + uint32_t(s) * (kABufs * kACols);
+    const uint64_t x0 = attn::smem_desc(smem_u32(smem), 0, 1024);
+    uint32_t a_use = 0, x_use = 0, i = 0;
+    for (int64_t u = blockIdx.x; u < n_units; u += gridDim.x, ++i, x_use += uint32_t(p.n_kb)) {
       const Unit un = unit(u);
-      int from = -1;
-      if (t < un.n) {
-        const int64_t s = p.src ? int64_t(p.src[un.r0 + t]) : int64_t(un.r0 + t);
-        if (s >= 0 && s < p.n_x) from = int(s);
-        else if (s >= p.n_x) atomicOr(p.flags, CSA2_FLAG_INDEX_OOB);
+      const uint32_t idesc = attn::instr_desc(128, false, false, (un.n + 15) / 16 * 16);
+      if (i > 0) wait(&sm.d_empty[s], i - 1);
+      attn::tc_fence_after();
+      bool first = true;
+      for (int k = MT == 2 ? 0 : s; k < p.n_kb; k += MT == 2 ? 1 : 2, first = false, ++a_use) {
+        const uint32_t xu = x_use + uint32_t(k), stage = xu % kStages, buf = a_use % kABufs;
+        wait(&sm.x_full[stage], xu / kStages);
+        wait(&sm.a_full[s][buf], a_use / kABufs);
+        __syncwarp();
+        attn::tc_fence_after();
+        const uint64_t xk = x0 + uint64_t(stage * (kStage / 16));
+        const uint32_t a = a0 + buf * kACols;
+#pragma unroll
+        for (uint32_t j = 0; j < kChan / 16; ++j)
+          umma_ts(d, a + j * 8u, xk + uint64_t((j >> 2) * (kTile * 128 / 16) + (j & 3u) * 2u), idesc, !first || j > 0);
+        commit_one(&sm.a_empty[s][buf]);
+        commit_one(&sm.x_empty[stage]);
       }
-      sm.idx[i & 1][t] = from;
-      asm volatile("bar.sync 2, 128;\n" ::: "memory");
-      const int* idx = sm.idx[i & 1];
-      for (int k = 0; k < p.n_kb; ++k, ++xu) {
+      commit_one(&sm.d_full);
+    }
+  } else if (warp == kWarpX) {
+    // x: a channel block of the unit's rows as two groups of 64 channels, each [kTile rows][128 bytes].  Rows past the
+    // unit's last are left as they are: they reach their own columns of the sums alone.
+    asm volatile("fence.proxy.async.global;\n" ::: "memory");
+    uint32_t xu = 0, begun = 0;
+    for (int64_t u = blockIdx.x; u < n_units; u += gridDim.x) {
+      const Unit un = unit(u);
+      const uint32_t bytes = uint32_t(un.n) * 128u;
+      const unsigned char* src = p.xs + int64_t(un.r0) * p.n_kb * (kChan * 2) + lane * bytes;
+      for (int k = 0; k < p.n_kb; ++k, ++xu, src += 2 * bytes) {
         const uint32_t stage = xu % kStages;
         if (xu >= kStages) wait(&sm.x_empty[stage], xu / kStages - 1);
-        const int64_t ch = int64_t(k) * kChan + 8 * j;
-        const uint32_t dst = smem_u32(smem) + stage * kStage + uint32_t(j >> 3) * (kTile * 128);
-        const uint16_t* src = p.xs + ch;
-#pragma unroll 4
-        for (int r = rr; r < un.n; r += 8) {
-          const int f = idx[r];
-          const bool on = f >= 0 && ch < p.n_in;
-          cp_async16(dst + uint32_t(r) * 128u + uint32_t(((j & 7) ^ (r & 7)) << 4), on ? static_cast<const void*>(src + int64_t(f) * p.n_in) : p.packed, on ? 16 : 0);
-        }
-        cp_async_commit();
-        if (xu >= kBehind) {
-          cp_async_wait<kBehind>();
-          hand_on(xu - kBehind);
-        }
+        late = __any_sync(0xffffffffu, late);
+        if (late) continue;  // no more copies
+        if (lane == 0) mbar_expect(&sm.x_full[stage], 2 * bytes);
+        __syncwarp();
+        ++begun;
+        if (lane < 2) bulk_copy(smem_u32(smem) + stage * kStage + uint32_t(lane) * (kTile * 128), src, bytes, &sm.x_full[stage]);
       }
     }
-    cp_async_wait<0>();
-    for (uint32_t b = min(uint32_t(kBehind), xu); b > 0; --b) hand_on(xu - b);
-  } else if (warp < kWarpEpi) {
-    const int me = warp - kWarpDeq, s = me >> 2;
-    const uint32_t lanes = uint32_t(32 * q) << 16, a0 = tmem + kACol + uint32_t(s) * (kABufs * kACols);
-    constexpr int kStep = MT == 2 ? 1 : 2;
-    const int k_first = MT == 2 ? 0 : s;
-    auto row_block = [&](const Unit& un) { return un.mt * (4 * MT) + (MT == 2 ? 4 * s : 0) + q; };
-    // the next block to copy
-    int64_t lu = int64_t(blockIdx.x) - gridDim.x;
-    int lk = p.n_kb;
-    const uint8_t* l_src = nullptr;
-    int copied = 0;
-    auto copy = [&](int slot) {  // one thread
-      while (lk >= p.n_kb) {
-        lu += gridDim.x;
-        if (lu >= n_units) return;
-        const Unit un = unit(lu);
-        const int rb = row_block(un);
-        if (rb >= p.n_rb) continue;
-        lk = k_first;
-        l_src = p.packed + int64_t(un.e) * p.w_bytes + (int64_t(rb) * p.n_kb + lk) * kBlock;
-      }
-      if (!late) block_copy(sm.ring[me][slot], l_src, &sm.full[me][slot]), ++copied;
-      lk += kStep, l_src += kStep * kBlock;
-    };
-    if (lane == 0)
-      for (int i = 0; i < kSlots; ++i) copy(i);
-    __syncwarp();
-    uint32_t a_use = 0, w_use = 0;
+    // no CTA leaves with a copy under way, even if nobody waits for it
+    for (uint32_t b = begun > kStages ? begun - kStages : 0; b < begun; ++b) bar_wait(smem_u32(&sm.x_full[b % kStages]), (b / kStages) & 1u);
+  } else if (warp < kWarpDeq) {
+    // the weight: a step is the channel block of a pipeline's four row blocks, of which the last may not be there
+    const int s = warp - kWarpCopy;
+    constexpr int kStep = MT == 2 ? 1 : 2;  // channel blocks from one step of a pipeline to the next
+    uint32_t wu = 0, begun = 0;
     for (int64_t u = blockIdx.x; u < n_units; u += gridDim.x) {
-      const bool on = row_block(unit(u)) < p.n_rb;
-      for (int k = k_first; k < p.n_kb; k += kStep, ++a_use) {
-        const uint32_t buf = a_use % kABufs, slot = w_use % kSlots;
+      const Unit un = unit(u);
+      const int rb = un.mt * (4 * MT) + (MT == 2 ? 4 * s : 0), n = min(max(p.n_rb - rb, 0), 4);
+      const int k0 = MT == 2 ? 0 : s;
+      const uint8_t* src = p.packed + int64_t(un.e) * p.w_bytes + (int64_t(rb + min(lane, 3)) * p.n_kb + k0) * kBlock;
+      for (int k = k0; k < p.n_kb; k += kStep, ++wu, src += kStep * kBlock) {
+        const uint32_t slot = wu % kSlots;
+        if (wu >= kSlots) wait(&sm.w_empty[s][slot], wu / kSlots - 1);
+        late = __any_sync(0xffffffffu, late);
+        if (late) continue;
+        ++begun;
+        if (lane == 0) mbar_expect(&sm.w_full[s][slot], uint32_t(n) * kBlock);
+        __syncwarp();
+        if (lane < n) bulk_copy(smem_u32(sm.ring[s][slot][lane]), src, kBlock, &sm.w_full[s][slot]);
+      }
+    }
+    for (uint32_t b = begun > kSlots ? begun - kSlots : 0; b < begun; ++b) bar_wait(smem_u32(&sm.w_full[s][b % kSlots]), (b / kSlots) & 1u);
+  } else if (warp < kWarpEpi) {
+    const int s = (warp - kWarpDeq) >> 3, grp = ((warp - kWarpDeq) >> 2) & 1;  // a group takes every other step
+    const uint32_t lanes = uint32_t(32 * q) << 16, a = tmem + kACol + uint32_t(s * kABufs + grp) * kACols;
+    const int n_blk = MT == 2 ? p.n_kb : (p.n_kb + 1 - s) / 2;  // steps of a unit
+    uint32_t wu = uint32_t(grp), a_use = 0, end = 0;            // the group's next step, counted over the units
+    for (int64_t u = blockIdx.x; u < n_units; u += gridDim.x) {
+      end += uint32_t(n_blk);
+      const bool on = unit(u).mt * (4 * MT) + (MT == 2 ? 4 * s : 0) + q < p.n_rb;
+      for (; wu != end && wu != end + 1; wu += 2, ++a_use) {
+        const uint32_t slot = wu % kSlots;
         uint4 c[4];
         uint2 sc;
-        if (on) {
-          wait(&sm.full[me][slot], w_use / kSlots);
-          const unsigned char* blk = sm.ring[me][slot];
+        wait(&sm.w_full[s][slot], wu / kSlots);
+        {
+          const unsigned char* blk = sm.ring[s][slot][q];
 #pragma unroll
           for (int j = 0; j < 4; ++j) c[j] = *reinterpret_cast<const uint4*>(blk + block_place(lane, j));
           sc = *reinterpret_cast<const uint2*>(blk + kCodeBytes + 8 * lane);
           attn::fence_async_smem();  // what the lanes have read comes before what the copy writes
           __syncwarp();
-          if (lane == 0) copy(int(slot));
-          ++w_use;
+          if (lane == 0) mbar_arrive(&sm.w_empty[s][slot]);
         }
-        if (a_use >= kABufs) wait(&sm.a_empty[s][buf], a_use / kABufs - 1);
+        if (a_use > 0) wait(&sm.a_empty[s][grp], a_use - 1);
         __syncwarp();
         attn::tc_fence_after();
         if (on) {
@@ -373,16 +392,15 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const Params p) {
 #pragma unroll
               for (int j = 0; j < 4; ++j) o[j] = attn::h2_bits(__hmul2(attn::bits_h2(o[j]), f));
             }
-            tmem_st32(a0 + lanes + buf * kACols + 32u * hf, v);
+            tmem_st32(a + lanes + 32u * hf, v);
           }
           asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
         }
         attn::tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.a_full[s][buf]);
+        if (lane == 0) mbar_arrive(&sm.a_full[s][grp]);
       }
     }
-    if (lane == 0 && late) bar_drain<kSlots>(sm.full[me], copied);
   } else {
     const uint32_t lanes = uint32_t(32 * q) << 16;
     const int t = tid - kWarpEpi * 32;
@@ -390,11 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const Params p) {
     uint32_t i = 0;
     for (int64_t u = blockIdx.x; u < n_units; u += gridDim.x, ++i) {
       const Unit un = unit(u);
-      float inv = 0.f;
-      if (t < un.n) {
-        const int64_t s = p.src ? int64_t(p.src[un.r0 + t]) : int64_t(un.r0 + t);
-        if (s >= 0 && s < p.n_x) inv = p.inv[s];
-      }
+      const float inv = t < un.n ? p.inv[un.r0 + t] : 0.f;
       asm volatile("bar.sync 1, 128;\n" ::: "memory");  // the last unit's are done with
       sm.inv[t] = inv;
       asm volatile("bar.sync 1, 128;\n" ::: "memory");
@@ -454,13 +468,13 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const Params p) {
   __syncwarp();
   attn::tc_fence_before();
   __syncthreads();
-  if (warp == kWarpProd) {
+  if (warp == kWarpX) {
     attn::tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(tmem) : "memory");
   }
 }
 
-inline size_t xs_bytes(int64_t n_x, int64_t n_in) { return size_t(n_x * n_in * 2 + 255) / 256 * 256; }
+inline size_t xs_bytes(int64_t rows, int64_t n_in) { return size_t(rows * ((n_in + kChan - 1) / kChan)) * (kChan * 2); }
 
 template <int MT>
 cudaError_t launch(Params p, int64_t tiles, int sms, cudaStream_t st) {
@@ -474,9 +488,9 @@ cudaError_t launch(Params p, int64_t tiles, int sms, cudaStream_t st) {
 
 }  // namespace grp
 
-size_t fp4_grouped_ws_bytes(int64_t n_x, int64_t n_in) {
-  if (n_x <= 0 || n_in <= 0 || n_in % CSA2_GROUP || n_x > (int64_t(1) << 31) || n_in > (1 << 28)) return 0;
-  return grp::xs_bytes(n_x, n_in) + size_t(n_x) * 4;
+size_t fp4_grouped_ws_bytes(int64_t rows, int64_t n_in) {
+  if (rows <= 0 || n_in <= 0 || n_in % CSA2_GROUP || rows >= (int64_t(1) << 31) || n_in > (1 << 24)) return 0;
+  return grp::xs_bytes(rows, n_in) + size_t(rows) * 4;
 }
 
 }  // namespace csa2
@@ -496,25 +510,24 @@ extern "C" csa2_status csa2_fp4_grouped(const uint16_t* x, int64_t n_x, int64_t 
   if ((!x && n_x > 0) || !packed || !offsets || !y) return CSA2_ERR_INVALID_ARG;
   if (!al(x, 16) || !al(packed, 16) || !al(row_scale, 4) || !al(offsets, 4) || !al(src, 4) || !al(y, 16) || !al(ws, 16))
     return CSA2_ERR_INVALID_ARG;
-  const size_t need = fp4_grouped_ws_bytes(n_x, n_in);
-  if (need && (!ws || ws_bytes < need)) return CSA2_ERR_WORKSPACE;
+  const size_t need = fp4_grouped_ws_bytes(rows, n_in);
+  if ((!ws || ws_bytes < need)) return CSA2_ERR_WORKSPACE;
   const int64_t width = act ? n_out / 2 : n_out, w_bytes = int64_t(csa2_fp4_packed_bytes(n_out, n_in));
-  const Span spans[] = {span(y, rows, width * (y_fp32 ? 4 : 2)), span(need ? ws : nullptr, int64_t(need), 1),
+  const Span spans[] = {span(y, rows, width * (y_fp32 ? 4 : 2)), span(ws, int64_t(need), 1),
                         span(x, n_x, n_in * 2), span(packed, E, w_bytes), span(row_scale, E, n_out * 4),
                         span(offsets, E + 1, 4), span(src, rows, 4)};
   if (any_overlap(spans, 2, 7)) return CSA2_ERR_INVALID_ARG;
   Params p = {};
   p.x = x, p.packed = packed, p.row_scale = row_scale, p.offsets = offsets, p.src = src, p.y = y;
-  p.xs = static_cast<uint16_t*>(ws);
-  p.inv = reinterpret_cast<float*>(static_cast<char*>(ws) + xs_bytes(n_x, n_in));
+  p.xs = static_cast<unsigned char*>(ws);
+  p.inv = reinterpret_cast<float*>(p.xs + xs_bytes(rows, n_in));
   p.n_out = n_out, p.n_in = n_in, p.w_bytes = w_bytes, p.rows = rows, p.n_x = n_x, p.E = E, p.y_fp32 = y_fp32, p.act = act;
   p.n_kb = int((n_in + kChan - 1) / kChan), p.n_rb = int((n_out + kRows - 1) / kRows);
   p.flags = device_flags_ptr();
   const int sms = sm_count();
   if (!p.flags || sms <= 0) return CSA2_ERR_CUDA;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = cudaSuccess;
-  if (n_x > 0) e = launch_pdl(scale_kernel, dim3(unsigned((n_x + 3) / 4)), dim3(128), 0, st, p);
+  cudaError_t e = launch_pdl(scale_kernel, dim3(unsigned((rows + 3) / 4)), dim3(128), 0, st, p);
   if (e != cudaSuccess) return CSA2_ERR_CUDA;
   // token tiles, at most and about
   const int64_t most = std::min<int64_t>(rows, E) + rows / kTile, about = std::max<int64_t>(std::min<int64_t>(rows, E), rows / kTile);

@@ -570,7 +570,7 @@ csa2_status csa2_expert_route(const float* logits, int m, int E, int k, const fl
  *   offsets int32 [E + 1], not descending, within [0, rows] (values outside are cut off there); rows of y before
  *           offsets[0] and from offsets[E] on are left as they were;
  *   y       bf16 (y_fp32 = 0) or fp32 (1) [rows][n_out, or half of it].
- *   ws      csa2_workspace_size(CSA2_OP_FP4_GROUPED, {B = n_x, cap = n_in}) bytes; calls that may overlap need one each.
+ *   ws      csa2_workspace_size(CSA2_OP_FP4_GROUPED, {B = rows, cap = n_in}) bytes; calls that may overlap need one each.
  * Accumulated in fp32, rounded once.  y and ws overlap nothing else.  E = 1 is a product of any number of rows with one
  * weight.
  */
@@ -631,7 +631,7 @@ csa2_status csa2_token_logprobs(const void* logits, int logits_fp32, int rows, i
 #define CSA2_OP_FP4_GROUPED 8
 
 typedef struct csa2_dims {
-  int B, Nq;            /* CSA2_OP_EXPERT_ROUTE: tokens; CSA2_OP_FP4_GROUPED: rows of x, both in B */
+  int B, Nq;            /* CSA2_OP_EXPERT_ROUTE: tokens; CSA2_OP_FP4_GROUPED: rows of y, both in B */
   int64_t cap;          /* cache capacity per sequence; CSA2_OP_FP4_GROUPED: n_in */
   int64_t n;            /* CSA2_OP_TOPK: columns per row; CSA2_OP_MERGE_PAIRS: shards;
                            CSA2_OP_EXPERT_ROUTE: experts */

@@ -212,7 +212,7 @@ def test_captured_and_on_another_stream():
                                                               ((m * k,), torch.int32), ((m, k), torch.int32))]
     y = torch.zeros((m * k, n_out // 2), dtype=torch.bfloat16, device="cuda")
     out = torch.zeros((m, n_out // 2), device="cuda")
-    ws = torch.empty(c.grouped_workspace_size(m, n_in), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(c.grouped_workspace_size(m * k, n_in), dtype=torch.uint8, device="cuda")
     rws = torch.empty(max(1, c.route_workspace_size(m, E)), dtype=torch.uint8, device="cuda")
 
     def step():
