@@ -1,10 +1,11 @@
 // Low-rank adapters of many requests: out[i] = base[i] + scale[l] B_l (A_l x_i), l the adapter of row i.
 //
-// A cluster of CTAs takes a tile of consecutive rows and one of the adapters that its rows use (a slot; the CTAs of a
-// slot without one leave).  Its CTAs share the input channels of A_l x, add their parts up through distributed shared
-// memory in order of rank, and share the output channels of B_l t: one launch, no workspace, no atomics.  Rows of other
-// adapters are multiplied along in the tile (rows of an MMA do not mix) and not written.  The sums are in one order
-// whatever else is in the batch, but not whatever the tile's height: that goes by m.
+// Rows in any order.  Every CTA looks through the adapters of a window of rows, counts the rows of each bucket (an
+// adapter's number modulo 256) and cuts the buckets into tiles of 16 or 64 rows, the same ones in every CTA.  A cluster
+// takes tiles in turn: it collects a tile's rows, and for each adapter among them (one, unless adapters share a bucket)
+// its CTAs share the input channels of A_l x, add their parts up through distributed shared memory in order of rank, and
+// share the output channels of B_l t.  One launch, no workspace, no atomics on sums: an adapter's weights are read once per
+// tile, and a row's result does not depend on the rows beside it (rows of an MMA do not mix).
 //
 // mma.m16n8k16 on bf16 as it lies in memory.  Channels are handed to the MMA in an order that lets a lane load 16
 // neighbouring bytes: the same for both operands, so that the sum over the channels does not change.  t = A x is fp32
@@ -23,6 +24,9 @@ namespace csa2 {
 namespace lora {
 
 constexpr int kThreads = 256, kWarps = 8, kMaxCluster = 8;
+constexpr int kWindow = 4096, kBuckets = 256;
+constexpr int kStages = 3, kStep = 64, kStepPitch = kStep + 32;  // channels of x and A under way (64 rows); rows apart by 192 bytes, so that 16-byte reads of eight rows miss each other
+static_assert(kBuckets == kThreads, "a thread per bucket");
 
 struct Params {
   const uint16_t *x, *a, *b;
@@ -30,7 +34,7 @@ struct Params {
   const float* scale;
   const void* base;
   void* out;
-  int m, n_in, n_out, r, L, slots;
+  int m, n_in, n_out, r, L;
   unsigned int* flags;
 };
 
@@ -43,113 +47,206 @@ __device__ __forceinline__ uint32_t bf2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// NR: groups of eight ranks, an even number; WM: warps along the rows, of MT tiles of 16 each.
+template <int NR, int WM>
+struct Shape {
+  static constexpr int WK = kWarps / WM, TM = 16 * WM, R = 8 * NR, kPitch = R + 8;
+  static constexpr bool kStaged = WM > 1;
+  static constexpr size_t kPart = size_t(WK) * TM * R * 4;
+  static constexpr size_t kStage = size_t(TM + R) * kStepPitch * 2;
+  static constexpr size_t kFirst = kStaged && kStages * kStage > kPart ? kStages * kStage : kPart;
+  static constexpr size_t kSmem = kFirst + size_t(2) * TM * kPitch * 2;
+};
+
+// NR: groups of eight ranks, an even number; WM: warps along the rows, 16 each.
 // kF32: base and out are fp32; kVec: rows of out are whole 16-byte pieces.
-template <int NR, int WM, int MT, bool kF32, bool kVec>
-__global__ void __launch_bounds__(kThreads) lora_kernel(const Params p, int C) {
-  constexpr int WK = kWarps / WM, TM = 16 * WM * MT, R = 8 * NR, kPitch = R + 8;
+template <int NR, int WM, bool kF32, bool kVec>
+__global__ void __launch_bounds__(kThreads, NR <= 8 ? 2 : 1) lora_kernel(const Params p, int C) {
+  using S = Shape<NR, WM>;
+  constexpr int WK = S::WK, TM = S::TM, R = S::R, kPitch = S::kPitch;
   extern __shared__ __align__(16) unsigned char smem[];
-  float* part = reinterpret_cast<float*>(smem);                     // [WK][TM][R]; then, from 0, this CTA's sums [TM][R]
-  uint16_t* hi = reinterpret_cast<uint16_t*>(part + WK * TM * R);   // [TM][kPitch], channels in the MMA's order
+  float* part = reinterpret_cast<float*>(smem);                       // [WK][TM][R]; then, from 0, this CTA's sums [TM][R]
+  uint16_t* hi = reinterpret_cast<uint16_t*>(smem + S::kFirst);       // [TM][kPitch], channels in the MMA's order
   uint16_t* lo = hi + TM * kPitch;
-  __shared__ int which[TM], list[TM];
+  __shared__ uint16_t bucket[kWindow];  // of the window's rows; 0xFFFF: no adapter
+  __shared__ int count[kBuckets], start[kBuckets + 1], seg[kWarps];
+  __shared__ int rows[TM], which[TM], list[TM];
   __shared__ int n_list;
+  __shared__ uint32_t tmp[32];
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, t = lane & 3, g = lane >> 2;
   const int rank = C > 1 ? int(blockIdx.x % unsigned(C)) : 0;
-  const int unit = int(blockIdx.x / unsigned(C)), slot = unit % p.slots, row0 = unit / p.slots * TM;
+  const int cluster = int(blockIdx.x / unsigned(C)), n_clusters = int(gridDim.x / unsigned(C));
   const int wm = warp % WM, wk = warp / WM;
+  const int n_blk = (p.n_out + 31) / 32;  // blocks of 32 output channels, taken in turn by the cluster's warps
+  const int blk0 = rank * kWarps + warp, blk_step = C * kWarps;
 
-  // the adapters of the tile's rows, in the order of their first rows
-  if (tid < TM) {
-    int l = row0 + tid < p.m ? p.adapter[row0 + tid] : -1;
-    if (l >= p.L) {
-      l = -1;
-      if (rank == 0 && slot == 0) atomicOr(p.flags, CSA2_FLAG_INDEX_OOB);
-    }
-    which[tid] = l < 0 ? -1 : l;
+  for (int w0 = 0; w0 < p.m; w0 += kWindow) {
+  const int n_w = min(kWindow, p.m - w0);
+  // the window's buckets and tiles
+  count[tid] = 0;
+  __syncthreads();
+#pragma unroll 4
+  for (int i = tid; i < n_w; i += kThreads) {
+    const int l = p.adapter[w0 + i];
+    const bool on = l >= 0 && l < p.L;
+    if (l >= p.L && cluster == 0 && rank == 0) atomicOr(p.flags, CSA2_FLAG_INDEX_OOB);
+    bucket[i] = on ? uint16_t(l % kBuckets) : uint16_t(0xFFFF);
+    if (on) atomicAdd(&count[l % kBuckets], 1);
   }
   __syncthreads();
-  if (warp == 0) {
+  uint32_t n_units;
+  const uint32_t at_unit = block_exclusive_scan(uint32_t((count[tid] + TM - 1) / TM), tmp, &n_units);
+  start[tid] = int(at_unit);
+  if (tid == 0) start[kBuckets] = int(n_units);
+  __syncthreads();
+
+  if (p.base != p.out) {  // rows without an adapter: a warp per row, of the CTA's share of the channels
+    constexpr int kSize = kF32 ? 4 : 2, kPiece = kVec ? 16 : kSize;
+    const int n_piece = p.n_out * kSize / kPiece;
+    const int p0 = int(int64_t(n_piece) * rank / C), p1 = int(int64_t(n_piece) * (rank + 1) / C);
+    for (int i = cluster + n_clusters * warp; i < n_w; i += n_clusters * kWarps) {
+      if (bucket[i] != 0xFFFF) continue;
+      const char* src = static_cast<const char*>(p.base) + int64_t(w0 + i) * p.n_out * kSize;
+      char* dst = static_cast<char*>(p.out) + int64_t(w0 + i) * p.n_out * kSize;
+#pragma unroll 4
+      for (int n = p0 + lane; n < p1; n += 32) {
+        if (kVec) reinterpret_cast<uint4*>(dst)[n] = reinterpret_cast<const uint4*>(src)[n];
+        else if (kF32) reinterpret_cast<float*>(dst)[n] = reinterpret_cast<const float*>(src)[n];
+        else reinterpret_cast<uint16_t*>(dst)[n] = reinterpret_cast<const uint16_t*>(src)[n];
+      }
+    }
+  }
+
+  for (int unit = cluster; unit < int(n_units); unit += n_clusters) {
+  // the rows of the tile, in order: the bucket's from `from` on
+  int from, n_rows;
+  {
+    int b = 0, end = kBuckets;  // start[b] <= unit < start[end]
+    while (end - b > 1) {
+      const int mid = (b + end) >> 1;
+      if (start[mid] <= unit) b = mid;
+      else end = mid;
+    }
+    from = (unit - start[b]) * TM, n_rows = min(TM, count[b] - from);
+    const int share = (n_w + kThreads - 1) / kThreads * 32, s0 = warp * share, s1 = min(n_w, s0 + share);
     int n = 0;
-    for (int i0 = 0; i0 < TM; i0 += 32) {
-      const int i = i0 + lane;
-      bool first = i < TM && which[i] >= 0;
-      for (int j = 0; first && j < i; ++j) first = which[j] != which[i];
-      const unsigned got = __ballot_sync(0xffffffffu, first);
-      if (first) list[n + __popc(got & ((1u << lane) - 1u))] = which[i];
-      n += __popc(got);
+    for (int i = s0; i < s1; i += 32)
+      n += __popc(__ballot_sync(0xffffffffu, i + lane < s1 && bucket[i + lane] == b));
+    if (lane == 0) seg[warp] = n;
+    __syncthreads();
+    int at = -from;
+    for (int w = 0; w < warp; ++w) at += seg[w];
+    for (int i = s0; i < s1 && at < TM; i += 32) {
+      const bool on = i + lane < s1 && bucket[i + lane] == b;
+      const unsigned got = __ballot_sync(0xffffffffu, on);
+      const int mine = at + __popc(got & ((1u << lane) - 1u));
+      if (on && mine >= 0 && mine < TM) rows[mine] = w0 + i + lane, which[mine] = p.adapter[w0 + i + lane];
+      at += __popc(got);
+    }
+    __syncthreads();
+    for (int i = n_rows + tid; i < TM; i += kThreads) rows[i] = rows[0], which[i] = -1;  // (read, not written)
+    __syncthreads();
+  }
+  // its adapters, in the order of their first rows
+  if (warp == 0) {
+    bool same = true;
+    for (int i = lane; i < n_rows; i += 32) same = same && which[i] == which[0];
+    int n = 0;
+    if (__all_sync(0xffffffffu, same)) {
+      if (lane == 0) list[0] = which[0];
+      n = 1;
+    } else {
+      for (int i0 = 0; i0 < n_rows; i0 += 32) {
+        const int i = i0 + lane;
+        bool first = i < n_rows;
+        for (int j = 0; first && j < i; ++j) first = which[j] != which[i];
+        const unsigned got = __ballot_sync(0xffffffffu, first);
+        if (first) list[n + __popc(got & ((1u << lane) - 1u))] = which[i];
+        n += __popc(got);
+      }
     }
     if (lane == 0) n_list = n;
   }
   __syncthreads();
   const int n_adapters = n_list;
 
-  const int n_blk = (p.n_out + 31) / 32;           // blocks of 32 output channels, taken in turn by the cluster's warps
-  const int blk0 = rank * kWarps + warp, blk_step = C * kWarps;
-
-  if (slot == 0 && p.base != p.out) {  // rows without an adapter
-    for (int i = 0; i < TM && row0 + i < p.m; ++i) {
-      if (which[i] >= 0) continue;
-      const int64_t at = int64_t(row0 + i) * p.n_out;
-      for (int n = (rank * kThreads + tid); n < p.n_out; n += C * kThreads) {
-        if (kF32) static_cast<float*>(p.out)[at + n] = static_cast<const float*>(p.base)[at + n];
-        else static_cast<uint16_t*>(p.out)[at + n] = static_cast<const uint16_t*>(p.base)[at + n];
-      }
-    }
-  }
-
-  const int n_chunk = (p.n_in + 31) / 32;
-  const int c0 = int(int64_t(n_chunk) * rank / C), c1 = int(int64_t(n_chunk) * (rank + 1) / C);
-  for (int s = slot; s < n_adapters; s += p.slots) {
+  for (int s = 0; s < n_adapters; ++s) {
     const int l = list[s];
     const int n_rank = p.ranks ? min(max(p.ranks[l], 0), p.r) : p.r;
+    const uint16_t* a = p.a + int64_t(l) * p.r * p.n_in;
     // t = A x over this CTA's channels
-    {
-      float acc[MT][NR][4];
+    float acc[NR][4];
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
+    for (int j = 0; j < NR; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+    auto multiply = [&](const uint4 (&xv)[2], const uint4 (&av)[NR]) {
 #pragma unroll
-        for (int j = 0; j < NR; ++j) acc[i][j][0] = acc[i][j][1] = acc[i][j][2] = acc[i][j][3] = 0.f;
-      const uint16_t* a = p.a + int64_t(l) * p.r * p.n_in;
+      for (int j = 0; j < NR; ++j) {
+        mma(acc[j], xv[0].x, xv[1].x, xv[0].y, xv[1].y, av[j].x, av[j].y);
+        mma(acc[j], xv[0].z, xv[1].z, xv[0].w, xv[1].w, av[j].z, av[j].w);
+      }
+    };
+    if constexpr (S::kStaged) {
+      // 64 channels of the tile's rows and of A at a time, by asynchronous copies into a ring
+      const int n_step = (p.n_in + kStep - 1) / kStep;
+      const int s0 = int(int64_t(n_step) * rank / C), n = int(int64_t(n_step) * (rank + 1) / C) - s0;
+      auto ask = [&](int i) {
+        if (i < n) {
+          const uint32_t dst = smem_u32(smem) + uint32_t(i % kStages) * uint32_t(S::kStage);
+          const int ch = (s0 + i) * kStep + 8 * (tid & 7);
+          const bool in = ch < p.n_in;
+#pragma unroll
+          for (int row = tid >> 3; row < TM; row += kThreads / 8)
+            cp_async16(dst + uint32_t(row * kStepPitch * 2 + (tid & 7) * 16), in ? p.x + int64_t(rows[row]) * p.n_in + ch : p.x, in ? 16 : 0);
+#pragma unroll
+          for (int row = tid >> 3; row < R; row += kThreads / 8) {
+            const bool on = in && row < n_rank;
+            cp_async16(dst + uint32_t((TM + row) * kStepPitch * 2 + (tid & 7) * 16), on ? a + int64_t(row) * p.n_in + ch : p.x, on ? 16 : 0);
+          }
+        }
+        cp_async_commit();
+      };
+      for (int i = 0; i < kStages - 1; ++i) ask(i);
+      for (int i = 0; i < n; ++i) {
+        cp_async_wait<kStages - 2>();
+        __syncthreads();  // this step is there for all, and the one before is done with
+        ask(i + kStages - 1);
+        const unsigned char* at = smem + (i % kStages) * S::kStage + (wk * 32 + 8 * t) * 2;
+        uint4 xv[2], av[NR];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) xv[h] = *reinterpret_cast<const uint4*>(at + (wm * 16 + 8 * h + g) * kStepPitch * 2);
+#pragma unroll
+        for (int j = 0; j < NR; ++j) av[j] = *reinterpret_cast<const uint4*>(at + (TM + 8 * j + g) * kStepPitch * 2);
+        multiply(xv, av);
+      }
+      cp_async_wait<0>();
+      __syncthreads();
+    } else {
+      const int n_chunk = (p.n_in + 31) / 32;
+      const int c0 = int(int64_t(n_chunk) * rank / C), c1 = int(int64_t(n_chunk) * (rank + 1) / C);
+      const uint16_t* x0 = p.x + int64_t(rows[g]) * p.n_in;
+      const uint16_t* x1 = p.x + int64_t(rows[g + 8]) * p.n_in;
 #pragma unroll 2
       for (int c = c0 + wk; c < c1; c += WK) {
         const int ch = c * 32 + 8 * t;
-        uint4 xv[MT][2], av[NR];
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int row = row0 + (wm * MT + i) * 16 + 8 * h + g;
-            xv[i][h] = row < p.m && ch < p.n_in ? __ldg(reinterpret_cast<const uint4*>(p.x + int64_t(row) * p.n_in + ch))
-                                                : make_uint4(0, 0, 0, 0);
-          }
+        const bool in = ch < p.n_in;
+        uint4 xv[2], av[NR];
+        xv[0] = in ? __ldg(reinterpret_cast<const uint4*>(x0 + ch)) : make_uint4(0, 0, 0, 0);
+        xv[1] = in && n_rows > 8 ? __ldg(reinterpret_cast<const uint4*>(x1 + ch)) : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int j = 0; j < NR; ++j) {
           const int rr = 8 * j + g;
-          av[j] = rr < n_rank && ch < p.n_in ? __ldg(reinterpret_cast<const uint4*>(a + int64_t(rr) * p.n_in + ch))
-                                             : make_uint4(0, 0, 0, 0);
+          av[j] = rr < n_rank && in ? __ldg(reinterpret_cast<const uint4*>(a + int64_t(rr) * p.n_in + ch)) : make_uint4(0, 0, 0, 0);
         }
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-          for (int j = 0; j < NR; ++j) {
-            mma(acc[i][j], xv[i][0].x, xv[i][1].x, xv[i][0].y, xv[i][1].y, av[j].x, av[j].y);
-            mma(acc[i][j], xv[i][0].z, xv[i][1].z, xv[i][0].w, xv[i][1].w, av[j].z, av[j].w);
-          }
+        multiply(xv, av);
       }
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NR; ++j)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int row = (wm * MT + i) * 16 + 8 * h + g;
-            *reinterpret_cast<float2*>(part + (wk * TM + row) * R + 8 * j + 2 * t) =
-                make_float2(acc[i][j][2 * h], acc[i][j][2 * h + 1]);
-          }
     }
+#pragma unroll
+    for (int j = 0; j < NR; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        *reinterpret_cast<float2*>(part + (wk * TM + wm * 16 + 8 * h + g) * R + 8 * j + 2 * t) =
+            make_float2(acc[j][2 * h], acc[j][2 * h + 1]);
     __syncthreads();
     for (int e = tid; e < TM * R / 4; e += kThreads) {
       float4 v = reinterpret_cast<float4*>(part)[e];
@@ -160,6 +257,51 @@ __global__ void __launch_bounds__(kThreads) lora_kernel(const Params p, int C) {
       }
       reinterpret_cast<float4*>(part)[e] = v;
     }
+    // out = base + B t over this warp's output channels, a block of 32 at a time: a lane gets eight neighbouring ones,
+    // 8t .. 8t + 7.  With few rows the next block is asked for before one is finished, the first before t is known
+    constexpr bool kAhead = TM == 16 && NR <= 8;
+    constexpr int kPieces = kF32 ? 2 : 1;
+    struct Block {
+      uint32_t b[4][R / 16][2];
+      uint4 base[TM / 16][2][kPieces];
+    };
+    Block next;
+    const uint16_t* b = p.b + int64_t(l) * p.n_out * p.r;
+    auto load = [&](int blk) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int n = blk * 32 + 8 * (g >> 1) + 2 * j + (g & 1);
+        const uint16_t* row = b + int64_t(n) * p.r;
+        if (R >= 32) {
+#pragma unroll
+          for (int k = 0; k < R / 32; ++k) {
+            const int rr = 32 * k + 8 * t;
+            const uint4 v = n < p.n_out && rr < n_rank ? __ldg(reinterpret_cast<const uint4*>(row + rr)) : make_uint4(0, 0, 0, 0);
+            next.b[j][2 * k][0] = v.x, next.b[j][2 * k][1] = v.y;
+            next.b[j][R >= 32 ? 2 * k + 1 : 0][0] = v.z, next.b[j][R >= 32 ? 2 * k + 1 : 0][1] = v.w;
+          }
+        } else {
+          const int rr = 4 * t;
+          const uint2 v = n < p.n_out && rr < n_rank ? __ldg(reinterpret_cast<const uint2*>(row + rr)) : make_uint2(0, 0);
+          next.b[j][0][0] = v.x, next.b[j][0][1] = v.y;
+        }
+      }
+      if (kVec) {
+        const int n0 = blk * 32 + 8 * t;
+#pragma unroll
+        for (int i = 0; i < TM / 16; ++i)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int row = 16 * i + 8 * h + g;
+            if (which[row] != l || n0 >= p.n_out) continue;  // (left as it was, and not used)
+#pragma unroll
+            for (int e = 0; e < kPieces; ++e)
+              next.base[i][h][e] = reinterpret_cast<const uint4*>(static_cast<const char*>(p.base) +
+                                                                  (int64_t(rows[row]) * p.n_out + n0) * (kF32 ? 4 : 2))[e];
+          }
+      }
+    };
+    if (kAhead && blk0 < n_blk) load(blk0);
     if (C > 1) cluster_arrive(), cluster_wait();
     else __syncthreads();
     // the cluster's sums, scaled, as two bf16 terms
@@ -200,28 +342,14 @@ __global__ void __launch_bounds__(kThreads) lora_kernel(const Params p, int C) {
     }
     __syncthreads();
     if (C > 1) cluster_arrive();
-    // out = base + B t over this warp's output channels: a lane gets eight neighbouring ones, 8t .. 8t + 7
-    const uint16_t* b = p.b + int64_t(l) * p.n_out * p.r;
     for (int blk = blk0; blk < n_blk; blk += blk_step) {
-      uint32_t bv[4][R / 16][2];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int n = blk * 32 + 8 * (g >> 1) + 2 * j + (g & 1);
-        const uint16_t* row = b + int64_t(n) * p.r;
-        if (R >= 32) {
-#pragma unroll
-          for (int k = 0; k < R / 32; ++k) {
-            const int rr = 32 * k + 8 * t;
-            const uint4 v = n < p.n_out && rr < n_rank ? __ldg(reinterpret_cast<const uint4*>(row + rr)) : make_uint4(0, 0, 0, 0);
-            bv[j][2 * k][0] = v.x, bv[j][2 * k][1] = v.y;
-            bv[j][R >= 32 ? 2 * k + 1 : 0][0] = v.z, bv[j][R >= 32 ? 2 * k + 1 : 0][1] = v.w;
-          }
-        } else {
-          const int rr = 4 * t;
-          const uint2 v = n < p.n_out && rr < n_rank ? __ldg(reinterpret_cast<const uint2*>(row + rr)) : make_uint2(0, 0);
-          bv[j][0][0] = v.x, bv[j][0][1] = v.y;
-        }
+      if (!kAhead || blk != blk0) load(blk);
+      Block now;
+      if (kAhead) {
+        now = next;
+        if (blk + blk_step < n_blk) load(blk + blk_step);
       }
+      Block& at = kAhead ? now : next;
       if (n_rank < R) {  // what lies past the adapter's rank is not used
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -230,8 +358,8 @@ __global__ void __launch_bounds__(kThreads) lora_kernel(const Params p, int C) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const int rr = R >= 32 ? 32 * (k >> 1) + 8 * t + 4 * (k & 1) + 2 * h : 4 * t + 2 * h;
-              if (rr >= n_rank) bv[j][k][h] = 0;
-              else if (rr + 1 >= n_rank) bv[j][k][h] &= 0xFFFFu;
+              if (rr >= n_rank) at.b[j][k][h] = 0;
+              else if (rr + 1 >= n_rank) at.b[j][k][h] &= 0xFFFFu;
             }
       }
       const int n0 = blk * 32 + 8 * t;
@@ -250,29 +378,28 @@ __global__ void __launch_bounds__(kThreads) lora_kernel(const Params p, int C) {
             uint32_t f[4];
             ldmatrix_x4(f[0], f[1], f[2], f[3], smem_u32(src));
 #pragma unroll
-            for (int j = 0; j < 4; ++j) mma(d[j], f[0], f[1], f[2], f[3], bv[j][k][0], bv[j][k][1]);
+            for (int j = 0; j < 4; ++j) mma(d[j], f[0], f[1], f[2], f[3], at.b[j][k][0], at.b[j][k][1]);
           }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if (!(h ? use1 : use0)) continue;
-          const int64_t at = int64_t(row0 + 16 * i + 8 * h + g) * p.n_out + n0;
+          const int64_t o = int64_t(rows[16 * i + 8 * h + g]) * p.n_out + n0;
           if (kVec) {
             if (n0 >= p.n_out) continue;
             if (kF32) {
-              const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(p.base) + at);
-              float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at);
+              float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + o);
 #pragma unroll
-              for (int q = 0; q < 2; ++q) {
-                float4 v = src[q];
-                v.x += d[2 * q][2 * h], v.y += d[2 * q][2 * h + 1], v.z += d[2 * q + 1][2 * h], v.w += d[2 * q + 1][2 * h + 1];
-                dst[q] = v;
+              for (int e = 0; e < 2; ++e) {
+                const uint4 v = at.base[i][h][e % kPieces];
+                dst[e] = make_float4(__uint_as_float(v.x) + d[2 * e][2 * h], __uint_as_float(v.y) + d[2 * e][2 * h + 1],
+                                     __uint_as_float(v.z) + d[2 * e + 1][2 * h], __uint_as_float(v.w) + d[2 * e + 1][2 * h + 1]);
               }
             } else {
-              const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.base) + at);
+              const uint4 v = at.base[i][h][0];
               uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
               for (int j = 0; j < 4; ++j) w[j] = bf2(bf16lo(w[j]) + d[j][2 * h], bf16hi(w[j]) + d[j][2 * h + 1]);
-              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + o) = make_uint4(w[0], w[1], w[2], w[3]);
             }
           } else {
 #pragma unroll
@@ -280,10 +407,10 @@ __global__ void __launch_bounds__(kThreads) lora_kernel(const Params p, int C) {
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 if (n0 + 2 * j + e >= p.n_out) continue;
-                const int64_t o = at + 2 * j + e;
+                const int64_t c = o + 2 * j + e;
                 const float v = d[j][2 * h + e];
-                if (kF32) static_cast<float*>(p.out)[o] = static_cast<const float*>(p.base)[o] + v;
-                else static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(bf16f(static_cast<const uint16_t*>(p.base)[o]) + v);
+                if (kF32) static_cast<float*>(p.out)[c] = static_cast<const float*>(p.base)[c] + v;
+                else static_cast<__nv_bfloat16*>(p.out)[c] = __float2bfloat16_rn(bf16f(static_cast<const uint16_t*>(p.base)[c]) + v);
               }
           }
         }
@@ -292,19 +419,20 @@ __global__ void __launch_bounds__(kThreads) lora_kernel(const Params p, int C) {
     if (C > 1) cluster_wait();  // the others have read this CTA's sums
     __syncthreads();
   }
+  }
+  __syncthreads();  // the window's buckets are done with
+  }
 }
 
-template <int NR, int WM, int MT, bool kF32, bool kVec>
-cudaError_t launch(Params p, int C, cudaStream_t st) {
-  constexpr int TM = 16 * WM * MT, R = 8 * NR;
-  constexpr size_t smem = size_t(kWarps / WM) * TM * R * 4 + size_t(2) * TM * (R + 8) * 2;
-  auto kern = lora_kernel<NR, WM, MT, kF32, kVec>;
+template <int NR, int WM, bool kF32, bool kVec>
+cudaError_t launch(const Params& p, int C, int clusters, cudaStream_t st) {
+  auto kern = lora_kernel<NR, WM, kF32, kVec>;
+  constexpr size_t smem = Shape<NR, WM>::kSmem;
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem, done);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = (int64_t(p.m) + TM - 1) / TM;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(tiles * p.slots * C));
+  cfg.gridDim = dim3(unsigned(clusters * C));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -319,18 +447,18 @@ cudaError_t launch(Params p, int C, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, kern, p, C);
 }
 
-template <int NR, int WM, int MT>
-cudaError_t launch_out(const Params& p, int C, bool f32, cudaStream_t st) {
-  if (p.n_out % 8 == 0) return f32 ? launch<NR, WM, MT, true, true>(p, C, st) : launch<NR, WM, MT, false, true>(p, C, st);
-  return f32 ? launch<NR, WM, MT, true, false>(p, C, st) : launch<NR, WM, MT, false, false>(p, C, st);
+template <int NR, int WM>
+cudaError_t launch_out(const Params& p, int C, int clusters, bool f32, cudaStream_t st) {
+  if (p.n_out % 8 == 0) return f32 ? launch<NR, WM, true, true>(p, C, clusters, st) : launch<NR, WM, false, true>(p, C, clusters, st);
+  return f32 ? launch<NR, WM, true, false>(p, C, clusters, st) : launch<NR, WM, false, false>(p, C, clusters, st);
 }
 
-template <int WM, int MT>
-cudaError_t launch_rank(const Params& p, int C, bool f32, cudaStream_t st) {
-  if (p.r <= 16) return launch_out<2, WM, MT>(p, C, f32, st);
-  if (p.r <= 32) return launch_out<4, WM, MT>(p, C, f32, st);
-  if (p.r <= 64) return launch_out<8, WM, MT>(p, C, f32, st);
-  return launch_out<16, WM, MT>(p, C, f32, st);
+template <int WM>
+cudaError_t launch_rank(const Params& p, int C, int clusters, bool f32, cudaStream_t st) {
+  if (p.r <= 16) return launch_out<2, WM>(p, C, clusters, f32, st);
+  if (p.r <= 32) return launch_out<4, WM>(p, C, clusters, f32, st);
+  if (p.r <= 64) return launch_out<8, WM>(p, C, clusters, f32, st);
+  return launch_out<16, WM>(p, C, clusters, f32, st);
 }
 
 }  // namespace lora
@@ -359,11 +487,16 @@ extern "C" csa2_status csa2_lora_add(const uint16_t* x, int m, int n_in, const u
   p.m = m, p.n_in = n_in, p.n_out = n_out, p.r = r, p.L = L;
   p.flags = device_flags_ptr();
   if (!p.flags || sms <= 0) return CSA2_ERR_CUDA;
-  const bool tall = m >= 512;
-  const int TM = tall ? 64 : 16, C = 8;
-  const int64_t tiles = (int64_t(m) + TM - 1) / TM;
-  p.slots = int(std::min<int64_t>(std::max<int64_t>(4 * sms / (tiles * C), 1), std::min(TM, std::max(L, 1))));
+  // Tiles of 64 rows where the adapters have about that many each.  The CTAs that run at once go to the tiles that a
+  // window is likely to have, up to eight to each.
+  const int64_t window = std::min(m, kWindow), used = std::min<int64_t>(std::max(L, 1), std::min<int64_t>(window, kBuckets));
+  const bool tall = window >= 64 && window >= 32 * used;
+  const int64_t TM = tall ? 64 : 16, tiles = std::max<int64_t>((window + TM - 1) / TM, used);
+  const int64_t room = (r <= 64 ? 2 : 1) * int64_t(sms);
+  int C = 1;
+  while (C < kMaxCluster && tiles * C * 2 <= room) C *= 2;
+  const int clusters = int(std::min<int64_t>(room / C, used + window / TM));  // (no window has more tiles)
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = tall ? launch_rank<2, 2>(p, C, out_fp32, st) : launch_rank<1, 1>(p, C, out_fp32, st);
+  const cudaError_t e = tall ? launch_rank<4>(p, C, clusters, out_fp32, st) : launch_rank<1>(p, C, clusters, out_fp32, st);
   return e == cudaSuccess ? CSA2_OK : CSA2_ERR_CUDA;
 }

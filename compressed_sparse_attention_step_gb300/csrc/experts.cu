@@ -25,6 +25,12 @@ inline int block_tokens(int64_t m) {
   return t;
 }
 
+// The lists by one cluster of kCluster CTAs, as far as its masks fit: [words][E] of bits and of counts before them.
+constexpr int kCluster = 8, kAlone = 256;  // kAlone: tokens up to which the cluster chooses too
+constexpr size_t kMaskBytes = 192 * 1024;
+inline size_t mask_bytes(int64_t m, int64_t E, int C) { return size_t(E * (((m + C - 1) / C + 31) / 32) * 6 + 15) / 16 * 16; }
+inline bool in_cluster(int64_t m, int64_t E) { return mask_bytes(m, E, kCluster) <= kMaskBytes; }
+
 struct Params {
   const float *logits, *bias;
   const int32_t* active;
@@ -96,17 +102,95 @@ __device__ __forceinline__ void choose(const Params& p, int t, int lane) {
   }
 }
 
-// The block's masks from the experts chosen for its tokens.
-__device__ __forceinline__ void set_masks(const Params& p, uint32_t* mask, int t0, int t1, int words) {
+// The block's masks from the experts chosen for its tokens; words and experts lie `word` and `expert` apart.
+__device__ __forceinline__ void set_masks(const Params& p, uint32_t* mask, int t0, int t1, int word, int expert) {
+#pragma unroll 4
   for (int i = threadIdx.x; i < (t1 - t0) * p.k; i += kThreads) {
     const int t = i / p.k, e = p.experts[int64_t(t0) * p.k + i];
-    if (e >= 0) atomicOr(&mask[e * words + (t >> 5)], 1u << (t & 31));
+    if (e >= 0) atomicOr(&mask[e * expert + (t >> 5) * word], 1u << (t & 31));
   }
+}
+
+// The choice alone: a warp per token.
+template <int NE>
+__global__ void __launch_bounds__(kThreads) choose_kernel(const Params p) {
+  pdl_wait();
+  pdl_trigger();
+  const int t = int((blockIdx.x * unsigned(kThreads) + threadIdx.x) >> 5);
+  if (t < p.m) choose<NE>(p, t, int(threadIdx.x & 31));
+}
+
+// The lists by one cluster: a CTA takes p.tokens neighbouring tokens, and learns the others' counts through distributed
+// shared memory.  kChoose: chooses for them too.
+template <int NE, bool kChoose>
+__global__ void __launch_bounds__(kThreads) list_kernel(const Params p, int C) {
+  extern __shared__ uint32_t mask[];  // [words][E], then the bits before each word
+  __shared__ uint32_t count[kMaxE], base[kMaxE], tmp[32];
+  pdl_wait();
+  pdl_trigger();
+  const int rank = int(blockIdx.x), t0 = min(p.m, rank * p.tokens), t1 = min(p.m, t0 + p.tokens), words = (p.tokens + 31) / 32;
+  uint16_t* ahead = reinterpret_cast<uint16_t*>(mask + p.E * words);
+  for (int i = threadIdx.x; i < p.E * words; i += kThreads) mask[i] = 0u;
+  if (kChoose)
+    for (int t = t0 + int(threadIdx.x >> 5); t < t1; t += kWarps) choose<NE>(p, t, int(threadIdx.x & 31));
+  __syncthreads();
+  set_masks(p, mask, t0, t1, p.E, 1);
+  __syncthreads();
+  for (int e = threadIdx.x; e < p.E; e += kThreads) {
+    uint32_t n = 0;
+#pragma unroll 4
+    for (int w = 0; w < words; ++w) {
+      ahead[w * p.E + e] = uint16_t(n);
+      n += __popc(mask[w * p.E + e]);
+    }
+    count[e] = n;
+  }
+  if (C > 1) cluster_arrive(), cluster_wait();
+  __syncthreads();
+  uint32_t listed = 0;
+  for (int e0 = 0; e0 < p.E; e0 += kThreads) {
+    const int e = e0 + int(threadIdx.x);
+    uint32_t all = 0, before = 0;
+    if (e < p.E) {
+      uint32_t n[kCluster];
+#pragma unroll
+      for (int c = 0; c < kCluster; ++c)
+        n[c] = c >= C ? 0u : C > 1 ? ld_cluster_u32(cluster_addr(smem_u32(&count[e]), uint32_t(c))) : count[e];
+#pragma unroll
+      for (int c = 0; c < kCluster; ++c) {
+        all += n[c];
+        before += c < rank ? n[c] : 0u;
+      }
+    }
+    uint32_t total;
+    const uint32_t at = listed + block_exclusive_scan(all, tmp, &total);
+    if (e < p.E) {
+      base[e] = at + before;
+      if (rank == 0) p.offsets[e] = int(at);
+    }
+    listed += total;
+  }
+  if (rank == 0 && threadIdx.x == 0) p.offsets[p.E] = int(listed);
+  __syncthreads();
+  if (C > 1) cluster_arrive();  // the others' counts are read
+#pragma unroll 4
+  for (int i = threadIdx.x; i < (t1 - t0) * p.k; i += kThreads) {
+    const int t = i / p.k, e = p.experts[int64_t(t0) * p.k + i];
+    int at = -1;
+    if (e >= 0) {
+      const int w = (t >> 5) * p.E + e;
+      at = int(base[e] + ahead[w] + __popc(mask[w] & ((1u << (t & 31)) - 1u)));
+      p.src[at] = t0 + t;
+    }
+    p.pos[int64_t(t0) * p.k + i] = at;
+  }
+  for (int64_t i = int64_t(listed) + rank * kThreads + threadIdx.x; i < int64_t(p.m) * p.k; i += C * kThreads) p.src[i] = -1;
+  if (C > 1) cluster_wait();
 }
 
 // Chooses for a block of tokens, and counts its share of each expert's list.
 template <int NE>
-__global__ void __launch_bounds__(kThreads) choose_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads) count_kernel(const Params p) {
   extern __shared__ uint32_t mask[];
   pdl_wait();
   pdl_trigger();
@@ -114,7 +198,7 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const Params p) {
   for (int i = threadIdx.x; i < p.E * words; i += kThreads) mask[i] = 0u;
   for (int t = t0 + int(threadIdx.x >> 5); t < t1; t += kWarps) choose<NE>(p, t, int(threadIdx.x & 31));
   __syncthreads();
-  set_masks(p, mask, t0, t1, words);
+  set_masks(p, mask, t0, t1, 1, words);
   __syncthreads();
   for (int e = threadIdx.x; e < p.E; e += kThreads) {
     uint32_t n = 0;
@@ -124,8 +208,6 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const Params p) {
 }
 
 // Places of a block's tokens in the lists: the experts before, the blocks before, the block's tokens before.
-// kAlone: the only block, which chooses too.
-template <int NE, bool kAlone>
 __global__ void __launch_bounds__(kThreads) order_kernel(const Params p) {
   extern __shared__ uint32_t mask[];
   __shared__ uint32_t base[kMaxE], tmp[32];
@@ -133,25 +215,19 @@ __global__ void __launch_bounds__(kThreads) order_kernel(const Params p) {
   pdl_trigger();
   const int t0 = int(blockIdx.x) * p.tokens, t1 = min(p.m, t0 + p.tokens), words = p.tokens / 32;
   for (int i = threadIdx.x; i < p.E * words; i += kThreads) mask[i] = 0u;
-  if (kAlone)
-    for (int t = t0 + int(threadIdx.x >> 5); t < t1; t += kWarps) choose<NE>(p, t, int(threadIdx.x & 31));
   __syncthreads();
-  set_masks(p, mask, t0, t1, words);
+  set_masks(p, mask, t0, t1, 1, words);
   __syncthreads();
-  uint32_t listed = 0;  // entries of the experts of this round's blocks before
+  uint32_t listed = 0;
   for (int e0 = 0; e0 < p.E; e0 += kThreads) {
     const int e = e0 + int(threadIdx.x);
     uint32_t all = 0, before = 0;
     if (e < p.E) {
-      if (kAlone) {
-        for (int w = 0; w < words; ++w) all += __popc(mask[e * words + w]);
-      } else {
 #pragma unroll 16
-        for (int b = 0; b < int(gridDim.x); ++b) {
-          const uint32_t c = p.counts[int64_t(b) * p.E + e];
-          all += c;
-          before += b < int(blockIdx.x) ? c : 0u;
-        }
+      for (int b = 0; b < int(gridDim.x); ++b) {
+        const uint32_t c = p.counts[int64_t(b) * p.E + e];
+        all += c;
+        before += b < int(blockIdx.x) ? c : 0u;
       }
     }
     uint32_t total;
@@ -181,18 +257,47 @@ __global__ void __launch_bounds__(kThreads) order_kernel(const Params p) {
     p.src[i] = -1;
 }
 
+template <int NE, bool kChoose>
+cudaError_t lists(Params p, cudaStream_t st) {
+  const int C = p.m > 32 ? kCluster : p.m > 16 ? 2 : 1;
+  p.tokens = (p.m + C - 1) / C;
+  auto kern = list_kernel<NE, kChoose>;
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), kMaskBytes, done);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(C));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = mask_bytes(p.m, p.E, C);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = unsigned(C);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = C > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, p, C);
+}
+
 template <int NE>
-cudaError_t route(const Params& p, cudaStream_t st) {
-  const int blocks = std::max((p.m + p.tokens - 1) / p.tokens, 1);  // (no tokens: the offsets are still written)
-  const size_t smem = size_t(p.E) * (p.tokens / 32) * 4;
-  static std::atomic<uint64_t> done[3];
-  const size_t most = size_t(NE) * 32 * (block_tokens(kMaxM) / 32) * 4;
+cudaError_t route(Params p, cudaStream_t st) {
   cudaError_t e;
-  if (blocks == 1) return launch_pdl(order_kernel<NE, true>, dim3(1), dim3(kThreads), smem, st, p);
-  if ((e = allow_smem(reinterpret_cast<const void*>(choose_kernel<NE>), most, done[0])) != cudaSuccess) return e;
-  if ((e = allow_smem(reinterpret_cast<const void*>(order_kernel<NE, false>), most, done[1])) != cudaSuccess) return e;
-  if ((e = launch_pdl(choose_kernel<NE>, dim3(unsigned(blocks)), dim3(kThreads), smem, st, p)) != cudaSuccess) return e;
-  return launch_pdl(order_kernel<NE, false>, dim3(unsigned(blocks)), dim3(kThreads), smem, st, p);
+  if (p.m <= kAlone) return lists<NE, true>(p, st);
+  if (in_cluster(p.m, p.E)) {
+    if ((e = launch_pdl(choose_kernel<NE>, dim3(unsigned((p.m + kWarps - 1) / kWarps)), dim3(kThreads), 0, st, p)) != cudaSuccess)
+      return e;
+    return lists<1, false>(p, st);
+  }
+  p.tokens = block_tokens(p.m);
+  const int blocks = (p.m + p.tokens - 1) / p.tokens;
+  const size_t smem = size_t(p.E) * (p.tokens / 32) * 4, most = size_t(kMaxE) * (block_tokens(kMaxM) / 32) * 4;
+  static std::atomic<uint64_t> done[2];
+  if ((e = allow_smem(reinterpret_cast<const void*>(count_kernel<NE>), most, done[0])) != cudaSuccess) return e;
+  if ((e = allow_smem(reinterpret_cast<const void*>(order_kernel), most, done[1])) != cudaSuccess) return e;
+  if ((e = launch_pdl(count_kernel<NE>, dim3(unsigned(blocks)), dim3(kThreads), smem, st, p)) != cudaSuccess) return e;
+  return launch_pdl(order_kernel, dim3(unsigned(blocks)), dim3(kThreads), smem, st, p);
 }
 
 struct Combine {
@@ -206,36 +311,33 @@ struct Combine {
   unsigned int* flags;
 };
 
+// V neighbouring channels as loaded.
 template <int V, bool kF32>
-__device__ __forceinline__ void load_row(const void* at, int64_t i, float (&v)[V]) {
-  if (kF32) {
-    const float* q = static_cast<const float*>(at) + i;
-    if (V == 8) {
-      const float4 a = __ldg(reinterpret_cast<const float4*>(q)), b = __ldg(reinterpret_cast<const float4*>(q) + 1);
-      const float w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+struct Piece {
+  static constexpr int kWords = V * (kF32 ? 4 : 2) < 4 ? 1 : V * (kF32 ? 4 : 2) / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const void* at, int64_t i) {
+    const char* q = static_cast<const char*>(at) + i * (kF32 ? 4 : 2);
+    if (kWords % 4 == 0) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) v[j] = w[j];
-    } else if (V == 2) {
-      const float2 a = __ldg(reinterpret_cast<const float2*>(q));
-      v[0] = a.x, v[V - 1] = a.y;
+      for (int j = 0; j < kWords / 4; ++j) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(q) + j);
+        w[4 * j] = v.x, w[(4 * j + 1) % kWords] = v.y, w[(4 * j + 2) % kWords] = v.z, w[(4 * j + 3) % kWords] = v.w;
+      }
+    } else if (V * (kF32 ? 4 : 2) == 2) {
+      w[0] = __ldg(reinterpret_cast<const uint16_t*>(q));
+    } else if (kWords == 2) {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(q));
+      w[0] = v.x, w[kWords - 1] = v.y;
     } else {
-      v[0] = __ldg(q);
-    }
-  } else {
-    const uint16_t* q = static_cast<const uint16_t*>(at) + i;
-    if (V == 8) {
-      const uint4 a = __ldg(reinterpret_cast<const uint4*>(q));
-      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-      for (int j = 0; j < V / 2; ++j) v[2 * j] = bf16lo(w[j]), v[2 * j + 1] = bf16hi(w[j]);
-    } else if (V == 2) {
-      const uint32_t a = __ldg(reinterpret_cast<const uint32_t*>(q));
-      v[0] = bf16lo(a), v[V - 1] = bf16hi(a);
-    } else {
-      v[0] = bf16f(__ldg(q));
+      w[0] = __ldg(reinterpret_cast<const uint32_t*>(q));
     }
   }
-}
+  __device__ __forceinline__ float operator[](int i) const {
+    if (kF32) return __uint_as_float(w[i]);
+    return (i & 1) ? bf16hi(w[i >> 1]) : bf16lo(w[i >> 1]);
+  }
+};
 
 // A thread per V neighbouring channels of a token; products and sums in fp32, in the order of the token's experts.
 template <int V, bool kY32, bool kOut32>
@@ -245,16 +347,13 @@ __global__ void __launch_bounds__(256) combine_kernel(const Combine p) {
   const int64_t it = int64_t(blockIdx.x) * 256 + threadIdx.x, t = it / p.chunks;
   if (t >= p.m) return;
   const int64_t c = (it - t * p.chunks) * V;
+  Piece<V, false> base;
+  if (p.add) base.load(p.add, t * p.n + c);
   float s[V];
-  if (p.add) {
-    load_row<V, false>(p.add, t * p.n + c, s);
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) s[i] = 0.f;
-  }
-  constexpr int kAhead = 4;  // experts whose rows are asked for together
-  for (int j0 = 0; j0 < p.k; j0 += kAhead) {
-    float v[kAhead][V], w[kAhead];
+  constexpr int kAhead = 8;  // experts whose rows are asked for together
+  for (int j0 = 0; j0 == 0 || j0 < p.k; j0 += kAhead) {
+    Piece<V, kY32> v[kAhead];
+    float w[kAhead];
     bool on[kAhead];
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
@@ -263,8 +362,12 @@ __global__ void __launch_bounds__(256) combine_kernel(const Combine p) {
         const int64_t r = __ldg(p.pos + t * p.k + j0 + j);
         on[j] = r >= 0 && r < p.rows;
         if (r >= p.rows && c == 0) atomicOr(p.flags, CSA2_FLAG_INDEX_OOB);
-        if (on[j]) w[j] = __ldg(p.weights + t * p.k + j0 + j), load_row<V, kY32>(p.y, r * p.n + c, v[j]);
+        if (on[j]) w[j] = __ldg(p.weights + t * p.k + j0 + j), v[j].load(p.y, r * p.n + c);
       }
+    }
+    if (j0 == 0) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) s[i] = p.add ? base[i] : 0.f;
     }
 #pragma unroll
     for (int j = 0; j < kAhead; ++j)
@@ -276,21 +379,22 @@ __global__ void __launch_bounds__(256) combine_kernel(const Combine p) {
   if (kOut32) {
     float* o = static_cast<float*>(p.out) + t * p.n + c;
     if (V == 8) {
-      reinterpret_cast<float4*>(o)[0] = make_float4(s[0], s[V > 1], s[V > 2 ? 2 : 0], s[V > 3 ? 3 : 0]);
-      reinterpret_cast<float4*>(o)[1] = make_float4(s[V > 4 ? 4 : 0], s[V > 5 ? 5 : 0], s[V > 6 ? 6 : 0], s[V > 7 ? 7 : 0]);
+      reinterpret_cast<float4*>(o)[0] = make_float4(s[0], s[1 % V], s[2 % V], s[3 % V]);
+      reinterpret_cast<float4*>(o)[1] = make_float4(s[4 % V], s[5 % V], s[6 % V], s[7 % V]);
     } else {
 #pragma unroll
       for (int i = 0; i < V; ++i) o[i] = s[i];
     }
   } else {
     __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + t * p.n + c;
-    uint32_t h[(V + 1) / 2];
+    constexpr int H = (V + 1) / 2;
+    uint32_t h[H];
 #pragma unroll
-    for (int i = 0; i < V / 2; ++i) {
-      const __nv_bfloat162 b = __floats2bfloat162_rn(s[2 * i], s[2 * i + 1]);
+    for (int i = 0; i < H; ++i) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(s[2 * i], s[(2 * i + 1) % V]);
       h[i] = *reinterpret_cast<const uint32_t*>(&b);
     }
-    if (V == 8) *reinterpret_cast<uint4*>(o) = make_uint4(h[0], h[V > 2], h[V > 4 ? 2 : 0], h[V > 6 ? 3 : 0]);
+    if (V == 8) *reinterpret_cast<uint4*>(o) = make_uint4(h[0], h[1 % H], h[2 % H], h[3 % H]);
     else if (V == 2) *reinterpret_cast<uint32_t*>(o) = h[0];
     else o[0] = __float2bfloat16_rn(s[0]);
   }
@@ -311,10 +415,9 @@ cudaError_t combine(Combine p, bool y32, bool out32, cudaStream_t st) {
 }  // namespace moe
 
 size_t expert_route_ws_bytes(int64_t m, int64_t E) {
-  if (m <= 0 || E <= 0 || m > moe::kMaxM || E > moe::kMaxE) return 0;
+  if (m <= 0 || E <= 0 || m > moe::kMaxM || E > moe::kMaxE || moe::in_cluster(m, E)) return 0;
   const int t = moe::block_tokens(m);
-  const int64_t blocks = (m + t - 1) / t;
-  return blocks > 1 ? size_t(blocks * E) * 4 : 0;
+  return size_t((m + t - 1) / t * E) * 4;
 }
 
 }  // namespace csa2
@@ -340,7 +443,6 @@ extern "C" csa2_status csa2_expert_route(const float* logits, int m, int E, int 
   p.logits = logits, p.bias = bias, p.active = active, p.m = m, p.E = E, p.k = k, p.renorm = renorm, p.scale = scale;
   p.experts = experts, p.weights = weights, p.offsets = offsets, p.src = src, p.pos = pos;
   p.counts = static_cast<uint32_t*>(ws);
-  p.tokens = block_tokens(m);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const int ne = (E + 31) / 32;
   const cudaError_t e = ne <= 1 ? route<1>(p, st) : ne <= 2 ? route<2>(p, st) : ne <= 4 ? route<4>(p, st)

@@ -607,7 +607,7 @@ csa2_status csa2_lora_add(const uint16_t* x, int m, int n_in, const uint16_t* a,
  * Log probabilities under softmax(inv_temp * logits[r]) of each row: of given tokens (a drafted node's children, the
  * next token of a prompt), the log-sum-exp, the entropy in nats, and the n_top likeliest tokens.
  *   logits  bf16 (logits_fp32 = 0) or fp32 (1), row r at logits + r * ld, V <= ld of them; aligned to an element.
- *           -inf rules a token out.  Neither NaN nor +inf.  inv_temp > 0;
+ *           -inf rules a token out.  Neither NaN nor +inf.  inv_temp from 1e-20 to 1e8;
  *   tokens  int32 [rows][n_tok], n_tok <= CSA2_MAX_TREE: logprobs fp32 [rows][n_tok]; a token below 0 is padding and
  *           gets 0, one at or past V gets -inf and sets CSA2_FLAG_INDEX_OOB;
  *   lse, entropy fp32 [rows] (nullable): a row whose tokens are all ruled out has lse = -inf, log probabilities -inf and

@@ -38,7 +38,8 @@ def check_route(got, logits, k, bias=None, active=None, **kw):
 
 @pytest.mark.parametrize("m,E,k", [
     (0, 5, 2), (1, 1, 1), (1, 384, 6), (2, 33, 16), (63, 32, 8), (64, 384, 6), (65, 31, 3), (200, 8, 2), (300, 512, 4),
-    (513, 100, 7), (1000, 1024, 16), (2049, 64, 1), (17000, 16, 2), (40000, 3, 3),
+    (256, 384, 6), (257, 40, 3), (513, 100, 7), (1000, 1024, 16),
+    (2049, 64, 1), (9000, 1024, 2), (17000, 16, 2), (40000, 3, 3), (100000, 90, 1),
 ])
 def test_route(m, E, k):
     g = np.random.default_rng(m * 31 + E + k)

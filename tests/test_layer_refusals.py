@@ -28,10 +28,11 @@ def test_expert_route(L):
         assert call(**{name: None}) == 1, name
         assert call(**{name: _p(9, 2)}) == 1, name
     assert call(logits=_p(0, 4)) == 1 and call(bias=_p(9, 1)) == 1 and call(active=_p(9, 1)) == 1
-    need = csa2.route_workspace_size(1000, 8)
-    assert need > 0 and csa2.route_workspace_size(64, 8) == 0
-    assert call(m=1000) == 4 and call(m=1000, ws=_p(8), n=need - 1) == 4 and call(m=1000, ws=_p(8, 4), n=need) == 1
-    assert call(m=1000, ws=_p(0), n=need) == 1                      # over the logits
+    need = csa2.route_workspace_size(100000, 100)
+    assert need > 0 and csa2.route_workspace_size(64, 384) == 0
+    big = dict(m=100000, E=100)
+    assert call(**big) == 4 and call(**big, ws=_p(8), n=need - 1) == 4 and call(**big, ws=_p(8, 4), n=need) == 1
+    assert call(**big, ws=_p(0), n=need) == 1                       # over the logits
     assert call(experts=_p(0)) == 1 and call(weights=_p(1)) == 1 and call(pos=_p(4)) == 1
     assert call(src=_p(0, 4 * 8 * 4 - 4)) == 1 and call(offsets=_p(2, 4 * 2 * 4 - 4)) == 1
     assert call(active=_p(5)) == 1 and call(bias=_p(3, 8 * 4)) == 1
@@ -92,7 +93,7 @@ def test_token_logprobs(L):
              top=None):
         return L.csa2_token_logprobs(x, f32, rows, V, ld, tok, n_tok, t, lp, lse, ent, n_top, ids, top, None)
     for bad in (dict(rows=-1), dict(V=0), dict(V=csa2.MAX_VOCAB + 1, ld=1 << 30), dict(ld=99), dict(n_tok=-1), dict(n_tok=65), dict(t=0.0),
-                dict(t=-1.0), dict(t=float("nan")), dict(t=float("inf")), dict(n_top=-1), dict(n_top=csa2.MAX_TOP + 1, ids=_p(3)),
+                dict(t=-1.0), dict(t=1e-21), dict(t=1.1e8), dict(t=float("nan")), dict(t=float("inf")), dict(n_top=-1), dict(n_top=csa2.MAX_TOP + 1, ids=_p(3)),
                 dict(n_top=2)):
         assert call(**bad) == 1, bad
     for name in ("x", "tok", "lp"):
