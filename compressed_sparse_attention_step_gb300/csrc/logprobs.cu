@@ -75,6 +75,7 @@ __device__ __forceinline__ float warp_max(float v) {
 
 template <bool kBf16>
 struct Row {
+  static_assert(kLoads == 4, "a bit for each of a lane's values of a group");
   static constexpr int E = kBf16 ? 8 : 4;         // tokens of a 16-byte load
   static constexpr int kGroup = kLoads * 32 * E;  // tokens of a group
   const unsigned char* at;  // the row, back to a 16-byte boundary
@@ -91,6 +92,8 @@ struct Row {
   }
   // the first token of load j of group g for a lane
   __device__ __forceinline__ int first(int g, int j, int lane) const { return g * kGroup + (j * 32 + lane) * E - shift; }
+  // whether a group lies within the row
+  __device__ __forceinline__ bool inner(int g) const { return g * kGroup >= shift && (g + 1) * kGroup - shift <= V; }
   // the values at tokens i .. i + E - 1, -inf outside of the row
   __device__ __forceinline__ void load(int i, uint4& v) const {
     if (i >= 0 && i + E <= V) {
@@ -140,14 +143,15 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 template <bool kBf16>
 __device__ __forceinline__ float group_max(const uint4 (&v)[kLoads]) {
   if (kBf16) {
-    __nv_bfloat162 m = *reinterpret_cast<const __nv_bfloat162*>(&v[0].x);
+    __nv_bfloat162 m[kLoads];
 #pragma unroll
     for (int j = 0; j < kLoads; ++j) {
       const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) m = __hmax2(m, *reinterpret_cast<const __nv_bfloat162*>(&w[e]));
+      const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(w);
+      m[j] = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
     }
-    return fmaxf(__low2float(m), __high2float(m));
+    const __nv_bfloat162 all = __hmax2(__hmax2(m[0], m[1]), __hmax2(m[2], m[3]));
+    return fmaxf(__low2float(all), __high2float(all));
   }
   float m = -INFINITY;
 #pragma unroll
@@ -169,7 +173,7 @@ __device__ __forceinline__ void add_group(const uint4 (&v)[kLoads], float top, f
   if (near(ref)) {
     // one rounding per exponent; what lies below kFloor (-inf among it) weighs nothing
     const uint64_t cc = pair(c2, c2), mm = pair(-ref, -ref);
-    uint64_t s = pair(st.s, 0.f), t = pair(st.t, 0.f);
+    uint64_t s[2] = {pair(st.s, 0.f), pair(0.f, 0.f)}, t[2] = {pair(st.t, 0.f), pair(0.f, 0.f)};  // chains of half the length
 #pragma unroll
     for (int j = 0; j < kLoads; ++j) {
       const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
@@ -187,13 +191,13 @@ __device__ __forceinline__ void add_group(const uint4 (&v)[kLoads], float top, f
         float d0, d1;
         unpair(d, d0, d1);
         const uint64_t p = pair(attn::ex2(d0), attn::ex2(d1));
-        s = add2(s, p);
-        t = fma2(p, d, t);
+        s[e & 1] = add2(s[e & 1], p);
+        t[e & 1] = fma2(p, d, t[e & 1]);
       }
     }
     float a, b;
-    unpair(s, a, b), st.s = a + b;
-    unpair(t, a, b), st.t = a + b;
+    unpair(add2(s[0], s[1]), a, b), st.s = a + b;
+    unpair(add2(t[0], t[1]), a, b), st.t = a + b;
   } else {
 #pragma unroll
     for (int j = 0; j < kLoads; ++j)
@@ -206,232 +210,515 @@ __device__ __forceinline__ void add_group(const uint4 (&v)[kLoads], float top, f
   }
 }
 
-template <bool kBf16, int kThreads>
-__global__ void __launch_bounds__(kThreads, kThreads == 512 ? 2 : kThreads == 256 ? 4 : 8) logprobs_kernel(const Params p, int C) {
-  constexpr int kWarps = kThreads / 32;
+// What the pass over a row leaves: every warp's sums, and the largest values of kParts equal parts of its lanes.
+struct Board {
+  alignas(16) float pmax[kParts];
+  Stat part[16];
+};
+struct Scratch {
+  int sel[kTop], ci[kCand], n_cand, n_group;
+  float cv[kCand], bound;
+};
+
+__device__ __forceinline__ Stat shuffle_join(Stat st, int o, float c2) {
+  const Stat b = {__shfl_xor_sync(0xffffffffu, st.m, o), __shfl_xor_sync(0xffffffffu, st.s, o), __shfl_xor_sync(0xffffffffu, st.t, o)};
+  return join(st, b, c2);
+}
+// n <= 32 parts, in every lane of the warp
+__device__ __forceinline__ Stat join_parts(const Stat* part, int n, int lane, float c2) {
+  Stat st = lane < n ? part[lane] : Stat{-INFINITY, 0.f, 0.f};
+#pragma unroll 1
+  for (int o = 1; o < n; o *= 2) st = shuffle_join(st, o, c2);
+  return Stat{__shfl_sync(0xffffffffu, st.m, 0), __shfl_sync(0xffffffffu, st.s, 0), __shfl_sync(0xffffffffu, st.t, 0)};
+}
+
+// A row's sums as the outputs need them.
+struct Final {
+  float m, c2, ref, log_s, inv_temp;
+  Stat st;
+  __device__ __forceinline__ Final(const Stat& a, const Params& p, float c) {
+    st = a, m = a.m, c2 = c, inv_temp = p.inv_temp;
+    ref = __fmul_rn(a.m, c), log_s = logf(a.s);
+  }
+  __device__ __forceinline__ bool empty() const { return !(m > -INFINITY); }
+  __device__ __forceinline__ float logprob(float x) const {
+    if (x == -INFINITY || empty()) return -INFINITY;
+    const float d = fmaf(x, c2, -ref);  // (-inf where the product with log2 e alone passes the type's end)
+    return near(ref) && d > -INFINITY ? fmaf(d, attn::kLn2, -log_s) : (x - m) * inv_temp - log_s;
+  }
+  // lse, entropy and the given tokens' log probabilities, by `n` threads
+  template <bool kBf16>
+  __device__ __forceinline__ void write(const Params& p, const Row<kBf16>& row, int r, int tid, int n) const {
+    if (tid == 0) {
+      if (p.lse) p.lse[r] = empty() ? -INFINITY : near(ref) ? fmaf(ref, attn::kLn2, log_s) : fmaf(m, inv_temp, log_s);
+      if (p.entropy) p.entropy[r] = empty() ? 0.f : log_s - st.t / st.s * attn::kLn2;
+    }
+    for (int i = tid; i < p.n_tok; i += n) {
+      const int tok = p.tokens[int64_t(r) * p.n_tok + i];
+      float v = 0.f;
+      if (tok >= p.V) v = -INFINITY, atomicOr(p.flags, CSA2_FLAG_INDEX_OOB);
+      else if (tok >= 0) v = logprob(row.one(tok));
+      p.logprobs[int64_t(r) * p.n_tok + i] = v;
+    }
+    for (int i = min(p.n_top, p.V) + tid; i < p.n_top; i += n) top(p, r, i, -1, -INFINITY);  // fewer tokens than that
+  }
+  __device__ __forceinline__ void top(const Params& p, int r, int place, int id, float x) const {
+    if (p.top_ids) p.top_ids[int64_t(r) * p.n_top + place] = id;
+    if (p.top_logprobs) p.top_logprobs[int64_t(r) * p.n_top + place] = logprob(x);
+  }
+};
+
+// A lane's running sums over groups g0 + warp, + kWarps, ... of a row; the next group is asked for before one is added.
+// With top_n the groups' largest values go to gmax.
+template <bool kBf16, int kWarps>
+__device__ __forceinline__ Stat pass(const Row<kBf16>& row, int g0, int g1, int warp, int lane, float c2, bool top_n, float* gmax) {
+  Stat st = {-INFINITY, 0.f, 0.f};
+  uint4 v[kLoads], next[kLoads];
+  if (g0 + warp < g1) {
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) row.load(row.first(g0 + warp, j, lane), next[j]);
+  }
+  for (int g = g0 + warp; g < g1; g += kWarps) {
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) v[j] = next[j];
+    if (g + kWarps < g1) {
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) row.load(row.first(g + kWarps, j, lane), next[j]);
+    }
+    const float top = group_max<kBf16>(v);
+    if (top_n) {
+      const float m = warp_max(top);
+      if (lane == 0) gmax[g - g0] = m;
+    }
+    add_group<kBf16>(v, top, c2, st);
+  }
+  return st;
+}
+template <int kWarps>
+__device__ __forceinline__ void post(Board& board, Stat st, int warp, int lane, float c2) {
+  constexpr int kLanes = kWarps * 32 / kParts;  // of a part
+  float v = st.m;
+#pragma unroll
+  for (int o = 1; o < kLanes; o *= 2) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  if (lane % kLanes == 0) board.pmax[(warp * 32 + lane) / kLanes] = v;
+#pragma unroll 1
+  for (int o = 16; o; o >>= 1) st = shuffle_join(st, o, c2);
+  if (lane == 0) board.part[warp] = st;
+}
+
+// Whether a value may be among the n likeliest: it reaches the bound, and is not ruled out.  (Where fewer than n tokens
+// are left, the lowest of the ruled out ones follow them: enough of those are among the first n.)
+__device__ __forceinline__ bool may_win(float v, float bound, int i, int n, int V) {
+  return i >= 0 && i < V && v >= bound && (v > -INFINITY || i < n);
+}
+
+// The n likeliest of groups [g0, g1) of a row: sink(place, value, token), by kThreads threads that meet at barrier kBar.
+template <bool kBf16, int kThreads, int kBar, typename Sink>
+__device__ __forceinline__ void likeliest(const Row<kBf16>& row, int g0, int g1, const float* gmax, int* group, const Board& board,
+                                          Scratch& sc, int n, int tid, Sink sink) {
   using R = Row<kBf16>;
+  const int lane = tid & 31, warp = tid >> 5;
+  auto meet = [] { asm volatile("bar.sync %0, %1;\n" ::"n"(kBar), "n"(kThreads) : "memory"); };
+  // n values reach the n-th largest of the parts' largest ones: nothing below it is among the n, and no group whose
+  // largest value is below it is looked at
+  if (tid == 0) sc.n_cand = sc.n_group = 0;
+  if (tid < kParts) {
+    const float v = board.pmax[tid];
+    int place = 0;
+#pragma unroll 4
+    for (int j = 0; j < kParts; j += 4) {
+      const float4 u = *reinterpret_cast<const float4*>(board.pmax + j);
+      place += (u.x > v || (u.x == v && j < tid)) + (u.y > v || (u.y == v && j + 1 < tid)) +
+               (u.z > v || (u.z == v && j + 2 < tid)) + (u.w > v || (u.w == v && j + 3 < tid));
+    }
+    if (place == n - 1) sc.bound = v;
+  }
+  meet();
+  const float low = sc.bound;
+  for (int i = tid; i < g1 - g0; i += kThreads)
+    if (gmax[i] >= low) group[atomicAdd(&sc.n_group, 1)] = i;  // (in any order)
+  meet();
+  const int G = sc.n_group;
+  for (int i = tid; i < G; i += kThreads) {
+    const int at = group[i];
+    const float v = gmax[at];
+    int place = 0;
+#pragma unroll 4
+    for (int j = 0; j < G; ++j) {
+      const int o = group[j];
+      const float u = gmax[o];
+      place += u > v || (u == v && o < at);
+    }
+    if (place < n) sc.sel[place] = at;
+  }
+  meet();
+  for (int place = warp; place < min(n, G); place += kThreads / 32) {
+    const int g = g0 + sc.sel[place];
+    uint4 v[kLoads];
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) row.load(row.first(g, j, lane), v[j]);
+    uint32_t left = 0;  // this lane's values that may win and are not taken yet
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      const int i = row.first(g, j, lane);
+#pragma unroll
+      for (int e = 0; e < R::E; ++e)
+        if (may_win(R::value(v[j], e), low, i + e, n, row.V)) left |= 1u << (j * R::E + e);
+    }
+    const int most = n - place;
+    const int mine = __popc(left), all = int(__reduce_add_sync(0xffffffffu, unsigned(mine)));
+    if (all <= most) {  // (the candidates' order does not matter)
+      int at = 0;
+      if (mine) at = atomicAdd(&sc.n_cand, mine);
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j)
+#pragma unroll
+        for (int e = 0; e < R::E; ++e)
+          if (left >> (j * R::E + e) & 1u) sc.cv[at] = R::value(v[j], e), sc.ci[at] = row.first(g, j, lane) + e, ++at;
+    } else {  // ties: the best of the group, one after the other
+#pragma unroll 1
+      for (int k = 0; k < most; ++k) {
+        float best = -INFINITY;
+        int where = -1;
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j)
+#pragma unroll
+          for (int e = 0; e < R::E; ++e) {
+            const float x = R::value(v[j], e);
+            if ((left >> (j * R::E + e) & 1u) && (where < 0 || x > best)) best = x, where = j * R::E + e;
+          }
+        const float m = warp_max(best);
+        const int id = where >= 0 && best == m ? row.first(g, where / R::E, lane) + where % R::E : 0x7FFFFFFF;
+        const int first = int(__reduce_min_sync(0xffffffffu, unsigned(id)));
+        if (id == first) {  // (some lane has one: fewer are taken than there are)
+          const int at = atomicAdd(&sc.n_cand, 1);
+          sc.cv[at] = m, sc.ci[at] = id, left &= ~(1u << where);
+        }
+        __syncwarp();
+      }
+    }
+  }
+  meet();
+  const int total = sc.n_cand;
+  for (int i = tid; i < total; i += kThreads) {
+    const int id = sc.ci[i];
+    const float v = sc.cv[i];
+    int place = 0;
+#pragma unroll 4
+    for (int j = 0; j < total; ++j) {
+      const float u = sc.cv[j];
+      place += u > v || (u == v && sc.ci[j] < id);
+    }
+    if (place < n) sink(place, v, id);
+  }
+  meet();
+}
+
+// Few rows: a cluster of C CTAs per row.
+template <bool kBf16>
+__global__ void __launch_bounds__(512, 2) few_rows_kernel(const Params p, int C) {
+  constexpr int kThreads = 512, kWarps = kThreads / 32;
   extern __shared__ float gmax[];  // the groups' largest values; behind them the numbers of those that are looked at
-  int* group = reinterpret_cast<int*>(gmax + p.max_groups);
-  __shared__ Stat part[kWarps];
+  __shared__ Board board;
+  __shared__ Scratch sc;
   __shared__ Stat whole[kMaxCluster];
-  __shared__ int sel[kTop];
-  __shared__ float cv[kCand];
-  __shared__ int ci[kCand];
-  __shared__ int n_cand, n_group;
-  __shared__ __align__(16) float pmax[kParts];  // the largest values of parts of a warp's lanes
-  __shared__ float bound;
   __shared__ float lv[kMaxCluster * kTop];  // the CTAs' winners, at the cluster's first CTA
   __shared__ int li[kMaxCluster * kTop];
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = p.n_top;
-  if (n) {
-    for (int i = tid; i < kMaxCluster * kTop; i += kThreads) li[i] = -1;
-    if (tid < kTop) sel[tid] = -1;
-    if (tid == 0) n_cand = n_group = 0;
-  }
+  for (int i = tid; i < kMaxCluster * kTop; i += kThreads) li[i] = -1;
   if (C > 1) cluster_arrive();
   const int rank = C > 1 ? int(blockIdx.x % unsigned(C)) : 0;
   const int r = int(blockIdx.x / unsigned(C));
-  const R row(p, r);
+  const Row<kBf16> row(p, r);
   const int ng = row.groups(), g0 = ng * rank / C, g1 = ng * (rank + 1) / C;
   const float c2 = p.inv_temp * kLog2e;
-
-  Stat st = {-INFINITY, 0.f, 0.f};
-  {
-    uint4 v[kLoads], next[kLoads];
-    if (g0 + warp < g1) {
-#pragma unroll
-      for (int j = 0; j < kLoads; ++j) row.load(row.first(g0 + warp, j, lane), next[j]);
-    }
-    for (int g = g0 + warp; g < g1; g += kWarps) {
-#pragma unroll
-      for (int j = 0; j < kLoads; ++j) v[j] = next[j];
-      if (g + kWarps < g1) {
-#pragma unroll
-        for (int j = 0; j < kLoads; ++j) row.load(row.first(g + kWarps, j, lane), next[j]);
-      }
-      const float top = group_max<kBf16>(v);
-      if (n) {
-        const float m = warp_max(top);
-        if (lane == 0) gmax[g - g0] = m;
-      }
-      add_group<kBf16>(v, top, c2, st);
-    }
-  }
-  if (n) {
-    float v = st.m;
-#pragma unroll
-    for (int o = 1; o < kThreads / kParts; o *= 2) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    if (tid % (kThreads / kParts) == 0) pmax[tid / (kThreads / kParts)] = v;
-  }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    const Stat b = {__shfl_xor_sync(0xffffffffu, st.m, o), __shfl_xor_sync(0xffffffffu, st.s, o),
-                    __shfl_xor_sync(0xffffffffu, st.t, o)};
-    st = join(st, b, c2);
-  }
-  if (lane == 0) part[warp] = st;
+  post<kWarps>(board, pass<kBf16, kWarps>(row, g0, g1, warp, lane, c2, n > 0, gmax), warp, lane, c2);
   if (C > 1) cluster_wait();  // the cluster's CTAs have all started
   __syncthreads();
-  if (tid == 0) {
-    Stat a = part[0];
-    for (int w = 1; w < kWarps; ++w) a = join(a, part[w], c2);
-    const uint32_t to = C > 1 ? cluster_addr(smem_u32(&whole[rank]), 0) : smem_u32(&whole[0]);
-    st_cluster(to, a.m), st_cluster(to + 4, a.s), st_cluster(to + 8, a.t);
+  if (warp == 0) {
+    const Stat a = join_parts(board.part, kWarps, lane, c2);
+    if (lane == 0) {
+      const uint32_t to = C > 1 ? cluster_addr(smem_u32(&whole[rank]), 0) : smem_u32(&whole[0]);
+      st_cluster(to, a.m), st_cluster(to + 4, a.s), st_cluster(to + 8, a.t);
+    }
   }
-
   if (n) {
-    // n values reach the n-th largest of the parts' largest ones: nothing below it is among the n, and no group whose
-    // largest value is below it is looked at
-    if (tid < kParts) {
-      const float v = pmax[tid];
-      int place = 0;
-#pragma unroll
-      for (int j = 0; j < kParts; j += 4) {
-        const float4 u = *reinterpret_cast<const float4*>(pmax + j);
-        place += (u.x > v || (u.x == v && j < tid)) + (u.y > v || (u.y == v && j + 1 < tid)) +
-                 (u.z > v || (u.z == v && j + 2 < tid)) + (u.w > v || (u.w == v && j + 3 < tid));
-      }
-      if (place == n - 1) bound = v;
-    }
-    __syncthreads();
-    const float low = bound;
-    for (int i = tid; i < g1 - g0; i += kThreads)
-      if (gmax[i] >= low) group[atomicAdd(&n_group, 1)] = i;  // (in any order)
-    __syncthreads();
-    const int G = n_group;
-    for (int i = tid; i < G; i += kThreads) {
-      const int at = group[i];
-      const float v = gmax[at];
-      int place = 0;
+    const uint32_t to_v = C > 1 ? cluster_addr(smem_u32(&lv[rank * kTop]), 0) : smem_u32(&lv[0]);
+    const uint32_t to_i = C > 1 ? cluster_addr(smem_u32(&li[rank * kTop]), 0) : smem_u32(&li[0]);
+    likeliest<kBf16, kThreads, 1>(row, g0, g1, gmax, reinterpret_cast<int*>(gmax + p.max_groups), board, sc, n, tid,
+                                  [&](int place, float v, int id) {
+                                    st_cluster(to_v + 4u * place, v), st_cluster_u32(to_i + 4u * place, uint32_t(id));
+                                  });
+  }
+  if (C > 1) cluster_arrive(), cluster_wait();
+  else __syncthreads();
+  if (rank != 0) return;
+  const Final f(join_parts(whole, C, lane, c2), p, c2);
+  f.template write<kBf16>(p, row, r, tid, kThreads);
+  if (tid < C * kTop && li[tid] >= 0) {  // a winner of one CTA: its place among all
+    const int id = li[tid];
+    const float v = lv[tid];
+    int place = 0;
+    for (int c = 0; c < C; ++c)
 #pragma unroll 4
-      for (int j = 0; j < G; ++j) {
-        const int o = group[j];
-        const float u = gmax[o];
-        place += u > v || (u == v && o < at);
+      for (int j = 0; j < n; ++j) {
+        const int o = li[c * kTop + j];
+        const float u = lv[c * kTop + j];
+        place += o >= 0 && (u > v || (u == v && o < id));
       }
-      if (place < n) sel[place] = at;
-    }
-    __syncthreads();
-    for (int place = warp; place < min(n, G); place += kWarps) {
-      const int g = g0 + sel[place];
-      uint4 v[kLoads];
+    if (place < n) f.top(p, r, place, id, v);
+  }
+}
+
+// Many rows: persistent CTAs whose eight streaming warps go through row after row, while four others finish the row
+// before.  A streaming warp has its own ring of groups, which one more warp fills by bulk copies, ahead into the next
+// rows (a lane per ring; a streaming warp that copied for itself was held up by some 300 cycles a group); the groups at a
+// row's ends are loaded plainly.
+constexpr int kStream = 8, kFinish = 4, kSlots = 4, kGroupBytes = kLoads * 32 * 16;
+template <bool kBf16>
+__global__ void __launch_bounds__((kStream + kFinish + 1) * 32, 2) many_rows_kernel(const Params p) {
+  using R = Row<kBf16>;
+  extern __shared__ __align__(128) unsigned char ring[];  // [kStream][kSlots][kGroupBytes]
+  // two rows' groups' largest values; behind them the numbers of those that are looked at
+  float* gmax = reinterpret_cast<float*>(ring + kStream * kSlots * kGroupBytes);
+  __shared__ Board board[2];
+  __shared__ Scratch sc;
+  __shared__ uint64_t full[2], done[2], landed[kStream][kSlots], free[kStream][kSlots];
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int n = p.n_top;
+  const float c2 = p.inv_temp * kLog2e;
+  auto init = [](uint64_t* b, int count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(smem_u32(b)), "r"(count) : "memory");
+  };
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) init(&full[i], kStream), init(&done[i], kFinish);
+    for (int w = 0; w < kStream; ++w)
+      for (int i = 0; i < kSlots; ++i) init(&landed[w][i], 1), init(&free[w][i], 1);
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  }
+  __syncthreads();
+  auto arrive = [&](uint64_t* b) {
+    __syncwarp();
+    if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_u32(b)) : "memory");
+  };
+  bool late = false;  // a wait ran out: flagged, and no more waiting or copying
+  auto wait = [&](uint64_t* b, int use) {
+    if (!late && !bar_wait(smem_u32(b), uint32_t(use) & 1u)) late = true, atomicOr(p.flags, CSA2_FLAG_TIMEOUT);
+    late = __any_sync(0xffffffffu, late);
+  };
+  if (warp < kStream) {
+    unsigned char* mine = ring + warp * (kSlots * kGroupBytes);
+    int i = 0, used = 0;
+    for (int r = blockIdx.x; r < p.rows; r += gridDim.x, ++i) {
+      const R row(p, r);
+      float* top_of = gmax + (i & 1) * p.max_groups;
+      if (i >= 2) wait(&done[i & 1], i / 2 - 1);
+      Stat st = {-INFINITY, 0.f, 0.f};
+      for (int g = warp, ng = row.groups(); g < ng; g += kStream) {
+        uint4 v[kLoads];
+        if (row.inner(g)) {
+          wait(&landed[warp][used % kSlots], used / kSlots);
+          const uint4* at = reinterpret_cast<const uint4*>(mine + used % kSlots * kGroupBytes) + lane;
 #pragma unroll
-      for (int j = 0; j < kLoads; ++j) row.load(row.first(g, j, lane), v[j]);
-      uint32_t left = 0;  // this lane's values that reach the bound and are not taken yet
+          for (int j = 0; j < kLoads; ++j) v[j] = at[32 * j];
+          attn::fence_async_smem();  // what the lanes have read comes before what the next copy writes
+          arrive(&free[warp][used % kSlots]);
+          ++used;
+        } else {
+#pragma unroll
+          for (int j = 0; j < kLoads; ++j) row.load(row.first(g, j, lane), v[j]);
+        }
+        const float top = group_max<kBf16>(v);
+        if (n) {
+          const float m = warp_max(top);
+          if (lane == 0) top_of[g] = m;
+        }
+        add_group<kBf16>(v, top, c2, st);
+      }
+      post<kStream>(board[i & 1], st, warp, lane, c2);
+      arrive(&full[i & 1]);
+    }
+  } else if (warp == kStream + kFinish) {
+    if (lane < kStream) {
+      int begun = 0;
+      for (int r = blockIdx.x; r < p.rows && !late; r += gridDim.x) {
+        const R row(p, r);
+        for (int g = lane, ng = row.groups(); g < ng; g += kStream) {
+          if (!row.inner(g)) continue;
+          const int slot = begun % kSlots;
+          if (begun >= kSlots && !bar_wait(smem_u32(&free[lane][slot]), uint32_t(begun / kSlots - 1) & 1u)) {
+            late = true, atomicOr(p.flags, CSA2_FLAG_TIMEOUT);
+            break;
+          }
+          const uint32_t bar = smem_u32(&landed[lane][slot]);
+          asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar), "r"(kGroupBytes) : "memory");
+          asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
+                           smem_u32(ring + (lane * kSlots + slot) * kGroupBytes)),
+                       "l"(row.at + int64_t(g) * kGroupBytes), "r"(kGroupBytes), "r"(bar)
+                       : "memory");
+          ++begun;
+        }
+      }
+      bar_drain<kSlots>(landed[lane], begun);  // no CTA leaves with a copy under way
+    }
+  } else {
+    const int t = tid - kStream * 32;
+    int i = 0;
+    for (int r = blockIdx.x; r < p.rows; r += gridDim.x, ++i) {
+      const R row(p, r);
+      wait(&full[i & 1], i / 2);
+      const Final f(join_parts(board[i & 1].part, kStream, lane, c2), p, c2);
+      f.template write<kBf16>(p, row, r, t, kFinish * 32);
+      if (n)
+        likeliest<kBf16, kFinish * 32, 1>(row, 0, row.groups(), gmax + (i & 1) * p.max_groups,
+                                          reinterpret_cast<int*>(gmax + 2 * p.max_groups), board[i & 1], sc, n, t,
+                                          [&](int place, float v, int id) { f.top(p, r, place, id, v); });
+      arrive(&done[i & 1]);
+    }
+  }
+}
+
+// Short rows, of up to kShort groups: a warp per row, which keeps the row in registers.
+constexpr int kShort = 4, kRowCand = 256;
+template <bool kBf16>
+__global__ void __launch_bounds__(128) short_rows_kernel(const Params p) {
+  using R = Row<kBf16>;
+  __shared__ float cv[4][kRowCand];
+  __shared__ int ci[4][kRowCand];
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int r = int(blockIdx.x) * 4 + warp, n = p.n_top;
+  if (r >= p.rows) return;
+  const float c2 = p.inv_temp * kLog2e;
+  const R row(p, r);
+  const int ng = row.groups();
+  uint4 v[kShort][kLoads];
+#pragma unroll
+  for (int g = 0; g < kShort; ++g)
+    if (g < ng) {
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) row.load(row.first(g, j, lane), v[g][j]);
+    }
+  Stat st = {-INFINITY, 0.f, 0.f};
+#pragma unroll
+  for (int g = 0; g < kShort; ++g)
+    if (g < ng) add_group<kBf16>(v[g], group_max<kBf16>(v[g]), c2, st);
+  const float mine = st.m;
+#pragma unroll 1
+  for (int o = 16; o; o >>= 1) st = shuffle_join(st, o, c2);
+  const Final f(st, p, c2);
+  f.template write<kBf16>(p, row, r, lane, 32);
+  if (n == 0) return;
+  // n values reach the n-th largest of the lanes' largest ones
+  int place = 0;
+#pragma unroll 4
+  for (int j = 0; j < 32; ++j) {
+    const float u = __shfl_sync(0xffffffffu, mine, j);
+    place += u > mine || (u == mine && j < lane);
+  }
+  const float low = __shfl_sync(0xffffffffu, mine, __ffs(__ballot_sync(0xffffffffu, place == n - 1)) - 1);
+  uint32_t left[kShort];
+  int count = 0;
+#pragma unroll
+  for (int g = 0; g < kShort; ++g) {
+    left[g] = 0;
+    if (g < ng) {
 #pragma unroll
       for (int j = 0; j < kLoads; ++j) {
         const int i = row.first(g, j, lane);
 #pragma unroll
         for (int e = 0; e < R::E; ++e)
-          if (i + e >= 0 && i + e < p.V && R::value(v[j], e) >= low) left |= 1u << (j * R::E + e);
+          if (may_win(R::value(v[g][j], e), low, i + e, n, p.V)) left[g] |= 1u << (j * R::E + e);
       }
-      const int most = n - place;
-      const int mine = __popc(left), all = int(__reduce_add_sync(0xffffffffu, unsigned(mine)));
-      if (all <= most) {  // (the candidates' order does not matter)
-        int at = 0;
-        if (mine) at = atomicAdd(&n_cand, mine);
+    }
+    count += __popc(left[g]);
+  }
+  int at = count;
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const int u = __shfl_up_sync(0xffffffffu, at, o);
+    if (lane >= o) at += u;
+  }
+  const int total = __shfl_sync(0xffffffffu, at, 31);
+  at -= count;
+  if (total <= kRowCand) {
+#pragma unroll
+    for (int g = 0; g < kShort; ++g)
+      if (g < ng) {
 #pragma unroll
         for (int j = 0; j < kLoads; ++j)
 #pragma unroll
           for (int e = 0; e < R::E; ++e)
-            if (left >> (j * R::E + e) & 1u) cv[at] = R::value(v[j], e), ci[at] = row.first(g, j, lane) + e, ++at;
-      } else {  // ties: the best of the group, one after the other
-        for (int k = 0; k < most; ++k) {
-          float best = -INFINITY;
-          int where = -1;
-#pragma unroll
-          for (int j = 0; j < kLoads; ++j)
-#pragma unroll
-            for (int e = 0; e < R::E; ++e) {
-              const float x = R::value(v[j], e);
-              if ((left >> (j * R::E + e) & 1u) && (where < 0 || x > best)) best = x, where = j * R::E + e;
-            }
-          const float m = warp_max(best);
-          const int id = where >= 0 && best == m ? row.first(g, where / R::E, lane) + where % R::E : 0x7FFFFFFF;
-          const int first = int(__reduce_min_sync(0xffffffffu, unsigned(id)));
-          if (id == first) {  // (some lane has one: fewer are taken than there are)
-            const int at = atomicAdd(&n_cand, 1);
-            cv[at] = m, ci[at] = id, left &= ~(1u << where);
-          }
-          __syncwarp();
-        }
+            if (left[g] >> (j * R::E + e) & 1u) cv[warp][at] = R::value(v[g][j], e), ci[warp][at] = row.first(g, j, lane) + e, ++at;
       }
-    }
-    __syncthreads();
-    // the winners' places; into the list of the cluster's first CTA
-    const int total = n_cand;
-    const uint32_t to_v = C > 1 ? cluster_addr(smem_u32(&lv[rank * kTop]), 0) : smem_u32(&lv[0]);
-    const uint32_t to_i = C > 1 ? cluster_addr(smem_u32(&li[rank * kTop]), 0) : smem_u32(&li[0]);
-    for (int i = tid; i < total; i += kThreads) {
-      const int id = ci[i];
-      const float v = cv[i];
-      int place = 0;
+    __syncwarp();
+    for (int i = lane; i < total; i += 32) {
+      const int id = ci[warp][i];
+      const float x = cv[warp][i];
+      int at_place = 0;
 #pragma unroll 4
       for (int j = 0; j < total; ++j) {
-        const float u = cv[j];
-        place += u > v || (u == v && ci[j] < id);
+        const float u = cv[warp][j];
+        at_place += u > x || (u == x && ci[warp][j] < id);
       }
-      if (place < n) st_cluster(to_v + 4u * place, v), st_cluster_u32(to_i + 4u * place, uint32_t(id));
+      if (at_place < n) f.top(p, r, at_place, id, x);
     }
+    return;
   }
-  if (C > 1) cluster_arrive(), cluster_wait();
-  else __syncthreads();
-  if (rank != 0) return;
-
-  Stat a = whole[0];
-  for (int i = 1; i < C; ++i) a = join(a, whole[i], c2);
-  const bool empty = !(a.m > -INFINITY);
-  const float log_s = logf(a.s), ref = __fmul_rn(a.m, c2);
-  auto logprob = [&](float x) {
-    if (x == -INFINITY || empty) return -INFINITY;
-    const float d = fmaf(x, c2, -ref);  // (-inf where the product with log2 e alone passes the type's end)
-    return near(ref) && d > -INFINITY ? fmaf(d, attn::kLn2, -log_s) : (x - a.m) * p.inv_temp - log_s;
-  };
-  if (tid == 0) {
-    if (p.lse) p.lse[r] = empty ? -INFINITY : near(ref) ? fmaf(ref, attn::kLn2, log_s) : fmaf(a.m, p.inv_temp, log_s);
-    if (p.entropy) p.entropy[r] = empty ? 0.f : log_s - a.t / a.s * attn::kLn2;
-  }
-  for (int i = tid; i < p.n_tok; i += kThreads) {
-    const int tok = p.tokens[int64_t(r) * p.n_tok + i];
-    float v = 0.f;
-    if (tok >= p.V) v = -INFINITY, atomicOr(p.flags, CSA2_FLAG_INDEX_OOB);
-    else if (tok >= 0) v = logprob(row.one(tok));
-    p.logprobs[int64_t(r) * p.n_tok + i] = v;
-  }
-  if (n) {
-    int32_t* ids = p.top_ids ? p.top_ids + int64_t(r) * n : nullptr;
-    float* vals = p.top_logprobs ? p.top_logprobs + int64_t(r) * n : nullptr;
-    for (int e = tid; e < C * n; e += kThreads) {
-      const int at = e / n * kTop + e % n, id = li[at];
-      if (id < 0) continue;
-      const float v = lv[at];
-      int place = 0;
-#pragma unroll 4
-      for (int o = 0; o < C * n; ++o) {
-        const int i = o / n * kTop + o % n;
-        const float u = lv[i];
-        place += li[i] >= 0 && (u > v || (u == v && li[i] < id));
+#pragma unroll 1
+  for (int k = 0; k < min(n, p.V); ++k) {  // ties: the best of the row, one after the other
+    float best = -INFINITY;
+    int where = -1;
+#pragma unroll
+    for (int g = 0; g < kShort; ++g)
+      if (g < ng) {
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j)
+#pragma unroll
+          for (int e = 0; e < R::E; ++e) {
+            const float x = R::value(v[g][j], e);
+            if ((left[g] >> (j * R::E + e) & 1u) && (where < 0 || x > best)) best = x, where = g * 32 + j * R::E + e;
+          }
       }
-      if (place >= n) continue;
-      if (ids) ids[place] = id;
-      if (vals) vals[place] = logprob(v);
+    const float m = warp_max(best);
+    const int id = where >= 0 && best == m ? row.first(where / 32, where % 32 / R::E, lane) + where % R::E : 0x7FFFFFFF;
+    const int first = int(__reduce_min_sync(0xffffffffu, unsigned(id)));
+    if (id == first) {
+#pragma unroll
+      for (int g = 0; g < kShort; ++g)
+        if (g == where / 32) left[g] &= ~(1u << (where % 32));
+      f.top(p, r, k, id, m);
     }
-    for (int i = min(n, p.V) + tid; i < n; i += kThreads) {  // fewer tokens than that
-      if (ids) ids[i] = -1;
-      if (vals) vals[i] = -INFINITY;
-    }
+    __syncwarp();
   }
 }
 
-template <bool kBf16, int kThreads>
-cudaError_t launch(Params p, int C, cudaStream_t st) {
-  p.max_groups = ((p.V + 15) / Row<kBf16>::kGroup + 2 + C - 1) / C + 1;  // groups of a CTA, whatever the alignment
+template <bool kBf16>
+cudaError_t launch(Params p, int sms, cudaStream_t st) {
+  const int groups = (p.V + Row<kBf16>::E - 1 + Row<kBf16>::kGroup - 1) / Row<kBf16>::kGroup;  // at most, whatever the alignment
+  if (groups <= kShort) return launch_pdl(short_rows_kernel<kBf16>, dim3(unsigned((p.rows + 3) / 4)), dim3(128), 0, st, p);
+  if (p.rows > 2 * sms) {
+    p.max_groups = groups;
+    constexpr size_t kRing = size_t(kStream) * kSlots * kGroupBytes;
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(many_rows_kernel<kBf16>),
+                                     kRing + (CSA2_MAX_VOCAB / Row<kBf16>::kGroup + 2) * 12, done);
+    if (e != cudaSuccess) return e;
+    const size_t smem = kRing + (p.n_top ? size_t(groups) * 12 : 0);
+    return launch_pdl(many_rows_kernel<kBf16>, dim3(unsigned(2 * sms)), dim3((kStream + kFinish + 1) * 32), smem, st, p);
+  }
+  int C = 1;
+  while (C < kMaxCluster && int64_t(p.rows) * C <= sms && groups >= 16 * C) C *= 2;
+  p.max_groups = (groups + C - 1) / C + 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(p.rows) * unsigned(C));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(512);
   cfg.dynamicSmemBytes = p.n_top ? size_t(p.max_groups) * 8 : 0;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
@@ -442,7 +729,7 @@ cudaError_t launch(Params p, int C, cudaStream_t st) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = C > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, logprobs_kernel<kBf16, kThreads>, p, C);
+  return cudaLaunchKernelEx(&cfg, few_rows_kernel<kBf16>, p, C);
 }
 
 }  // namespace lp
@@ -474,14 +761,7 @@ extern "C" csa2_status csa2_token_logprobs(const void* logits, int logits_fp32, 
   p.flags = device_flags_ptr();
   const int sms = sm_count();
   if (!p.flags || sms <= 0) return CSA2_ERR_CUDA;
-  const int groups = V / (logits_fp32 ? Row<false>::kGroup : Row<true>::kGroup) + 1;
-  int C = 1;
-  while (C < kMaxCluster && int64_t(rows) * C * 2 <= 2 * sms && groups >= 16 * C) C *= 2;
-  const int threads = groups <= 16 ? 128 : C > 1 ? 512 : 256;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = logits_fp32 ? (threads == 128 ? launch<false, 128>(p, C, st) : threads == 256 ? launch<false, 256>(p, C, st)
-                                                                                             : launch<false, 512>(p, C, st))
-                                    : (threads == 128 ? launch<true, 128>(p, C, st) : threads == 256 ? launch<true, 256>(p, C, st)
-                                                                                           : launch<true, 512>(p, C, st));
+  const cudaError_t e = logits_fp32 ? launch<false>(p, sms, st) : launch<true>(p, sms, st);
   return e == cudaSuccess ? CSA2_OK : CSA2_ERR_CUDA;
 }
