@@ -1,7 +1,7 @@
 // Low-rank adapters of many requests: out[i] = base[i] + scale[l] B_l (A_l x_i), l the adapter of row i.
 //
 // Rows in any order.  Every CTA looks through the adapters of a window of rows, counts the rows of each bucket (an
-// adapter's number modulo 256) and cuts the buckets into tiles of 16 or 64 rows, the same ones in every CTA.  A cluster
+// adapter's number modulo 255) and cuts the buckets into tiles of 16 or 64 rows, the same ones in every CTA.  A cluster
 // takes tiles in turn: it collects a tile's rows, and for each adapter among them (one, unless adapters share a bucket)
 // its CTAs share the input channels of A_l x, add their parts up through distributed shared memory in order of rank, and
 // share the output channels of B_l t.  One launch, no workspace, no atomics on sums: an adapter's weights are read once per
@@ -24,9 +24,9 @@ namespace csa2 {
 namespace lora {
 
 constexpr int kThreads = 256, kWarps = 8, kMaxCluster = 8;
-constexpr int kWindow = 4096, kBuckets = 256;
-constexpr int kStages = 3, kStep = 64, kStepPitch = kStep + 32;  // channels of x and A under way (64 rows); rows apart by 192 bytes, so that 16-byte reads of eight rows miss each other
-static_assert(kBuckets == kThreads, "a thread per bucket");
+constexpr int kWindow = 8192, kBuckets = 255;
+constexpr int kStages = 4;  // of a ring of 128-byte rows (64 rows): x and A, then base and B
+static_assert(kBuckets < kThreads && kBuckets < 256, "a thread per bucket; a byte holds one, or none");
 
 struct Params {
   const uint16_t *x, *a, *b;
@@ -42,6 +42,10 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
   const uint32_t a[4] = {a0, a1, a2, a3};
   mma_bf16_16816(d, a, b0, b1);
 }
+// cp_async16 that has the row's next 128 bytes brought to L2 as well: they are the next step's
+__device__ __forceinline__ void cp_async16_row(uint32_t dst, const void* src, int src_bytes) {
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+}
 __device__ __forceinline__ uint32_t bf2(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -51,11 +55,15 @@ template <int NR, int WM>
 struct Shape {
   static constexpr int WK = kWarps / WM, TM = 16 * WM, R = 8 * NR, kPitch = R + 8;
   static constexpr bool kStaged = WM > 1;
-  static constexpr size_t kPart = size_t(WK) * TM * R * 4;
-  static constexpr size_t kStage = size_t(TM + R) * kStepPitch * 2;
-  static constexpr size_t kFirst = kStaged && kStages * kStage > kPart ? kStages * kStage : kPart;
-  static constexpr size_t kSmem = kFirst + size_t(2) * TM * kPitch * 2;
+  static constexpr size_t kStage = size_t(TM + R) * 128;
+  static constexpr size_t kPart = size_t(WK) * TM * R * 4;   // the warps' sums; staged: in the ring's place
+  static constexpr size_t kFirst = kStaged ? kStages * kStage : kPart;
+  static constexpr size_t kSums = kStaged ? size_t(TM) * R * 4 : 0;  // this CTA's; else in the place of the first warp's
+  static constexpr size_t kSmem = kFirst + kSums + size_t(2) * TM * kPitch * 2;
+  static_assert(kPart <= kFirst, "shared memory");
 };
+// where 16-byte piece j of a 128-byte row lies: eight lanes that read four pieces of two rows miss each other
+__device__ __forceinline__ uint32_t piece_at(int row, int j) { return uint32_t(row) * 128u + uint32_t(j ^ ((row & 1) << 2)) * 16u; }
 
 // NR: groups of eight ranks, an even number; WM: warps along the rows, 16 each.
 // kF32: base and out are fp32; kVec: rows of out are whole 16-byte pieces.
@@ -64,11 +72,12 @@ __global__ void __launch_bounds__(kThreads, NR <= 8 ? 2 : 1) lora_kernel(const P
   using S = Shape<NR, WM>;
   constexpr int WK = S::WK, TM = S::TM, R = S::R, kPitch = S::kPitch;
   extern __shared__ __align__(16) unsigned char smem[];
-  float* part = reinterpret_cast<float*>(smem);                       // [WK][TM][R]; then, from 0, this CTA's sums [TM][R]
-  uint16_t* hi = reinterpret_cast<uint16_t*>(smem + S::kFirst);       // [TM][kPitch], channels in the MMA's order
+  float* part = reinterpret_cast<float*>(smem);                                   // [WK][TM][R]
+  float* sums = reinterpret_cast<float*>(smem + (S::kStaged ? S::kFirst : 0));    // [TM][R]
+  uint16_t* hi = reinterpret_cast<uint16_t*>(smem + S::kFirst + S::kSums);        // [TM][kPitch], channels in the MMA's order
   uint16_t* lo = hi + TM * kPitch;
-  __shared__ uint16_t bucket[kWindow];  // of the window's rows; 0xFFFF: no adapter
-  __shared__ int count[kBuckets], start[kBuckets + 1], seg[kWarps];
+  __shared__ uint8_t bucket[kWindow];  // of the window's rows; kBuckets: no adapter
+  __shared__ int count[kThreads], start[kBuckets + 1], seg[kWarps];
   __shared__ int rows[TM], which[TM], list[TM];
   __shared__ int n_list;
   __shared__ uint32_t tmp[32];
@@ -86,37 +95,28 @@ __global__ void __launch_bounds__(kThreads, NR <= 8 ? 2 : 1) lora_kernel(const P
   // the window's buckets and tiles
   count[tid] = 0;
   __syncthreads();
-#pragma unroll 4
-  for (int i = tid; i < n_w; i += kThreads) {
-    const int l = p.adapter[w0 + i];
-    const bool on = l >= 0 && l < p.L;
-    if (l >= p.L && cluster == 0 && rank == 0) atomicOr(p.flags, CSA2_FLAG_INDEX_OOB);
-    bucket[i] = on ? uint16_t(l % kBuckets) : uint16_t(0xFFFF);
-    if (on) atomicAdd(&count[l % kBuckets], 1);
+  for (int i0 = warp * 32; i0 < n_w; i0 += 8 * kThreads) {
+    int l[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) l[j] = i0 + j * kThreads + lane < n_w ? __ldg(p.adapter + w0 + i0 + j * kThreads + lane) : -1;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int i = i0 + j * kThreads + lane;
+      if (i - lane >= n_w) break;
+      const bool on = l[j] >= 0 && l[j] < p.L;
+      if (l[j] >= p.L && cluster == 0 && rank == 0) atomicOr(p.flags, CSA2_FLAG_INDEX_OOB);
+      const int b = on ? l[j] % kBuckets : kBuckets;
+      if (i < n_w) bucket[i] = uint8_t(b);
+      // (neighbouring rows often have one adapter: added together)
+      const unsigned same = __match_any_sync(0xffffffffu, b);
+      if (on && lane == __ffs(same) - 1) atomicAdd(&count[b], __popc(same));
+    }
   }
   __syncthreads();
   uint32_t n_units;
   const uint32_t at_unit = block_exclusive_scan(uint32_t((count[tid] + TM - 1) / TM), tmp, &n_units);
-  start[tid] = int(at_unit);
-  if (tid == 0) start[kBuckets] = int(n_units);
+  if (tid <= kBuckets) start[tid] = int(at_unit);  // (the last one: their number)
   __syncthreads();
-
-  if (p.base != p.out) {  // rows without an adapter: a warp per row, of the CTA's share of the channels
-    constexpr int kSize = kF32 ? 4 : 2, kPiece = kVec ? 16 : kSize;
-    const int n_piece = p.n_out * kSize / kPiece;
-    const int p0 = int(int64_t(n_piece) * rank / C), p1 = int(int64_t(n_piece) * (rank + 1) / C);
-    for (int i = cluster + n_clusters * warp; i < n_w; i += n_clusters * kWarps) {
-      if (bucket[i] != 0xFFFF) continue;
-      const char* src = static_cast<const char*>(p.base) + int64_t(w0 + i) * p.n_out * kSize;
-      char* dst = static_cast<char*>(p.out) + int64_t(w0 + i) * p.n_out * kSize;
-#pragma unroll 4
-      for (int n = p0 + lane; n < p1; n += 32) {
-        if (kVec) reinterpret_cast<uint4*>(dst)[n] = reinterpret_cast<const uint4*>(src)[n];
-        else if (kF32) reinterpret_cast<float*>(dst)[n] = reinterpret_cast<const float*>(src)[n];
-        else reinterpret_cast<uint16_t*>(dst)[n] = reinterpret_cast<const uint16_t*>(src)[n];
-      }
-    }
-  }
 
   for (int unit = cluster; unit < int(n_units); unit += n_clusters) {
   // the rows of the tile, in order: the bucket's from `from` on
@@ -131,21 +131,26 @@ __global__ void __launch_bounds__(kThreads, NR <= 8 ? 2 : 1) lora_kernel(const P
     from = (unit - start[b]) * TM, n_rows = min(TM, count[b] - from);
     const int share = (n_w + kThreads - 1) / kThreads * 32, s0 = warp * share, s1 = min(n_w, s0 + share);
     int n = 0;
+#pragma unroll 8
     for (int i = s0; i < s1; i += 32)
       n += __popc(__ballot_sync(0xffffffffu, i + lane < s1 && bucket[i + lane] == b));
     if (lane == 0) seg[warp] = n;
     __syncthreads();
     int at = -from;
     for (int w = 0; w < warp; ++w) at += seg[w];
+#pragma unroll 4
     for (int i = s0; i < s1 && at < TM; i += 32) {
       const bool on = i + lane < s1 && bucket[i + lane] == b;
       const unsigned got = __ballot_sync(0xffffffffu, on);
       const int mine = at + __popc(got & ((1u << lane) - 1u));
-      if (on && mine >= 0 && mine < TM) rows[mine] = w0 + i + lane, which[mine] = p.adapter[w0 + i + lane];
+      if (on && mine >= 0 && mine < TM) rows[mine] = w0 + i + lane;
       at += __popc(got);
     }
     __syncthreads();
-    for (int i = n_rows + tid; i < TM; i += kThreads) rows[i] = rows[0], which[i] = -1;  // (read, not written)
+    for (int i = tid; i < TM; i += kThreads) {
+      if (i < n_rows) which[i] = __ldg(p.adapter + rows[i]);
+      else rows[i] = rows[0], which[i] = -1;  // (read, not written)
+    }
     __syncthreads();
   }
   // its adapters, in the order of their first rows
@@ -188,20 +193,20 @@ __global__ void __launch_bounds__(kThreads, NR <= 8 ? 2 : 1) lora_kernel(const P
     };
     if constexpr (S::kStaged) {
       // 64 channels of the tile's rows and of A at a time, by asynchronous copies into a ring
-      const int n_step = (p.n_in + kStep - 1) / kStep;
+      const int n_step = (p.n_in + 63) / 64;
       const int s0 = int(int64_t(n_step) * rank / C), n = int(int64_t(n_step) * (rank + 1) / C) - s0;
       auto ask = [&](int i) {
         if (i < n) {
           const uint32_t dst = smem_u32(smem) + uint32_t(i % kStages) * uint32_t(S::kStage);
-          const int ch = (s0 + i) * kStep + 8 * (tid & 7);
+          const int j = tid & 7, ch = (s0 + i) * 64 + 8 * j;
           const bool in = ch < p.n_in;
 #pragma unroll
           for (int row = tid >> 3; row < TM; row += kThreads / 8)
-            cp_async16(dst + uint32_t(row * kStepPitch * 2 + (tid & 7) * 16), in ? p.x + int64_t(rows[row]) * p.n_in + ch : p.x, in ? 16 : 0);
+            cp_async16_row(dst + piece_at(row, j), in ? p.x + int64_t(rows[row]) * p.n_in + ch : p.x, in ? 16 : 0);
 #pragma unroll
           for (int row = tid >> 3; row < R; row += kThreads / 8) {
             const bool on = in && row < n_rank;
-            cp_async16(dst + uint32_t((TM + row) * kStepPitch * 2 + (tid & 7) * 16), on ? a + int64_t(row) * p.n_in + ch : p.x, on ? 16 : 0);
+            cp_async16(dst + TM * 128 + piece_at(row, j), on ? a + int64_t(row) * p.n_in + ch : p.x, on ? 16 : 0);
           }
         }
         cp_async_commit();
@@ -211,12 +216,12 @@ __global__ void __launch_bounds__(kThreads, NR <= 8 ? 2 : 1) lora_kernel(const P
         cp_async_wait<kStages - 2>();
         __syncthreads();  // this step is there for all, and the one before is done with
         ask(i + kStages - 1);
-        const unsigned char* at = smem + (i % kStages) * S::kStage + (wk * 32 + 8 * t) * 2;
+        const unsigned char* at = smem + (i % kStages) * S::kStage;
         uint4 xv[2], av[NR];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) xv[h] = *reinterpret_cast<const uint4*>(at + (wm * 16 + 8 * h + g) * kStepPitch * 2);
+        for (int h = 0; h < 2; ++h) xv[h] = *reinterpret_cast<const uint4*>(at + piece_at(wm * 16 + 8 * h + g, 4 * wk + t));
 #pragma unroll
-        for (int j = 0; j < NR; ++j) av[j] = *reinterpret_cast<const uint4*>(at + (TM + 8 * j + g) * kStepPitch * 2);
+        for (int j = 0; j < NR; ++j) av[j] = *reinterpret_cast<const uint4*>(at + TM * 128 + piece_at(8 * j + g, 4 * wk + t));
         multiply(xv, av);
       }
       cp_async_wait<0>();
@@ -255,7 +260,34 @@ __global__ void __launch_bounds__(kThreads, NR <= 8 ? 2 : 1) lora_kernel(const P
         const float4 u = reinterpret_cast<float4*>(part)[w * (TM * R / 4) + e];
         v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
       }
-      reinterpret_cast<float4*>(part)[e] = v;
+      reinterpret_cast<float4*>(sums)[e] = v;
+    }
+    // staged: base and B of kCols output channels at a time, in the same ring; the first are asked for before t is known
+    constexpr bool kRing = S::kStaged && kVec;
+    constexpr int J = kF32 ? 2 : 4, kCols = 16 * J;
+    const int n_col = (p.n_out + kCols - 1) / kCols;
+    const int q0 = int(int64_t(n_col) * rank / C), q1 = int(int64_t(n_col) * (rank + 1) / C);
+    auto ask_out = [&](int i) {
+      if (q0 + i < q1) {
+        const uint32_t dst = smem_u32(smem) + uint32_t(i % kStages) * uint32_t(S::kStage);
+        const int n0 = (q0 + i) * kCols, n = n0 + (tid & 7) * 2 * J;
+        const bool in = n < p.n_out;
+#pragma unroll
+        for (int row = tid >> 3; row < TM; row += kThreads / 8)
+          cp_async16_row(dst + piece_at(row, tid & 7),
+                     in ? static_cast<const char*>(p.base) + (int64_t(rows[row]) * p.n_out + n) * (kF32 ? 4 : 2) : p.base, in ? 16 : 0);
+        for (int e = tid; e < kCols * (R / 8); e += kThreads) {
+          const int row = e / (R / 8), j = e % (R / 8);
+          const bool on = n0 + row < p.n_out && 8 * j < n_rank;
+          cp_async16(dst + TM * 128 + uint32_t(row * (R * 2)) + uint32_t(R >= 64 ? j ^ ((row & 1) << 2) : j) * 16u,
+                     on ? static_cast<const void*>(p.b + (int64_t(l) * p.n_out + n0 + row) * p.r + 8 * j) : p.base, on ? 16 : 0);
+        }
+      }
+      cp_async_commit();
+    };
+    if constexpr (kRing) {
+      __syncthreads();  // the warps' sums, in the ring's place, are added up
+      for (int i = 0; i < kStages - 1; ++i) ask_out(i);
     }
     // out = base + B t over this warp's output channels, a block of 32 at a time: a lane gets eight neighbouring ones,
     // 8t .. 8t + 7.  With few rows the next block is asked for before one is finished, the first before t is known
@@ -301,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, NR <= 8 ? 2 : 1) lora_kernel(const P
           }
       }
     };
-    if (kAhead && blk0 < n_blk) load(blk0);
+    if (!kRing && kAhead && blk0 < n_blk) load(blk0);
     if (C > 1) cluster_arrive(), cluster_wait();
     else __syncthreads();
     // the cluster's sums, scaled, as two bf16 terms
@@ -312,13 +344,13 @@ __global__ void __launch_bounds__(kThreads, NR <= 8 ? 2 : 1) lora_kernel(const P
         float4 u[kMaxCluster];
 #pragma unroll
         for (int c = 0; c < kMaxCluster; ++c)
-          if (c < C) u[c] = ld_cluster4(cluster_addr(smem_u32(part + 4 * e), uint32_t(c)));
+          if (c < C) u[c] = ld_cluster4(cluster_addr(smem_u32(sums + 4 * e), uint32_t(c)));
         v = u[0];
 #pragma unroll
         for (int c = 1; c < kMaxCluster; ++c)
           if (c < C) v.x += u[c].x, v.y += u[c].y, v.z += u[c].z, v.w += u[c].w;
       } else {
-        v = reinterpret_cast<const float4*>(part)[e];
+        v = reinterpret_cast<const float4*>(sums)[e];
       }
       v.x *= scale, v.y *= scale, v.z *= scale, v.w *= scale;
       const int row = e / (R / 4), rr = e % (R / 4) * 4;
@@ -342,7 +374,73 @@ __global__ void __launch_bounds__(kThreads, NR <= 8 ? 2 : 1) lora_kernel(const P
     }
     __syncthreads();
     if (C > 1) cluster_arrive();
-    for (int blk = blk0; blk < n_blk; blk += blk_step) {
+    if constexpr (kRing) {
+      uint32_t f[2][R / 16][4];  // t of this warp's rows
+#pragma unroll
+      for (int k = 0; k < R / 16; ++k)
+#pragma unroll
+        for (int term = 0; term < 2; ++term)
+          ldmatrix_x4(f[term][k][0], f[term][k][1], f[term][k][2], f[term][k][3],
+                      smem_u32((term ? lo : hi) + (16 * wm + (lane & 15)) * kPitch + 16 * k + 8 * (lane >> 4)));
+      const int64_t row0 = rows[16 * wm + g], row1 = rows[16 * wm + 8 + g];
+      const bool use0 = which[16 * wm + g] == l, use1 = which[16 * wm + 8 + g] == l;
+      for (int i = 0; i < q1 - q0; ++i) {
+        cp_async_wait<kStages - 2>();
+        __syncthreads();
+        ask_out(i + kStages - 1);
+        const unsigned char* at = smem + (i % kStages) * S::kStage;
+        float d[J][4];
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          d[j][0] = d[j][1] = d[j][2] = d[j][3] = 0.f;
+          const int row = wk * (8 * J) + 2 * J * (g >> 1) + 2 * j + (g & 1);  // a lane's channels: wk * 8J + 2J t and on
+          const unsigned char* br = at + TM * 128 + row * (R * 2);
+          uint32_t bv[R / 16][2];
+          if (R >= 32) {
+#pragma unroll
+            for (int k = 0; k < R / 32; ++k) {
+              const int c = 4 * k + t;
+              const uint4 v = *reinterpret_cast<const uint4*>(br + (R >= 64 ? c ^ ((row & 1) << 2) : c) * 16);
+              bv[2 * k][0] = v.x, bv[2 * k][1] = v.y;
+              bv[R >= 32 ? 2 * k + 1 : 0][0] = v.z, bv[R >= 32 ? 2 * k + 1 : 0][1] = v.w;
+            }
+          } else {
+            const uint2 v = *reinterpret_cast<const uint2*>(br + 8 * t);
+            bv[0][0] = v.x, bv[0][1] = v.y;
+          }
+          if (n_rank < R) {  // what lies past the adapter's rank is not used
+#pragma unroll
+            for (int k = 0; k < R / 16; ++k)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int rr = R >= 32 ? 32 * (k >> 1) + 8 * t + 4 * (k & 1) + 2 * h : 4 * t + 2 * h;
+                if (rr >= n_rank) bv[k][h] = 0;
+                else if (rr + 1 >= n_rank) bv[k][h] &= 0xFFFFu;
+              }
+          }
+#pragma unroll
+          for (int k = 0; k < R / 16; ++k)
+#pragma unroll
+            for (int term = 0; term < 2; ++term)
+              mma(d[j], f[term][k][0], f[term][k][1], f[term][k][2], f[term][k][3], bv[k][0], bv[k][1]);
+        }
+        const int n = (q0 + i) * kCols + wk * (8 * J) + 2 * J * t;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (!(h ? use1 : use0) || n >= p.n_out) continue;
+          const uint4 v = *reinterpret_cast<const uint4*>(at + piece_at(16 * wm + 8 * h + g, 4 * wk + t));
+          uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            w[e] = kF32 ? __float_as_uint(__uint_as_float(w[e]) + d[e / 2 % J][2 * h + (e & 1)])
+                        : bf2(bf16lo(w[e]) + d[e % J][2 * h], bf16hi(w[e]) + d[e % J][2 * h + 1]);
+          *reinterpret_cast<uint4*>(static_cast<char*>(p.out) + ((h ? row1 : row0) * p.n_out + n) * (kF32 ? 4 : 2)) =
+              make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+      cp_async_wait<0>();
+    }
+    for (int blk = kRing ? n_blk : blk0; blk < n_blk; blk += blk_step) {
       if (!kAhead || blk != blk0) load(blk);
       Block now;
       if (kAhead) {
@@ -420,6 +518,26 @@ __global__ void __launch_bounds__(kThreads, NR <= 8 ? 2 : 1) lora_kernel(const P
     __syncthreads();
   }
   }
+  // rows without an adapter, by the clusters that have no tile, or else by all: a warp per row, of the CTA's share of the
+  // channels
+  const int idle = max(n_clusters - int(n_units), 0), copier = idle ? cluster - int(n_units) : cluster, copiers = idle ? idle : n_clusters;
+  if (p.base != p.out && copier >= 0) {
+    constexpr int kSize = kF32 ? 4 : 2, kPiece = kVec ? 16 : kSize;
+    const int n_piece = p.n_out * kSize / kPiece;
+    const int p0 = int(int64_t(n_piece) * rank / C), p1 = int(int64_t(n_piece) * (rank + 1) / C);
+    for (int i = copier + copiers * warp; i < n_w; i += copiers * kWarps) {
+      if (bucket[i] != kBuckets) continue;
+      const char* src = static_cast<const char*>(p.base) + int64_t(w0 + i) * p.n_out * kSize;
+      char* dst = static_cast<char*>(p.out) + int64_t(w0 + i) * p.n_out * kSize;
+#pragma unroll 4
+      for (int n = p0 + lane; n < p1; n += 32) {
+        if (kVec) reinterpret_cast<uint4*>(dst)[n] = reinterpret_cast<const uint4*>(src)[n];
+        else if (kF32) reinterpret_cast<float*>(dst)[n] = reinterpret_cast<const float*>(src)[n];
+        else reinterpret_cast<uint16_t*>(dst)[n] = reinterpret_cast<const uint16_t*>(src)[n];
+      }
+    }
+  }
+
   __syncthreads();  // the window's buckets are done with
   }
 }
