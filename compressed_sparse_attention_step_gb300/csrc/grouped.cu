@@ -13,6 +13,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "attn_common.cuh"
 
@@ -23,9 +24,8 @@ constexpr int kRows = 32, kChan = 128;  // of a block of the packed weight (matv
 constexpr int kCodeBytes = kRows * kChan / 2;
 constexpr int kBlock = kCodeBytes + kRows * kChan / CSA2_GROUP;  // 2304 bytes
 
-constexpr int kTile = 128;       // token rows of a unit, at most
-constexpr int kStages = 4;       // channel blocks of x under way
-constexpr int kStage = kTile * kChan * 2;
+constexpr int kMaxTile = 128;    // token rows of a unit, at most: 32 or 128 of them by the launch (kTile)
+constexpr int kXBytes = 128 * 1024;  // channel blocks of x under way: 16 of 32 rows, 4 of 128
 constexpr int kSlots = 4;        // steps of four weight blocks (128 outputs) under way per pipeline
 constexpr int kABufs = 2;        // dequantised blocks per pipeline
 // Two pipelines (s = 0, 1), each of a copying warp, two groups of four dequantising warps, a block in tensor memory for
@@ -33,25 +33,25 @@ constexpr int kABufs = 2;        // dequantised blocks per pipeline
 // share its channel blocks, even and odd, and the accumulators are added.  The groups of a pipeline take its blocks in
 // turn.  (A buffer has one filler and one user: none waits for a phase of a barrier that lies two ahead.)
 constexpr int kDequant = 8 * kABufs, kEpilogue = 4;
-constexpr int kWarpX = 2, kWarpCopy = 3, kWarpDeq = 5, kWarpEpi = kWarpDeq + kDequant;
+constexpr int kIssuers = 2, kWarpX = 2, kWarpCopy = 3, kWarpDeq = 5, kWarpEpi = kWarpDeq + kDequant;
 constexpr int kThreads = (kWarpEpi + kEpilogue) * 32;
-constexpr uint32_t kACols = kChan / 2, kDCols = kTile;
+constexpr uint32_t kACols = kChan / 2, kDCols = kMaxTile;
 constexpr uint32_t kACol = 2 * kDCols;
 static_assert(kACol + 2 * kABufs * kACols <= 512, "tensor memory");
 static_assert(kThreads <= 1024, "warps");
 
 struct Tail {
   alignas(16) unsigned char ring[2][kSlots][4][kBlock];
-  float inv[kTile];
+  alignas(16) float inv[kMaxTile];
   int off[CSA2_MAX_EXPERTS + 1];    // the experts' first rows, within [0, rows]
   int start[CSA2_MAX_EXPERTS + 1];  // their first token tiles
   uint32_t tmp[32];
   uint64_t w_full[2][kSlots], w_empty[2][kSlots];
-  uint64_t x_full[kStages], x_empty[kStages];
+  uint64_t x_full[16], x_empty[16];
   uint64_t a_full[2][kABufs], a_empty[2][kABufs], d_full, d_empty[2];
   uint32_t tmem;
 };
-constexpr size_t kSmem = size_t(kStages) * kStage + sizeof(Tail);
+constexpr size_t kSmem = size_t(kXBytes) + sizeof(Tail);
 static_assert(kSmem <= 227 * 1024, "shared memory");
 
 // Row r of expert rows [first, first + n): the first row and the rows of its tile.  The tiles of an expert are as few as
@@ -59,12 +59,12 @@ static_assert(kSmem <= 227 * 1024, "shared memory");
 struct Span16 {
   int r0, n;
 };
-__device__ __forceinline__ Span16 tile_of(int first, int n, int tile) {
-  const int tiles = (n + kTile - 1) / kTile, per = ((n + tiles - 1) / tiles + 15) / 16 * 16, at = tile * per;
+__device__ __forceinline__ Span16 tile_of(int most, int first, int n, int tile) {
+  const int tiles = (n + most - 1) / most, per = ((n + tiles - 1) / tiles + 15) / 16 * 16, at = tile * per;
   return Span16{first + at, min(per, n - at)};
 }
-__device__ __forceinline__ int tile_at(int n, int r) {  // the tile of the r-th row of n
-  const int tiles = (n + kTile - 1) / kTile;
+__device__ __forceinline__ int tile_at(int most, int n, int r) {  // the tile of the r-th row of n
+  const int tiles = (n + most - 1) / most;
   return r / (((n + tiles - 1) / tiles + 15) / 16 * 16);
 }
 
@@ -77,7 +77,7 @@ struct Params {
   const int32_t *offsets, *src;
   void* y;
   int64_t n_out, n_in, w_bytes, rows, n_x;
-  int E, n_kb, n_rb, n_mt, y_fp32, act;
+  int E, n_kb, n_rb, n_mt, y_fp32, act, tile;
   unsigned int* flags;
 };
 
@@ -124,14 +124,11 @@ __device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t (&r)[32]) {
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
-__device__ __forceinline__ void tmem_ld16(uint32_t a, uint32_t (&r)[16]) {  // valid after tcgen05.wait::ld
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
-      "[%16];\n"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(a)
-      : "memory");
+__device__ __forceinline__ void tmem_ld8(uint32_t a, uint32_t (&r)[8]) {  // valid after tcgen05.wait::ld
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(a)
+               : "memory");
 }
 // A loaded register used behind the wait (which the compiler does not tie to the load).
 __device__ __forceinline__ float tmem_value(uint32_t& r) {
@@ -159,7 +156,7 @@ __global__ void __launch_bounds__(128) scale_kernel(const Params p) {
   }
   if (r < off[lo] || r >= off[lo + 1]) return;
   const int n_e = off[lo + 1] - off[lo];
-  const Span16 tile = tile_of(off[lo], n_e, tile_at(n_e, r - off[lo]));
+  const Span16 tile = tile_of(p.tile, off[lo], n_e, tile_at(p.tile, n_e, r - off[lo]));
   const int i = r - tile.r0;
   const int64_t from = p.src ? int64_t(p.src[r]) : row;
   const bool on = from >= 0 && from < p.n_x;
@@ -215,10 +212,12 @@ struct Unit {
   int e, r0, n, mt;  // expert, first row, rows, row tile of the weight
 };
 
-template <int MT>
+template <int MT, int kTile>
 __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const Params p) {
+  constexpr int kStage = kTile * kChan * 2, kStages = kXBytes / kStage;
+  static_assert(kStages <= 16 && kTile <= kMaxTile, "barriers and columns");
   extern __shared__ __align__(1024) unsigned char smem[];
-  Tail& sm = *reinterpret_cast<Tail*>(smem + kStages * kStage);
+  Tail& sm = *reinterpret_cast<Tail*>(smem + kXBytes);
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, q = warp & 3;
@@ -237,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const Params p) {
       for (int i = 0; i < kABufs; ++i) mbar_init(&sm.a_full[s][i], 4), mbar_init(&sm.a_empty[s][i], 1);
       mbar_init(&sm.d_empty[s], kEpilogue);
     }
-    mbar_init(&sm.d_full, 2);
+    mbar_init(&sm.d_full, kIssuers);
     for (int s = 0; s < 2; ++s)
       for (int i = 0; i < kSlots; ++i) mbar_init(&sm.w_full[s][i], 1), mbar_init(&sm.w_empty[s][i], 4);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
@@ -274,11 +273,11 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const Params p) {
       if (sm.start[mid] <= tile) lo = mid;
       else hi = mid;
     }
-    const Span16 rows = tile_of(sm.off[lo], sm.off[lo + 1] - sm.off[lo], tile - sm.start[lo]);
+    const Span16 rows = tile_of(kTile, sm.off[lo], sm.off[lo + 1] - sm.off[lo], tile - sm.start[lo]);
     return Unit{lo, rows.r0, rows.n, int(u - int64_t(tile) * p.n_mt)};
   };
 
-  if (warp < 2) {
+  if (warp < kIssuers) {
     // The whole warp runs the loop, so that the operands of the MMAs are the same in all lanes; one lane issues them.
     const int s = warp;
     const uint32_t d = tmem + uint32_t(s) * kDCols, a0 = tmem + kACol + uint32_t(s) * (kABufs * kACols);
@@ -404,7 +403,6 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const Params p) {
   } else {
     const uint32_t lanes = uint32_t(32 * q) << 16;
     const int t = tid - kWarpEpi * 32;
-    const int64_t width = p.act ? p.n_out / 2 : p.n_out;
     uint32_t i = 0;
     for (int64_t u = blockIdx.x; u < n_units; u += gridDim.x, ++i) {
       const Unit un = unit(u);
@@ -419,43 +417,56 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const Params p) {
       for (int s = 0; s < MT; ++s) {
         const int64_t n = int64_t(un.mt) * (128 * MT) + 128 * s + 32 * q + lane;
         const float rs = p.row_scale && n < p.n_out ? __ldg(p.row_scale + int64_t(un.e) * p.n_out + n) : 1.f;
+        const uint32_t d0 = tmem + lanes + uint32_t(s) * kDCols;
+        // the unit's rows of y: kAct, kF32
+        auto finish = [&](auto act, auto f32) {
+          constexpr bool kAct = decltype(act)::value, kF32 = decltype(f32)::value;
+          constexpr int kSize = kF32 ? 4 : 2;
+          // with the activation, outputs 2i and 2i + 1 are neighbouring lanes': the even one finishes every other row, the
+          // odd one the others
+          const bool odd = lane & 1;
+          const uint32_t stride = uint32_t(kAct ? p.n_out / 2 : p.n_out) * kSize;  // of a row, in bytes
+          char* to = static_cast<char*>(p.y) + int64_t(un.r0 + (kAct && odd)) * stride + (kAct ? n >> 1 : n) * kSize;
+          const int n_rows = n < p.n_out ? un.n - (kAct && odd) : 0;
 #pragma unroll 1
-        for (int c = 0; c < un.n; c += 16) {
-          uint32_t d[2][16];
-          tmem_ld16(tmem + lanes + uint32_t(s) * kDCols + uint32_t(c), d[0]);
-          if (MT == 1) tmem_ld16(tmem + lanes + kDCols + uint32_t(c), d[1]);
-          asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
-          float v[16];
+          for (int c = 0; c < un.n; c += 8, to += 8 * int64_t(stride)) {
+            uint32_t d[MT == 1 ? 2 : 1][8];
+            tmem_ld8(d0 + uint32_t(c), d[0]);
+            if (MT == 1) tmem_ld8(d0 + kDCols + uint32_t(c), d[MT == 1 ? 1 : 0]);
+            asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
+            const float4 f0 = *reinterpret_cast<const float4*>(&sm.inv[c]), f1 = *reinterpret_cast<const float4*>(&sm.inv[c + 4]);
+            const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+            float v[8];
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            v[j] = tmem_value(d[0][j]);
-            if (MT == 1 && p.n_kb > 1) v[j] += tmem_value(d[1][j]);
-            v[j] = v[j] * sm.inv[c + j] * rs;
-          }
-          if (p.act) {
-            // outputs 2i and 2i + 1 are neighbouring lanes': the even one finishes every other row, the odd one the others
-            const bool odd = lane & 1;
-#pragma unroll
-            for (int j = 0; j < 16; j += 2) {
-              const float got = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
-              const float o = odd ? silu(got) * v[j + 1] : silu(v[j]) * got;
-              const int r = c + j + (odd ? 1 : 0);
-              if (n >= p.n_out || r >= un.n) continue;
-              const int64_t at = int64_t(un.r0 + r) * width + (n >> 1);
-              if (p.y_fp32) static_cast<float*>(p.y)[at] = o;
-              else static_cast<__nv_bfloat16*>(p.y)[at] = __float2bfloat16_rn(o);
+            for (int j = 0; j < 8; ++j) {
+              v[j] = tmem_value(d[0][j]);
+              if (MT == 1 && p.n_kb > 1) v[j] += tmem_value(d[MT == 1 ? 1 : 0][j]);
+              v[j] = v[j] * f[j] * rs;
             }
-          } else if (n < p.n_out) {
+            auto put = [&](int j, float o) {
+              if (c + j >= n_rows) return;
+              if (kF32) *reinterpret_cast<float*>(to + uint32_t(j) * stride) = o;
+              else *reinterpret_cast<__nv_bfloat16*>(to + uint32_t(j) * stride) = __float2bfloat16_rn(o);
+            };
+            if (kAct) {
+              float o[4];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              if (c + j >= un.n) break;
-              const int64_t at = int64_t(un.r0 + c + j) * width + n;
-              if (p.y_fp32) static_cast<float*>(p.y)[at] = v[j];
-              else static_cast<__nv_bfloat16*>(p.y)[at] = __float2bfloat16_rn(v[j]);
+              for (int j = 0; j < 8; j += 2) {
+                const float got = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
+                o[j / 2] = silu(odd ? got : v[j]) * (odd ? v[j + 1] : got);
+              }
+#pragma unroll
+              for (int j = 0; j < 8; j += 2) put(j, o[j / 2]);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) put(j, v[j]);
             }
           }
-          __syncwarp();
-        }
+        };
+        using T = std::true_type;
+        using F = std::false_type;
+        if (p.act) p.y_fp32 ? finish(T{}, T{}) : finish(T{}, F{});
+        else p.y_fp32 ? finish(F{}, T{}) : finish(F{}, F{});
         attn::tc_fence_before();
         __syncwarp();
         if (lane == 0) {
@@ -476,14 +487,16 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const Params p) {
 
 inline size_t xs_bytes(int64_t rows, int64_t n_in) { return size_t(rows * ((n_in + kChan - 1) / kChan)) * (kChan * 2); }
 
-template <int MT>
-cudaError_t launch(Params p, int64_t tiles, int sms, cudaStream_t st) {
-  p.n_mt = (p.n_rb + 4 * MT - 1) / (4 * MT);
-  static std::atomic<uint64_t> done{0};
-  auto kern = grouped_kernel<MT>;
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), kSmem, done);
+template <int MT, int kTile>
+cudaError_t launch(Params p, int sms, cudaStream_t st) {
+  p.n_mt = (p.n_rb + 4 * MT - 1) / (4 * MT), p.tile = kTile;
+  cudaError_t e = launch_pdl(scale_kernel, dim3(unsigned((p.rows + 3) / 4)), dim3(128), 0, st, p);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(unsigned(std::min<int64_t>(tiles * p.n_mt, sms))), dim3(kThreads), kSmem, st, p);
+  static std::atomic<uint64_t> done{0};
+  auto kern = grouped_kernel<MT, kTile>;
+  if ((e = allow_smem(reinterpret_cast<const void*>(kern), kSmem, done)) != cudaSuccess) return e;
+  const int64_t most = std::min<int64_t>(p.rows, p.E) + p.rows / kTile;  // token tiles
+  return launch_pdl(kern, dim3(unsigned(std::min<int64_t>(most * p.n_mt, sms))), dim3(kThreads), kSmem, st, p);
 }
 
 }  // namespace grp
@@ -502,7 +515,7 @@ extern "C" csa2_status csa2_fp4_grouped(const uint16_t* x, int64_t n_x, int64_t 
   using namespace csa2;
   using namespace csa2::grp;
   if (n_x < 0 || n_x >= (1ll << 31) || rows < 0 || rows >= (1ll << 31) || E < 0 || E > CSA2_MAX_EXPERTS || n_in <= 0 ||
-      n_in % CSA2_GROUP || n_in > (1 << 24) || n_out < 0 || n_out > (1 << 24) ||
+      n_in % CSA2_GROUP || n_in > (1 << 24) || n_out < 0 || n_out > (1 << 22) ||
       (act != CSA2_ACT_NONE && act != CSA2_ACT_SWIGLU) || (act == CSA2_ACT_SWIGLU && n_out % 2))
     return CSA2_ERR_INVALID_ARG;
   if (!src && n_x < rows) return CSA2_ERR_INVALID_ARG;
@@ -527,11 +540,11 @@ extern "C" csa2_status csa2_fp4_grouped(const uint16_t* x, int64_t n_x, int64_t 
   const int sms = sm_count();
   if (!p.flags || sms <= 0) return CSA2_ERR_CUDA;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_pdl(scale_kernel, dim3(unsigned((rows + 3) / 4)), dim3(128), 0, st, p);
-  if (e != cudaSuccess) return CSA2_ERR_CUDA;
-  // token tiles, at most and about
-  const int64_t most = std::min<int64_t>(rows, E) + rows / kTile, about = std::max<int64_t>(std::min<int64_t>(rows, E), rows / kTile);
-  if (about * ((p.n_rb + 7) / 8) >= 2 * sms) e = launch<2>(p, most, sms, st);
-  else e = launch<1>(p, most, sms, st);
+  // Few rows for each expert: tiles of 32 rows, whose x runs further ahead.  Two row tiles of the weight at a time where
+  // there are units enough.
+  const int64_t used = std::min<int64_t>(rows, E), pairs = (p.n_rb + 7) / 8;
+  cudaError_t e;
+  if (rows <= 16 * used) e = used * pairs >= 2 * sms ? launch<2, 32>(p, sms, st) : launch<1, 32>(p, sms, st);
+  else e = std::max(used, rows / kMaxTile) * pairs >= 2 * sms ? launch<2, 128>(p, sms, st) : launch<1, 128>(p, sms, st);
   return e == cudaSuccess ? CSA2_OK : CSA2_ERR_CUDA;
 }
