@@ -278,7 +278,9 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const Params p) {
   };
 
   if (warp < kIssuers) {
-    // The whole warp runs the loop, so that the operands of the MMAs are the same in all lanes; one lane issues them.
+    // The whole warp runs the loop, so that the operands of the MMAs are the same in all lanes; one lane issues them.  The
+    // tensor core has nothing to do while an issuing warp waits or commits for long, so it does as little of that as can
+    // be: the dequantising warps wait for x, and hand it back, on its behalf.
     const int s = warp;
     const uint32_t d = tmem + uint32_t(s) * kDCols, a0 = tmem + kACol + uint32_t(s) * (kABufs * kACols);
     const uint64_t x0 = attn::smem_desc(smem_u32(smem), 0, 1024);
@@ -290,9 +292,8 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const Params p) {
       attn::tc_fence_after();
       bool first = true;
       for (int k = MT == 2 ? 0 : s; k < p.n_kb; k += MT == 2 ? 1 : 2, first = false, ++a_use) {
-        const uint32_t xu = x_use + uint32_t(k), stage = xu % kStages, buf = a_use % kABufs;
-        wait(&sm.x_full[stage], xu / kStages);
-        wait(&sm.a_full[s][buf], a_use / kABufs);
+        const uint32_t stage = (x_use + uint32_t(k)) % kStages, buf = a_use % kABufs;
+        wait(&sm.a_full[s][buf], a_use / kABufs);  // and x: the dequantising warps have waited for it
         __syncwarp();
         attn::tc_fence_after();
         const uint64_t xk = x0 + uint64_t(stage * (kStage / 16));
@@ -301,7 +302,6 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const Params p) {
         for (uint32_t j = 0; j < kChan / 16; ++j)
           umma_ts(d, a + j * 8u, xk + uint64_t((j >> 2) * (kTile * 128 / 16) + (j & 3u) * 2u), idesc, !first || j > 0);
         commit_one(&sm.a_empty[s][buf]);
-        commit_one(&sm.x_empty[stage]);
       }
       commit_one(&sm.d_full);
     }
@@ -354,11 +354,13 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const Params p) {
     const uint32_t lanes = uint32_t(32 * q) << 16, a = tmem + kACol + uint32_t(s * kABufs + grp) * kACols;
     const int n_blk = MT == 2 ? p.n_kb : (p.n_kb + 1 - s) / 2;  // steps of a unit
     uint32_t wu = uint32_t(grp), a_use = 0, end = 0;            // the group's next step, counted over the units
-    for (int64_t u = blockIdx.x; u < n_units; u += gridDim.x) {
+    uint32_t x_use = 0, x_last = 0;                             // channel blocks before the unit; the one of the last step
+    for (int64_t u = blockIdx.x; u < n_units; u += gridDim.x, x_use += uint32_t(p.n_kb)) {
+      const uint32_t begin = end;
       end += uint32_t(n_blk);
       const bool on = unit(u).mt * (4 * MT) + (MT == 2 ? 4 * s : 0) + q < p.n_rb;
       for (; wu != end && wu != end + 1; wu += 2, ++a_use) {
-        const uint32_t slot = wu % kSlots;
+        const uint32_t slot = wu % kSlots, j = wu - begin;
         uint4 c[4];
         uint2 sc;
         wait(&sm.w_full[s][slot], wu / kSlots);
@@ -371,7 +373,10 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const Params p) {
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.w_empty[s][slot]);
         }
-        if (a_use > 0) wait(&sm.a_empty[s][grp], a_use - 1);
+        if (a_use > 0) {
+          wait(&sm.a_empty[s][grp], a_use - 1);
+          if (q == 0 && lane == 0) mbar_arrive(&sm.x_empty[x_last % kStages]);  // that block's products are done with x too
+        }
         __syncwarp();
         attn::tc_fence_after();
         if (on) {
@@ -395,6 +400,8 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const Params p) {
           }
           asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
         }
+        x_last = x_use + uint32_t(MT == 2 ? j : 2 * j + s);
+        if (q == 0) wait(&sm.x_full[x_last % kStages], x_last / kStages);
         attn::tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.a_full[s][grp]);
