@@ -35,6 +35,7 @@ struct Params {
   const float *logits, *bias;
   const int32_t* active;
   int m, E, k, renorm, tokens;  // tokens: of a block
+  uint32_t magic;               // token_of
   float scale;
   int32_t *experts, *offsets, *src, *pos;
   float* weights;
@@ -102,11 +103,15 @@ __device__ __forceinline__ void choose(const Params& p, int t, int lane) {
   }
 }
 
+// The token of entry i of a block, i / k: with magic = ceil(2^32 / k) exact while i (k - 1) < 2^32.
+__device__ __forceinline__ int token_of(const Params& p, int i) { return p.k == 1 ? i : int(__umulhi(uint32_t(i), p.magic)); }
+
 // The block's masks from the experts chosen for its tokens; words and experts lie `word` and `expert` apart.
+template <int kBlock>
 __device__ __forceinline__ void set_masks(const Params& p, uint32_t* mask, int t0, int t1, int word, int expert) {
 #pragma unroll 4
-  for (int i = threadIdx.x; i < (t1 - t0) * p.k; i += kThreads) {
-    const int t = i / p.k, e = p.experts[int64_t(t0) * p.k + i];
+  for (int i = threadIdx.x; i < (t1 - t0) * p.k; i += kBlock) {
+    const int t = token_of(p, i), e = p.experts[int64_t(t0) * p.k + i];
     if (e >= 0) atomicOr(&mask[e * expert + (t >> 5) * word], 1u << (t & 31));
   }
 }
@@ -123,20 +128,21 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const Params p) {
 // The lists by one cluster: a CTA takes p.tokens neighbouring tokens, and learns the others' counts through distributed
 // shared memory.  kChoose: chooses for them too.
 template <int NE, bool kChoose>
-__global__ void __launch_bounds__(kThreads) list_kernel(const Params p, int C) {
+__global__ void __launch_bounds__(kChoose ? kThreads : 1024) list_kernel(const Params p, int C) {
+  constexpr int kBlock = kChoose ? kThreads : 1024;
   extern __shared__ uint32_t mask[];  // [words][E], then the bits before each word
   __shared__ uint32_t count[kMaxE], base[kMaxE], tmp[32];
   pdl_wait();
   pdl_trigger();
   const int rank = int(blockIdx.x), t0 = min(p.m, rank * p.tokens), t1 = min(p.m, t0 + p.tokens), words = (p.tokens + 31) / 32;
   uint16_t* ahead = reinterpret_cast<uint16_t*>(mask + p.E * words);
-  for (int i = threadIdx.x; i < p.E * words; i += kThreads) mask[i] = 0u;
+  for (int i = threadIdx.x; i < p.E * words; i += kBlock) mask[i] = 0u;
   if (kChoose)
     for (int t = t0 + int(threadIdx.x >> 5); t < t1; t += kWarps) choose<NE>(p, t, int(threadIdx.x & 31));
   __syncthreads();
-  set_masks(p, mask, t0, t1, p.E, 1);
+  set_masks<kBlock>(p, mask, t0, t1, p.E, 1);
   __syncthreads();
-  for (int e = threadIdx.x; e < p.E; e += kThreads) {
+  for (int e = threadIdx.x; e < p.E; e += kBlock) {
     uint32_t n = 0;
 #pragma unroll 4
     for (int w = 0; w < words; ++w) {
@@ -148,7 +154,7 @@ __global__ void __launch_bounds__(kThreads) list_kernel(const Params p, int C) {
   if (C > 1) cluster_arrive(), cluster_wait();
   __syncthreads();
   uint32_t listed = 0;
-  for (int e0 = 0; e0 < p.E; e0 += kThreads) {
+  for (int e0 = 0; e0 < p.E; e0 += kBlock) {
     const int e = e0 + int(threadIdx.x);
     uint32_t all = 0, before = 0;
     if (e < p.E) {
@@ -174,8 +180,8 @@ __global__ void __launch_bounds__(kThreads) list_kernel(const Params p, int C) {
   __syncthreads();
   if (C > 1) cluster_arrive();  // the others' counts are read
 #pragma unroll 4
-  for (int i = threadIdx.x; i < (t1 - t0) * p.k; i += kThreads) {
-    const int t = i / p.k, e = p.experts[int64_t(t0) * p.k + i];
+  for (int i = threadIdx.x; i < (t1 - t0) * p.k; i += kBlock) {
+    const int t = token_of(p, i), e = p.experts[int64_t(t0) * p.k + i];
     int at = -1;
     if (e >= 0) {
       const int w = (t >> 5) * p.E + e;
@@ -184,7 +190,7 @@ __global__ void __launch_bounds__(kThreads) list_kernel(const Params p, int C) {
     }
     p.pos[int64_t(t0) * p.k + i] = at;
   }
-  for (int64_t i = int64_t(listed) + rank * kThreads + threadIdx.x; i < int64_t(p.m) * p.k; i += C * kThreads) p.src[i] = -1;
+  for (int64_t i = int64_t(listed) + rank * kBlock + threadIdx.x; i < int64_t(p.m) * p.k; i += C * kBlock) p.src[i] = -1;
   if (C > 1) cluster_wait();
 }
 
@@ -198,7 +204,7 @@ __global__ void __launch_bounds__(kThreads) count_kernel(const Params p) {
   for (int i = threadIdx.x; i < p.E * words; i += kThreads) mask[i] = 0u;
   for (int t = t0 + int(threadIdx.x >> 5); t < t1; t += kWarps) choose<NE>(p, t, int(threadIdx.x & 31));
   __syncthreads();
-  set_masks(p, mask, t0, t1, 1, words);
+  set_masks<kThreads>(p, mask, t0, t1, 1, words);
   __syncthreads();
   for (int e = threadIdx.x; e < p.E; e += kThreads) {
     uint32_t n = 0;
@@ -216,7 +222,7 @@ __global__ void __launch_bounds__(kThreads) order_kernel(const Params p) {
   const int t0 = int(blockIdx.x) * p.tokens, t1 = min(p.m, t0 + p.tokens), words = p.tokens / 32;
   for (int i = threadIdx.x; i < p.E * words; i += kThreads) mask[i] = 0u;
   __syncthreads();
-  set_masks(p, mask, t0, t1, 1, words);
+  set_masks<kThreads>(p, mask, t0, t1, 1, words);
   __syncthreads();
   uint32_t listed = 0;
   for (int e0 = 0; e0 < p.E; e0 += kThreads) {
@@ -241,7 +247,7 @@ __global__ void __launch_bounds__(kThreads) order_kernel(const Params p) {
   if (blockIdx.x == 0 && threadIdx.x == 0) p.offsets[p.E] = int(listed);
   __syncthreads();
   for (int i = threadIdx.x; i < (t1 - t0) * p.k; i += kThreads) {
-    const int t = i / p.k, e = p.experts[int64_t(t0) * p.k + i];
+    const int t = token_of(p, i), e = p.experts[int64_t(t0) * p.k + i];
     int at = -1;
     if (e >= 0) {
       uint32_t n = base[e];
@@ -267,7 +273,7 @@ cudaError_t lists(Params p, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(C));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kChoose ? kThreads : 1024);
   cfg.dynamicSmemBytes = mask_bytes(p.m, p.E, C);
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
@@ -443,6 +449,7 @@ extern "C" csa2_status csa2_expert_route(const float* logits, int m, int E, int 
   p.logits = logits, p.bias = bias, p.active = active, p.m = m, p.E = E, p.k = k, p.renorm = renorm, p.scale = scale;
   p.experts = experts, p.weights = weights, p.offsets = offsets, p.src = src, p.pos = pos;
   p.counts = static_cast<uint32_t*>(ws);
+  p.magic = uint32_t(((int64_t(1) << 32) + k - 1) / k);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const int ne = (E + 31) / 32;
   const cudaError_t e = ne <= 1 ? route<1>(p, st) : ne <= 2 ? route<2>(p, st) : ne <= 4 ? route<4>(p, st)
