@@ -9,8 +9,8 @@
 //
 // mma.m16n8k16 on bf16 as it lies in memory.  Channels are handed to the MMA in an order that lets a lane load 16
 // neighbouring bytes: the same for both operands, so that the sum over the channels does not change.  t = A x is fp32
-// and enters the second product as two bf16 terms (off by 2^-17 of it at most); all sums are fp32, and out is rounded
-// once.
+// and enters the second product as two bf16 terms (off by 2^-17 of it at most, where out is rounded to 2^-8), or as three
+// where out is fp32 (2^-25); all sums are fp32, and out is rounded once.
 //
 // Bound: for few rows the adapters' bytes, each once, and the chain load, sum, exchange, load, store; for many rows x
 // and base read and out written.
@@ -25,7 +25,6 @@ namespace lora {
 
 constexpr int kThreads = 256, kWarps = 8, kMaxCluster = 8;
 constexpr int kWindow = 8192, kBuckets = 255;
-constexpr int kStages = 4;  // of a ring of 128-byte rows (64 rows): x and A, then base and B
 static_assert(kBuckets < kThreads && kBuckets < 256, "a thread per bucket; a byte holds one, or none");
 
 struct Params {
@@ -51,15 +50,17 @@ __device__ __forceinline__ uint32_t bf2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-template <int NR, int WM>
+template <int NR, int WM, bool kF32>
 struct Shape {
+  static constexpr int kTerms = kF32 ? 3 : 2;
+  static constexpr int kStages = kF32 ? 3 : 4;  // of a ring of 128-byte rows (64 rows): x and A, then base and B
   static constexpr int WK = kWarps / WM, TM = 16 * WM, R = 8 * NR, kPitch = R + 8;
   static constexpr bool kStaged = WM > 1;
   static constexpr size_t kStage = size_t(TM + R) * 128;
   static constexpr size_t kPart = size_t(WK) * TM * R * 4;   // the warps' sums; staged: in the ring's place
   static constexpr size_t kFirst = kStaged ? kStages * kStage : kPart;
   static constexpr size_t kSums = kStaged ? size_t(TM) * R * 4 : 0;  // this CTA's; else in the place of the first warp's
-  static constexpr size_t kSmem = kFirst + kSums + size_t(2) * TM * kPitch * 2;
+  static constexpr size_t kSmem = kFirst + kSums + size_t(kTerms) * TM * kPitch * 2;
   static_assert(kPart <= kFirst, "shared memory");
 };
 // where 16-byte piece j of a 128-byte row lies: eight lanes that read four pieces of two rows miss each other
@@ -69,13 +70,13 @@ __device__ __forceinline__ uint32_t piece_at(int row, int j) { return uint32_t(r
 // kF32: base and out are fp32; kVec: rows of out are whole 16-byte pieces.
 template <int NR, int WM, bool kF32, bool kVec>
 __global__ void __launch_bounds__(kThreads, NR <= 8 ? 2 : 1) lora_kernel(const Params p, int C) {
-  using S = Shape<NR, WM>;
+  using S = Shape<NR, WM, kF32>;
+  constexpr int kTerms = S::kTerms, kStages = S::kStages;
   constexpr int WK = S::WK, TM = S::TM, R = S::R, kPitch = S::kPitch;
   extern __shared__ __align__(16) unsigned char smem[];
   float* part = reinterpret_cast<float*>(smem);                                   // [WK][TM][R]
   float* sums = reinterpret_cast<float*>(smem + (S::kStaged ? S::kFirst : 0));    // [TM][R]
-  uint16_t* hi = reinterpret_cast<uint16_t*>(smem + S::kFirst + S::kSums);        // [TM][kPitch], channels in the MMA's order
-  uint16_t* lo = hi + TM * kPitch;
+  uint16_t* terms = reinterpret_cast<uint16_t*>(smem + S::kFirst + S::kSums);     // [kTerms][TM][kPitch], in the MMA's order
   __shared__ uint8_t bucket[kWindow];  // of the window's rows; kBuckets: no adapter
   __shared__ int count[kThreads], start[kBuckets + 1], seg[kWarps];
   __shared__ int rows[TM], which[TM], list[TM];
@@ -336,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, NR <= 8 ? 2 : 1) lora_kernel(const P
     if (!kRing && kAhead && blk0 < n_blk) load(blk0);
     if (C > 1) cluster_arrive(), cluster_wait();
     else __syncthreads();
-    // the cluster's sums, scaled, as two bf16 terms
+    // the cluster's sums, scaled, as bf16 terms
     const float scale = p.scale ? p.scale[l] : 1.f;
     for (int e = tid; e < TM * R / 4; e += kThreads) {
       float4 v;
@@ -360,28 +361,29 @@ __global__ void __launch_bounds__(kThreads, NR <= 8 ? 2 : 1) lora_kernel(const P
         if (rr + 2 >= n_rank) v.z = 0.f;
         v.w = 0.f;
       }
-      const uint32_t h0 = bf2(v.x, v.y), h1 = bf2(v.z, v.w);
-      const uint32_t l0 = bf2(v.x - bf16lo(h0), v.y - bf16hi(h0)), l1 = bf2(v.z - bf16lo(h1), v.w - bf16hi(h1));
       // four neighbouring ranks are a lane's of one step: places 2q, 2q + 1, 2q + 8, 2q + 9.  With 32 ranks and more a
       // lane has eight neighbouring ones, the first four of one step, the others of the next
       int step, q;
       if (R >= 32) step = rr / 32 * 2 + (rr % 8) / 4, q = rr % 32 / 8;
       else step = 0, q = rr / 4;
-      uint16_t* at_h = hi + row * kPitch + step * 16 + 2 * q;
-      uint16_t* at_l = lo + row * kPitch + step * 16 + 2 * q;
-      *reinterpret_cast<uint32_t*>(at_h) = h0, *reinterpret_cast<uint32_t*>(at_h + 8) = h1;
-      *reinterpret_cast<uint32_t*>(at_l) = l0, *reinterpret_cast<uint32_t*>(at_l + 8) = l1;
+      uint16_t* at = terms + row * kPitch + step * 16 + 2 * q;
+#pragma unroll
+      for (int term = 0; term < kTerms; ++term, at += TM * kPitch) {  // each what the ones before leave
+        const uint32_t a0 = bf2(v.x, v.y), a1 = bf2(v.z, v.w);
+        v.x -= bf16lo(a0), v.y -= bf16hi(a0), v.z -= bf16lo(a1), v.w -= bf16hi(a1);
+        *reinterpret_cast<uint32_t*>(at) = a0, *reinterpret_cast<uint32_t*>(at + 8) = a1;
+      }
     }
     __syncthreads();
     if (C > 1) cluster_arrive();
     if constexpr (kRing) {
-      uint32_t f[2][R / 16][4];  // t of this warp's rows
+      uint32_t f[kTerms][R / 16][4];  // t of this warp's rows
 #pragma unroll
       for (int k = 0; k < R / 16; ++k)
 #pragma unroll
-        for (int term = 0; term < 2; ++term)
+        for (int term = 0; term < kTerms; ++term)
           ldmatrix_x4(f[term][k][0], f[term][k][1], f[term][k][2], f[term][k][3],
-                      smem_u32((term ? lo : hi) + (16 * wm + (lane & 15)) * kPitch + 16 * k + 8 * (lane >> 4)));
+                      smem_u32(terms + (term * TM + 16 * wm + (lane & 15)) * kPitch + 16 * k + 8 * (lane >> 4)));
       const int64_t row0 = rows[16 * wm + g], row1 = rows[16 * wm + 8 + g];
       const bool use0 = which[16 * wm + g] == l, use1 = which[16 * wm + 8 + g] == l;
       for (int i = 0; i < q1 - q0; ++i) {
@@ -421,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, NR <= 8 ? 2 : 1) lora_kernel(const P
 #pragma unroll
           for (int k = 0; k < R / 16; ++k)
 #pragma unroll
-            for (int term = 0; term < 2; ++term)
+            for (int term = 0; term < kTerms; ++term)
               mma(d[j], f[term][k][0], f[term][k][1], f[term][k][2], f[term][k][3], bv[k][0], bv[k][1]);
         }
         const int n = (q0 + i) * kCols + wk * (8 * J) + 2 * J * t;
@@ -471,8 +473,8 @@ __global__ void __launch_bounds__(kThreads, NR <= 8 ? 2 : 1) lora_kernel(const P
 #pragma unroll
         for (int k = 0; k < R / 16; ++k)
 #pragma unroll
-          for (int term = 0; term < 2; ++term) {
-            const uint16_t* src = (term ? lo : hi) + (16 * i + (lane & 15)) * kPitch + 16 * k + 8 * (lane >> 4);
+          for (int term = 0; term < kTerms; ++term) {
+            const uint16_t* src = terms + (term * TM + 16 * i + (lane & 15)) * kPitch + 16 * k + 8 * (lane >> 4);
             uint32_t f[4];
             ldmatrix_x4(f[0], f[1], f[2], f[3], smem_u32(src));
 #pragma unroll
@@ -545,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, NR <= 8 ? 2 : 1) lora_kernel(const P
 template <int NR, int WM, bool kF32, bool kVec>
 cudaError_t launch(const Params& p, int C, int clusters, cudaStream_t st) {
   auto kern = lora_kernel<NR, WM, kF32, kVec>;
-  constexpr size_t smem = Shape<NR, WM>::kSmem;
+  constexpr size_t smem = Shape<NR, WM, kF32>::kSmem;
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem, done);
   if (e != cudaSuccess) return e;

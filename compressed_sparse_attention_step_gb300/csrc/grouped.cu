@@ -264,6 +264,10 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const Params p) {
   const uint32_t tmem = sm.tmem;
   const int64_t n_units = int64_t(tiles) * p.n_mt;
 
+  // The place of x of a pipeline's step among the stages, both counted over the units.  A stage belongs to one group of
+  // dequantising warps, or to the two (one of each pipeline) that take the same blocks: whoever waits for its n-th filling
+  // has waited for the one before, and does not take that for it.
+  auto x_of = [](uint32_t step, int s) { return MT == 2 ? step : 2 * step + uint32_t(s); };
   // Unit u: neighbouring units share their rows of x.
   auto unit = [&](int64_t u) {
     const int tile = int(u / p.n_mt);
@@ -284,15 +288,15 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const Params p) {
     const int s = warp;
     const uint32_t d = tmem + uint32_t(s) * kDCols, a0 = tmem + kACol + uint32_t(s) * (kABufs * kACols);
     const uint64_t x0 = attn::smem_desc(smem_u32(smem), 0, 1024);
-    uint32_t a_use = 0, x_use = 0, i = 0;
-    for (int64_t u = blockIdx.x; u < n_units; u += gridDim.x, ++i, x_use += uint32_t(p.n_kb)) {
+    uint32_t a_use = 0, i = 0;
+    for (int64_t u = blockIdx.x; u < n_units; u += gridDim.x, ++i) {
       const Unit un = unit(u);
       const uint32_t idesc = attn::instr_desc(128, false, false, (un.n + 15) / 16 * 16);
       if (i > 0) wait(&sm.d_empty[s], i - 1);
       attn::tc_fence_after();
       bool first = true;
       for (int k = MT == 2 ? 0 : s; k < p.n_kb; k += MT == 2 ? 1 : 2, first = false, ++a_use) {
-        const uint32_t stage = (x_use + uint32_t(k)) % kStages, buf = a_use % kABufs;
+        const uint32_t stage = x_of(a_use, s) % kStages, buf = a_use % kABufs;
         wait(&sm.a_full[s][buf], a_use / kABufs);  // and x: the dequantising warps have waited for it
         __syncwarp();
         attn::tc_fence_after();
@@ -309,24 +313,28 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const Params p) {
     // x: a channel block of the unit's rows as two groups of 64 channels, each [kTile rows][128 bytes].  Rows past the
     // unit's last are left as they are: they reach their own columns of the sums alone.
     asm volatile("fence.proxy.async.global;\n" ::: "memory");
-    uint32_t xu = 0, begun = 0;
+    uint32_t steps[2] = {0, 0};  // of each pipeline; with two row tiles [0] counts for both
     for (int64_t u = blockIdx.x; u < n_units; u += gridDim.x) {
       const Unit un = unit(u);
       const uint32_t bytes = uint32_t(un.n) * 128u;
       const unsigned char* src = p.xs + int64_t(un.r0) * p.n_kb * (kChan * 2) + lane * bytes;
-      for (int k = 0; k < p.n_kb; ++k, ++xu, src += 2 * bytes) {
-        const uint32_t stage = xu % kStages;
+      for (int k = 0; k < p.n_kb; ++k, src += 2 * bytes) {
+        const int s = MT == 2 ? 0 : k & 1;
+        const uint32_t xu = x_of(steps[s], s), stage = xu % kStages;
         if (xu >= kStages) wait(&sm.x_empty[stage], xu / kStages - 1);
         late = __any_sync(0xffffffffu, late);
         if (late) continue;  // no more copies
         if (lane == 0) mbar_expect(&sm.x_full[stage], 2 * bytes);
         __syncwarp();
-        ++begun;
+        ++steps[s];
         if (lane < 2) bulk_copy(smem_u32(smem) + stage * kStage + uint32_t(lane) * (kTile * 128), src, bytes, &sm.x_full[stage]);
       }
     }
-    // no CTA leaves with a copy under way, even if nobody waits for it
-    for (uint32_t b = begun > kStages ? begun - kStages : 0; b < begun; ++b) bar_wait(smem_u32(&sm.x_full[b % kStages]), (b / kStages) & 1u);
+    // no CTA leaves with a copy under way, even if nobody waits for it: the last filling of every stage
+    constexpr uint32_t kOwn = MT == 2 ? kStages : kStages / 2;  // stages of a pipeline
+    for (int s = 0; s < 3 - MT; ++s)
+      for (uint32_t b = steps[s] > kOwn ? steps[s] - kOwn : 0; b < steps[s]; ++b)
+        if (!bar_wait(smem_u32(&sm.x_full[x_of(b, s) % kStages]), (x_of(b, s) / kStages) & 1u)) atomicOr(p.flags, CSA2_FLAG_TIMEOUT);
   } else if (warp < kWarpDeq) {
     // the weight: a step is the channel block of a pipeline's four row blocks, of which the last may not be there
     const int s = warp - kWarpCopy;
@@ -348,19 +356,18 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const Params p) {
         if (lane < n) bulk_copy(smem_u32(sm.ring[s][slot][lane]), src, kBlock, &sm.w_full[s][slot]);
       }
     }
-    for (uint32_t b = begun > kSlots ? begun - kSlots : 0; b < begun; ++b) bar_wait(smem_u32(&sm.w_full[s][b % kSlots]), (b / kSlots) & 1u);
+    for (uint32_t b = begun > kSlots ? begun - kSlots : 0; b < begun; ++b)
+      if (!bar_wait(smem_u32(&sm.w_full[s][b % kSlots]), (b / kSlots) & 1u)) atomicOr(p.flags, CSA2_FLAG_TIMEOUT);
   } else if (warp < kWarpEpi) {
     const int s = (warp - kWarpDeq) >> 3, grp = ((warp - kWarpDeq) >> 2) & 1;  // a group takes every other step
     const uint32_t lanes = uint32_t(32 * q) << 16, a = tmem + kACol + uint32_t(s * kABufs + grp) * kACols;
     const int n_blk = MT == 2 ? p.n_kb : (p.n_kb + 1 - s) / 2;  // steps of a unit
     uint32_t wu = uint32_t(grp), a_use = 0, end = 0;            // the group's next step, counted over the units
-    uint32_t x_use = 0, x_last = 0;                             // channel blocks before the unit; the one of the last step
-    for (int64_t u = blockIdx.x; u < n_units; u += gridDim.x, x_use += uint32_t(p.n_kb)) {
-      const uint32_t begin = end;
+    for (int64_t u = blockIdx.x; u < n_units; u += gridDim.x) {
       end += uint32_t(n_blk);
       const bool on = unit(u).mt * (4 * MT) + (MT == 2 ? 4 * s : 0) + q < p.n_rb;
       for (; wu != end && wu != end + 1; wu += 2, ++a_use) {
-        const uint32_t slot = wu % kSlots, j = wu - begin;
+        const uint32_t slot = wu % kSlots, xu = x_of(wu, s);
         uint4 c[4];
         uint2 sc;
         wait(&sm.w_full[s][slot], wu / kSlots);
@@ -375,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const Params p) {
         }
         if (a_use > 0) {
           wait(&sm.a_empty[s][grp], a_use - 1);
-          if (q == 0 && lane == 0) mbar_arrive(&sm.x_empty[x_last % kStages]);  // that block's products are done with x too
+          if (q == 0 && lane == 0) mbar_arrive(&sm.x_empty[x_of(wu - 2, s) % kStages]);  // that block's products are done with x too
         }
         __syncwarp();
         attn::tc_fence_after();
@@ -400,8 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const Params p) {
           }
           asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
         }
-        x_last = x_use + uint32_t(MT == 2 ? j : 2 * j + s);
-        if (q == 0) wait(&sm.x_full[x_last % kStages], x_last / kStages);
+        if (q == 0) wait(&sm.x_full[xu % kStages], xu / kStages);
         attn::tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.a_full[s][grp]);

@@ -73,8 +73,9 @@ def rounded(exact, tol, bf16):
     return tol + (np.abs(exact) + tol) * (HBF if bf16 else H32) + 2.0 ** -133
 
 
-def adapters(x, a, b, adapter, base, ranks=None, scale=None):
-    """(exact, tolerance before the last rounding), all float64 but adapter and ranks."""
+def adapters(x, a, b, adapter, base, ranks=None, scale=None, split=2.0 ** -16):
+    """(exact, tolerance before the last rounding), all float64 but adapter and ranks; split: how far t may be off that
+    enters the second product, in two bf16 terms."""
     m, K = x.shape
     L, r, _ = a.shape
     out, tol = base.copy(), np.zeros_like(base)
@@ -86,8 +87,8 @@ def adapters(x, a, b, adapter, base, ranks=None, scale=None):
         s = 1.0 if scale is None else float(scale[l])
         al, bl = a[l, :n], b[l, :, :n]
         t = (al @ x[i]) * s
-        # K / 16 accumulations of the first product, its sums over warps and CTAs, the scale; two bf16 terms
-        et = (np.abs(al) @ np.abs(x[i])) * abs(s) * (-(-K // 16) + 24) * ACC + np.abs(t) * 2.0 ** -16
+        # K / 16 accumulations of the first product, its sums over warps and CTAs, the scale; t as bf16 terms
+        et = (np.abs(al) @ np.abs(x[i])) * abs(s) * (-(-K // 16) + 24) * ACC + np.abs(t) * split
         delta = bl @ t
         out[i] = base[i] + delta
         tol[i] = np.abs(bl) @ et + (np.abs(bl) @ (np.abs(t) + et)) * (-(-r // 16) * 2 + 4) * ACC + np.abs(out[i]) * 2 * H32

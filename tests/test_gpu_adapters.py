@@ -49,7 +49,8 @@ def test_adapters(m, n_in, n_out, r, L, fp32, order):
     args = (bf16_dev(x), ad, bd, to_dev(adapter), base)
     kw = dict(ranks=None if ranks is None else to_dev(ranks), scale=None if scale is None else to_dev(scale))
     c.csa2_lora_add(*args, out, **kw)
-    exact, tol = P.adapters(V.f64(x), V.f64(a), V.f64(b), adapter, host(base), ranks, scale)
+    exact, tol = P.adapters(V.f64(x), V.f64(a), V.f64(b), adapter, host(base), ranks, scale,
+                            split=2.0 ** -24 if fp32 else 2.0 ** -16)   # fp32: three terms
     err = np.abs(host(out) - exact)
     tol = P.rounded(exact, tol, not fp32)
     assert (err <= tol).all(), f"{np.max(err - tol):.3e} over the bound"

@@ -110,6 +110,7 @@ def run_grouped(seed, counts, n_in, n_out, act=False, fp32=False, n_x=None, idle
     before = y.clone()
     c.csa2_fp4_grouped(bf16_dev(xb), packed, to_dev(offsets), y, src=to_dev(src), row_scale=None if rs is None else to_dev(rs),
                        act=c.ACT_SWIGLU if act else c.ACT_NONE)
+    assert c.csa2_device_flags() == 0   # no wait ran out
     check_grouped(y, V.f64(xb), w, None if rs is None else rs.astype(np.float64), offsets, src, act, before)
 
 
@@ -123,6 +124,15 @@ def run_grouped(seed, counts, n_in, n_out, act=False, fp32=False, n_x=None, idle
 def test_grouped(counts, n_in, n_out, act, fp32):
     run_grouped(sum(counts) + n_in, counts, n_in, n_out, act, fp32, n_x=sum(counts) // 2 + 3, idle=4, lead=sum(counts) % 3,
                 with_rs=n_in != 512)
+
+
+@pytest.mark.parametrize("counts,n_in,n_out", [
+    ([1250, 1250, 1250], 320, 970), ([14] * 24, 320, 794), ([300, 0, 280, 290, 5], 656, 1074), ([900, 300, 1300, 9], 304, 170),
+    ([1000], 384, 2000), ([16] * 120, 112, 1000), ([700, 700], 256, 1026),
+])
+def test_grouped_many_units(counts, n_in, n_out):
+    """More units than CTAs, odd and even numbers of channel blocks: buffers go round over the ends of units."""
+    run_grouped(n_in + len(counts), counts, n_in, n_out, n_out % 4 == 2, n_in % 256 == 0)
 
 
 def test_grouped_scales_of_x():
