@@ -212,6 +212,9 @@ __global__ void __launch_bounds__(kThreads, NR <= 8 ? 2 : 1) lora_kernel(const P
         }
         cp_async_commit();
       };
+      float sum[NR][4];
+#pragma unroll
+      for (int j = 0; j < NR; ++j) sum[j][0] = sum[j][1] = sum[j][2] = sum[j][3] = 0.f;
       for (int i = 0; i < kStages - 1; ++i) ask(i);
       for (int i = 0; i < n; ++i) {
         cp_async_wait<kStages - 2>();
@@ -224,6 +227,20 @@ __global__ void __launch_bounds__(kThreads, NR <= 8 ? 2 : 1) lora_kernel(const P
 #pragma unroll
         for (int j = 0; j < NR; ++j) av[j] = *reinterpret_cast<const uint4*>(at + TM * 128 + piece_at(8 * j + g, 4 * wk + t));
         multiply(xv, av);
+        // An MMA cuts its sum off, so that the error grows with the number of MMAs one after the other: where out is fp32
+        // they are 16 (one chain over 64 steps: 1.1e-6 of the result, chains of eight steps 3e-7)
+        if (kF32 && (i & 7) == 7) {
+#pragma unroll
+          for (int j = 0; j < NR; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[j][e] += acc[j][e], acc[j][e] = 0.f;
+        }
+      }
+      if (kF32) {
+#pragma unroll
+        for (int j = 0; j < NR; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[j][e] += sum[j][e];
       }
       cp_async_wait<0>();
       __syncthreads();

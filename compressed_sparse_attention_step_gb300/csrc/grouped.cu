@@ -557,7 +557,11 @@ extern "C" csa2_status csa2_fp4_grouped(const uint16_t* x, int64_t n_x, int64_t 
   // there are units enough.
   const int64_t used = std::min<int64_t>(rows, E), pairs = (p.n_rb + 7) / 8;
   cudaError_t e;
-  if (rows <= 16 * used) e = used * pairs >= 2 * sms ? launch<2, 32>(p, sms, st) : launch<1, 32>(p, sms, st);
-  else e = std::max(used, rows / kMaxTile) * pairs >= 2 * sms ? launch<2, 128>(p, sms, st) : launch<1, 128>(p, sms, st);
+  // An MMA cuts its sum off, so that the error grows with the number of MMAs one after the other: an fp32 y takes the
+  // form whose sums are in two halves (2528 channels and the activation: 4.6e-7 of the
+  // result, in one 1.1e-6).
+  const bool two = !y_fp32;
+  if (rows <= 16 * used) e = two && used * pairs >= 2 * sms ? launch<2, 32>(p, sms, st) : launch<1, 32>(p, sms, st);
+  else e = two && std::max(used, rows / kMaxTile) * pairs >= 2 * sms ? launch<2, 128>(p, sms, st) : launch<1, 128>(p, sms, st);
   return e == cudaSuccess ? CSA2_OK : CSA2_ERR_CUDA;
 }
