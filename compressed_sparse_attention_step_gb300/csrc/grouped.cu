@@ -24,8 +24,10 @@ constexpr int kRows = 32, kChan = 128;  // of a block of the packed weight (matv
 constexpr int kCodeBytes = kRows * kChan / 2;
 constexpr int kBlock = kCodeBytes + kRows * kChan / CSA2_GROUP;  // 2304 bytes
 
-constexpr int kMaxTile = 128;    // token rows of a unit, at most: 32 or 128 of them by the launch (kTile)
-constexpr int kXBytes = 128 * 1024;  // channel blocks of x under way: 16 of 32 rows, 4 of 128
+constexpr int kTile = 128;       // token rows of a unit, at most
+constexpr int kStages = 4;       // channel blocks of x under way
+constexpr int kStage = kTile * kChan * 2;
+constexpr int kFew = 8;          // token rows up to which a unit's products are mma.m16n8k16
 constexpr int kSlots = 4;        // steps of four weight blocks (128 outputs) under way per pipeline
 constexpr int kABufs = 2;        // dequantised blocks per pipeline
 // Two pipelines (s = 0, 1), each of a copying warp, two groups of four dequantising warps, a block in tensor memory for
@@ -35,23 +37,24 @@ constexpr int kABufs = 2;        // dequantised blocks per pipeline
 constexpr int kDequant = 8 * kABufs, kEpilogue = 4;
 constexpr int kIssuers = 2, kWarpX = 2, kWarpCopy = 3, kWarpDeq = 5, kWarpEpi = kWarpDeq + kDequant;
 constexpr int kThreads = (kWarpEpi + kEpilogue) * 32;
-constexpr uint32_t kACols = kChan / 2, kDCols = kMaxTile;
+constexpr uint32_t kACols = kChan / 2, kDCols = kTile;
 constexpr uint32_t kACol = 2 * kDCols;
 static_assert(kACol + 2 * kABufs * kACols <= 512, "tensor memory");
-static_assert(kThreads <= 1024, "warps");
+static_assert(kThreads <= 1024 && kABufs == 2, "warps; a buffer for each of two groups");
 
 struct Tail {
   alignas(16) unsigned char ring[2][kSlots][4][kBlock];
-  alignas(16) float inv[kMaxTile];
+  alignas(16) float inv[kTile];
+  alignas(16) float red[4][4][kFew][kRows];  // sums of a unit of few rows: [pipeline and group][row block][row of x][output]
   int off[CSA2_MAX_EXPERTS + 1];    // the experts' first rows, within [0, rows]
   int start[CSA2_MAX_EXPERTS + 1];  // their first token tiles
   uint32_t tmp[32];
   uint64_t w_full[2][kSlots], w_empty[2][kSlots];
-  uint64_t x_full[16], x_empty[16];
+  uint64_t x_full[kStages], x_empty[kStages];
   uint64_t a_full[2][kABufs], a_empty[2][kABufs], d_full, d_empty[2];
   uint32_t tmem;
 };
-constexpr size_t kSmem = size_t(kXBytes) + sizeof(Tail);
+constexpr size_t kSmem = size_t(kStages) * kStage + sizeof(Tail);
 static_assert(kSmem <= 227 * 1024, "shared memory");
 
 // Row r of expert rows [first, first + n): the first row and the rows of its tile.  The tiles of an expert are as few as
@@ -59,12 +62,12 @@ static_assert(kSmem <= 227 * 1024, "shared memory");
 struct Span16 {
   int r0, n;
 };
-__device__ __forceinline__ Span16 tile_of(int most, int first, int n, int tile) {
-  const int tiles = (n + most - 1) / most, per = ((n + tiles - 1) / tiles + 15) / 16 * 16, at = tile * per;
+__device__ __forceinline__ Span16 tile_of(int first, int n, int tile) {
+  const int tiles = (n + kTile - 1) / kTile, per = ((n + tiles - 1) / tiles + 15) / 16 * 16, at = tile * per;
   return Span16{first + at, min(per, n - at)};
 }
-__device__ __forceinline__ int tile_at(int most, int n, int r) {  // the tile of the r-th row of n
-  const int tiles = (n + most - 1) / most;
+__device__ __forceinline__ int tile_at(int n, int r) {  // the tile of the r-th row of n
+  const int tiles = (n + kTile - 1) / kTile;
   return r / (((n + tiles - 1) / tiles + 15) / 16 * 16);
 }
 
@@ -77,7 +80,7 @@ struct Params {
   const int32_t *offsets, *src;
   void* y;
   int64_t n_out, n_in, w_bytes, rows, n_x;
-  int E, n_kb, n_rb, n_mt, y_fp32, act, tile;
+  int E, n_kb, n_rb, n_mt, y_fp32, act;
   unsigned int* flags;
 };
 
@@ -94,8 +97,8 @@ __device__ __forceinline__ void mbar_expect(uint64_t* bar, uint32_t bytes) {  //
 __device__ __forceinline__ void mbar_init(uint64_t* b, int n) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(smem_u32(b)), "r"(n) : "memory");
 }
-__device__ __forceinline__ void mbar_arrive(uint64_t* b) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_u32(b)) : "memory");
+__device__ __forceinline__ void mbar_arrive(uint64_t* b, uint32_t n = 1) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;\n" ::"r"(smem_u32(b)), "r"(n) : "memory");
 }
 // D (+)= A B with A in tensor memory; called by a whole warp, issued by one lane (the same each time)
 __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
@@ -124,6 +127,12 @@ __device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t (&r)[32]) {
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+__device__ __forceinline__ void tmem_st8(uint32_t a, const float (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"r"(a),
+               "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3])),
+               "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])), "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7]))
+               : "memory");
+}
 __device__ __forceinline__ void tmem_ld8(uint32_t a, uint32_t (&r)[8]) {  // valid after tcgen05.wait::ld
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
@@ -134,6 +143,13 @@ __device__ __forceinline__ void tmem_ld8(uint32_t a, uint32_t (&r)[8]) {  // val
 __device__ __forceinline__ float tmem_value(uint32_t& r) {
   asm volatile("" : "+r"(r));
   return __uint_as_float(r);
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 // off by a few 2^-22 of it: the exponent's rounding, the hardware's exponential, sum and quotient
 __device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.f + attn::ex2(v * -1.4426950408889634f)); }
@@ -156,7 +172,7 @@ __global__ void __launch_bounds__(128) scale_kernel(const Params p) {
   }
   if (r < off[lo] || r >= off[lo + 1]) return;
   const int n_e = off[lo + 1] - off[lo];
-  const Span16 tile = tile_of(p.tile, off[lo], n_e, tile_at(p.tile, n_e, r - off[lo]));
+  const Span16 tile = tile_of(off[lo], n_e, tile_at(n_e, r - off[lo]));
   const int i = r - tile.r0;
   const int64_t from = p.src ? int64_t(p.src[r]) : row;
   const bool on = from >= 0 && from < p.n_x;
@@ -212,12 +228,10 @@ struct Unit {
   int e, r0, n, mt;  // expert, first row, rows, row tile of the weight
 };
 
-template <int MT, int kTile>
+template <int MT>
 __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const Params p) {
-  constexpr int kStage = kTile * kChan * 2, kStages = kXBytes / kStage;
-  static_assert(kStages <= 16 && kTile <= kMaxTile, "barriers and columns");
   extern __shared__ __align__(1024) unsigned char smem[];
-  Tail& sm = *reinterpret_cast<Tail*>(smem + kXBytes);
+  Tail& sm = *reinterpret_cast<Tail*>(smem + kStages * kStage);
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, q = warp & 3;
@@ -231,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const Params p) {
   };
 
   if (tid == 0) {
-    for (int i = 0; i < kStages; ++i) mbar_init(&sm.x_full[i], 1), mbar_init(&sm.x_empty[i], MT);
+    for (int i = 0; i < kStages; ++i) mbar_init(&sm.x_full[i], 1), mbar_init(&sm.x_empty[i], 4 * MT);
     for (int s = 0; s < 2; ++s) {
       for (int i = 0; i < kABufs; ++i) mbar_init(&sm.a_full[s][i], 4), mbar_init(&sm.a_empty[s][i], 1);
       mbar_init(&sm.d_empty[s], kEpilogue);
@@ -277,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const Params p) {
       if (sm.start[mid] <= tile) lo = mid;
       else hi = mid;
     }
-    const Span16 rows = tile_of(kTile, sm.off[lo], sm.off[lo + 1] - sm.off[lo], tile - sm.start[lo]);
+    const Span16 rows = tile_of(sm.off[lo], sm.off[lo + 1] - sm.off[lo], tile - sm.start[lo]);
     return Unit{lo, rows.r0, rows.n, int(u - int64_t(tile) * p.n_mt)};
   };
 
@@ -288,23 +302,38 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const Params p) {
     const int s = warp;
     const uint32_t d = tmem + uint32_t(s) * kDCols, a0 = tmem + kACol + uint32_t(s) * (kABufs * kACols);
     const uint64_t x0 = attn::smem_desc(smem_u32(smem), 0, 1024);
-    uint32_t a_use = 0, i = 0;
+    const int n_blk = MT == 2 ? p.n_kb : (p.n_kb + 1 - s) / 2;  // steps of a unit
+    uint32_t step = 0, use0 = 0, use1 = 0, i = 0;               // steps over the units; uses of the two buffers
     for (int64_t u = blockIdx.x; u < n_units; u += gridDim.x, ++i) {
       const Unit un = unit(u);
+      if (un.n <= kFew) {  // no MMAs: passes on that the sums are in shared memory, and then that they have been read
+        step += uint32_t(n_blk);
+        if (i > 0) wait(&sm.d_empty[s], i - 1);
+        wait(&sm.a_full[s][0], use0++);
+        wait(&sm.a_full[s][1], use1++);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.d_full);
+        wait(&sm.d_empty[s], i);
+        __syncwarp();
+        if (lane == 0)
+          for (int b = 0; b < kABufs; ++b) mbar_arrive(&sm.a_empty[s][b]);
+        continue;
+      }
       const uint32_t idesc = attn::instr_desc(128, false, false, (un.n + 15) / 16 * 16);
       if (i > 0) wait(&sm.d_empty[s], i - 1);
       attn::tc_fence_after();
       bool first = true;
-      for (int k = MT == 2 ? 0 : s; k < p.n_kb; k += MT == 2 ? 1 : 2, first = false, ++a_use) {
-        const uint32_t stage = x_of(a_use, s) % kStages, buf = a_use % kABufs;
-        wait(&sm.a_full[s][buf], a_use / kABufs);  // and x: the dequantising warps have waited for it
+      for (int j = 0; j < n_blk; ++j, first = false, ++step) {
+        const uint32_t stage = x_of(step, s) % kStages, buf = step % kABufs;
+        wait(&sm.a_full[s][buf], buf ? use1 : use0);  // and x: the dequantising warps have waited for it
+        buf ? ++use1 : ++use0;
         __syncwarp();
         attn::tc_fence_after();
         const uint64_t xk = x0 + uint64_t(stage * (kStage / 16));
         const uint32_t a = a0 + buf * kACols;
 #pragma unroll
-        for (uint32_t j = 0; j < kChan / 16; ++j)
-          umma_ts(d, a + j * 8u, xk + uint64_t((j >> 2) * (kTile * 128 / 16) + (j & 3u) * 2u), idesc, !first || j > 0);
+        for (uint32_t c = 0; c < kChan / 16; ++c)
+          umma_ts(d, a + c * 8u, xk + uint64_t((c >> 2) * (kTile * 128 / 16) + (c & 3u) * 2u), idesc, !first || c > 0);
         commit_one(&sm.a_empty[s][buf]);
       }
       commit_one(&sm.d_full);
@@ -363,9 +392,76 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const Params p) {
     const uint32_t lanes = uint32_t(32 * q) << 16, a = tmem + kACol + uint32_t(s * kABufs + grp) * kACols;
     const int n_blk = MT == 2 ? p.n_kb : (p.n_kb + 1 - s) / 2;  // steps of a unit
     uint32_t wu = uint32_t(grp), a_use = 0, end = 0;            // the group's next step, counted over the units
+    bool x_held = false;                                        // x of the group's last step has not been handed back
     for (int64_t u = blockIdx.x; u < n_units; u += gridDim.x) {
       end += uint32_t(n_blk);
-      const bool on = unit(u).mt * (4 * MT) + (MT == 2 ? 4 * s : 0) + q < p.n_rb;
+      const Unit un = unit(u);
+      const bool on = un.mt * (4 * MT) + (MT == 2 ? 4 * s : 0) + q < p.n_rb;
+      if (un.n <= kFew) {
+        // Few rows: a warp multiplies its row block itself.  An MMA of tcgen05 takes 70 cycles and more with the weight in
+        // tensor memory, however few rows: 16 of them for the two row tiles of a channel block take longer than its bytes.
+        if (x_held) {
+          wait(&sm.a_empty[s][grp], a_use - 1);
+          if (q == 0 && lane == 0) mbar_arrive(&sm.x_empty[x_of(wu - 2, s) % kStages], 4);
+          x_held = false;
+        }
+        const int t = lane & 3, g = lane >> 2;
+        float acc[2][4] = {};
+        for (; wu != end && wu != end + 1; wu += 2) {
+          const uint32_t slot = wu % kSlots, xu = x_of(wu, s), stage = xu % kStages;
+          wait(&sm.w_full[s][slot], wu / kSlots);
+          wait(&sm.x_full[stage], xu / kStages);
+          __syncwarp();
+          if (on) {
+            const unsigned char* blk = sm.ring[s][slot][q];
+            const unsigned char* xr = smem + stage * kStage + (t >> 1) * (kTile * 128) + g * 128;  // channels 32t .. 32t + 31 of row g
+            float d[2][4] = {};
+            uint4 xb[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) xb[i] = *reinterpret_cast<const uint4*>(xr + (((4 * (t & 1) + i) ^ g) << 4));
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              uint4 cw[2];
+              __half2 sc[2][2];
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int row = 16 * r + 8 * h + g;
+                cw[h] = *reinterpret_cast<const uint4*>(blk + block_place(row, t));
+                const __half2 s2 = attn::bits_h2(attn::e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(blk + kCodeBytes + row * 8 + 2 * t)));
+                sc[h][0] = __low2half2(s2), sc[h][1] = __high2half2(s2);
+              }
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                uint32_t w[2][4];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  attn::e2m1x8_to_f16x2x4(i == 0 ? cw[h].x : i == 1 ? cw[h].y : i == 2 ? cw[h].z : cw[h].w, w[h][0], w[h][1], w[h][2], w[h][3]);
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) w[h][e] = attn::h2_bits(__hmul2(attn::bits_h2(w[h][e]), sc[h][i >> 1]));
+                }
+                mma_f16(d[r], w[0][0], w[1][0], w[0][1], w[1][1], xb[i].x, xb[i].y);
+                mma_f16(d[r], w[0][2], w[1][2], w[0][3], w[1][3], xb[i].z, xb[i].w);
+              }
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[r][e] += d[r][e];
+            }
+          }
+          attn::fence_async_smem();  // what the lanes have read comes before what the copies write
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.w_empty[s][slot]), mbar_arrive(&sm.x_empty[stage]);
+        }
+        if (a_use > 0) wait(&sm.a_empty[s][grp], a_use - 1);  // the last such unit's sums have been read
+        __syncwarp();
+        // acc[r]: outputs 16r + g (0, 1) and + 8 (2, 3), rows 2t and 2t + 1 of the unit
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sm.red[2 * s + grp][q][2 * t + (e & 1)][16 * r + 8 * (e >> 1) + g] = acc[r][e];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.a_full[s][grp]);
+        ++a_use;
+        continue;
+      }
       for (; wu != end && wu != end + 1; wu += 2, ++a_use) {
         const uint32_t slot = wu % kSlots, xu = x_of(wu, s);
         uint4 c[4];
@@ -380,10 +476,10 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const Params p) {
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.w_empty[s][slot]);
         }
-        if (a_use > 0) {
-          wait(&sm.a_empty[s][grp], a_use - 1);
-          if (q == 0 && lane == 0) mbar_arrive(&sm.x_empty[x_of(wu - 2, s) % kStages]);  // that block's products are done with x too
-        }
+        if (a_use > 0) wait(&sm.a_empty[s][grp], a_use - 1);
+        // that block's products are done with x too (one warp for all four: the last of them would be late)
+        if (x_held && q == 0 && lane == 0) mbar_arrive(&sm.x_empty[x_of(wu - 2, s) % kStages], 4);
+        x_held = true;
         __syncwarp();
         attn::tc_fence_after();
         if (on) {
@@ -431,6 +527,23 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const Params p) {
         const int64_t n = int64_t(un.mt) * (128 * MT) + 128 * s + 32 * q + lane;
         const float rs = p.row_scale && n < p.n_out ? __ldg(p.row_scale + int64_t(un.e) * p.n_out + n) : 1.f;
         const uint32_t d0 = tmem + lanes + uint32_t(s) * kDCols;
+        if (un.n <= kFew) {
+          // the sums of the two groups, or with one row tile of the four of both pipelines, to where MMAs leave theirs
+          // (a way of their own through what follows made the others' 8% slower)
+          float v[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            v[j] = sm.red[2 * s][q][j][lane] + sm.red[2 * s + 1][q][j][lane];
+            if (MT == 1) v[j] += sm.red[2][q][j][lane] + sm.red[3][q][j][lane];
+          }
+          tmem_st8(d0, v);
+          if (MT == 1) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = 0.f;
+            tmem_st8(d0 + kDCols, v);
+          }
+          asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
+        }
         // the unit's rows of y: kAct, kF32
         auto finish = [&](auto act, auto f32) {
           constexpr bool kAct = decltype(act)::value, kF32 = decltype(f32)::value;
@@ -500,13 +613,13 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_kernel(const Params p) {
 
 inline size_t xs_bytes(int64_t rows, int64_t n_in) { return size_t(rows * ((n_in + kChan - 1) / kChan)) * (kChan * 2); }
 
-template <int MT, int kTile>
+template <int MT>
 cudaError_t launch(Params p, int sms, cudaStream_t st) {
-  p.n_mt = (p.n_rb + 4 * MT - 1) / (4 * MT), p.tile = kTile;
+  p.n_mt = (p.n_rb + 4 * MT - 1) / (4 * MT);
   cudaError_t e = launch_pdl(scale_kernel, dim3(unsigned((p.rows + 3) / 4)), dim3(128), 0, st, p);
   if (e != cudaSuccess) return e;
   static std::atomic<uint64_t> done{0};
-  auto kern = grouped_kernel<MT, kTile>;
+  auto kern = grouped_kernel<MT>;
   if ((e = allow_smem(reinterpret_cast<const void*>(kern), kSmem, done)) != cudaSuccess) return e;
   const int64_t most = std::min<int64_t>(p.rows, p.E) + p.rows / kTile;  // token tiles
   return launch_pdl(kern, dim3(unsigned(std::min<int64_t>(most * p.n_mt, sms))), dim3(kThreads), kSmem, st, p);
@@ -553,15 +666,11 @@ extern "C" csa2_status csa2_fp4_grouped(const uint16_t* x, int64_t n_x, int64_t 
   const int sms = sm_count();
   if (!p.flags || sms <= 0) return CSA2_ERR_CUDA;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  // Few rows for each expert: tiles of 32 rows, whose x runs further ahead.  Two row tiles of the weight at a time where
-  // there are units enough.
-  const int64_t used = std::min<int64_t>(rows, E), pairs = (p.n_rb + 7) / 8;
-  cudaError_t e;
-  // An MMA cuts its sum off, so that the error grows with the number of MMAs one after the other: an fp32 y takes the
-  // form whose sums are in two halves (2528 channels and the activation: 4.6e-7 of the
-  // result, in one 1.1e-6).
-  const bool two = !y_fp32;
-  if (rows <= 16 * used) e = two && used * pairs >= 2 * sms ? launch<2, 32>(p, sms, st) : launch<1, 32>(p, sms, st);
-  else e = two && std::max(used, rows / kMaxTile) * pairs >= 2 * sms ? launch<2, 128>(p, sms, st) : launch<1, 128>(p, sms, st);
+  // Two row tiles of the weight at a time where there are units enough.  An MMA cuts its sum off, so that the error grows
+  // with the number of MMAs one after the other: an fp32 y takes the form whose sums are in two halves (2528 channels and
+  // the activation: 4.6e-7 of the result, in one 1.1e-6).
+  const int64_t tiles = std::max<int64_t>(std::min<int64_t>(rows, E), rows / kTile);
+  const bool two = !y_fp32 && tiles * ((p.n_rb + 7) / 8) >= 2 * sms;
+  const cudaError_t e = two ? launch<2>(p, sms, st) : launch<1>(p, sms, st);
   return e == cudaSuccess ? CSA2_OK : CSA2_ERR_CUDA;
 }
