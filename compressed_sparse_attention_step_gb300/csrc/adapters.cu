@@ -409,40 +409,45 @@ __global__ void __launch_bounds__(kThreads, NR <= 8 ? 2 : 1) lora_kernel(const P
         ask_out(i + kStages - 1);
         const unsigned char* at = smem + (i % kStages) * S::kStage;
         float d[J][4];
+        uint32_t bv[J][R / 16][2];
 #pragma unroll
         for (int j = 0; j < J; ++j) {
           d[j][0] = d[j][1] = d[j][2] = d[j][3] = 0.f;
           const int row = wk * (8 * J) + 2 * J * (g >> 1) + 2 * j + (g & 1);  // a lane's channels: wk * 8J + 2J t and on
           const unsigned char* br = at + TM * 128 + row * (R * 2);
-          uint32_t bv[R / 16][2];
           if (R >= 32) {
 #pragma unroll
             for (int k = 0; k < R / 32; ++k) {
               const int c = 4 * k + t;
               const uint4 v = *reinterpret_cast<const uint4*>(br + (R >= 64 ? c ^ ((row & 1) << 2) : c) * 16);
-              bv[2 * k][0] = v.x, bv[2 * k][1] = v.y;
-              bv[R >= 32 ? 2 * k + 1 : 0][0] = v.z, bv[R >= 32 ? 2 * k + 1 : 0][1] = v.w;
+              bv[j][2 * k][0] = v.x, bv[j][2 * k][1] = v.y;
+              bv[j][R >= 32 ? 2 * k + 1 : 0][0] = v.z, bv[j][R >= 32 ? 2 * k + 1 : 0][1] = v.w;
             }
           } else {
             const uint2 v = *reinterpret_cast<const uint2*>(br + 8 * t);
-            bv[0][0] = v.x, bv[0][1] = v.y;
+            bv[j][0][0] = v.x, bv[j][0][1] = v.y;
           }
-          if (n_rank < R) {  // what lies past the adapter's rank is not used
+        }
+        if (n_rank < R) {  // what lies past the adapter's rank is not used
+#pragma unroll
+          for (int j = 0; j < J; ++j)
 #pragma unroll
             for (int k = 0; k < R / 16; ++k)
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
                 const int rr = R >= 32 ? 32 * (k >> 1) + 8 * t + 4 * (k & 1) + 2 * h : 4 * t + 2 * h;
-                if (rr >= n_rank) bv[k][h] = 0;
-                else if (rr + 1 >= n_rank) bv[k][h] &= 0xFFFFu;
+                if (rr >= n_rank) bv[j][k][h] = 0;
+                else if (rr + 1 >= n_rank) bv[j][k][h] &= 0xFFFFu;
               }
-          }
-#pragma unroll
-          for (int k = 0; k < R / 16; ++k)
-#pragma unroll
-            for (int term = 0; term < kTerms; ++term)
-              mma(d[j], f[term][k][0], f[term][k][1], f[term][k][2], f[term][k][3], bv[k][0], bv[k][1]);
         }
+        // (an MMA waits for the one before it on the same sums: the channels' groups take turns)
+#pragma unroll
+        for (int k = 0; k < R / 16; ++k)
+#pragma unroll
+          for (int term = 0; term < kTerms; ++term)
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+              mma(d[j], f[term][k][0], f[term][k][1], f[term][k][2], f[term][k][3], bv[j][k][0], bv[j][k][1]);
         const int n = (q0 + i) * kCols + wk * (8 * J) + 2 * J * t;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {

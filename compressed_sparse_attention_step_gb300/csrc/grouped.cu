@@ -1,15 +1,25 @@
 // Products of the token rows of each expert with its 4-bit weight (E2M1 codes, one E4M3 scale per 16 channels):
 // y[r] = act(row_scale[e] * W_e x[src[r]]) for the rows offsets[e] <= r < offsets[e + 1] of expert e.
 //
-// The weight is the M = 128 operand of tcgen05.mma, dequantised into tensor memory, the token rows are the other one
-// (N = 16 .. 128, by the rows that a tile has): a weight element costs one conversion and one multiplication whatever
-// the number of rows, and a tile with few rows little tensor time.  The packed weight's layout and numbers are those
-// of matvec.cu: a code times a scale is exact in f16, and so is x scaled by the power of two that brings a row's
-// largest magnitude into [2^14, 2^15), down to 2^-28 of it (off by less than 2^-38 of it below).
+// The packed weight's layout and numbers are those of matvec.cu: a code times a scale is exact in f16, and so is x scaled
+// by the power of two that brings a row's largest magnitude into [2^14, 2^15), down to 2^-28 of it (off by less than
+// 2^-38 of it below).  Sums are fp32 and rounded once.
 //
-// Two launches: scale_kernel writes the rows as f16 into the workspace, each unit's in the order in which the products
-// read them, and each row's factor; grouped_kernel, one persistent CTA per SM, takes units of an expert, up to 128 of
-// its rows, and 128 or 256 outputs.
+// Two launches.  scale_kernel writes the rows of the lists as f16 into the workspace, each unit's in the order in which the
+// products read them, and each row's factor (rows gathered by 16-byte copies took twice as long as the products, by
+// gathering tensor copies three times).  grouped_kernel, one persistent CTA per SM, takes units of an expert, up to 128
+// of its rows, and 256 outputs, or 128:
+//   * more than eight rows: the weight is the M = 128 operand of tcgen05.mma, dequantised into tensor memory, so that a
+//     weight element costs one conversion and one multiplication whatever the number of rows; the rows are N = 16 .. 128;
+//   * up to eight rows: mma.m16n8k16 by the dequantising warps (198 -> 191 us below).
+//
+// What bounds it: for few rows the weight's bytes; beyond some 80 rows an expert the tensor core, 16 MMAs of 64 cycles for
+// a channel block of 256 outputs and 128 rows (1024 of the 1400 that it takes), and the units' number in whole waves.  In
+// front of both stand 14 us of a call: two launches, the lists, the first copies and the last sums (19 experts of 4096 x
+// 2048 take 30 us, each 19 more 15.6; at the copy bandwidth 13.2).
+// Measured (us, in brackets at the copy bandwidth or the bf16 rate): 64 tokens x 6 of 384 experts, 4096 x 2048, 191 (170);
+// 4096 tokens x 2 of 8 experts, 4096 x 4096, 202 (145); 247 experts of 2, 16 and 128 rows, 4096 x 2048, 223 (172), 248
+// (172) and 416 (280); 37 tokens x 2 of 9 experts, 1040 x 1000, 9.4 (0.8).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -628,7 +638,7 @@ cudaError_t launch(Params p, int sms, cudaStream_t st) {
 }  // namespace grp
 
 size_t fp4_grouped_ws_bytes(int64_t rows, int64_t n_in) {
-  if (rows <= 0 || n_in <= 0 || n_in % CSA2_GROUP || rows >= (int64_t(1) << 31) || n_in > (1 << 24)) return 0;
+  if (rows <= 0 || n_in <= 0 || n_in % CSA2_GROUP || rows >= (int64_t(1) << 30) || n_in > (1 << 24)) return 0;
   return grp::xs_bytes(rows, n_in) + size_t(rows) * 4;
 }
 
@@ -640,7 +650,7 @@ extern "C" csa2_status csa2_fp4_grouped(const uint16_t* x, int64_t n_x, int64_t 
                                         csa2_stream_t stream) {
   using namespace csa2;
   using namespace csa2::grp;
-  if (n_x < 0 || n_x >= (1ll << 31) || rows < 0 || rows >= (1ll << 31) || E < 0 || E > CSA2_MAX_EXPERTS || n_in <= 0 ||
+  if (n_x < 0 || n_x >= (1ll << 31) || rows < 0 || rows >= (1ll << 30) || E < 0 || E > CSA2_MAX_EXPERTS || n_in <= 0 ||
       n_in % CSA2_GROUP || n_in > (1 << 24) || n_out < 0 || n_out > (1 << 22) ||
       (act != CSA2_ACT_NONE && act != CSA2_ACT_SWIGLU) || (act == CSA2_ACT_SWIGLU && n_out % 2))
     return CSA2_ERR_INVALID_ARG;
@@ -666,11 +676,14 @@ extern "C" csa2_status csa2_fp4_grouped(const uint16_t* x, int64_t n_x, int64_t 
   const int sms = sm_count();
   if (!p.flags || sms <= 0) return CSA2_ERR_CUDA;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  // Two row tiles of the weight at a time where there are units enough.  An MMA cuts its sum off, so that the error grows
+  // Two row tiles of the weight at a time where three quarters of the SMs have a unit.  Measured, us, one and two (experts x
+  // rows each x channels x outputs): 8 x 1 x 4096 x 2048 20.5 / 25.0, 1 x 512 x 4096 x 4096 27.8 / 33.0, 9 x 8 x 1040 x 1000
+  // 13.0 / 13.6; 16 x 300 x 1024 x 1024 27.3 / 27.9, 8 x 256 x 4096 x 2048 44.7 / 39.5, 19 x 2 x 4096 x 2048 35.8 / 29.9,
+  // 60 x 8 x 2048 x 1024 33.2 / 27.5, 247 x 2 x 4096 x 2048 292 / 223, 8 x 1024 x 4096 x 2048 134 / 121.  An MMA cuts its sum off, so that the error grows
   // with the number of MMAs one after the other: an fp32 y takes the form whose sums are in two halves (2528 channels and
   // the activation: 4.6e-7 of the result, in one 1.1e-6).
   const int64_t tiles = std::max<int64_t>(std::min<int64_t>(rows, E), rows / kTile);
-  const bool two = !y_fp32 && tiles * ((p.n_rb + 7) / 8) >= 2 * sms;
+  const bool two = !y_fp32 && tiles * ((p.n_rb + 7) / 8) * 4 >= 3 * int64_t(sms);
   const cudaError_t e = two ? launch<2>(p, sms, st) : launch<1>(p, sms, st);
   return e == cudaSuccess ? CSA2_OK : CSA2_ERR_CUDA;
 }

@@ -43,7 +43,7 @@ def test_fp4_grouped(L):
              n=1 << 20):
         return L.csa2_fp4_grouped(x, n_x, n_in, w, E, n_out, rs, off, src, rows, act, y, 0, ws, n, None)
     for bad in (dict(n_x=-1), dict(n_in=24), dict(n_in=0), dict(n_in=-16), dict(E=-1), dict(E=csa2.MAX_EXPERTS + 1), dict(n_out=-1),
-                dict(rows=-1), dict(act=2), dict(act=1, n_out=7), dict(n_x=1 << 31), dict(rows=1 << 31), dict(n_in=1 << 25)):
+                dict(rows=-1), dict(act=2), dict(act=1, n_out=7), dict(n_x=1 << 31), dict(rows=1 << 30), dict(n_in=1 << 25), dict(n_out=1 << 23)):
         assert call(**bad) == 1, bad
     for name in ("x", "w", "off", "y"):
         assert call(**{name: None}) == 1, name
