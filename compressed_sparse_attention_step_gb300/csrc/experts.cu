@@ -4,6 +4,11 @@
 // Order.  A token has an expert at most once, so a block of tokens is, for each expert, a bit mask over the block's
 // tokens: the number of bits is the block's share of the expert's list, the bits below a token's own are its place in
 // it.  Masks are set by atomic ORs, whose order changes nothing; the lists are in order of token whatever the schedule.
+//
+// Bound: for routing the chain of its steps (k rounds of a warp's largest key; masks; the cluster's counts; a scan; the
+// places), for the sum the rows of y.  Measured (us, in brackets at the copy bandwidth): 64 tokens x 384 experts, six each,
+// 7.4 (0.02), by one CTA 17; 8192 tokens 19 (2.0), by 128 CTAs with their counts in global memory 35; the sum of 8192 x 6 rows
+// of 4096 channels 114 (79; a plain copy of as many bytes takes 92), with four rows asked for together 144.
 #include <cuda_bf16.h>
 
 #include <algorithm>

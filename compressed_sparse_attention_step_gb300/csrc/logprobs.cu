@@ -11,7 +11,15 @@
 // the n groups are read again (from L2), at most n (n + 1) / 2 candidates are kept, each counts those that beat it, and
 // that is its place: whole numbers throughout, whatever the number of ties.
 //
-// Bound: one read of the logits.
+// Three kernels.  Rows of up to four groups: a warp each, the row in registers.  More rows than two CTAs per SM: persistent
+// CTAs that stream through the rows while other warps finish the one before (a CTA that did both after one another took
+// 125 us where this took 112; four finishing warps with a row each, 114 where they share one takes 106).  Fewer: a cluster
+// per row.
+//
+// Bound: one read of the logits.  Measured (us, in brackets at the copy bandwidth): 2048 rows of 129283 bf16 logits, eight
+// alternatives, 106 (78: instruction issue, and seven rows a CTA where 6.7 would do; 94 without alternatives, 151 with 32);
+// one row of 129280, 20 alternatives, 14 (0.04): a chain of the pass (2 us), two cluster barriers, and some ten short
+// steps between barriers, most of them an instruction cache's first reading of their code.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -35,7 +43,7 @@ constexpr float kFloor = -1e30f;      // logits are cut off here: with inv_temp 
 struct Params {
   const void* logits;
   int64_t ld;
-  int rows, V, n_tok, n_top, max_groups;
+  int rows, V, n_tok, n_top, max_groups, deep;
   float inv_temp;
   const int32_t* tokens;
   float *logprobs, *lse, *entropy, *top_logprobs;
@@ -312,6 +320,84 @@ __device__ __forceinline__ bool may_win(float v, float bound, int i, int n, int 
   return i >= 0 && i < V && v >= bound && (v > -INFINITY || i < n);
 }
 
+// The candidates of group g, which holds at most `most` of the n likeliest.
+constexpr int kHits = 4;
+template <bool kBf16>
+__device__ __forceinline__ void take(const Row<kBf16>& row, int g, const uint4 (&v)[kLoads], float low, int n, int most, int lane,
+                                     Scratch& sc) {
+  using R = Row<kBf16>;
+  // Most groups have one or two lanes with a value that reaches the bound: all lanes look at such a lane's values, one
+  // each, instead of each at all of its own (2048 rows of 129280, 8 and 32 alternatives: 106 and 151 us for 113 and 198).
+  const unsigned hits = __ballot_sync(0xffffffffu, group_max<kBf16>(v) >= low);
+  if (low > -INFINITY && __popc(hits) <= kHits) {
+    float x[kHits];
+    unsigned found[kHits], rest = hits;
+    int all = 0;
+#pragma unroll
+    for (int k = 0; k < kHits; ++k) {
+      const int i = rest ? row.first(g, lane / R::E, __ffs(rest) - 1) + lane % R::E : -1;
+      x[k] = lane < kLoads * R::E && i >= 0 && i < row.V ? row.one(i) : -INFINITY;
+      rest &= rest - 1;
+    }
+#pragma unroll
+    for (int k = 0; k < kHits; ++k) found[k] = __ballot_sync(0xffffffffu, x[k] >= low), all += __popc(found[k]);
+    if (all <= most) {
+      int at = 0;
+      if (lane == 0) at = atomicAdd(&sc.n_cand, all);
+      at = __shfl_sync(0xffffffffu, at, 0);
+      rest = hits;
+#pragma unroll
+      for (int k = 0; k < kHits; ++k) {
+        if (found[k] >> lane & 1u) {
+          const int o = at + __popc(found[k] & ((1u << lane) - 1u));
+          sc.cv[o] = x[k], sc.ci[o] = row.first(g, lane / R::E, __ffs(rest) - 1) + lane % R::E;
+        }
+        at += __popc(found[k]), rest &= rest - 1;
+      }
+      return;
+    }
+  }
+  uint32_t left = 0;  // this lane's values that may win and are not taken yet
+#pragma unroll
+  for (int j = 0; j < kLoads; ++j) {
+    const int i = row.first(g, j, lane);
+#pragma unroll
+    for (int e = 0; e < R::E; ++e)
+      if (may_win(R::value(v[j], e), low, i + e, n, row.V)) left |= 1u << (j * R::E + e);
+  }
+  const int mine = __popc(left), all = int(__reduce_add_sync(0xffffffffu, unsigned(mine)));
+  if (all <= most) {  // (the candidates' order does not matter)
+    int at = 0;
+    if (mine) at = atomicAdd(&sc.n_cand, mine);
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j)
+#pragma unroll
+      for (int e = 0; e < R::E; ++e)
+        if (left >> (j * R::E + e) & 1u) sc.cv[at] = R::value(v[j], e), sc.ci[at] = row.first(g, j, lane) + e, ++at;
+  } else {  // ties: the best of the group, one after the other
+#pragma unroll 1
+    for (int k = 0; k < most; ++k) {
+      float best = -INFINITY;
+      int where = -1;
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j)
+#pragma unroll
+        for (int e = 0; e < R::E; ++e) {
+          const float x = R::value(v[j], e);
+          if ((left >> (j * R::E + e) & 1u) && (where < 0 || x > best)) best = x, where = j * R::E + e;
+        }
+      const float m = warp_max(best);
+      const int id = where >= 0 && best == m ? row.first(g, where / R::E, lane) + where % R::E : 0x7FFFFFFF;
+      const int first = int(__reduce_min_sync(0xffffffffu, unsigned(id)));
+      if (id == first) {  // (some lane has one: fewer are taken than there are)
+        const int at = atomicAdd(&sc.n_cand, 1);
+        sc.cv[at] = m, sc.ci[at] = id, left &= ~(1u << where);
+      }
+      __syncwarp();
+    }
+  }
+}
+
 // The n likeliest of groups [g0, g1) of a row: sink(place, value, token), by kThreads threads that meet at barrier kBar.
 template <bool kBf16, int kThreads, int kBar, typename Sink>
 __device__ __forceinline__ void likeliest(const Row<kBf16>& row, int g0, int g1, const float* gmax, int* group, const Board& board,
@@ -357,46 +443,7 @@ __device__ __forceinline__ void likeliest(const Row<kBf16>& row, int g0, int g1,
     uint4 v[kLoads];
 #pragma unroll
     for (int j = 0; j < kLoads; ++j) row.load(row.first(g, j, lane), v[j]);
-    uint32_t left = 0;  // this lane's values that may win and are not taken yet
-#pragma unroll
-    for (int j = 0; j < kLoads; ++j) {
-      const int i = row.first(g, j, lane);
-#pragma unroll
-      for (int e = 0; e < R::E; ++e)
-        if (may_win(R::value(v[j], e), low, i + e, n, row.V)) left |= 1u << (j * R::E + e);
-    }
-    const int most = n - place;
-    const int mine = __popc(left), all = int(__reduce_add_sync(0xffffffffu, unsigned(mine)));
-    if (all <= most) {  // (the candidates' order does not matter)
-      int at = 0;
-      if (mine) at = atomicAdd(&sc.n_cand, mine);
-#pragma unroll
-      for (int j = 0; j < kLoads; ++j)
-#pragma unroll
-        for (int e = 0; e < R::E; ++e)
-          if (left >> (j * R::E + e) & 1u) sc.cv[at] = R::value(v[j], e), sc.ci[at] = row.first(g, j, lane) + e, ++at;
-    } else {  // ties: the best of the group, one after the other
-#pragma unroll 1
-      for (int k = 0; k < most; ++k) {
-        float best = -INFINITY;
-        int where = -1;
-#pragma unroll
-        for (int j = 0; j < kLoads; ++j)
-#pragma unroll
-          for (int e = 0; e < R::E; ++e) {
-            const float x = R::value(v[j], e);
-            if ((left >> (j * R::E + e) & 1u) && (where < 0 || x > best)) best = x, where = j * R::E + e;
-          }
-        const float m = warp_max(best);
-        const int id = where >= 0 && best == m ? row.first(g, where / R::E, lane) + where % R::E : 0x7FFFFFFF;
-        const int first = int(__reduce_min_sync(0xffffffffu, unsigned(id)));
-        if (id == first) {  // (some lane has one: fewer are taken than there are)
-          const int at = atomicAdd(&sc.n_cand, 1);
-          sc.cv[at] = m, sc.ci[at] = id, left &= ~(1u << where);
-        }
-        __syncwarp();
-      }
-    }
+    take<kBf16>(row, g, v, low, n, n - place, lane, sc);
   }
   meet();
   const int total = sc.n_cand;
@@ -461,14 +508,22 @@ __global__ void __launch_bounds__(512, 2) few_rows_kernel(const Params p, int C)
   if (tid < C * kTop && li[tid] >= 0) {  // a winner of one CTA: its place among all
     const int id = li[tid];
     const float v = lv[tid];
-    int place = 0;
-    for (int c = 0; c < C; ++c)
-#pragma unroll 4
-      for (int j = 0; j < n; ++j) {
-        const int o = li[c * kTop + j];
-        const float u = lv[c * kTop + j];
-        place += o >= 0 && (u > v || (u == v && o < id));
+    int place = tid % kTop;
+#pragma unroll
+    for (int c = 0; c < kMaxCluster; ++c) {
+      if (c >= C || c == tid / kTop) continue;
+      // how many of that CTA's winners beat it: they are in order, nothing behind the last
+      int lo = 0;
+#pragma unroll
+      for (int step = kTop / 2; step; step /= 2) {
+        const int at = c * kTop + lo + step - 1, o = li[at];
+        const float u = lv[at];
+        if (o >= 0 && (u > v || (u == v && o < id))) lo += step;
       }
+      const int at = c * kTop + lo, o = li[at];
+      const float u = lv[at];
+      place += lo + (o >= 0 && (u > v || (u == v && o < id)));
+    }
     if (place < n) f.top(p, r, place, id, v);
   }
 }
@@ -702,7 +757,10 @@ __global__ void __launch_bounds__(128) short_rows_kernel(const Params p) {
 template <bool kBf16>
 cudaError_t launch(Params p, int sms, cudaStream_t st) {
   const int groups = (p.V + Row<kBf16>::E - 1 + Row<kBf16>::kGroup - 1) / Row<kBf16>::kGroup;  // at most, whatever the alignment
+  // us by warps, by CTAs that stream, by clusters: 1000 rows of 4000 tokens 10.4, 21, 31; 64 of 4000 8.0, 7.7, 9.7
   if (groups <= kShort) return launch_pdl(short_rows_kernel<kBf16>, dim3(unsigned((p.rows + 3) / 4)), dim3(128), 0, st, p);
+  // Streaming and clusters: 300 rows of 129280 20.2 and 20.3, 450 34.7 and 32.6, 600 35.2 and 39.1, 2048 106 and 123, 64
+  // 20.4 and 15.2; 300 rows of 16384 9.9 and 10.8, 600 15.4 and 18.7
   if (p.rows > 2 * sms) {
     p.max_groups = groups;
     constexpr size_t kRing = size_t(kStream) * kSlots * kGroupBytes;
