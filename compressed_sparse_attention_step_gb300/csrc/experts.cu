@@ -30,8 +30,11 @@ inline int block_tokens(int64_t m) {
   return t;
 }
 
-// The lists by one cluster of kCluster CTAs, as far as its masks fit: [words][E] of bits and of counts before them.
-constexpr int kCluster = 8, kAlone = 256;  // kAlone: tokens up to which the cluster chooses too
+// The lists by one cluster of kCluster CTAs, as far as its masks fit: [words][E] of bits and of counts before them.  Up to
+// kAlone tokens it chooses too (384 experts; it does, another launch does: 64 tokens 7.6 and 8.0 us, 128 7.9 and 8.0, 256
+// 11.4 and 8.0).  (Lists by the cluster, by blocks with counts in global memory: 1024 tokens 8.7 and 18.7, 8192 18.9 and
+// 34.3, 20000 37.0 and 59.1; 64 experts: 8192 tokens 12.4 and 16.9, 100000 88.7 and 82.0.)
+constexpr int kCluster = 8, kAlone = 128;
 constexpr size_t kMaskBytes = 192 * 1024;
 inline size_t mask_bytes(int64_t m, int64_t E, int C) { return size_t(E * (((m + C - 1) / C + 31) / 32) * 6 + 15) / 16 * 16; }
 inline bool in_cluster(int64_t m, int64_t E) { return mask_bytes(m, E, kCluster) <= kMaskBytes; }
