@@ -14,10 +14,10 @@
 //
 // Bound: for few rows the adapters' bytes, each once, and the chain of looking through the window, load, sum, exchange,
 // load, store; for many rows x and base read and out written.  Measured (us, in brackets at the copy bandwidth): 4100 rows
-// of 8192 channels to 8192, rank 64, runs of eight adapters, 97 (31): 64 rows a tile, of whose 330 MB from L2 and HBM each
+// of 8192 channels to 8192, rank 64, runs of eight adapters, 93 (31): 64 rows a tile, of whose 330 MB from L2 and HBM each
 // tile's 2 MB of adapter are 130, at 3.5 TB/s; a step of 64 channels is a chain of copy, barrier, 16-byte reads and MMAs
 // that two CTAs an SM overlap to a half.  Taking neighbouring rows as tiles, with A from registers, took 354.  64 rows x
-// 32 adapters, 4096 to 8200, rank 32, 13.5 (2.7); one row, rank 16, 7.1 (0.03).
+// 32 adapters, 4096 to 8200, rank 32, 13.4 (2.7); one row, rank 16, 7.0 (0.03).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -200,18 +200,25 @@ __global__ void __launch_bounds__(kThreads, NR <= 8 ? 2 : 1) lora_kernel(const P
       // 64 channels of the tile's rows and of A at a time, by asynchronous copies into a ring
       const int n_step = (p.n_in + 63) / 64;
       const int s0 = int(int64_t(n_step) * rank / C), n = int(int64_t(n_step) * (rank + 1) / C) - s0;
+      constexpr int kLines = kThreads / 8;  // rows that the CTA copies 128 bytes of at a time
+      const uint16_t *from_x[TM / kLines], *from_a[(R + kLines - 1) / kLines];
+      const int piece = tid & 7, line = tid >> 3;
+#pragma unroll
+      for (int k = 0; k < TM / kLines; ++k) from_x[k] = p.x + int64_t(rows[line + k * kLines]) * p.n_in + s0 * 64 + 8 * piece;
+#pragma unroll
+      for (int k = 0; k < (R + kLines - 1) / kLines; ++k) from_a[k] = a + int64_t(line + k * kLines) * p.n_in + s0 * 64 + 8 * piece;
       auto ask = [&](int i) {
         if (i < n) {
           const uint32_t dst = smem_u32(smem) + uint32_t(i % kStages) * uint32_t(S::kStage);
-          const int j = tid & 7, ch = (s0 + i) * 64 + 8 * j;
-          const bool in = ch < p.n_in;
+          const bool in = (s0 + i) * 64 + 8 * piece < p.n_in;
 #pragma unroll
-          for (int row = tid >> 3; row < TM; row += kThreads / 8)
-            cp_async16_row(dst + piece_at(row, j), in ? p.x + int64_t(rows[row]) * p.n_in + ch : p.x, in ? 16 : 0);
+          for (int k = 0; k < TM / kLines; ++k)
+            cp_async16_row(dst + piece_at(line + k * kLines, piece), in ? from_x[k] + i * 64 : p.x, in ? 16 : 0);
 #pragma unroll
-          for (int row = tid >> 3; row < R; row += kThreads / 8) {
-            const bool on = in && row < n_rank;
-            cp_async16(dst + TM * 128 + piece_at(row, j), on ? a + int64_t(row) * p.n_in + ch : p.x, on ? 16 : 0);
+          for (int k = 0; k < (R + kLines - 1) / kLines; ++k) {
+            if (R % kLines && line + k * kLines >= R) continue;
+            const bool on = in && line + k * kLines < n_rank;
+            cp_async16(dst + TM * 128 + piece_at(line + k * kLines, piece), on ? from_a[k] + i * 64 : p.x, on ? 16 : 0);
           }
         }
         cp_async_commit();
@@ -289,15 +296,22 @@ __global__ void __launch_bounds__(kThreads, NR <= 8 ? 2 : 1) lora_kernel(const P
     constexpr int J = kF32 ? 2 : 4, kCols = 16 * J;
     const int n_col = (p.n_out + kCols - 1) / kCols;
     const int q0 = int(int64_t(n_col) * rank / C), q1 = int(int64_t(n_col) * (rank + 1) / C);
+    const char* from_base[TM / 16];  // (of which the ring uses those of its rows)
+    if constexpr (kRing) {
+#pragma unroll
+      for (int k = 0; k < TM / 32; ++k)
+        from_base[k] = static_cast<const char*>(p.base) +
+                       (int64_t(rows[(tid >> 3) + 32 * k]) * p.n_out + q0 * kCols + (tid & 7) * 2 * J) * (kF32 ? 4 : 2);
+    }
     auto ask_out = [&](int i) {
       if (q0 + i < q1) {
         const uint32_t dst = smem_u32(smem) + uint32_t(i % kStages) * uint32_t(S::kStage);
-        const int n0 = (q0 + i) * kCols, n = n0 + (tid & 7) * 2 * J;
-        const bool in = n < p.n_out;
+        const int n0 = (q0 + i) * kCols;
+        const bool in = n0 + (tid & 7) * 2 * J < p.n_out;
 #pragma unroll
-        for (int row = tid >> 3; row < TM; row += kThreads / 8)
-          cp_async16_row(dst + piece_at(row, tid & 7),
-                     in ? static_cast<const char*>(p.base) + (int64_t(rows[row]) * p.n_out + n) * (kF32 ? 4 : 2) : p.base, in ? 16 : 0);
+        for (int k = 0; k < TM / 32; ++k)
+          cp_async16_row(dst + piece_at((tid >> 3) + 32 * k, tid & 7), in ? from_base[k] + i * 128 : p.base, in ? 16 : 0);
+#pragma unroll
         for (int e = tid; e < kCols * (R / 8); e += kThreads) {
           const int row = e / (R / 8), j = e % (R / 8);
           const bool on = n0 + row < p.n_out && 8 * j < n_rank;
