@@ -10,6 +10,7 @@ bf16 tensors may be torch.bfloat16 or torch.int16/uint16 bit patterns.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -664,9 +665,10 @@ def _scratch(ws, need, device, dev, stream):
     if ws is None:
         if not need:
             return None, 0, None
-        ws = _torch().empty(need, dtype=_torch().uint8, device=device)
-        if stream is not None and ws.is_cuda:  # its memory is not handed on before that stream is done with it
-            ws.record_stream(stream)
+        torch = _torch()
+        # (as memory of the stream that uses it: not what earlier work of another still writes, nor handed on to one)
+        with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+            ws = torch.empty(need, dtype=torch.uint8, device=device)
     return _arg(ws, "ws", _U8, (ws.numel(),) if hasattr(ws, "numel") else (), dev), _nbytes(ws), ws
 
 

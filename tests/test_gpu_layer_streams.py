@@ -1,0 +1,136 @@
+"""Two layers' steps at once, on two streams: the operators share no scratch.  And what the binding refuses of GPU tensors."""
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("no CUDA device", allow_module_level=True)
+import compressed_sparse_attention_step_gb300 as c  # noqa: E402
+from tests import _layer as P  # noqa: E402
+from tests.test_gpu_layer_step import Step  # noqa: E402
+
+
+def alone(steps):
+    want = []
+    for i, s in enumerate(steps):
+        s.requests(11 + i)
+        s.run()
+        torch.cuda.synchronize()
+        want.append(s.outputs())
+    return want
+
+
+def same(steps, want):
+    torch.cuda.synchronize()
+    for s, outs in zip(steps, want):
+        for got, ref in zip(s.outputs(), outs):
+            assert torch.equal(got, ref)
+    assert c.csa2_device_flags() == 0
+
+
+def test_two_streams():
+    steps = [Step(), Step()]
+    want = alone(steps)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        for s, st in zip(steps, streams):
+            with torch.cuda.stream(st):
+                s.run()
+    same(steps, want)
+
+
+def test_two_graphs_at_once():
+    steps = [Step(), Step()]
+    want = alone(steps)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    graphs = []
+    for s in steps:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            s.run()
+    for _ in range(5):
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+    same(steps, want)
+
+
+def test_workspaces_of_their_own_on_a_given_stream():
+    """Calls without a workspace on a stream that is not the current one, while the current one is busy with memory that it
+    has freed."""
+    m, E, k, n = 3000, 40, 4, 64
+    g = np.random.default_rng(5)
+    logits = torch.from_numpy(g.standard_normal((m, E)).astype(np.float32)).cuda()
+    want = P.route(logits.cpu().numpy(), k, None, None, scale=1.0)
+    x = torch.from_numpy(g.standard_normal((m, n)).astype(np.float32)).bfloat16().cuda()
+    codes = torch.from_numpy(g.integers(0, 256, (E, 32, n // 2), dtype=np.uint8)).cuda()
+    scales = torch.from_numpy(g.integers(0x28, 0x40, (E, 32, n // 16), dtype=np.uint8)).cuda()
+    packed = c.fp4_pack_experts(codes, scales)
+    y0, y = (torch.zeros((m * k, 32), device="cuda") for _ in range(2))
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")  # noqa: E731
+    out = i32(m, k), torch.zeros((m, k), device="cuda"), i32(E + 1), i32(m * k), i32(m, k)
+    c.csa2_expert_route(logits, *out)
+    c.csa2_fp4_grouped(x, packed, out[2], y0, src=out[3])
+    torch.cuda.synchronize()
+    other = torch.cuda.Stream()
+    big = torch.zeros(1 << 28, device="cuda")
+    for _ in range(4):
+        junk = torch.empty(c.grouped_workspace_size(m * k, n), dtype=torch.uint8, device="cuda")
+        for _ in range(3):
+            big.add_(1)
+        junk.fill_(255)
+        del junk
+        y.zero_()
+        other.wait_stream(torch.cuda.current_stream())
+        c.csa2_expert_route(logits, *out, stream=other)
+        c.csa2_fp4_grouped(x, packed, out[2], y, src=out[3], stream=other)
+        torch.cuda.synchronize()
+        for i, what in ((0, "experts"), (2, "offsets"), (3, "src"), (4, "pos")):
+            assert np.array_equal(out[i].cpu().numpy(), want[i]), what
+        assert torch.equal(y, y0)
+    assert c.csa2_device_flags() == 0
+
+
+def test_refusals_of_gpu_tensors():
+    f = lambda *s: torch.zeros(s, device="cuda")  # noqa: E731
+    b = lambda *s: torch.zeros(s, device="cuda", dtype=torch.bfloat16)  # noqa: E731
+    i = lambda *s: torch.zeros(s, device="cuda", dtype=torch.int32)  # noqa: E731
+    u = lambda *s: torch.zeros(s, device="cuda", dtype=torch.uint8)  # noqa: E731
+    m, E, k = 4, 8, 2
+    route = dict(experts=i(m, k), weights=f(m, k), offsets=i(E + 1), src=i(m * k), pos=i(m, k))
+    with pytest.raises(TypeError, match="logits"):
+        c.csa2_expert_route(b(m, E), **route)
+    with pytest.raises(ValueError, match="pos"):
+        c.csa2_expert_route(f(m, E), **{**route, "pos": torch.zeros((m, k), dtype=torch.int32)})  # of the host
+    with pytest.raises(ValueError, match="contiguous"):
+        c.csa2_expert_route(f(E, m).t(), **route)
+    with pytest.raises(ValueError, match="offsets"):
+        c.csa2_expert_route(f(m, E), **{**route, "offsets": i(E)})
+    packed = c.fp4_pack_experts(u(E, 32, 32), u(E, 32, 4))
+    with pytest.raises(TypeError, match="y"):
+        c.csa2_fp4_grouped(b(m, 64), packed, i(E + 1), torch.zeros((m, 32), device="cuda", dtype=torch.float16))
+    with pytest.raises(ValueError, match="packed"):
+        c.csa2_fp4_grouped(b(m, 64), packed, i(E + 1), b(m, 32), act=c.ACT_SWIGLU)
+    with pytest.raises(ValueError, match="x"):
+        c.csa2_fp4_grouped(b(m, 64), packed, i(E + 1), b(m + 1, 32))
+    with pytest.raises(c.Csa2Error):  # an output over what is read
+        y = b(m, 32)
+        c.csa2_fp4_grouped(b(m, 64), packed, i(E + 1), y, src=y.view(torch.int32).view(-1)[:m])
+    with pytest.raises(TypeError, match="weights"):
+        c.csa2_expert_combine(b(m, 32), i(m, k), b(m, k), b(m, 32))
+    with pytest.raises(ValueError, match="out"):
+        c.csa2_expert_combine(b(m, 32), i(m, k), f(m, k), b(m, 31))
+    with pytest.raises(TypeError, match="out"):
+        c.csa2_lora_add(b(m, 64), b(3, 8, 64), b(3, 32, 8), i(m), b(m, 32), f(m, 32))
+    with pytest.raises(ValueError, match="b"):
+        c.csa2_lora_add(b(m, 64), b(3, 8, 64), b(3, 8, 32), i(m), b(m, 32), b(m, 32))
+    with pytest.raises(TypeError, match="logits"):
+        c.csa2_token_logprobs(torch.zeros((m, 50), device="cuda", dtype=torch.float16), i(m, 1), f(m, 1))
+    with pytest.raises(ValueError, match="strides"):
+        c.csa2_token_logprobs(f(50, m).t(), i(m, 1), f(m, 1))
+    with pytest.raises(ValueError, match="top_logprobs"):
+        c.csa2_token_logprobs(f(m, 50), top_ids=i(m, 4), top_logprobs=f(m, 5))
+    torch.cuda.synchronize()
+    assert c.csa2_device_flags() == 0
