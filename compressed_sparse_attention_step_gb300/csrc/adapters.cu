@@ -560,22 +560,28 @@ __global__ void __launch_bounds__(kThreads, NR <= 8 ? 2 : 1) lora_kernel(const P
     __syncthreads();
   }
   }
-  // rows without an adapter, by the clusters that have no tile, or else by all: a warp per row, of the CTA's share of the
-  // channels
-  const int idle = max(n_clusters - int(n_units), 0), copier = idle ? cluster - int(n_units) : cluster, copiers = idle ? idle : n_clusters;
-  if (p.base != p.out && copier >= 0) {
+  // rows without an adapter, by the clusters that have no tile where these are an eighth and more, or else by all: the
+  // rows go to the warps in turn, a warp looks at 32 of its own at a time, and copies the CTA's share of the channels
+  // (a row at a time, by any idle cluster, 4096 rows of one adapter took 42 us where they take 29)
+  const int idle = n_clusters - int(n_units), first = idle * 8 >= n_clusters ? int(n_units) : 0;
+  if (p.base != p.out && cluster >= first) {
     constexpr int kSize = kF32 ? 4 : 2, kPiece = kVec ? 16 : kSize;
     const int n_piece = p.n_out * kSize / kPiece;
     const int p0 = int(int64_t(n_piece) * rank / C), p1 = int(int64_t(n_piece) * (rank + 1) / C);
-    for (int i = copier + copiers * warp; i < n_w; i += copiers * kWarps) {
-      if (bucket[i] != kBuckets) continue;
-      const char* src = static_cast<const char*>(p.base) + int64_t(w0 + i) * p.n_out * kSize;
-      char* dst = static_cast<char*>(p.out) + int64_t(w0 + i) * p.n_out * kSize;
+    const int warps = (n_clusters - first) * kWarps;
+    for (int i0 = cluster - first + (n_clusters - first) * warp; i0 < n_w; i0 += 32 * warps) {
+      const int own = i0 + lane * warps;
+      unsigned todo = __ballot_sync(0xffffffffu, own < n_w && bucket[own] == kBuckets);
+      for (; todo; todo &= todo - 1) {
+        const int i = i0 + (__ffs(todo) - 1) * warps;
+        const char* src = static_cast<const char*>(p.base) + int64_t(w0 + i) * p.n_out * kSize;
+        char* dst = static_cast<char*>(p.out) + int64_t(w0 + i) * p.n_out * kSize;
 #pragma unroll 4
-      for (int n = p0 + lane; n < p1; n += 32) {
-        if (kVec) reinterpret_cast<uint4*>(dst)[n] = reinterpret_cast<const uint4*>(src)[n];
-        else if (kF32) reinterpret_cast<float*>(dst)[n] = reinterpret_cast<const float*>(src)[n];
-        else reinterpret_cast<uint16_t*>(dst)[n] = reinterpret_cast<const uint16_t*>(src)[n];
+        for (int n = p0 + lane; n < p1; n += 32) {
+          if (kVec) reinterpret_cast<uint4*>(dst)[n] = reinterpret_cast<const uint4*>(src)[n];
+          else if (kF32) reinterpret_cast<float*>(dst)[n] = reinterpret_cast<const float*>(src)[n];
+          else reinterpret_cast<uint16_t*>(dst)[n] = reinterpret_cast<const uint16_t*>(src)[n];
+        }
       }
     }
   }
@@ -650,8 +656,9 @@ extern "C" csa2_status csa2_lora_add(const uint16_t* x, int m, int n_in, const u
   // Tiles of 16 or 64 rows, and clusters of C: the least time by what tiles of both took, in us, with w the channels'
   // work of 16 rows: 7 + w / C and 16 + 2.4 w / C, as often as the tiles that a window is likely to have take turns.
   // Measured by tiles of 16 and of 64, 4096 to 4096 channels, rank 32, rows in mixed order: 64 rows of 1 adapter 8.4 and
-  // 15.6, 1024 of 4 15.1 and 23.6, 2048 of 8 23.0 and 29.0, 2048 of 64 41.8 and 37.7, 4096 of 8 47.1 and 40.5, 4096 of 32
-  // 51.4 and 65.6; 8192 to 8192, rank 64, runs: 512 of 1 22.6 and 37.8, 1024 of 2 34.8 and 53.0, 4100 of 8 137 and 95.
+  // 15.6, 1024 of 4 15.1 and 23.6, 2048 of 8 23.4 and 26.0, 2048 of 64 40.6 and 35.0, 4096 of 8 47.5 and 39.8, 4096 of 32
+  // 52.0 and 61.9; 8192 to 8192, rank 64, runs: 512 of 1 23.0 and 36.0, 1024 of 2 35.2 and 51.0, 4100 of 8 137 and 90.
+  // (Tiles of 128 rows, one CTA of 16 warps an SM, took 94 for the last, 45 for 4096 of 8 and 34 for 2048 of 8.)
   const int64_t window = std::min(m, kWindow), used = std::min<int64_t>(std::max(L, 1), std::min<int64_t>(window, kBuckets));
   const int64_t room = (r <= 64 ? 2 : 1) * int64_t(sms);
   const double work = (double(n_in) + n_out) * (r + 32) * 8e-5;
