@@ -7,7 +7,7 @@
 //
 // Bound: for routing the chain of its steps (k rounds of a warp's largest key; masks; the cluster's counts; a scan; the
 // places), for the sum the rows of y.  Measured (us, in brackets at the copy bandwidth): 64 tokens x 384 experts, six each,
-// 7.4 (0.02), by one CTA 17; 8192 tokens 19 (2.0), by 128 CTAs with their counts in global memory 35; the sum of 8192 x 6 rows
+// 7.4 (0.02), by one CTA 17; 8192 tokens 18 (2.0), by 128 CTAs with their counts in global memory 35; the sum of 8192 x 6 rows
 // of 4096 channels 114 (79; a plain copy of as many bytes takes 92), with four rows asked for together 144.
 #include <cuda_bf16.h>
 
@@ -30,14 +30,16 @@ inline int block_tokens(int64_t m) {
   return t;
 }
 
-// The lists by one cluster of kCluster CTAs, as far as its masks fit: [words][E] of bits and of counts before them.  Up to
-// kAlone tokens it chooses too (384 experts; it does, another launch does: 64 tokens 7.6 and 8.0 us, 128 7.9 and 8.0, 256
-// 11.4 and 8.0).  (Lists by the cluster, by blocks with counts in global memory: 1024 tokens 8.7 and 18.7, 8192 18.9 and
-// 34.3, 20000 37.0 and 59.1; 64 experts: 8192 tokens 12.4 and 16.9, 100000 88.7 and 82.0.)
-constexpr int kCluster = 8, kAlone = 128;
+// The lists by one cluster of CTAs, as far as the masks of eight fit, [words][E] of bits and of counts before them: lists by
+// the cluster and by blocks with counts in global memory take, with 384 experts, 1024 tokens 8.5 and 18.7 us, 8192 17.5 and
+// 34.3, 20000 33.6 and 59.1; with 64 experts 8192 tokens 11.1 and 16.9, 100000 66 and 82.  It has eight CTAs, from kWide
+// tokens on sixteen (by eight and by sixteen 1024 tokens 8.6 and 9.3, 4096 12.5 and 12.3, 8192 18.6 and 17.5, 20000 37.0
+// and 33.6, the 100000 88 and 66).  Up to kAlone tokens it chooses too (it, another launch: 64 tokens 7.6 and 8.0, 128 7.9
+// and 8.0, 256 11.4 and 8.0).
+constexpr int kCluster = 16, kAlone = 128, kWide = 4096;
 constexpr size_t kMaskBytes = 192 * 1024;
 inline size_t mask_bytes(int64_t m, int64_t E, int C) { return size_t(E * (((m + C - 1) / C + 31) / 32) * 6 + 15) / 16 * 16; }
-inline bool in_cluster(int64_t m, int64_t E) { return mask_bytes(m, E, kCluster) <= kMaskBytes; }
+inline bool in_cluster(int64_t m, int64_t E) { return mask_bytes(m, E, 8) <= kMaskBytes; }
 
 struct Params {
   const float *logits, *bias;
@@ -134,8 +136,8 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const Params p) {
 }
 
 // The lists by one cluster: a CTA takes p.tokens neighbouring tokens, and learns the others' counts through distributed
-// shared memory.  kChoose: chooses for them too.
-template <int NE, bool kChoose>
+// shared memory.  kChoose: chooses for them too.  kMost: C at most.
+template <int NE, bool kChoose, int kMost>
 __global__ void __launch_bounds__(kChoose ? kThreads : 1024) list_kernel(const Params p, int C) {
   constexpr int kBlock = kChoose ? kThreads : 1024;
   extern __shared__ uint32_t mask[];  // [words][E], then the bits before each word
@@ -166,12 +168,12 @@ __global__ void __launch_bounds__(kChoose ? kThreads : 1024) list_kernel(const P
     const int e = e0 + int(threadIdx.x);
     uint32_t all = 0, before = 0;
     if (e < p.E) {
-      uint32_t n[kCluster];
+      uint32_t n[kMost];
 #pragma unroll
-      for (int c = 0; c < kCluster; ++c)
+      for (int c = 0; c < kMost; ++c)
         n[c] = c >= C ? 0u : C > 1 ? ld_cluster_u32(cluster_addr(smem_u32(&count[e]), uint32_t(c))) : count[e];
 #pragma unroll
-      for (int c = 0; c < kCluster; ++c) {
+      for (int c = 0; c < kMost; ++c) {
         all += n[c];
         before += c < rank ? n[c] : 0u;
       }
@@ -271,14 +273,18 @@ __global__ void __launch_bounds__(kThreads) order_kernel(const Params p) {
     p.src[i] = -1;
 }
 
-template <int NE, bool kChoose>
+template <int NE, bool kChoose, int kMost>
 cudaError_t lists(Params p, cudaStream_t st) {
-  const int C = p.m > 32 ? kCluster : p.m > 16 ? 2 : 1;
+  const int C = p.m > 32 ? kMost : p.m > 16 ? 2 : 1;
   p.tokens = (p.m + C - 1) / C;
-  auto kern = list_kernel<NE, kChoose>;
+  auto kern = list_kernel<NE, kChoose, kMost>;
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), kMaskBytes, done);
   if (e != cudaSuccess) return e;
+  if (kMost > 8) {  // more than eight are asked for
+    const cudaError_t w = cudaFuncSetAttribute(reinterpret_cast<const void*>(kern), cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (w != cudaSuccess) return w;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(C));
   cfg.blockDim = dim3(kChoose ? kThreads : 1024);
@@ -298,11 +304,11 @@ cudaError_t lists(Params p, cudaStream_t st) {
 template <int NE>
 cudaError_t route(Params p, cudaStream_t st) {
   cudaError_t e;
-  if (p.m <= kAlone) return lists<NE, true>(p, st);
+  if (p.m <= kAlone) return lists<NE, true, 8>(p, st);
   if (in_cluster(p.m, p.E)) {
     if ((e = launch_pdl(choose_kernel<NE>, dim3(unsigned((p.m + kWarps - 1) / kWarps)), dim3(kThreads), 0, st, p)) != cudaSuccess)
       return e;
-    return lists<1, false>(p, st);
+    return p.m < kWide ? lists<1, false, 8>(p, st) : lists<1, false, kCluster>(p, st);
   }
   p.tokens = block_tokens(p.m);
   const int blocks = (p.m + p.tokens - 1) / p.tokens;
