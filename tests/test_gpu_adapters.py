@@ -102,3 +102,51 @@ def test_captured(m):
         graph.replay()
         exact, tol = P.adapters(V.f64(x), V.f64(a), V.f64(b), adapter, host(base))
         assert (np.abs(host(out) - exact) <= P.rounded(exact, tol, True)).all()
+
+
+# Many rows of few adapters: tiles of 64 rows, over the end of a window of 8192 too
+TALL = [(5600, 520, 512, 16, 5), (5000, 1000, 333, 64, 8), (9000, 264, 776, 32, 3), (6000, 512, 520, 128, 6), (8192, 600, 500, 40, 1),
+        (6100, 1024, 264, 8, 7), (16500, 328, 712, 64, 4), (4900, 2056, 72, 24, 2)]
+
+
+@pytest.mark.parametrize("m,n_in,n_out,r,L", TALL)
+@pytest.mark.parametrize("fp32", [False, True])
+@pytest.mark.parametrize("order", ["mixed", "runs"])
+def test_tall_tiles(m, n_in, n_out, r, L, fp32, order):
+    test_adapters(m, n_in, n_out, r, L, fp32, order)
+
+
+def test_tall_tiles_other_rows_do_not_matter():
+    g, adapter, x, a, b, base = make(1, 6000, 512, 520, 64, 4, True, none=0.0)
+    adapter[:] = np.arange(6000) % 4
+    outs = []
+    for other in (0.0, float("inf"), float("nan")):
+        xd, out = bf16_dev(x), torch.zeros_like(base)
+        xd[to_dev(adapter != 2)] = other
+        c.csa2_lora_add(xd, bf16_dev(a), bf16_dev(b), to_dev(adapter), base, out)
+        outs.append(out[to_dev(adapter == 2)])
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
+def test_rows_of_a_shared_bucket():
+    """Adapters whose numbers are equal modulo 255 meet in tiles, tall ones among them."""
+    for m in (50, 8192):
+        L = 700
+        g, adapter, x, a, b, base = make(6, m, 72, 1032, 40, L, False)
+        adapter[:] = np.where(adapter < 0, -1, adapter % 3 * 255 + g.integers(0, 2, m))
+        out = torch.zeros_like(base)
+        c.csa2_lora_add(bf16_dev(x), bf16_dev(a), bf16_dev(b), to_dev(adapter), base, out)
+        exact, tol = P.adapters(V.f64(x), V.f64(a), V.f64(b), adapter, host(base))
+        assert (np.abs(host(out) - exact) <= P.rounded(exact, tol, True)).all()
+
+
+@pytest.mark.parametrize("none", [0.0, 0.03, 0.97, 1.0])
+@pytest.mark.parametrize("m", [70, 5000])
+def test_rows_without_an_adapter(m, none):
+    g, adapter, x, a, b, base = make(7, m, 512, 520, 32, 3, False, none=none)
+    out = torch.full_like(base, 9.0)
+    c.csa2_lora_add(bf16_dev(x), bf16_dev(a), bf16_dev(b), to_dev(adapter), base, out)
+    exact, tol = P.adapters(V.f64(x), V.f64(a), V.f64(b), adapter, host(base))
+    assert (np.abs(host(out) - exact) <= P.rounded(exact, tol, True)).all()
+    off = to_dev(adapter < 0)
+    assert torch.equal(out[off], base[off])

@@ -144,3 +144,26 @@ def test_offsets_past_32_bits():
     assert torch.allclose(lse[:-3], torch.full((R - 3,), float(np.log(V)), device="cuda"), atol=1e-5, rtol=0)
     want = P.logprobs(host(x[-3:]), np.zeros((3, 1), np.int32), 1.0, 2)
     assert np.array_equal(host(ids[-3:]), want[3])
+
+
+@pytest.mark.parametrize("R,V", [(700, 20000), (330, 66001), (1300, 5200)])
+def test_ties_and_masks_of_many_rows(R, V):
+    test_ties_and_masks(R, V)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("R", [3, 400])
+@pytest.mark.parametrize("n_top", [1, 5, 32])
+def test_candidates_of_few_and_many_lanes(R, n_top, dtype):
+    """The likeliest tokens one, four, five or all 32 to a group, in one lane or in several, and more of them than count."""
+    V = 30011
+    g = np.random.default_rng(R + n_top)
+    x = draw(g, R, V, dtype).clamp(max=3.0)
+    for i in range(R):
+        start = int(g.integers(0, V - 300))
+        step = (1, 8, 9, 3)[i % 4]
+        count = (1, 4, 5, 33)[i // 4 % 4]
+        at = start + step * np.arange(count)
+        values = 50.0 + (0.5 * (np.arange(count) % 3) if i % 2 else np.zeros(count))
+        x[i, torch.from_numpy(at).cuda()] = torch.from_numpy(values).to(dtype).cuda()
+    check(x, g.integers(0, V, (R, 2)).astype(np.int32), 1.0, n_top)
